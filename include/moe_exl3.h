@@ -347,6 +347,101 @@ int moe_exl3_repack(const uint16_t *src, uint16_t *dst, int32_t count, int32_t n
 int moe_exl3_expand_block_scales(const uint16_t *block, int32_t n_trellis, int32_t hidden, int32_t inter,
                                  uint16_t *const *suh, uint16_t *const *svh, void *stream);
 
+/*
+ * Dense operators beside the layer: a gated feed-forward block with its
+ * backward pass, and a projection with the low-rank adapters of many requests.
+ * The block and then the projection make a dense feed-forward layer (a model's
+ * leading dense layers, or a shared expert run or tuned on its own).
+ *
+ * Types: F16 or BF16, one for all 16-bit tensors of a call; products are
+ * summed in fp32 on the matrix cores.  Sizes: hidden, inter, n_in, n_out and
+ * rank are multiples of 8, at most 65536 (rank: 256); any number of tokens T
+ * >= 0.  Activations are row-major with a row stride ld in elements, a
+ * multiple of 8, at least the row's length and at most 2^20; weights are
+ * contiguous nn.Linear matrices [out][in].  Every 16-bit tensor spans less
+ * than 2 GiB (MOE_EXL3_ERR_UNSUPPORTED).  An output may not overlap an input
+ * or another output (INVALID_ARG; column ranges of one buffer with the same
+ * ld do not overlap), except where noted.  The workspace is as for
+ * moe_exl3_layer: 256-byte aligned, ignored on entry, one per call in flight;
+ * its need does not shrink with T, so the size for the largest T serves all.
+ * The same inputs give the same bits on every call.
+ */
+#define MOE_EXL3_ACT_SILU 0
+#define MOE_EXL3_ACT_GELU_TANH 1
+
+typedef struct moe_exl3_glu_desc {
+    int32_t hidden;     /* H, columns of x */
+    int32_t inter;      /* I, columns of the result */
+    int32_t act_dtype;  /* MOE_EXL3_DT_F16 or MOE_EXL3_DT_BF16 */
+    int32_t act;        /* MOE_EXL3_ACT_* */
+} moe_exl3_glu_desc;
+
+/* Workspace bytes of moe_exl3_glu / moe_exl3_glu_backward for up to max_tokens. */
+int moe_exl3_glu_workspace_size(const moe_exl3_glu_desc *desc, int64_t max_tokens, size_t *bytes);
+int moe_exl3_glu_backward_workspace_size(const moe_exl3_glu_desc *desc, int64_t max_tokens, size_t *bytes);
+
+/*
+ * out = act(x w_gate^T) * (x w_up^T), rounded once.  x: device [T][H], out:
+ * device [T][I], w_gate, w_up: device [I][H].  pre: NULL, or device fp32
+ * [2][T][I], which receives the two products (gate, then up) for the backward
+ * pass.  T = 0 is a no-op.
+ */
+int moe_exl3_glu(const moe_exl3_glu_desc *desc, const void *x, int64_t ldx, const void *w_gate, const void *w_up,
+                 int64_t T, void *out, int64_t ldo, float *pre, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Gradients of moe_exl3_glu from dout, the gradient of its output, and the
+ * `pre` of the same x and weights:
+ *   dg = dout * up * act'(gate), du = dout * act(gate)
+ *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
+ * dx: device [T][H] or NULL; dw_gate, dw_up: device [I][H], both or neither
+ * NULL.  Outputs are written, not added to.  dg and du are rounded to the
+ * 16-bit type before the products, every output once more.  With T = 0 the
+ * weights' gradients are set to zero and x, pre and dout are not read (NULL
+ * is allowed).
+ */
+int moe_exl3_glu_backward(const moe_exl3_glu_desc *desc, const void *x, int64_t ldx, const void *w_gate,
+                          const void *w_up, const float *pre, const void *dout, int64_t lddo, int64_t T, void *dx,
+                          int64_t lddx, void *dw_gate, void *dw_up, void *workspace, size_t ws_bytes, void *stream);
+
+typedef struct moe_exl3_lora_desc {
+    int32_t n_in;        /* K, columns of x */
+    int32_t n_out;       /* N, columns of y */
+    int32_t n_adapters;  /* adapters in the stacks, 1 .. 65536 */
+    int32_t rank;        /* rows of an adapter's A in the stacks */
+    int32_t act_dtype;   /* MOE_EXL3_DT_F16 or MOE_EXL3_DT_BF16 */
+} moe_exl3_lora_desc;
+
+/* The adapters' stacks, device memory, contiguous.  From its own rank on an
+ * adapter's rows of a and columns of b take no part, whatever they hold. */
+typedef struct moe_exl3_lora_adapters {
+    const void *a;         /* [n_adapters][rank][K] */
+    const void *b;         /* [n_adapters][N][rank] */
+    const float *scales;   /* fp32 [n_adapters], or NULL: 1 */
+    const int32_t *ranks;  /* int32 [n_adapters], the rank of each, 0 .. desc.rank, or NULL: desc.rank */
+} moe_exl3_lora_adapters;
+
+/* Workspace bytes of moe_exl3_lora_linear for up to max_tokens. */
+int moe_exl3_lora_workspace_size(const moe_exl3_lora_desc *desc, int64_t max_tokens, size_t *bytes);
+
+/*
+ * y[t] = x[t] w^T + base[t] + scales[e] * b[e] (a[e] x[t]),  e = ids[t],
+ * rounded once; a token with id -1 has no adapter.  x: device [T][K]; w:
+ * device [N][K], or NULL (no projection: the adapters alone, beside one that
+ * is computed elsewhere); ids: device int32 [T], in any order; base: device
+ * [T][N] or NULL, may be y itself (same address and ld); y: device [T][N].
+ * scales[e] * a[e] x[t] is rounded to the 16-bit type for the second product
+ * where that runs on the matrix cores; y is rounded once.  A token's row
+ * depends on its own adapter only: another adapter's infinities or NaNs do
+ * not reach it.  T = 0 is a no-op.
+ *
+ * The status word (see MOE_EXL3_STATUS_OFFSET) reports BAD_INDEX for an id outside [-1, n_adapters) (the token then has no
+ * adapter) and BAD_WIDTH for a rank outside [0, desc.rank] (clamped).
+ */
+int moe_exl3_lora_linear(const moe_exl3_lora_desc *desc, const void *x, int64_t ldx, const void *w,
+                         const moe_exl3_lora_adapters *adapters, const int32_t *ids, const void *base, int64_t ldbase,
+                         int64_t T, void *y, int64_t ldy, void *workspace, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,7 +28,10 @@ STATUS_OFFSET = 8
 # every symbol the header declares
 EXPORTS = ("moe_exl3_version", "moe_exl3_strerror", "moe_exl3_workspace_size",
            "moe_exl3_layer", "moe_exl3_layer_profiled", "moe_exl3_route", "moe_exl3_decode",
-           "moe_exl3_repack", "moe_exl3_expand_block_scales", "moe_exl3_layer_noalloc")
+           "moe_exl3_repack", "moe_exl3_expand_block_scales", "moe_exl3_layer_noalloc",
+           "moe_exl3_glu_workspace_size", "moe_exl3_glu_backward_workspace_size", "moe_exl3_glu",
+           "moe_exl3_glu_backward", "moe_exl3_lora_workspace_size", "moe_exl3_lora_linear")
+ACT_SILU, ACT_GELU_TANH = 0, 1
 SCRATCH_BYTES = 64 << 20
 ORDER_ROWMAJOR, ORDER_COLMAJOR, ORDER_COLGROUPS128 = 0, 1, 2
 # launch steps of moe_exl3_layer_profiled (events[i] is recorded before step i)
@@ -49,6 +52,19 @@ class Weights(C.Structure):
                 ("router_w", C.c_void_p), ("router_bias", C.c_void_p),
                 ("shared_w", C.c_void_p * 3), ("signs", C.c_void_p), ("code_tab", C.c_void_p),
                 ("k_tab", C.c_void_p)]
+
+
+class GluDesc(C.Structure):
+    _fields_ = [("hidden", C.c_int32), ("inter", C.c_int32), ("act_dtype", C.c_int32), ("act", C.c_int32)]
+
+
+class LoraDesc(C.Structure):
+    _fields_ = [("n_in", C.c_int32), ("n_out", C.c_int32), ("n_adapters", C.c_int32), ("rank", C.c_int32),
+                ("act_dtype", C.c_int32)]
+
+
+class LoraAdapters(C.Structure):
+    _fields_ = [("a", C.c_void_p), ("b", C.c_void_p), ("scales", C.c_void_p), ("ranks", C.c_void_p)]
 
 
 class MoeError(RuntimeError):
@@ -88,6 +104,20 @@ def lib():
                                       C.c_int32, C.c_void_p]
         l.moe_exl3_expand_block_scales.argtypes = [C.c_void_p, C.c_int32, C.c_int32, C.c_int32,
                                                    C.POINTER(C.c_void_p), C.POINTER(C.c_void_p), C.c_void_p]
+        for f in ("moe_exl3_glu_workspace_size", "moe_exl3_glu_backward_workspace_size"):
+            getattr(l, f).argtypes = [C.POINTER(GluDesc), C.c_int64, C.POINTER(C.c_size_t)]
+        l.moe_exl3_lora_workspace_size.argtypes = [C.POINTER(LoraDesc), C.c_int64, C.POINTER(C.c_size_t)]
+        l.moe_exl3_glu.argtypes = [C.POINTER(GluDesc), C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int64,
+                                   C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]
+        l.moe_exl3_glu_backward.argtypes = [
+            C.POINTER(GluDesc), C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64,
+            C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]
+        l.moe_exl3_lora_linear.argtypes = [
+            C.POINTER(LoraDesc), C.c_void_p, C.c_int64, C.c_void_p, C.POINTER(LoraAdapters), C.c_void_p, C.c_void_p,
+            C.c_int64, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_size_t, C.c_void_p]
+        for f in ("moe_exl3_glu_workspace_size", "moe_exl3_glu_backward_workspace_size", "moe_exl3_glu",
+                  "moe_exl3_glu_backward", "moe_exl3_lora_workspace_size", "moe_exl3_lora_linear"):
+            getattr(l, f).restype = C.c_int
         for f in ("moe_exl3_workspace_size", "moe_exl3_layer", "moe_exl3_layer_profiled",
                   "moe_exl3_route", "moe_exl3_decode", "moe_exl3_repack", "moe_exl3_expand_block_scales",
                   "moe_exl3_layer_noalloc"):
@@ -275,3 +305,150 @@ def expand_block_scales(block, n_trellis: int, hidden: int, inter: int, suh: Seq
     vp = (C.c_void_p * 3)(*[_ptr(t) for t in svh])
     _check(lib().moe_exl3_expand_block_scales(_ptr(block), n_trellis, hidden, inter, sp, vp, _stream(stream)),
            "moe_exl3_expand_block_scales")
+
+
+# ---- dense operators: the gated feed-forward block and the projection with adapters
+
+
+def make_glu_desc(hidden: int, inter: int, act_dtype: int = DT_BF16, act: int = ACT_SILU) -> GluDesc:
+    return GluDesc(hidden, inter, act_dtype, act)
+
+
+def make_lora_desc(n_in: int, n_out: int, n_adapters: int, rank: int, act_dtype: int = DT_BF16) -> LoraDesc:
+    return LoraDesc(n_in, n_out, n_adapters, rank, act_dtype)
+
+
+def _size(fn: str, desc, max_tokens: int) -> int:
+    n = C.c_size_t(0)
+    _check(getattr(lib(), fn)(C.byref(desc), max_tokens, C.byref(n)), fn)
+    return n.value
+
+
+def glu_workspace_size(desc: GluDesc, max_tokens: int) -> int:
+    return _size("moe_exl3_glu_workspace_size", desc, max_tokens)
+
+
+def glu_backward_workspace_size(desc: GluDesc, max_tokens: int) -> int:
+    return _size("moe_exl3_glu_backward_workspace_size", desc, max_tokens)
+
+
+def lora_workspace_size(desc: LoraDesc, max_tokens: int) -> int:
+    return _size("moe_exl3_lora_workspace_size", desc, max_tokens)
+
+
+_dense_types = None
+
+
+def _dense_dtypes(act_dtype: int):
+    """Tensor dtypes accepted for a 16-bit argument (its own, or raw int16)."""
+    global _dense_types
+    if _dense_types is None:
+        import torch
+        _dense_types = {DT_BF16: (torch.bfloat16, torch.int16), DT_F16: (torch.float16, torch.int16)}
+    if act_dtype not in _dense_types:
+        raise ValueError(f"act_dtype {act_dtype} is neither DT_F16 nor DT_BF16")
+    return _dense_types[act_dtype]
+
+
+def _rows(t, rows: int, cols: int, types, device, what: str) -> int:
+    """Row stride of a [rows][cols] activation (unit column stride, rows apart
+    by any stride; a single row has none)."""
+    if t.shape != (rows, cols) or t.dtype not in types or t.device != device:
+        raise ValueError(f"{what}: expected [{rows}][{cols}] {types[0]} on {device}, got {tuple(t.shape)} {t.dtype} "
+                         f"on {t.device}")
+    ld, step = t.stride()
+    if rows <= 1:
+        ld = cols
+    if step != 1 or ld < cols:
+        raise ValueError(f"{what}: rows must be contiguous and apart, got strides {t.stride()}")
+    return ld
+
+
+def _whole(t, shape, types, device, what: str):
+    """A contiguous tensor of exactly this shape."""
+    if t.shape != shape or t.dtype not in types or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {shape} {types[0]} on {device}, got {tuple(t.shape)} "
+                         f"{t.dtype} on {t.device}")
+
+
+def _dense_device(x, workspace, what: str):
+    """The device of a call: that of x, which must be the current one, and of
+    the workspace."""
+    import torch
+    d = x.device
+    if d.type != "cuda":
+        raise ValueError(f"{what}: tensors must be on the GPU, got {d}")
+    if d.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: tensors on {d}, the current device is {torch.cuda.current_device()}")
+    if workspace is None or workspace.device != d or not workspace.is_contiguous():
+        raise ValueError(f"{what}: workspace must be a contiguous tensor on {d}")
+    return d
+
+
+def glu(desc: GluDesc, x, w_gate, w_up, out, workspace, pre=None, stream=None) -> None:
+    """out = act(x w_gate^T) * (x w_up^T) (moe_exl3_glu).  x [T][hidden], out
+    [T][inter], weights [inter][hidden]; pre: optional fp32 [2][T][inter] that
+    receives the two products for glu_backward()."""
+    d = _dense_device(x, workspace, "glu")
+    types, T, H, I = _dense_dtypes(desc.act_dtype), x.shape[0], desc.hidden, desc.inter
+    ldx, ldo = _rows(x, T, H, types, d, "glu: x"), _rows(out, T, I, types, d, "glu: out")
+    _whole(w_gate, (I, H), types, d, "glu: w_gate")
+    _whole(w_up, (I, H), types, d, "glu: w_up")
+    if pre is not None:
+        import torch
+        _whole(pre, (2, T, I), (torch.float32,), d, "glu: pre")
+    _check(lib().moe_exl3_glu(C.byref(desc), x.data_ptr(), ldx, w_gate.data_ptr(), w_up.data_ptr(), T,
+                              out.data_ptr(), ldo, _ptr(pre), workspace.data_ptr(), workspace.nbytes,
+                              _stream(stream)), "moe_exl3_glu")
+
+
+def glu_backward(desc: GluDesc, x, w_gate, w_up, pre, dout, workspace, dx=None, dw_gate=None, dw_up=None,
+                 stream=None) -> None:
+    """Gradients of glu() from dout and its `pre` (moe_exl3_glu_backward): dx
+    [T][hidden] and / or dw_gate and dw_up [inter][hidden], written."""
+    import torch
+    d = _dense_device(x, workspace, "glu_backward")
+    types, T, H, I = _dense_dtypes(desc.act_dtype), x.shape[0], desc.hidden, desc.inter
+    ldx, lddo = _rows(x, T, H, types, d, "glu_backward: x"), _rows(dout, T, I, types, d, "glu_backward: dout")
+    _whole(pre, (2, T, I), (torch.float32,), d, "glu_backward: pre")
+    lddx = H
+    if dx is not None:
+        lddx = _rows(dx, T, H, types, d, "glu_backward: dx")
+    for t, what in ((w_gate, "w_gate"), (w_up, "w_up"), (dw_gate, "dw_gate"), (dw_up, "dw_up")):
+        if t is not None:
+            _whole(t, (I, H), types, d, "glu_backward: " + what)
+    _check(lib().moe_exl3_glu_backward(C.byref(desc), x.data_ptr(), ldx, _ptr(w_gate), _ptr(w_up), pre.data_ptr(),
+                                       dout.data_ptr(), lddo, T, _ptr(dx), lddx, _ptr(dw_gate), _ptr(dw_up),
+                                       workspace.data_ptr(), workspace.nbytes, _stream(stream)),
+           "moe_exl3_glu_backward")
+
+
+def lora_linear(desc: LoraDesc, x, w, lora_a, lora_b, ids, out, workspace, base=None, scales=None, ranks=None,
+                stream=None) -> None:
+    """out[t] = x[t] w^T + base[t] + scales[e] lora_b[e] (lora_a[e] x[t]), e =
+    ids[t] (-1: no adapter) (moe_exl3_lora_linear).  x [T][n_in]; w
+    [n_out][n_in] or None; lora_a [n_adapters][rank][n_in]; lora_b
+    [n_adapters][n_out][rank]; ids int32 [T]; base [T][n_out] or None, may be
+    out; scales fp32 and ranks int32 [n_adapters] or None.  status(workspace)
+    reports ids and ranks out of range."""
+    import torch
+    d = _dense_device(x, workspace, "lora_linear")
+    types, T = _dense_dtypes(desc.act_dtype), x.shape[0]
+    K, N, n, r = desc.n_in, desc.n_out, desc.n_adapters, desc.rank
+    ldx, ldy = _rows(x, T, K, types, d, "lora_linear: x"), _rows(out, T, N, types, d, "lora_linear: out")
+    ldb = N
+    if base is not None:
+        ldb = _rows(base, T, N, types, d, "lora_linear: base")
+    if w is not None:
+        _whole(w, (N, K), types, d, "lora_linear: w")
+    _whole(lora_a, (n, r, K), types, d, "lora_linear: lora_a")
+    _whole(lora_b, (n, N, r), types, d, "lora_linear: lora_b")
+    _whole(ids, (T,), (torch.int32,), d, "lora_linear: ids")
+    if scales is not None:
+        _whole(scales, (n,), (torch.float32,), d, "lora_linear: scales")
+    if ranks is not None:
+        _whole(ranks, (n,), (torch.int32,), d, "lora_linear: ranks")
+    ad = LoraAdapters(lora_a.data_ptr(), lora_b.data_ptr(), _ptr(scales), _ptr(ranks))
+    _check(lib().moe_exl3_lora_linear(C.byref(desc), x.data_ptr(), ldx, _ptr(w), C.byref(ad), ids.data_ptr(),
+                                      _ptr(base), ldb, T, out.data_ptr(), ldy, workspace.data_ptr(),
+                                      workspace.nbytes, _stream(stream)), "moe_exl3_lora_linear")

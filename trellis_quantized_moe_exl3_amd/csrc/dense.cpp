@@ -1,0 +1,457 @@
+// Host side of the dense operators: argument checks, workspace plans, launch
+// sequences.  Declarations and the full contract are in include/moe_exl3.h.
+#include "dense.h"
+
+#include <algorithm>
+
+using namespace moe;
+
+namespace {
+
+constexpr size_t kAlign = 256;
+constexpr int64_t kMaxSize = 65536;
+constexpr int64_t kMaxLd = 1 << 20;
+constexpr int kMaxRank = 256;
+constexpr int64_t kSpanLimit = (int64_t)1 << 31;
+
+// k splits: a launch of fewer tiles than this leaves CUs idle, so its k range
+// is cut until about kSplitBlocks blocks run (two per CU), each with at least
+// kSplitStages stages (256 k) to do.
+constexpr int64_t kFullTiles = 192;
+constexpr int64_t kSplitBlocks = 512;
+constexpr int64_t kSplitStages = 8;
+
+size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+template <class T>
+T *at(void *ws, size_t off)
+{
+    return (T *)((char *)ws + off);
+}
+
+// A row-major 16-bit matrix argument.
+struct Mat {
+    const void *p;
+    int64_t rows, cols, ld;
+    int64_t span() const { return rows > 0 ? ((rows - 1) * ld + cols) * 2 : 0; }
+};
+
+// The rules of one matrix: address, row stride, extent.
+int check_mat(const Mat &m)
+{
+    if (m.rows == 0)
+        return MOE_EXL3_OK;
+    if (!m.p || m.ld < m.cols)
+        return MOE_EXL3_ERR_INVALID_ARG;
+    if (m.ld > kMaxLd)
+        return MOE_EXL3_ERR_UNSUPPORTED;
+    if (!aligned16(m.p) || m.ld % 8)
+        return MOE_EXL3_ERR_MISALIGNED;
+    if (m.rows > kSpanLimit || m.span() >= kSpanLimit)
+        return MOE_EXL3_ERR_UNSUPPORTED;
+    return MOE_EXL3_OK;
+}
+
+bool spans_meet(const void *a, int64_t an, const void *b, int64_t bn)
+{
+    return an > 0 && bn > 0 && (uintptr_t)a < (uintptr_t)b + (uint64_t)bn && (uintptr_t)b < (uintptr_t)a + (uint64_t)an;
+}
+
+// Whether two matrices share an element: their spans meet, unless they are
+// column ranges apart of one buffer (same ld).
+bool overlap(const Mat &a, const Mat &b)
+{
+    if (!a.p || !b.p || !spans_meet(a.p, a.span(), b.p, b.span()))
+        return false;
+    if (a.ld != b.ld)
+        return true;
+    const int64_t d = ((intptr_t)b.p - (intptr_t)a.p) / 2;
+    const int64_t r = ((d % a.ld) + a.ld) % a.ld;   // b's first column, from a's
+    return !(r >= a.cols && r + b.cols <= a.ld);
+}
+
+int check_dtype(int dt)
+{
+    return dt == MOE_EXL3_DT_F16 || dt == MOE_EXL3_DT_BF16 ? MOE_EXL3_OK : MOE_EXL3_ERR_UNSUPPORTED;
+}
+
+int check_size(int64_t v)
+{
+    if (v <= 0 || v % 8)
+        return MOE_EXL3_ERR_INVALID_ARG;
+    return v > kMaxSize ? MOE_EXL3_ERR_UNSUPPORTED : MOE_EXL3_OK;
+}
+
+int check_desc(const moe_exl3_glu_desc *d)
+{
+    if (!d)
+        return MOE_EXL3_ERR_INVALID_ARG;
+    for (const int rc : {check_size(d->hidden), check_size(d->inter), check_dtype(d->act_dtype)})
+        if (rc)
+            return rc;
+    if (d->act != MOE_EXL3_ACT_SILU && d->act != MOE_EXL3_ACT_GELU_TANH)
+        return MOE_EXL3_ERR_UNSUPPORTED;
+    return (int64_t)d->hidden * d->inter * 2 >= kSpanLimit ? MOE_EXL3_ERR_UNSUPPORTED : MOE_EXL3_OK;
+}
+
+int check_desc(const moe_exl3_lora_desc *d)
+{
+    if (!d || d->n_adapters <= 0)
+        return MOE_EXL3_ERR_INVALID_ARG;
+    for (const int rc : {check_size(d->n_in), check_size(d->n_out), check_size(d->rank), check_dtype(d->act_dtype)})
+        if (rc)
+            return rc;
+    if (d->rank > kMaxRank || d->n_adapters > kMaxSize)
+        return MOE_EXL3_ERR_UNSUPPORTED;
+    return (int64_t)d->n_in * d->n_out * 2 >= kSpanLimit ? MOE_EXL3_ERR_UNSUPPORTED : MOE_EXL3_OK;
+}
+
+// T tokens of contiguous rows of this length must be addressable.
+bool rows_fit(int64_t T, int64_t cols) { return T < kSpanLimit && T * cols * 2 < kSpanLimit; }
+
+int64_t tile_cols(int mode) { return mode == DENSE_GLU ? kDenseBN / 2 : kDenseBN; }
+
+// Tiles and k splits of a launch.
+struct Tiles {
+    int64_t mt, nt, splits, per;
+    size_t part() const { return splits > 1 ? (size_t)(mt * nt * splits) * kDenseBM * kDenseBN * sizeof(float) : 0; }
+};
+
+int64_t stages_of(int mode, int64_t K) { return (mode == DENSE_DX ? 2 : 1) * cdiv(K, kDenseBK); }
+
+Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K)
+{
+    Tiles t{};
+    t.mt = (mode == DENSE_DW ? 2 : 1) * cdiv(M, kDenseBM);
+    t.nt = cdiv(N, tile_cols(mode));
+    const int64_t tiles = t.mt * t.nt, stages = stages_of(mode, K);
+    int64_t s = 1;
+    if (tiles < kFullTiles)
+        s = std::max<int64_t>(1, std::min(kSplitBlocks / std::max<int64_t>(1, tiles), stages / kSplitStages));
+    t.per = std::max<int64_t>(1, cdiv(stages, s));
+    t.splits = std::max<int64_t>(1, cdiv(stages, t.per));
+    return t;
+}
+
+// Bytes of partial tiles that any launch of at most this size can need
+// (tiles x splits never exceeds kSplitBlocks or tiles x stages / kSplitStages).
+size_t part_bound(int mode, int64_t M, int64_t N, int64_t K)
+{
+    const int64_t tiles = (mode == DENSE_DW ? 2 : 1) * cdiv(M, kDenseBM) * cdiv(N, tile_cols(mode));
+    const int64_t most = stages_of(mode, K) / kSplitStages;
+    if (most <= 1 || tiles == 0)
+        return 0;
+    const int64_t blocks = tiles > kSplitBlocks ? kSplitBlocks : std::min(kSplitBlocks, tiles * most);
+    return (size_t)blocks * kDenseBM * kDenseBN * sizeof(float);
+}
+
+void set_tiles(DenseArgs &a, const Tiles &t, void *part)
+{
+    a.mt = (int)t.mt;
+    a.nt = (int)t.nt;
+    a.splits = (int)t.splits;
+    a.per = (int)t.per;
+    a.part = (float *)part;
+}
+
+struct GluPlan {
+    size_t dg, du, part, total;
+};
+
+GluPlan plan_glu(const moe_exl3_glu_desc &d, int64_t T)
+{
+    GluPlan p{};
+    p.part = kAlign;
+    p.total = p.part + align_up(part_bound(DENSE_GLU, T, d.inter, d.hidden));
+    return p;
+}
+
+GluPlan plan_glu_backward(const moe_exl3_glu_desc &d, int64_t T)
+{
+    GluPlan p{};
+    size_t o = kAlign;
+    p.dg = o;
+    o += align_up((size_t)T * d.inter * 2);
+    p.du = o;
+    o += align_up((size_t)T * d.inter * 2);
+    p.part = o;
+    o += align_up(std::max(part_bound(DENSE_DX, T, d.hidden, d.inter), part_bound(DENSE_DW, d.inter, d.hidden, T)));
+    p.total = o;
+    return p;
+}
+
+struct LoraPlan {
+    size_t mid, part, total;
+    int rpad, splits;
+};
+
+// k splits of the shrink: enough blocks to fill the GPU, each of at least 256
+// k (64 per wavefront).
+int shrink_splits(const moe_exl3_lora_desc &d, int64_t T)
+{
+    const int64_t blocks = T <= kLoraTokenBlocks ? T : cdiv(T, 16);
+    const int64_t most = std::max<int64_t>(1, d.n_in / 256);
+    return (int)std::min<int64_t>(std::min<int64_t>(most, 8), std::max<int64_t>(1, 512 / std::max<int64_t>(1, blocks)));
+}
+
+LoraPlan plan_lora(const moe_exl3_lora_desc &d, int64_t T)
+{
+    LoraPlan p{};
+    p.rpad = (int)cdiv(d.rank, 32) * 32;
+    p.splits = shrink_splits(d, T);
+    size_t o = kAlign;
+    p.mid = o;
+    // splits * T is at most 8 T, and T or 512 blocks of 16 tokens
+    const int64_t rows = std::min<int64_t>(8 * T, T + 512 * 16);
+    o += align_up((size_t)rows * p.rpad * sizeof(float));
+    p.part = o;
+    o += align_up(part_bound(DENSE_LIN, T, d.n_out, d.n_in));
+    p.total = o;
+    return p;
+}
+
+int check_ws(const void *ws, size_t have, size_t need)
+{
+    if (!ws)
+        return MOE_EXL3_ERR_INVALID_ARG;
+    if ((uintptr_t)ws % kAlign)
+        return MOE_EXL3_ERR_MISALIGNED;
+    return have < need ? MOE_EXL3_ERR_WORKSPACE : MOE_EXL3_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_exl3_glu_workspace_size(const moe_exl3_glu_desc *desc, int64_t max_tokens, size_t *bytes)
+{
+    const int rc = check_desc(desc);
+    if (rc)
+        return rc;
+    if (!bytes || max_tokens < 0)
+        return MOE_EXL3_ERR_INVALID_ARG;
+    if (!rows_fit(max_tokens, desc->hidden) || !rows_fit(max_tokens, desc->inter))
+        return MOE_EXL3_ERR_UNSUPPORTED;
+    *bytes = plan_glu(*desc, max_tokens).total;
+    return MOE_EXL3_OK;
+}
+
+int moe_exl3_glu_backward_workspace_size(const moe_exl3_glu_desc *desc, int64_t max_tokens, size_t *bytes)
+{
+    const int rc = check_desc(desc);
+    if (rc)
+        return rc;
+    if (!bytes || max_tokens < 0)
+        return MOE_EXL3_ERR_INVALID_ARG;
+    if (!rows_fit(max_tokens, desc->hidden) || !rows_fit(max_tokens, desc->inter))
+        return MOE_EXL3_ERR_UNSUPPORTED;
+    *bytes = plan_glu_backward(*desc, max_tokens).total;
+    return MOE_EXL3_OK;
+}
+
+int moe_exl3_lora_workspace_size(const moe_exl3_lora_desc *desc, int64_t max_tokens, size_t *bytes)
+{
+    const int rc = check_desc(desc);
+    if (rc)
+        return rc;
+    if (!bytes || max_tokens < 0)
+        return MOE_EXL3_ERR_INVALID_ARG;
+    if (!rows_fit(max_tokens, desc->n_in) || !rows_fit(max_tokens, desc->n_out))
+        return MOE_EXL3_ERR_UNSUPPORTED;
+    *bytes = plan_lora(*desc, max_tokens).total;
+    return MOE_EXL3_OK;
+}
+
+int moe_exl3_glu(const moe_exl3_glu_desc *desc, const void *x, int64_t ldx, const void *w_gate, const void *w_up,
+                 int64_t T, void *out, int64_t ldo, float *pre, void *workspace, size_t ws_bytes, void *stream)
+{
+    int rc = check_desc(desc);
+    if (rc)
+        return rc;
+    if (T < 0)
+        return MOE_EXL3_ERR_INVALID_ARG;
+    if (T == 0)
+        return MOE_EXL3_OK;
+    const int64_t H = desc->hidden, I = desc->inter;
+    const Mat mx{x, T, H, ldx}, mg{w_gate, I, H, H}, mu{w_up, I, H, H}, mo{out, T, I, ldo};
+    for (const Mat &m : {mx, mg, mu, mo})
+        if ((rc = check_mat(m)))
+            return rc;
+    if (!rows_fit(T, H) || !rows_fit(T, I))
+        return MOE_EXL3_ERR_UNSUPPORTED;
+    if (pre && !aligned16(pre))
+        return MOE_EXL3_ERR_MISALIGNED;
+    for (const Mat &m : {mx, mg, mu})
+        if (overlap(mo, m) || (pre && spans_meet(pre, 8 * T * I, m.p, m.span())))
+            return MOE_EXL3_ERR_INVALID_ARG;
+    if (pre && spans_meet(pre, 8 * T * I, out, mo.span()))
+        return MOE_EXL3_ERR_INVALID_ARG;
+    const GluPlan p = plan_glu(*desc, T);
+    if ((rc = check_ws(workspace, ws_bytes, p.total)))
+        return rc;
+    DenseArgs a{};
+    a.p[0] = (const uint16_t *)x;
+    a.q[0] = (const uint16_t *)w_gate;
+    a.q[1] = (const uint16_t *)w_up;
+    a.ldp = ldx;
+    a.ldq = H;
+    a.pbytes = (uint32_t)mx.span();
+    a.qbytes = (uint32_t)mg.span();
+    a.M = (int)T;
+    a.N = (int)I;
+    a.K = (int)H;
+    a.out[0] = (uint16_t *)out;
+    a.ldo = ldo;
+    a.pre = pre;
+    a.act = desc->act;
+    set_tiles(a, plan_tiles(DENSE_GLU, T, I, H), at<float>(workspace, p.part));
+    return launch_dense(DENSE_GLU, desc->act_dtype == MOE_EXL3_DT_BF16, a, (hipStream_t)stream) == hipSuccess
+               ? MOE_EXL3_OK
+               : MOE_EXL3_ERR_HIP;
+}
+
+int moe_exl3_glu_backward(const moe_exl3_glu_desc *desc, const void *x, int64_t ldx, const void *w_gate,
+                          const void *w_up, const float *pre, const void *dout, int64_t lddo, int64_t T, void *dx,
+                          int64_t lddx, void *dw_gate, void *dw_up, void *workspace, size_t ws_bytes, void *stream)
+{
+    int rc = check_desc(desc);
+    if (rc)
+        return rc;
+    if (T < 0 || !dw_gate != !dw_up || (!dx && !dw_gate))
+        return MOE_EXL3_ERR_INVALID_ARG;
+    const int64_t H = desc->hidden, I = desc->inter;
+    const Mat mx{x, T, H, ldx}, mg{w_gate, I, H, H}, mu{w_up, I, H, H}, mo{dout, T, I, lddo};
+    const Mat mdx{dx, dx ? T : 0, H, lddx}, mdg{dw_gate, dw_gate ? I : 0, H, H}, mdu{dw_up, dw_up ? I : 0, H, H};
+    for (const Mat &m : {mx, mg, mu, mo, mdx, mdg, mdu})
+        if ((rc = check_mat(m)))
+            return rc;
+    if (!rows_fit(T, H) || !rows_fit(T, I))
+        return MOE_EXL3_ERR_UNSUPPORTED;
+    if (T > 0) {
+        if (!pre)
+            return MOE_EXL3_ERR_INVALID_ARG;
+        if (!aligned16(pre))
+            return MOE_EXL3_ERR_MISALIGNED;
+    }
+    for (const Mat &o : {mdx, mdg, mdu}) {
+        for (const Mat &m : {mx, mg, mu, mo})
+            if (overlap(o, m))
+                return MOE_EXL3_ERR_INVALID_ARG;
+        if (pre && o.p && spans_meet(pre, 8 * T * I, o.p, o.span()))
+            return MOE_EXL3_ERR_INVALID_ARG;
+    }
+    if (overlap(mdx, mdg) || overlap(mdx, mdu) || overlap(mdg, mdu))
+        return MOE_EXL3_ERR_INVALID_ARG;
+    const GluPlan p = plan_glu_backward(*desc, T);
+    if ((rc = check_ws(workspace, ws_bytes, p.total)))
+        return rc;
+    const bool bf16 = desc->act_dtype == MOE_EXL3_DT_BF16;
+    hipStream_t s = (hipStream_t)stream;
+    uint16_t *dg = at<uint16_t>(workspace, p.dg), *du = at<uint16_t>(workspace, p.du);
+    if (T > 0 && launch_glu_grad(bf16, desc->act, pre, (const uint16_t *)dout, lddo, T, (int)I, dg, du, s) != hipSuccess)
+        return MOE_EXL3_ERR_HIP;
+    DenseArgs a{};
+    a.p[0] = dg;
+    a.p[1] = du;
+    a.ldp = I;
+    a.pbytes = (uint32_t)(T * I * 2);
+    a.ldq = H;
+    if (dx && T > 0) {
+        a.q[0] = (const uint16_t *)w_gate;
+        a.q[1] = (const uint16_t *)w_up;
+        a.qbytes = (uint32_t)mg.span();
+        a.M = (int)T;
+        a.N = (int)H;
+        a.K = (int)I;
+        a.out[0] = (uint16_t *)dx;
+        a.ldo = lddx;
+        set_tiles(a, plan_tiles(DENSE_DX, T, H, I), at<float>(workspace, p.part));
+        if (launch_dense(DENSE_DX, bf16, a, s) != hipSuccess)
+            return MOE_EXL3_ERR_HIP;
+    }
+    if (dw_gate) {
+        a.q[0] = (const uint16_t *)x;
+        a.q[1] = nullptr;
+        a.ldq = ldx;
+        a.qbytes = (uint32_t)mx.span();
+        a.M = (int)I;
+        a.N = (int)H;
+        a.K = (int)T;
+        a.out[0] = (uint16_t *)dw_gate;
+        a.out[1] = (uint16_t *)dw_up;
+        a.ldo = H;
+        set_tiles(a, plan_tiles(DENSE_DW, I, H, T), at<float>(workspace, p.part));
+        if (launch_dense(DENSE_DW, bf16, a, s) != hipSuccess)
+            return MOE_EXL3_ERR_HIP;
+    }
+    return MOE_EXL3_OK;
+}
+
+int moe_exl3_lora_linear(const moe_exl3_lora_desc *desc, const void *x, int64_t ldx, const void *w,
+                         const moe_exl3_lora_adapters *adapters, const int32_t *ids, const void *base, int64_t ldbase,
+                         int64_t T, void *y, int64_t ldy, void *workspace, size_t ws_bytes, void *stream)
+{
+    int rc = check_desc(desc);
+    if (rc)
+        return rc;
+    if (T < 0)
+        return MOE_EXL3_ERR_INVALID_ARG;
+    if (T == 0)
+        return MOE_EXL3_OK;
+    if (!adapters || !adapters->a || !adapters->b || !ids)
+        return MOE_EXL3_ERR_INVALID_ARG;
+    const int64_t K = desc->n_in, N = desc->n_out, n = desc->n_adapters, r = desc->rank;
+    const Mat mx{x, T, K, ldx}, mw{w, w ? N : 0, K, K}, mb{base, base ? T : 0, N, ldbase}, my{y, T, N, ldy};
+    for (const Mat &m : {mx, mw, mb, my})
+        if ((rc = check_mat(m)))
+            return rc;
+    if (!rows_fit(T, K) || !rows_fit(T, N))
+        return MOE_EXL3_ERR_UNSUPPORTED;
+    for (const void *q : {adapters->a, adapters->b, (const void *)adapters->scales, (const void *)adapters->ranks,
+                          (const void *)ids})
+        if (!aligned16(q))
+            return MOE_EXL3_ERR_MISALIGNED;
+    if (overlap(my, mx) || overlap(my, mw) || (overlap(my, mb) && !(base == y && ldbase == ldy)) ||
+        spans_meet(y, my.span(), adapters->a, 2 * n * r * K) || spans_meet(y, my.span(), adapters->b, 2 * n * r * N) ||
+        spans_meet(y, my.span(), ids, 4 * T))
+        return MOE_EXL3_ERR_INVALID_ARG;
+    const LoraPlan p = plan_lora(*desc, T);
+    if ((rc = check_ws(workspace, ws_bytes, p.total)))
+        return rc;
+    const bool bf16 = desc->act_dtype == MOE_EXL3_DT_BF16;
+    hipStream_t s = (hipStream_t)stream;
+    DenseArgs a{};
+    LoraArgs &l = a.lora;
+    l.a = (const uint16_t *)adapters->a;
+    l.b = (const uint16_t *)adapters->b;
+    l.ids = ids;
+    l.scales = adapters->scales;
+    l.ranks = adapters->ranks;
+    l.status = at<int32_t>(workspace, MOE_EXL3_STATUS_OFFSET);
+    l.mid = at<float>(workspace, p.mid);
+    l.n = (int)n;
+    l.rank = (int)r;
+    l.rpad = p.rpad;
+    l.splits = p.splits;
+    if (launch_lora_shrink(bf16, (const uint16_t *)x, ldx, T, (int)K, l, s) != hipSuccess)
+        return MOE_EXL3_ERR_HIP;
+    a.p[0] = (const uint16_t *)x;
+    a.q[0] = (const uint16_t *)w;
+    a.ldp = ldx;
+    a.ldq = K;
+    a.pbytes = (uint32_t)mx.span();
+    a.qbytes = (uint32_t)mw.span();
+    a.M = (int)T;
+    a.N = (int)N;
+    a.K = w ? (int)K : 0;   // without a projection the tiles start from zero
+    a.out[0] = (uint16_t *)y;
+    a.ldo = ldy;
+    a.base = (const uint16_t *)base;
+    a.ldbase = ldbase;
+    set_tiles(a, plan_tiles(DENSE_LIN, T, N, a.K), at<float>(workspace, p.part));
+    return launch_dense(DENSE_LIN, bf16, a, s) == hipSuccess ? MOE_EXL3_OK : MOE_EXL3_ERR_HIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,66 @@
+// Internal launchers of the dense operators (the gated feed-forward block and
+// the projection with adapters), shared with their host entry points.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "moe_exl3.h"
+
+namespace moe {
+
+// Rows (m) and columns (n) of one output tile, and the k extent of one
+// pipeline stage.
+constexpr int kDenseBM = 128;
+constexpr int kDenseBN = 128;
+constexpr int kDenseBK = 32;
+// Adapters' tokens up to which the shrink takes one token a block.
+constexpr int64_t kLoraTokenBlocks = 128;
+
+// What a tile launch computes, D[m][n] = sum_k P[m][k] Q[n][k]:
+//   GLU  P = x [T][H], Q = gate and up rows: h = act(g) * u, pre = (g, u)
+//   DX   P = dg | du [T][I], Q = Wg | Wu [I][H] read along their rows (k is
+//        the slow index): dx = dg Wg + du Wu
+//   DW   P = dg or du, Q = x, both with the token as the slow index:
+//        dWg = dg^T x, dWu = du^T x
+//   LIN  P = x [T][K], Q = W [N][K]: y = x W^T + base + the adapters' rows
+enum DenseMode { DENSE_GLU = 0, DENSE_DX = 1, DENSE_DW = 2, DENSE_LIN = 3 };
+
+// The adapters of a LIN launch.
+struct LoraArgs {
+    const uint16_t *a;       // [n][rank][K]
+    const uint16_t *b;       // [n][N][rank]
+    const int32_t *ids;      // [T], < 0: no adapter
+    const float *scales;     // [n] or NULL (1)
+    const int32_t *ranks;    // [n] or NULL (rank)
+    int32_t *status;         // status word of the call
+    float *mid;              // [splits][T][rpad] fp32: the shrink's partial sums, x A^T
+    int n, rank, rpad;       // rpad: rank rounded up to 32
+    int splits;              // k splits of the shrink
+};
+
+struct DenseArgs {
+    const uint16_t *p[2], *q[2];
+    int64_t ldp, ldq;        // elements between rows in memory
+    uint32_t pbytes, qbytes; // bytes of each tensor, from its first to its last element
+    int M, N, K;             // DX: K = I per segment; DW: M = I per tensor; GLU: N = I
+    uint16_t *out[2];
+    int64_t ldo;
+    float *pre;              // GLU: fp32 [2][T][I] or NULL
+    int act;
+    int mt, nt;              // tiles (DW: mt counts both tensors')
+    int splits, per;         // k splits and stages of each
+    float *part;             // splits > 1: partial tiles, fragment order
+    const uint16_t *base;    // LIN: added rows or NULL
+    int64_t ldbase;
+    LoraArgs lora;
+};
+
+hipError_t launch_dense(int mode, bool bf16, const DenseArgs &a, hipStream_t s);
+hipError_t launch_glu_grad(bool bf16, int act, const float *pre, const uint16_t *dh, int64_t lddh, int64_t T, int I,
+                           uint16_t *dg, uint16_t *du, hipStream_t s);
+hipError_t launch_lora_shrink(bool bf16, const uint16_t *x, int64_t ldx, int64_t T, int K, const LoraArgs &l,
+                              hipStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,139 @@
+// Tile pieces of the dense operators' matrix products: operand loaders,
+// fragment reads and the pipelined k loop.
+//
+// D[m][n] = sum_k P[m][k] Q[n][k] on v_mfma_f32_16x16x32 with Q as the
+// instruction's row operand, so that a lane ends with four consecutive n of
+// one m: lane l of a 16 x 16 block holds m = l % 16, n = 4 (l / 16) + 0..3,
+// one 8-byte store of 16-bit results.  Both operands pass through LDS in a
+// ring of four stages of 32 k, filled by LDS-direct buffer loads (16 bytes a
+// lane, 1 KiB an instruction); lanes past the matrix or past k read through an
+// offset beyond the descriptor's range, for which the load writes zeros.
+//
+// An operand's layout in memory decides its LDS image:
+//   KC  k contiguous ([row][k]): 64-byte rows of four 16-byte pieces, piece p
+//       of row r in slot p ^ ((r >> 2) & 3), so that the 16 rows a fragment
+//       reads at one piece hit 16 distinct 4-bank groups (of 64 banks)
+//   KS  k strided ([k][row]): one LDS row per k, its 16-row chunks of 32 bytes
+//       in slot c ^ f(k), f(k) = k % 4 + 4 (k / 8 % 2): the eight k rows
+//       32 lanes read at once hit distinct 8-bank groups.  The fragment comes
+//       out of the transposing LDS read: in a group of 16 lanes, lane i passes
+//       the address of row i / 4, 8 bytes i % 4, and receives column i of
+//       those four rows (layout checked on the card).
+#pragma once
+
+#include "common.h"
+#include "dense.h"
+#include "gemm.h"
+
+namespace moe {
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
+enum Layout { KC = 0, KS = 1 };
+
+constexpr uint32_t kOutOfRange = 0x7FFFFFF0u;   // every tensor is below 2 GiB
+
+template <bool BF16>
+MOE_DEV f32x4 dense_mfma(u32x4 q, u32x4 p, f32x4 c)
+{
+    if constexpr (BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, q), __builtin_bit_cast(bf16x8, p), c,
+                                                        0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, q), __builtin_bit_cast(f16x8, p), c,
+                                                       0, 0, 0);
+}
+
+template <bool BF16>
+MOE_DEV uint32_t pack16(float lo, float hi)
+{
+    if constexpr (BF16)
+        return f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
+    else
+        return f32_to_f16_bits(lo) | ((uint32_t)f32_to_f16_bits(hi) << 16);
+}
+
+// One operand of R tile rows, loaded by NW wavefronts.
+template <int R, int LAYOUT, int NW>
+struct Operand {
+    static constexpr int kLoads = R * 64 / 1024 / NW;   // 1-KiB loads per wavefront and stage
+    static_assert(kLoads * 1024 * NW == R * 64, "whole loads");
+    uint32_t off[kLoads];                  // byte offset of the lane's 16 bytes at k = 0
+    int kp[LAYOUT == KS ? kLoads : 1];     // first k of the lane's 16 bytes
+
+    // Tile row of the lane's piece of load j (KC), and its source piece.
+    MOE_DEV static int kc_row(int w, int l, int j) { return 16 * (w + NW * j) + (l >> 2); }
+    MOE_DEV static int kc_piece(int l) { return (l & 3) ^ ((l >> 4) & 3); }
+
+    // KC: `row(r)` is the memory row of tile row r
+    template <class F>
+    MOE_DEV void init_kc(int w, int l, int64_t ld, F row)
+    {
+        kp[0] = 8 * kc_piece(l);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            off[j] = (uint32_t)(row(kc_row(w, l, j)) * ld * 2 + 2 * kp[0]);
+    }
+    // KS: tile rows are memory columns c0 ..
+    MOE_DEV void init_ks(int w, int l, int64_t ld, int c0)
+    {
+        constexpr int kPieces = R / 8;   // 16-byte pieces of an LDS row
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int piece = 64 * (w + NW * j) + l;
+            const int k = piece / kPieces, q = piece % kPieces;
+            const int f = (k & 3) | ((k >> 1) & 4);
+            const int c = 16 * ((q >> 1) ^ f) + 8 * (q & 1);
+            kp[j] = k;
+            off[j] = (uint32_t)(k * ld * 2 + (c0 + c) * 2);
+        }
+    }
+    // The loads of the stage at k0 (kend: first k past the operand or the
+    // block's share of it; the lanes from there on read zeros).
+    MOE_DEV void issue(__amdgpu_buffer_rsrc_t rs, LDS_AS uint16_t *lds, int w, int k0, int kend, uint32_t kbytes)
+    {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int k = k0 + kp[LAYOUT == KS ? j : 0];
+            const uint32_t o = k < kend ? off[j] + (uint32_t)k0 * kbytes : kOutOfRange;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LDS_AS void *)(lds + 512 * (w + NW * j)), 16, o, 0, 0, 0);
+        }
+    }
+    // Fragment of the 16 tile rows r0 + 16 i: lane l holds row l % 16,
+    // k = 8 (l / 16) + 0..7.
+    MOE_DEV static uint32_t frag_base(int l, int r0)
+    {
+        if constexpr (LAYOUT == KC)
+            return (uint32_t)((r0 + (l & 15)) * 64 + (((l >> 4) ^ ((l >> 2) & 3)) << 4));
+        const int i = l & 15, g = l >> 4, k = 8 * g + (i >> 2);
+        const int f = (k & 3) | ((k >> 1) & 4);
+        return (uint32_t)(k * 2 * R + (((r0 >> 4) ^ f) << 5) + (i & 3) * 8);
+    }
+    MOE_DEV static u32x4 frag(const LDS_AS uint16_t *lds, uint32_t base, int i)
+    {
+        if constexpr (LAYOUT == KC)
+            return *(const LDS_AS u32x4 *)((const LDS_AS char *)lds + base + 1024 * i);
+        const uint32_t o = base ^ (uint32_t)(i << 5);   // r0 is a multiple of 16 x the blocks read
+        auto at = [&](uint32_t b) {
+            return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                 (LDS_AS i16x4 *)((LDS_AS char *)const_cast<LDS_AS uint16_t *>(lds) + b)));
+        };
+        const u32x2 lo = at(o), hi = at(o + 4 * 2 * R);
+        return (u32x4){lo[0], lo[1], hi[0], hi[1]};
+    }
+};
+
+// Tile of a block: contiguous runs of tiles per XCD (blocks are dealt to the 8
+// XCDs round-robin), walked in groups of 8 row tiles so that the 32 tiles an
+// XCD holds at a time share their rows and columns in its L2.
+MOE_DEV void dense_tile(int L, int total, int mt, int nt, int &m, int &n)
+{
+    const int x = L & 7, j = L >> 3, q = total >> 3, r = total & 7;
+    const int id = x * q + min(x, r) + j;
+    const int group = id / (8 * nt), in = id - group * 8 * nt;
+    const int rows = min(8, mt - 8 * group);
+    m = 8 * group + in % rows;
+    n = in / rows;
+}
+
+}  // namespace moe
