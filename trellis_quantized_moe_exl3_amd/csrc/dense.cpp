@@ -156,6 +156,20 @@ void set_tiles(DenseArgs &a, const Tiles &t, void *part)
     a.part = (float *)part;
 }
 
+// GLU or LIN: few tokens stream the weights through the few-token kernel.
+int launch_forward(int mode, int dtype, DenseArgs &a, float *part, void *stream)
+{
+    const bool bf16 = dtype == MOE_EXL3_DT_BF16;
+    hipError_t e;
+    if (a.M <= kSkinnyTokens) {
+        e = launch_dense_skinny(mode, bf16, a, (hipStream_t)stream);
+    } else {
+        set_tiles(a, plan_tiles(mode, a.M, a.N, a.K), part);
+        e = launch_dense(mode, bf16, a, (hipStream_t)stream);
+    }
+    return e == hipSuccess ? MOE_EXL3_OK : MOE_EXL3_ERR_HIP;
+}
+
 struct GluPlan {
     size_t dg, du, part, total;
 };
@@ -164,7 +178,7 @@ GluPlan plan_glu(const moe_exl3_glu_desc &d, int64_t T)
 {
     GluPlan p{};
     p.part = kAlign;
-    p.total = p.part + align_up(part_bound(DENSE_GLU, T, d.inter, d.hidden));
+    p.total = p.part + (T <= kSkinnyTokens ? 0 : align_up(part_bound(DENSE_GLU, T, d.inter, d.hidden)));
     return p;
 }
 
@@ -187,13 +201,16 @@ struct LoraPlan {
     int rpad, splits;
 };
 
-// k splits of the shrink: enough blocks to fill the GPU, each of at least 256
-// k (64 per wavefront).
+// k splits of the shrink: a block then streams at most 128 KiB of its adapter,
+// as long as there are CUs for more blocks.
+constexpr int64_t kShrinkBytes = 128 << 10;
+constexpr int64_t kShrinkSplits = 8, kShrinkBlocks = 512;
+
 int shrink_splits(const moe_exl3_lora_desc &d, int64_t T)
 {
     const int64_t blocks = T <= kLoraTokenBlocks ? T : cdiv(T, 16);
-    const int64_t most = std::max<int64_t>(1, d.n_in / 256);
-    return (int)std::min<int64_t>(std::min<int64_t>(most, 8), std::max<int64_t>(1, 512 / std::max<int64_t>(1, blocks)));
+    const int64_t want = cdiv((int64_t)d.n_in * d.rank * 2, kShrinkBytes);
+    return (int)std::min(std::min(want, kShrinkSplits), std::max<int64_t>(1, kShrinkBlocks / std::max<int64_t>(1, blocks)));
 }
 
 LoraPlan plan_lora(const moe_exl3_lora_desc &d, int64_t T)
@@ -204,10 +221,10 @@ LoraPlan plan_lora(const moe_exl3_lora_desc &d, int64_t T)
     size_t o = kAlign;
     p.mid = o;
     // splits * T is at most 8 T, and T or 512 blocks of 16 tokens
-    const int64_t rows = std::min<int64_t>(8 * T, T + 512 * 16);
+    const int64_t rows = std::min(kShrinkSplits * T, T + kShrinkBlocks * 16);
     o += align_up((size_t)rows * p.rpad * sizeof(float));
     p.part = o;
-    o += align_up(part_bound(DENSE_LIN, T, d.n_out, d.n_in));
+    o += T <= kSkinnyTokens ? 0 : align_up(part_bound(DENSE_LIN, T, d.n_out, d.n_in));
     p.total = o;
     return p;
 }
@@ -306,10 +323,7 @@ int moe_exl3_glu(const moe_exl3_glu_desc *desc, const void *x, int64_t ldx, cons
     a.ldo = ldo;
     a.pre = pre;
     a.act = desc->act;
-    set_tiles(a, plan_tiles(DENSE_GLU, T, I, H), at<float>(workspace, p.part));
-    return launch_dense(DENSE_GLU, desc->act_dtype == MOE_EXL3_DT_BF16, a, (hipStream_t)stream) == hipSuccess
-               ? MOE_EXL3_OK
-               : MOE_EXL3_ERR_HIP;
+    return launch_forward(DENSE_GLU, desc->act_dtype, a, at<float>(workspace, p.part), stream);
 }
 
 int moe_exl3_glu_backward(const moe_exl3_glu_desc *desc, const void *x, int64_t ldx, const void *w_gate,
@@ -450,8 +464,7 @@ int moe_exl3_lora_linear(const moe_exl3_lora_desc *desc, const void *x, int64_t 
     a.ldo = ldy;
     a.base = (const uint16_t *)base;
     a.ldbase = ldbase;
-    set_tiles(a, plan_tiles(DENSE_LIN, T, N, a.K), at<float>(workspace, p.part));
-    return launch_dense(DENSE_LIN, bf16, a, s) == hipSuccess ? MOE_EXL3_OK : MOE_EXL3_ERR_HIP;
+    return launch_forward(DENSE_LIN, desc->act_dtype, a, at<float>(workspace, p.part), stream);
 }
 
 }  // extern "C"

@@ -15,7 +15,9 @@ namespace moe {
 constexpr int kDenseBM = 128;
 constexpr int kDenseBN = 128;
 constexpr int kDenseBK = 32;
-// Adapters' tokens up to which the shrink takes one token a block.
+// Tokens up to which the forward operators take the few-token kernel.
+constexpr int64_t kSkinnyTokens = 64;
+// Tokens up to which the shrink takes one token a block.
 constexpr int64_t kLoraTokenBlocks = 128;
 
 // What a tile launch computes, D[m][n] = sum_k P[m][k] Q[n][k]:
@@ -58,6 +60,8 @@ struct DenseArgs {
 };
 
 hipError_t launch_dense(int mode, bool bf16, const DenseArgs &a, hipStream_t s);
+// GLU or LIN of at most kSkinnyTokens tokens.
+hipError_t launch_dense_skinny(int mode, bool bf16, const DenseArgs &a, hipStream_t s);
 hipError_t launch_glu_grad(bool bf16, int act, const float *pre, const uint16_t *dh, int64_t lddh, int64_t T, int I,
                            uint16_t *dg, uint16_t *du, hipStream_t s);
 hipError_t launch_lora_shrink(bool bf16, const uint16_t *x, int64_t ldx, int64_t T, int K, const LoraArgs &l,

@@ -53,6 +53,37 @@ constexpr int kDenseNI = kDenseTM / 16, kDenseNJ = kDenseTN / 16;
 template <int MODE>
 constexpr int kDenseCols = MODE == DENSE_GLU ? kDenseBN / 2 : kDenseBN;
 
+// Four consecutive columns n of row m: h, and pre where it is kept (in fp32:
+// 16-bit pre-activations would add their rounding to every gradient).
+template <bool BF16>
+MOE_DEV void glu_store(const DenseArgs &a, int m, int n, f32x4 g, f32x4 u)
+{
+    float h[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        h[r] = act_value(a.act, g[r]) * u[r];
+    *(u32x2 *)(a.out[0] + (int64_t)m * a.ldo + n) = (u32x2){pack16<BF16>(h[0], h[1]), pack16<BF16>(h[2], h[3])};
+    if (a.pre) {
+        float *p = a.pre + (int64_t)m * a.N + n;
+        *(f32x4 *)p = g;
+        *(f32x4 *)(p + (int64_t)a.M * a.N) = u;
+    }
+}
+
+// Four consecutive columns n of row m of y, with the base added.
+template <bool BF16>
+MOE_DEV void lin_store(const DenseArgs &a, int m, int n, f32x4 y)
+{
+    if (a.base) {
+        const u32x2 b = *(const u32x2 *)(a.base + (int64_t)m * a.ldbase + n);
+        y[0] += act_to_f32<BF16>((uint16_t)b[0]);
+        y[1] += act_to_f32<BF16>((uint16_t)(b[0] >> 16));
+        y[2] += act_to_f32<BF16>((uint16_t)b[1]);
+        y[3] += act_to_f32<BF16>((uint16_t)(b[1] >> 16));
+    }
+    *(u32x2 *)(a.out[0] + (int64_t)m * a.ldo + n) = (u32x2){pack16<BF16>(y[0], y[1]), pack16<BF16>(y[2], y[3])};
+}
+
 // Epilogue of the 16 rows m0 .. of a wavefront's NJ column blocks from n0 on
 // (GLU: n0 is the first of its NJ / 2 x 16 intermediate columns).
 template <int MODE, bool BF16, int NJ>
@@ -61,46 +92,19 @@ MOE_DEV void dense_store(const DenseArgs &a, int z, int m0, int n0, int l, f32x4
     const int m = m0 + (l & 15), nl = 4 * (l >> 4);
     if (m >= a.M)
         return;
-    if constexpr (MODE == DENSE_GLU) {
+    constexpr int kBlocks = MODE == DENSE_GLU ? NJ / 2 : NJ;
 #pragma unroll
-        for (int j = 0; j < NJ / 2; ++j) {
-            const int n = n0 + 16 * j + nl;
-            if (n >= a.N)
-                continue;
-            const f32x4 g = v[j], u = v[j + NJ / 2];
-            float h[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                h[r] = act_value(a.act, g[r]) * u[r];
-            *(u32x2 *)(a.out[0] + (int64_t)m * a.ldo + n) =
-                (u32x2){pack16<BF16>(h[0], h[1]), pack16<BF16>(h[2], h[3])};
-            if (a.pre) {
-                // kept in fp32: 16-bit pre-activations would add their rounding
-                // to every gradient
-                float *p = a.pre + (int64_t)m * a.N + n;
-                *(f32x4 *)p = g;
-                *(f32x4 *)(p + (int64_t)a.M * a.N) = u;
-            }
-        }
-    } else {
-        uint16_t *out = a.out[MODE == DENSE_DW ? z : 0];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int n = n0 + 16 * j + nl;
-            if (n >= a.N)
-                continue;
-            f32x4 y = v[j];
-            if constexpr (MODE == DENSE_LIN) {
-                if (a.base) {
-                    const u32x2 b = *(const u32x2 *)(a.base + (int64_t)m * a.ldbase + n);
-                    y[0] += act_to_f32<BF16>((uint16_t)b[0]);
-                    y[1] += act_to_f32<BF16>((uint16_t)(b[0] >> 16));
-                    y[2] += act_to_f32<BF16>((uint16_t)b[1]);
-                    y[3] += act_to_f32<BF16>((uint16_t)(b[1] >> 16));
-                }
-            }
-            *(u32x2 *)(out + (int64_t)m * a.ldo + n) = (u32x2){pack16<BF16>(y[0], y[1]), pack16<BF16>(y[2], y[3])};
-        }
+    for (int j = 0; j < kBlocks; ++j) {
+        const int n = n0 + 16 * j + nl;
+        if (n >= a.N)
+            continue;
+        if constexpr (MODE == DENSE_GLU)
+            glu_store<BF16>(a, m, n, v[j], v[j + kBlocks]);
+        else if constexpr (MODE == DENSE_LIN)
+            lin_store<BF16>(a, m, n, v[j]);
+        else
+            *(u32x2 *)(a.out[MODE == DENSE_DW ? z : 0] + (int64_t)m * a.ldo + n) =
+                (u32x2){pack16<BF16>(v[j][0], v[j][1]), pack16<BF16>(v[j][2], v[j][3])};
     }
 }
 

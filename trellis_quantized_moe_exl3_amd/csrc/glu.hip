@@ -1,6 +1,6 @@
 // The gated feed-forward block: both projections, the activation and the
 // product in one tile kernel, and its backward pass.
-#include "dense_kernel.h"
+#include "dense_skinny.h"
 
 namespace moe {
 
@@ -51,6 +51,7 @@ hipError_t launch_glu_grad(bool bf16, int act, const float *pre, const uint16_t 
 }
 
 hipError_t launch_dense_lin(bool bf16, const DenseArgs &a, hipStream_t s);
+hipError_t launch_skinny_lin(bool bf16, const DenseArgs &a, hipStream_t s);
 
 hipError_t launch_dense(int mode, bool bf16, const DenseArgs &a, hipStream_t s)
 {
@@ -60,6 +61,13 @@ hipError_t launch_dense(int mode, bool bf16, const DenseArgs &a, hipStream_t s)
     case DENSE_DW: return launch_dense_mode<DENSE_DW>(bf16, a, s);
     default: return launch_dense_lin(bf16, a, s);
     }
+}
+
+hipError_t launch_dense_skinny(int mode, bool bf16, const DenseArgs &a, hipStream_t s)
+{
+    if (mode == DENSE_LIN)
+        return launch_skinny_lin(bf16, a, s);
+    return bf16 ? launch_skinny<DENSE_GLU, true>(a, s) : launch_skinny<DENSE_GLU, false>(a, s);
 }
 
 }  // namespace moe
