@@ -18,6 +18,8 @@ constexpr int64_t kSpanLimit = (int64_t)1 << 31;
 // is cut until about kSplitBlocks blocks run (two per CU), each with at least
 // kSplitStages stages (256 k) to do.
 constexpr int64_t kFullTiles = 192;
+// Large tiles from this many on.
+constexpr int64_t kLargeTiles = 192;
 constexpr int64_t kSplitBlocks = 512;
 constexpr int64_t kSplitStages = 8;
 
@@ -111,24 +113,29 @@ int check_desc(const moe_exl3_lora_desc *d)
 // T tokens of contiguous rows of this length must be addressable.
 bool rows_fit(int64_t T, int64_t cols) { return T < kSpanLimit && T * cols * 2 < kSpanLimit; }
 
-int64_t tile_cols(int mode) { return mode == DENSE_GLU ? kDenseBN / 2 : kDenseBN; }
+int64_t tile_cols(int mode, int64_t b) { return mode == DENSE_GLU ? b / 2 : b; }
 
 // Tiles and k splits of a launch.
 struct Tiles {
-    int64_t mt, nt, splits, per;
-    size_t part() const { return splits > 1 ? (size_t)(mt * nt * splits) * kDenseBM * kDenseBN * sizeof(float) : 0; }
+    int64_t bm, mt, nt, splits, per;
 };
 
 int64_t stages_of(int mode, int64_t K) { return (mode == DENSE_DX ? 2 : 1) * cdiv(K, kDenseBK); }
 
+int64_t tiles_of(int mode, int64_t M, int64_t N, int64_t b)
+{
+    return (mode == DENSE_DW ? 2 : 1) * cdiv(M, b) * cdiv(N, tile_cols(mode, b));
+}
+
 Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K)
 {
     Tiles t{};
-    t.mt = (mode == DENSE_DW ? 2 : 1) * cdiv(M, kDenseBM);
-    t.nt = cdiv(N, tile_cols(mode));
+    t.bm = tiles_of(mode, M, N, kDenseLarge) >= kLargeTiles ? kDenseLarge : kDenseSmall;
+    t.mt = (mode == DENSE_DW ? 2 : 1) * cdiv(M, t.bm);
+    t.nt = cdiv(N, tile_cols(mode, t.bm));
     const int64_t tiles = t.mt * t.nt, stages = stages_of(mode, K);
     int64_t s = 1;
-    if (tiles < kFullTiles)
+    if (t.bm == kDenseSmall && tiles < kFullTiles)
         s = std::max<int64_t>(1, std::min(kSplitBlocks / std::max<int64_t>(1, tiles), stages / kSplitStages));
     t.per = std::max<int64_t>(1, cdiv(stages, s));
     t.splits = std::max<int64_t>(1, cdiv(stages, t.per));
@@ -139,16 +146,16 @@ Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K)
 // (tiles x splits never exceeds kSplitBlocks or tiles x stages / kSplitStages).
 size_t part_bound(int mode, int64_t M, int64_t N, int64_t K)
 {
-    const int64_t tiles = (mode == DENSE_DW ? 2 : 1) * cdiv(M, kDenseBM) * cdiv(N, tile_cols(mode));
-    const int64_t most = stages_of(mode, K) / kSplitStages;
+    const int64_t tiles = tiles_of(mode, M, N, kDenseSmall), most = stages_of(mode, K) / kSplitStages;
     if (most <= 1 || tiles == 0)
         return 0;
     const int64_t blocks = tiles > kSplitBlocks ? kSplitBlocks : std::min(kSplitBlocks, tiles * most);
-    return (size_t)blocks * kDenseBM * kDenseBN * sizeof(float);
+    return (size_t)blocks * kDenseSmall * kDenseSmall * sizeof(float);
 }
 
 void set_tiles(DenseArgs &a, const Tiles &t, void *part)
 {
+    a.bm = (int)t.bm;
     a.mt = (int)t.mt;
     a.nt = (int)t.nt;
     a.splits = (int)t.splits;
@@ -198,31 +205,16 @@ GluPlan plan_glu_backward(const moe_exl3_glu_desc &d, int64_t T)
 
 struct LoraPlan {
     size_t mid, part, total;
-    int rpad, splits;
+    int rpad;
 };
-
-// k splits of the shrink: a block then streams at most 128 KiB of its adapter,
-// as long as there are CUs for more blocks.
-constexpr int64_t kShrinkBytes = 128 << 10;
-constexpr int64_t kShrinkSplits = 8, kShrinkBlocks = 512;
-
-int shrink_splits(const moe_exl3_lora_desc &d, int64_t T)
-{
-    const int64_t blocks = T <= kLoraTokenBlocks ? T : cdiv(T, 16);
-    const int64_t want = cdiv((int64_t)d.n_in * d.rank * 2, kShrinkBytes);
-    return (int)std::min(std::min(want, kShrinkSplits), std::max<int64_t>(1, kShrinkBlocks / std::max<int64_t>(1, blocks)));
-}
 
 LoraPlan plan_lora(const moe_exl3_lora_desc &d, int64_t T)
 {
     LoraPlan p{};
     p.rpad = (int)cdiv(d.rank, 32) * 32;
-    p.splits = shrink_splits(d, T);
     size_t o = kAlign;
     p.mid = o;
-    // splits * T is at most 8 T, and T or 512 blocks of 16 tokens
-    const int64_t rows = std::min(kShrinkSplits * T, T + kShrinkBlocks * 16);
-    o += align_up((size_t)rows * p.rpad * sizeof(float));
+    o += align_up((size_t)T * p.rpad * 2);
     p.part = o;
     o += T <= kSkinnyTokens ? 0 : align_up(part_bound(DENSE_LIN, T, d.n_out, d.n_in));
     p.total = o;
@@ -275,7 +267,7 @@ int moe_exl3_lora_workspace_size(const moe_exl3_lora_desc *desc, int64_t max_tok
         return rc;
     if (!bytes || max_tokens < 0)
         return MOE_EXL3_ERR_INVALID_ARG;
-    if (!rows_fit(max_tokens, desc->n_in) || !rows_fit(max_tokens, desc->n_out))
+    if (!rows_fit(max_tokens, desc->n_in) || !rows_fit(max_tokens, desc->n_out) || !rows_fit(max_tokens, kMaxRank))
         return MOE_EXL3_ERR_UNSUPPORTED;
     *bytes = plan_lora(*desc, max_tokens).total;
     return MOE_EXL3_OK;
@@ -421,7 +413,7 @@ int moe_exl3_lora_linear(const moe_exl3_lora_desc *desc, const void *x, int64_t 
     for (const Mat &m : {mx, mw, mb, my})
         if ((rc = check_mat(m)))
             return rc;
-    if (!rows_fit(T, K) || !rows_fit(T, N))
+    if (!rows_fit(T, K) || !rows_fit(T, N) || !rows_fit(T, kMaxRank))
         return MOE_EXL3_ERR_UNSUPPORTED;
     for (const void *q : {adapters->a, adapters->b, (const void *)adapters->scales, (const void *)adapters->ranks,
                           (const void *)ids})
@@ -444,12 +436,11 @@ int moe_exl3_lora_linear(const moe_exl3_lora_desc *desc, const void *x, int64_t 
     l.scales = adapters->scales;
     l.ranks = adapters->ranks;
     l.status = at<int32_t>(workspace, MOE_EXL3_STATUS_OFFSET);
-    l.mid = at<float>(workspace, p.mid);
+    l.mid = at<uint16_t>(workspace, p.mid);
     l.n = (int)n;
     l.rank = (int)r;
     l.rpad = p.rpad;
-    l.splits = p.splits;
-    if (launch_lora_shrink(bf16, (const uint16_t *)x, ldx, T, (int)K, l, s) != hipSuccess)
+    if (launch_lora_shrink(bf16, (const uint16_t *)x, ldx, (uint32_t)mx.span(), T, (int)K, l, s) != hipSuccess)
         return MOE_EXL3_ERR_HIP;
     a.p[0] = (const uint16_t *)x;
     a.q[0] = (const uint16_t *)w;

@@ -10,16 +10,13 @@
 
 namespace moe {
 
-// Rows (m) and columns (n) of one output tile, and the k extent of one
-// pipeline stage.
-constexpr int kDenseBM = 128;
-constexpr int kDenseBN = 128;
+// Rows and columns of the two output tiles (a GLU tile's columns are half gate,
+// half up), and the k extent of one pipeline stage.
+constexpr int kDenseSmall = 128;
+constexpr int kDenseLarge = 256;
 constexpr int kDenseBK = 32;
 // Tokens up to which the forward operators take the few-token kernel.
 constexpr int64_t kSkinnyTokens = 64;
-// Tokens up to which the shrink takes one token a block.
-constexpr int64_t kLoraTokenBlocks = 128;
-
 // What a tile launch computes, D[m][n] = sum_k P[m][k] Q[n][k]:
 //   GLU  P = x [T][H], Q = gate and up rows: h = act(g) * u, pre = (g, u)
 //   DX   P = dg | du [T][I], Q = Wg | Wu [I][H] read along their rows (k is
@@ -37,9 +34,8 @@ struct LoraArgs {
     const float *scales;     // [n] or NULL (1)
     const int32_t *ranks;    // [n] or NULL (rank)
     int32_t *status;         // status word of the call
-    float *mid;              // [splits][T][rpad] fp32: the shrink's partial sums, x A^T
+    uint16_t *mid;           // [T][rpad] s_a x A_a^T in 16 bits, zeros from the adapter's rank on
     int n, rank, rpad;       // rpad: rank rounded up to 32
-    int splits;              // k splits of the shrink
 };
 
 struct DenseArgs {
@@ -51,6 +47,7 @@ struct DenseArgs {
     int64_t ldo;
     float *pre;              // GLU: fp32 [2][T][I] or NULL
     int act;
+    int bm;                  // tile: kDenseSmall or kDenseLarge
     int mt, nt;              // tiles (DW: mt counts both tensors')
     int splits, per;         // k splits and stages of each
     float *part;             // splits > 1: partial tiles, fragment order
@@ -64,7 +61,7 @@ hipError_t launch_dense(int mode, bool bf16, const DenseArgs &a, hipStream_t s);
 hipError_t launch_dense_skinny(int mode, bool bf16, const DenseArgs &a, hipStream_t s);
 hipError_t launch_glu_grad(bool bf16, int act, const float *pre, const uint16_t *dh, int64_t lddh, int64_t T, int I,
                            uint16_t *dg, uint16_t *du, hipStream_t s);
-hipError_t launch_lora_shrink(bool bf16, const uint16_t *x, int64_t ldx, int64_t T, int K, const LoraArgs &l,
-                              hipStream_t s);
+hipError_t launch_lora_shrink(bool bf16, const uint16_t *x, int64_t ldx, uint32_t xbytes, int64_t T, int K,
+                              const LoraArgs &l, hipStream_t s);
 
 }  // namespace moe

@@ -41,17 +41,23 @@ struct DenseTraits {
     static constexpr int kQL = (MODE == DENSE_DX || MODE == DENSE_DW) ? KS : KC;
 };
 
-constexpr int kDenseWM = 2, kDenseWN = 2;                     // wavefronts over m and n
-constexpr int kDenseNW = kDenseWM * kDenseWN;
-constexpr int kDenseTM = kDenseBM / kDenseWM, kDenseTN = kDenseBN / kDenseWN;
-constexpr int kDenseNI = kDenseTM / 16, kDenseNJ = kDenseTN / 16;
+// Tile shapes: WM x WN wavefronts of TM x TN outputs each.  TN = 64 in all of
+// them (see kDenseCols).
+template <int BM_, int BN_, int WM_, int WN_>
+struct DenseShape {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NW = WM * WN;
+    static constexpr int TM = BM / WM, TN = BN / WN, NI = TM / 16, NJ = TN / 16;
+    static_assert(TN == 64 && NW % 4 == 0, "GLU column interleave");
+};
+using SmallTile = DenseShape<kDenseSmall, kDenseSmall, 2, 2>;
+using LargeTile = DenseShape<kDenseLarge, kDenseLarge, 2, 4>;
 
 // Result columns n0 + .. of a tile: GLU tiles hold BN / 2 columns of both
 // projections, interleaved by 32 (tile rows 64 s + 0..31 of Q are gate columns
 // 32 s + .., the next 32 the same columns of up), so that a wavefront's 64
 // tile columns hold gate and up of the same 32 intermediate columns.
-template <int MODE>
-constexpr int kDenseCols = MODE == DENSE_GLU ? kDenseBN / 2 : kDenseBN;
+template <int MODE, class S>
+constexpr int kDenseCols = MODE == DENSE_GLU ? S::BN / 2 : S::BN;
 
 // Four consecutive columns n of row m: h, and pre where it is kept (in fp32:
 // 16-bit pre-activations would add their rounding to every gradient).
@@ -108,101 +114,19 @@ MOE_DEV void dense_store(const DenseArgs &a, int z, int m0, int n0, int l, f32x4
     }
 }
 
-// The adapters' share of a wavefront's NI x NJ blocks: for each adapter that
-// some of its tokens name, B_a's rows against s_a x A_a^T of the tokens (the
-// shrink's sums, rounded to 16 bits for the matrix cores), added to the
-// accumulators of that adapter's tokens only: another token's sum never meets
-// a product with this adapter, not even times zero, so one adapter's
-// infinities stay with its own tokens.
-template <bool BF16, int NI, int NJ>
-MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int l, f32x4 (&acc)[NI][NJ])
-{
-    const LoraArgs &lo = a.lora;
-    int id[NI];
-    uint32_t left = 0;   // bit i: this lane's token of block i is not done yet
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int t = m0 + 16 * i + (l & 15);
-        id[i] = t < a.M ? lo.ids[t] : -1;
-        if (id[i] < 0 || id[i] >= lo.n)
-            id[i] = -1;
-        else
-            left |= 1u << i;
-    }
-    for (;;) {
-        const uint64_t any = __ballot(left != 0);
-        if (!any)
-            break;
-        int mine = 0;
-#pragma unroll
-        for (int i = NI - 1; i >= 0; --i)
-            mine = (left >> i) & 1 ? id[i] : mine;
-        const int e = __builtin_amdgcn_readlane(mine, __ffsll((unsigned long long)any) - 1);
-        const float sc = lo.scales ? lo.scales[e] : 1.0f;
-        const int rk = lo.ranks ? min(max(lo.ranks[e], 0), lo.rank) : lo.rank;
-        for (int k0 = 0; k0 < rk; k0 += 32) {
-            const int k = k0 + 8 * (l >> 4);
-            u32x4 q[NJ];
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int n = n0 + 16 * j + (l & 15);
-                q[j] = (u32x4){};
-                if (n < a.N && k < rk) {
-                    q[j] = *(const u32x4 *)(lo.b + ((int64_t)e * a.N + n) * lo.rank + k);
-                    // columns from the adapter's own rank on are not part of it
-#pragma unroll
-                    for (int d = 0; d < 4; ++d)
-                        q[j][d] &= (k + 2 * d < rk ? 0xFFFFu : 0u) | (k + 2 * d + 1 < rk ? 0xFFFF0000u : 0u);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const bool hit = id[i] == e;
-                if (!__ballot(hit))
-                    continue;
-                float u[8] = {};
-                if (hit && k < rk) {
-                    const int64_t t = m0 + 16 * i + (l & 15);
-                    for (int z = 0; z < lo.splits; ++z) {
-                        const f32x4 *p = (const f32x4 *)(lo.mid + ((int64_t)z * a.M + t) * lo.rpad + k);
-                        const f32x4 x0 = p[0], x1 = p[1];
-#pragma unroll
-                        for (int d = 0; d < 4; ++d) {
-                            u[d] += x0[d];
-                            u[4 + d] += x1[d];
-                        }
-                    }
-                }
-                u32x4 p;
-#pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    p[d] = pack16<BF16>(u[2 * d] * sc, u[2 * d + 1] * sc);
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    const f32x4 y = dense_mfma<BF16>(q[j], p, (f32x4){});
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[i][j][r] = hit ? acc[i][j][r] + y[r] : acc[i][j][r];
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-            if (id[i] == e)
-                left &= ~(1u << i);
-    }
-}
-
 // Fragments of one stage: NI row blocks of P and NJ of Q.
+template <class S>
 struct DenseFrags {
-    u32x4 p[kDenseNI], q[kDenseNJ];
+    u32x4 p[S::NI], q[S::NJ];
 };
 
-template <int MODE, bool BF16>
+template <int MODE, bool BF16, class S>
 struct DenseTile {
+    static constexpr int NI = S::NI, NJ = S::NJ;
+    using Frags = DenseFrags<S>;
     using TR = DenseTraits<MODE>;
-    using OP = Operand<kDenseBM, TR::kPL, kDenseNW>;
-    using OQ = Operand<kDenseBN, TR::kQL, kDenseNW>;
+    using OP = Operand<S::BM, TR::kPL, S::NW>;
+    using OQ = Operand<S::BN, TR::kQL, S::NW>;
     static constexpr int kLoads = OP::kLoads + OQ::kLoads;
     OP po;
     OQ qo;
@@ -217,24 +141,24 @@ struct DenseTile {
         const int k0 = kDenseBK * (second ? s - nsk : s);
         const int end = s < send ? kend : 0;
         po.issue(second ? pr[1] : pr[0], ring, w, k0, end, pstep);
-        qo.issue(second ? qr[1] : qr[0], ring + kDenseBM * kDenseBK, w, k0, end, qstep);
+        qo.issue(second ? qr[1] : qr[0], ring + S::BM * kDenseBK, w, k0, end, qstep);
     }
-    MOE_DEV void read(const LDS_AS uint16_t *ring, DenseFrags &f)
+    MOE_DEV void read(const LDS_AS uint16_t *ring, Frags &f)
     {
 #pragma unroll
-        for (int i = 0; i < kDenseNI; ++i)
+        for (int i = 0; i < S::NI; ++i)
             f.p[i] = OP::frag(ring, pbase, i);
 #pragma unroll
-        for (int j = 0; j < kDenseNJ; ++j)
-            f.q[j] = OQ::frag(ring + kDenseBM * kDenseBK, qbase, j);
+        for (int j = 0; j < S::NJ; ++j)
+            f.q[j] = OQ::frag(ring + S::BM * kDenseBK, qbase, j);
     }
     // Stage s in ring slot `cur`, whose fragments `f` were read during stage
     // s - 1.  "At most 2 loads' worth outstanding" (stages s + 2 and s + 3)
     // proves that this wavefront's loads of stage s + 1 have landed; past the
     // barrier every wavefront's have, and every wavefront has read slot `cur`,
     // which stage s + 4 refills.
-    MOE_DEV void stage(int s, LDS_AS uint16_t *cur, const LDS_AS uint16_t *next, const DenseFrags &f, DenseFrags &fn,
-                       f32x4 (&acc)[kDenseNI][kDenseNJ])
+    MOE_DEV void stage(int s, LDS_AS uint16_t *cur, const LDS_AS uint16_t *next, const Frags &f, Frags &fn,
+                       f32x4 (&acc)[S::NI][S::NJ])
     {
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
@@ -244,13 +168,13 @@ struct DenseTile {
         load(s + 4, cur);
         read(next, fn);
 #pragma unroll
-        for (int i = 0; i < kDenseNI; ++i)
+        for (int i = 0; i < S::NI; ++i)
 #pragma unroll
-            for (int j = 0; j < kDenseNJ; ++j)
+            for (int j = 0; j < S::NJ; ++j)
                 acc[i][j] = dense_mfma<BF16>(f.q[j], f.p[i], acc[i][j]);
     }
     MOE_DEV void run(int s0, LDS_AS uint16_t *r0, LDS_AS uint16_t *r1, LDS_AS uint16_t *r2, LDS_AS uint16_t *r3,
-                     f32x4 (&acc)[kDenseNI][kDenseNJ])
+                     f32x4 (&acc)[S::NI][S::NJ])
     {
         if (s0 >= send)
             return;
@@ -261,7 +185,7 @@ struct DenseTile {
         __builtin_amdgcn_sched_barrier(0);
         wait_vmcnt<3 * kLoads>();
         __builtin_amdgcn_s_barrier();
-        DenseFrags f0, f1;
+        Frags f0, f1;
         read(r0, f0);
         for (int s = s0; s < send; s += 4) {
             stage(s, r0, r1, f0, f1, acc);
@@ -273,14 +197,166 @@ struct DenseTile {
     }
 };
 
-template <int MODE, bool BF16>
-__global__ __launch_bounds__(64 * kDenseNW, 2) void dense_kernel(DenseArgs a)
+// The adapters of a tile's tokens, each in turn with its k stages.
+template <int BM>
+struct AdapterList {
+    static constexpr int kGroups = BM / 64;
+    int id[kGroups];           // of token 64 g + l, -1: none
+    uint64_t left[kGroups];    // tokens whose adapter is still to come
+    int e, k0, rk;             // current adapter, first k of its stage, its rank (e < 0: past the last)
+
+    MOE_DEV void next_adapter(const LoraArgs &lo)
+    {
+        e = -1;
+#pragma unroll
+        for (int g = kGroups - 1; g >= 0; --g)
+            if (left[g])
+                e = __builtin_amdgcn_readlane(id[g], __ffsll((unsigned long long)left[g]) - 1);
+        k0 = 0;
+        rk = 0;
+        if (e < 0)
+            return;
+        rk = lo.ranks ? min(max(lo.ranks[e], 0), lo.rank) : lo.rank;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+            left[g] &= ~__ballot(id[g] == e);
+    }
+    MOE_DEV void next(const LoraArgs &lo)
+    {
+        k0 += kDenseBK;
+        while (e >= 0 && k0 >= rk)   // adapters of rank 0 have no stage
+            next_adapter(lo);
+    }
+    MOE_DEV void start(const LoraArgs &lo, const LDS_AS int *ids, int l)
+    {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            id[g] = ids[64 * g + l];
+            left[g] = __ballot(id[g] >= 0);
+        }
+        e = 0;
+        rk = 0;
+        k0 = 0;
+        next(lo);
+    }
+};
+
+// The adapters' share of a tile, added to its accumulators: stages like those
+// of the k loop, one for every 32 ranks of every adapter that a token of the
+// tile names, P = the tokens' s_a x A_a^T, Q = B_a's rows, through the same
+// ring.  A stage's products are added to the sums of its adapter's tokens
+// only: another token's sum never meets them, not even times zero, so one
+// adapter's infinities stay with its own tokens.
+template <bool BF16, class S>
+MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, LDS_AS int *ids, LDS_AS uint16_t *r0,
+                         LDS_AS uint16_t *r1, LDS_AS uint16_t *r2, LDS_AS uint16_t *r3, f32x4 (&acc)[S::NI][S::NJ])
 {
-    using T = DenseTile<MODE, BF16>;
-    constexpr int kHalves = (kDenseBM + kDenseBN) * kDenseBK;
+    using OP = Operand<S::BM, KC, S::NW>;
+    using OQ = Operand<S::BN, KC, S::NW>;
+    constexpr int kLoads = OP::kLoads + OQ::kLoads;
+    const LoraArgs &lo = a.lora;
+    const int l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = w / S::WN, wn = w % S::WN;
+    if (tid < S::BM) {
+        const int id = m0 + tid < a.M ? lo.ids[m0 + tid] : -1;
+        ids[tid] = id >= 0 && id < lo.n ? id : -1;
+    }
+    __syncthreads();   // ids, and the end of the k loop's reads of the ring
+    AdapterList<S::BM> ahead, now;
+    now.start(lo, ids, l);
+    if (now.e < 0)
+        return;
+    ahead = now;
+    OP po;
+    OQ qo;
+    po.init_kc(w, l, lo.rpad, [&](int r) { return (int64_t)(m0 + r); });
+    qo.init_kc(w, l, lo.rank, [&](int r) { return (int64_t)(n0 + r); });
+    const __amdgpu_buffer_rsrc_t pr = buf_rsrc(lo.mid, (uint32_t)((int64_t)a.M * lo.rpad * 2));
+    const uint32_t bbytes = (uint32_t)((int64_t)a.N * lo.rank * 2);
+    const uint32_t pbase = OP::frag_base(l, wm * S::TM), qbase = OQ::frag_base(l, wn * S::TN);
+    int id[S::NI];
+#pragma unroll
+    for (int i = 0; i < S::NI; ++i)
+        id[i] = ids[wm * S::TM + 16 * i + (l & 15)];
+
+    auto load = [&](LDS_AS uint16_t *ring) __attribute__((always_inline)) {
+        const int e = max(ahead.e, 0);
+        const __amdgpu_buffer_rsrc_t qr = buf_rsrc(lo.b + (int64_t)e * a.N * lo.rank, bbytes);
+        po.issue(pr, ring, w, ahead.k0, ahead.rk, 2);
+        qo.issue(qr, ring + S::BM * kDenseBK, w, ahead.k0, ahead.rk, 2);
+        if (ahead.e >= 0)
+            ahead.next(lo);
+    };
+    auto stage = [&](const LDS_AS uint16_t *cur, LDS_AS uint16_t *refill) __attribute__((always_inline)) {
+        __builtin_amdgcn_sched_barrier(0);
+        wait_vmcnt<2 * kLoads>();   // stages t + 1 and t + 2 stay in flight
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        load(refill);
+        u32x4 q[S::NJ];
+#pragma unroll
+        for (int j = 0; j < S::NJ; ++j)
+            q[j] = OQ::frag(cur + S::BM * kDenseBK, qbase, j);
+        if (now.rk & 7) {
+            // an octet that the rank ends in: what follows in it is not part
+            // of the adapter (whole octets read zeros)
+            const int k = now.k0 + 8 * (l >> 4);
+#pragma unroll
+            for (int j = 0; j < S::NJ; ++j)
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    q[j][d] &= (k + 2 * d < now.rk ? 0xFFFFu : 0u) | (k + 2 * d + 1 < now.rk ? 0xFFFF0000u : 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < S::NI; ++i) {
+            const bool hit = id[i] == now.e;
+            const uint64_t any = __ballot(hit);
+            if (!any)
+                continue;
+            const u32x4 p = OP::frag(cur, pbase, i);
+            if (any == ~(uint64_t)0) {
+#pragma unroll
+                for (int j = 0; j < S::NJ; ++j)
+                    acc[i][j] = dense_mfma<BF16>(q[j], p, acc[i][j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < S::NJ; ++j) {
+                    const f32x4 y = dense_mfma<BF16>(q[j], p, (f32x4){});
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[i][j][r] = hit ? acc[i][j][r] + y[r] : acc[i][j][r];
+                }
+            }
+        }
+        now.next(lo);
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): reads done before the next barrier
+    };
+    load(r0);
+    load(r1);
+    load(r2);
+    while (now.e >= 0) {
+        stage(r0, r3);
+        if (now.e < 0)
+            break;
+        stage(r1, r0);
+        if (now.e < 0)
+            break;
+        stage(r2, r1);
+        if (now.e < 0)
+            break;
+        stage(r3, r2);
+    }
+    wait_vmcnt<0>();   // the loads past the end still write LDS
+}
+
+template <int MODE, bool BF16, class S>
+__global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
+{
+    using T = DenseTile<MODE, BF16, S>;
+    constexpr int kHalves = (S::BM + S::BN) * kDenseBK;
     __shared__ __align__(1024) uint16_t ring0[kHalves], ring1[kHalves], ring2[kHalves], ring3[kHalves];
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = w / kDenseWN, wn = w % kDenseWN;
+    const int wm = w / S::WN, wn = w % S::WN;
     const int tiles = a.mt * a.nt;
     const int split = blockIdx.x / tiles;
     int m, n;
@@ -288,7 +364,7 @@ __global__ __launch_bounds__(64 * kDenseNW, 2) void dense_kernel(DenseArgs a)
     // DW: the row tiles of the second tensor follow those of the first
     const int half = MODE == DENSE_DW ? a.mt / 2 : a.mt;
     const int z = m >= half ? 1 : 0;
-    const int m0 = (m - z * half) * kDenseBM, n0 = n * kDenseCols<MODE>;
+    const int m0 = (m - z * half) * S::BM, n0 = n * (kDenseCols<MODE, S>);
 
     T t;
     t.w = w;
@@ -301,7 +377,7 @@ __global__ __launch_bounds__(64 * kDenseNW, 2) void dense_kernel(DenseArgs a)
     t.pr[1] = MODE == DENSE_DX ? buf_rsrc(a.p[1], a.pbytes) : t.pr[0];
     if constexpr (MODE == DENSE_GLU) {
         // a wavefront's loads (16 tile rows each) all lie in one projection
-        static_assert(kDenseNW % 4 == 0, "projection of a wavefront's loads");
+        static_assert(S::NW % 4 == 0, "projection of a wavefront's loads");
         t.qr[0] = buf_rsrc(a.q[(w >> 1) & 1], a.qbytes);
         t.qr[1] = t.qr[0];
     } else {
@@ -324,83 +400,83 @@ __global__ __launch_bounds__(64 * kDenseNW, 2) void dense_kernel(DenseArgs a)
         t.qo.init_ks(w, l, a.ldq, n0);
         t.qstep = (uint32_t)(2 * a.ldq);
     }
-    t.pbase = T::OP::frag_base(l, wm * kDenseTM);
-    t.qbase = T::OQ::frag_base(l, wn * kDenseTN);
+    t.pbase = T::OP::frag_base(l, wm * S::TM);
+    t.qbase = T::OQ::frag_base(l, wn * S::TN);
 
-    f32x4 acc[kDenseNI][kDenseNJ];
+    f32x4 acc[S::NI][S::NJ];
 #pragma unroll
-    for (int i = 0; i < kDenseNI; ++i)
+    for (int i = 0; i < S::NI; ++i)
 #pragma unroll
-        for (int j = 0; j < kDenseNJ; ++j)
+        for (int j = 0; j < S::NJ; ++j)
             acc[i][j] = (f32x4){};
     t.run(s0, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1, (LDS_AS uint16_t *)ring2, (LDS_AS uint16_t *)ring3,
           acc);
 
+    // the adapters' share goes with the first k split
+    if constexpr (MODE == DENSE_LIN) {
+        __shared__ int ids[S::BM];
+        if (split == 0)
+            lora_expand<BF16, S>(a, m0, n0, tid, (LDS_AS int *)ids, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1,
+                                 (LDS_AS uint16_t *)ring2, (LDS_AS uint16_t *)ring3, acc);
+    }
     if (a.splits > 1) {
-        f32x4 *part = (f32x4 *)a.part + ((int64_t)blockIdx.x * kDenseNI * kDenseNJ) * (64 * kDenseNW) + tid;
+        f32x4 *part = (f32x4 *)a.part + ((int64_t)blockIdx.x * S::NI * S::NJ) * (64 * S::NW) + tid;
 #pragma unroll
-        for (int i = 0; i < kDenseNI; ++i)
+        for (int i = 0; i < S::NI; ++i)
 #pragma unroll
-            for (int j = 0; j < kDenseNJ; ++j)
-                part[(i * kDenseNJ + j) * (64 * kDenseNW)] = acc[i][j];
+            for (int j = 0; j < S::NJ; ++j)
+                part[(i * S::NJ + j) * (64 * S::NW)] = acc[i][j];
         return;
     }
-    const int mw = m0 + wm * kDenseTM, nw = n0 + wn * (kDenseCols<MODE> / kDenseWN);
-    if constexpr (MODE == DENSE_LIN)
-        if (a.lora.rank > 0)
-            lora_expand<BF16, kDenseNI, kDenseNJ>(a, mw, nw, l, acc);
+    const int mw = m0 + wm * S::TM, nw = n0 + wn * ((kDenseCols<MODE, S>) / S::WN);
 #pragma unroll
-    for (int i = 0; i < kDenseNI; ++i)
-        dense_store<MODE, BF16, kDenseNJ>(a, z, mw + 16 * i, nw, l, acc[i]);
+    for (int i = 0; i < S::NI; ++i)
+        dense_store<MODE, BF16, S::NJ>(a, z, mw + 16 * i, nw, l, acc[i]);
 }
 
 // Sum of the k splits' partial tiles, in split order, and the epilogue: block
 // (tile, i) finishes the 16-row blocks i of the tile's wavefronts.
-template <int MODE, bool BF16>
-__global__ __launch_bounds__(64 * kDenseNW) void dense_finish_kernel(DenseArgs a)
+template <int MODE, bool BF16, class S>
+__global__ __launch_bounds__(64 * S::NW) void dense_finish_kernel(DenseArgs a)
 {
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = w / kDenseWN, wn = w % kDenseWN;
+    const int wm = w / S::WN, wn = w % S::WN;
     const int tiles = a.mt * a.nt;
-    const int L = blockIdx.x / kDenseNI, i = blockIdx.x % kDenseNI;
+    const int L = blockIdx.x / S::NI, i = blockIdx.x % S::NI;
     int m, n;
     dense_tile(L, tiles, a.mt, a.nt, m, n);
     const int half = MODE == DENSE_DW ? a.mt / 2 : a.mt;
     const int z = m >= half ? 1 : 0;
-    const int m0 = (m - z * half) * kDenseBM, n0 = n * kDenseCols<MODE>;
-    const f32x4 *part = (const f32x4 *)a.part + ((int64_t)L * kDenseNI + i) * kDenseNJ * (64 * kDenseNW) + tid;
-    const int64_t step = (int64_t)tiles * kDenseNI * kDenseNJ * (64 * kDenseNW);
-    f32x4 acc[1][kDenseNJ];
+    const int m0 = (m - z * half) * S::BM, n0 = n * (kDenseCols<MODE, S>);
+    const f32x4 *part = (const f32x4 *)a.part + ((int64_t)L * S::NI + i) * S::NJ * (64 * S::NW) + tid;
+    const int64_t step = (int64_t)tiles * S::NI * S::NJ * (64 * S::NW);
+    f32x4 acc[1][S::NJ];
 #pragma unroll
-    for (int j = 0; j < kDenseNJ; ++j)
-        acc[0][j] = part[j * (64 * kDenseNW)];
+    for (int j = 0; j < S::NJ; ++j)
+        acc[0][j] = part[j * (64 * S::NW)];
     for (int k = 1; k < a.splits; ++k)
 #pragma unroll
-        for (int j = 0; j < kDenseNJ; ++j)
-            acc[0][j] += part[k * step + j * (64 * kDenseNW)];
-    const int mw = m0 + wm * kDenseTM + 16 * i, nw = n0 + wn * (kDenseCols<MODE> / kDenseWN);
-    if constexpr (MODE == DENSE_LIN)
-        if (a.lora.rank > 0)
-            lora_expand<BF16, 1, kDenseNJ>(a, mw, nw, l, acc);
-    dense_store<MODE, BF16, kDenseNJ>(a, z, mw, nw, l, acc[0]);
+        for (int j = 0; j < S::NJ; ++j)
+            acc[0][j] += part[k * step + j * (64 * S::NW)];
+    const int mw = m0 + wm * S::TM + 16 * i, nw = n0 + wn * ((kDenseCols<MODE, S>) / S::WN);
+    dense_store<MODE, BF16, S::NJ>(a, z, mw, nw, l, acc[0]);
+}
+
+template <int MODE, bool BF16, class S>
+hipError_t launch_dense_shape(const DenseArgs &a, hipStream_t s)
+{
+    dense_kernel<MODE, BF16, S><<<(unsigned)(a.mt * a.nt * a.splits), 64 * S::NW, 0, s>>>(a);
+    if (a.splits > 1)
+        dense_finish_kernel<MODE, BF16, S><<<(unsigned)(a.mt * a.nt * S::NI), 64 * S::NW, 0, s>>>(a);
+    return hipGetLastError();
 }
 
 template <int MODE>
 hipError_t launch_dense_mode(bool bf16, const DenseArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)(a.mt * a.nt * a.splits)), block(64 * kDenseNW);
-    if (bf16)
-        dense_kernel<MODE, true><<<grid, block, 0, s>>>(a);
-    else
-        dense_kernel<MODE, false><<<grid, block, 0, s>>>(a);
-    if (a.splits > 1) {
-        const dim3 fin((unsigned)(a.mt * a.nt * kDenseNI));
-        if (bf16)
-            dense_finish_kernel<MODE, true><<<fin, block, 0, s>>>(a);
-        else
-            dense_finish_kernel<MODE, false><<<fin, block, 0, s>>>(a);
-    }
-    return hipGetLastError();
+    if (a.bm == kDenseLarge)
+        return bf16 ? launch_dense_shape<MODE, true, LargeTile>(a, s) : launch_dense_shape<MODE, false, LargeTile>(a, s);
+    return bf16 ? launch_dense_shape<MODE, true, SmallTile>(a, s) : launch_dense_shape<MODE, false, SmallTile>(a, s);
 }
 
 }  // namespace moe

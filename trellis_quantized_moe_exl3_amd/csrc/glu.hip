@@ -1,6 +1,6 @@
 // The gated feed-forward block: both projections, the activation and the
 // product in one tile kernel, and its backward pass.
-#include "dense_skinny.h"
+#include "dense_stream.h"
 
 namespace moe {
 

@@ -1,57 +1,51 @@
 // A shared projection with the low-rank adapters of many requests: the
 // shrink x A^T per token, and the tile kernel whose epilogue expands it.
-#include "dense_skinny.h"
+#include "dense_stream.h"
 
 namespace moe {
 
-constexpr int kShrinkWaves = 8;
-
-// mid[split][t][0..rpad) = the split's share of x[t] A_a^T, a = ids[t]; zeros
-// from the adapter's own rank on; tokens without an adapter are not written.
+// mid[t][0..rpad) = scales[e] x[t] A_e^T, e = ids[t], in 16 bits for the second
+// product; zeros from the adapter's own rank on.  Tokens without an adapter are
+// not written.
 //
-// Block (f, split): `tpf` tokens (16, or 1 for few tokens) against their
-// adapters, the k share cut over the eight wavefronts.  Tokens are the matrix
-// instruction's columns, so a 16-token block that names several adapters runs
-// once per adapter and keeps each token's own result.  One token a block lets
-// all the adapters of a decode step stream at once.
-template <bool BF16, int NR>
-__global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(const uint16_t *x, int64_t ldx, int T, int K, int tpf,
-                                                          LoraArgs lo)
+// Block (f, r): `tpf` tokens (1 or 16) against 32 rows of their adapters, k cut
+// over the NW wavefronts.  Tokens are the matrix instruction's columns, so a
+// 16-token block that names several adapters runs once per adapter and each
+// token keeps its own result.  One token a block lets all the adapters of a
+// decode step stream at once, at the price of reading an adapter once per
+// token; 16 tokens a block read it once where a request's tokens stand together.
+template <bool BF16, int NW>
+__global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(const uint16_t *x, int64_t ldx, uint32_t xbytes, int T,
+                                                              int K, int tpf, LoraArgs lo)
 {
-    __shared__ f32x4 red[kShrinkWaves][NR][64];
+    using S = Stream<BF16, 1, 2, 3>;
+    __shared__ __align__(1024) uint16_t ring0[NW * S::kHalves], ring1[NW * S::kHalves], ring2[NW * S::kHalves];
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int f = blockIdx.x, z = blockIdx.y, c = l & 15, kl = 8 * (l >> 4);
+    const int f = blockIdx.x, r0 = 32 * blockIdx.y, c = l & 15;
 
-    const int r0 = blockIdx.z * 16 * NR;   // ranks above 128 take several blocks
-
-    if (f == 0 && z == 0 && r0 == 0) {
+    if (f == 0 && r0 == 0) {
         // the call's status word: ids and ranks outside their ranges
         int bad = 0;
-        for (int t = tid; t < T; t += 64 * kShrinkWaves)
-            bad |= (lo.ids[t] < -1 || lo.ids[t] >= lo.n) ? (int)MOE_EXL3_STATUS_BAD_INDEX : 0;
+        for (int t = tid; t < T; t += 64 * NW)
+            bad |= (lo.ids[t] < -1 || lo.ids[t] >= lo.n) ? 1 : 0;
         if (lo.ranks)
-            for (int e = tid; e < lo.n; e += 64 * kShrinkWaves)
-                bad |= (lo.ranks[e] < 0 || lo.ranks[e] > lo.rank) ? (int)MOE_EXL3_STATUS_BAD_WIDTH : 0;
-        const int any = __syncthreads_or(bad & (int)MOE_EXL3_STATUS_BAD_INDEX);
-        const int wide = __syncthreads_or(bad & (int)MOE_EXL3_STATUS_BAD_WIDTH);
+            for (int e = tid; e < lo.n; e += 64 * NW)
+                bad |= (lo.ranks[e] < 0 || lo.ranks[e] > lo.rank) ? 2 : 0;
+        const int index = __syncthreads_or(bad & 1), width = __syncthreads_or(bad & 2);
         if (tid == 0)
-            *lo.status = (any ? (int)MOE_EXL3_STATUS_BAD_INDEX : 0) | (wide ? (int)MOE_EXL3_STATUS_BAD_WIDTH : 0);
+            *lo.status = (index ? (int)MOE_EXL3_STATUS_BAD_INDEX : 0) | (width ? (int)MOE_EXL3_STATUS_BAD_WIDTH : 0);
     }
 
     const int t = f * tpf + c;
     int id = c < tpf && t < T ? lo.ids[t] : -1;
     if (id >= lo.n)
         id = -1;
-    // shares of 32 k, interleaved over the wavefronts of all splits
-    const int steps = (K + 31) / 32, whole = K / 32;
-    const int waves = kShrinkWaves * lo.splits, s0 = kShrinkWaves * z + w;
-    const uint16_t *xr = x + (int64_t)min(f * tpf + min(c, tpf - 1), T - 1) * ldx + kl;
-
-    f32x4 sum[NR];
-#pragma unroll
-    for (int j = 0; j < NR; ++j)
-        sum[j] = (f32x4){};
-    int rank = 0;   // of this lane's token
+    S st;
+    st.p = buf_rsrc(x, xbytes);
+    // rows past the block's tokens read zeros
+    st.init(l, K, ldx, K, [&](int r) { return (int64_t)(r < tpf ? f * tpf + r : T); },
+            [&](int r) { return (int64_t)(r0 + r); });
+    f32x4 sum[2] = {};
     bool left = id >= 0;
     for (;;) {
         const uint64_t any = __ballot(left);
@@ -59,90 +53,57 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(const ui
             break;
         const int e = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)any) - 1);
         const int rk = lo.ranks ? min(max(lo.ranks[e], 0), lo.rank) : lo.rank;
-        // rows from the adapter's own rank on repeat its last one; what they
-        // give is left out below
-        const uint16_t *ar[NR];
-#pragma unroll
-        for (int j = 0; j < NR; ++j)
-            ar[j] = lo.a + ((int64_t)e * lo.rank + max(0, min(r0 + 16 * j + c, rk - 1))) * K + kl;
-        f32x4 acc[NR];
-#pragma unroll
-        for (int j = 0; j < NR; ++j)
-            acc[j] = (f32x4){};
-        // kBatch shares' loads first, then their products
-        constexpr int kBatch = NR <= 2 ? 8 : NR == 4 ? 4 : 2;
-        for (int s = s0; s < whole; s += kBatch * waves) {
-            u32x4 p[kBatch], q[kBatch][NR];
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                const int64_t k = s + b * waves < whole ? 32 * (int64_t)(s + b * waves) : 0;
-                p[b] = *(const u32x4 *)(xr + k);
-#pragma unroll
-                for (int j = 0; j < NR; ++j)
-                    q[b][j] = *(const u32x4 *)(ar[j] + k);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b)
-                if (s + b * waves < whole)
-#pragma unroll
-                    for (int j = 0; j < NR; ++j)
-                        acc[j] = dense_mfma<BF16>(q[b][j], p[b], acc[j]);
-        }
-        if (steps > whole && whole % waves == s0) {
-            const bool in = 32 * whole + kl < K;
-            const u32x4 p = in ? *(const u32x4 *)(xr + 32 * whole) : (u32x4){};
-#pragma unroll
-            for (int j = 0; j < NR; ++j)
-                acc[j] = dense_mfma<BF16>(in ? *(const u32x4 *)(ar[j] + 32 * whole) : (u32x4){}, p, acc[j]);
-        }
+        const float sc = lo.scales ? lo.scales[e] : 1.0f;
+        // rows from the adapter's own rank on lie past its buffer: zeros
+        st.q[0] = buf_rsrc(lo.a + (int64_t)e * lo.rank * K, (uint32_t)rk * (uint32_t)K * 2u);
+        st.q[1] = st.q[0];
+        f32x4 acc[1][2] = {};
+        const int at = w * S::kHalves;
+        st.run(w, NW, (LDS_AS uint16_t *)ring0 + at, (LDS_AS uint16_t *)ring1 + at, (LDS_AS uint16_t *)ring2 + at,
+               nullptr, acc);
         if (id == e) {
-#pragma unroll
-            for (int j = 0; j < NR; ++j)
-                sum[j] = acc[j];
-            rank = rk;
+            sum[0] = acc[0][0] * sc;
+            sum[1] = acc[0][1] * sc;
             left = false;
         }
     }
-#pragma unroll
-    for (int j = 0; j < NR; ++j)
-        red[w][j][l] = sum[j];
+    // the wavefronts' sums, each in its own part of the first ring array
+    LDS_AS f32x4 *red = (LDS_AS f32x4 *)((LDS_AS uint16_t *)ring0);
+    constexpr int kStep = S::kHalves / 8;
+    red[w * kStep + l] = sum[0];
+    red[w * kStep + 64 + l] = sum[1];
     __syncthreads();
-    for (int j = w; j < NR; j += kShrinkWaves) {
-        f32x4 v = red[0][j][l];
+    if (w >= 2 || id < 0)
+        return;
+    f32x4 v = red[64 * w + l];
 #pragma unroll
-        for (int s = 1; s < kShrinkWaves; ++s)
-            v += red[s][j][l];
-        const int r = r0 + 16 * j + 4 * (l >> 4);
-#pragma unroll
-        for (int d = 0; d < 4; ++d)
-            v[d] = r + d < rank ? v[d] : 0.0f;
-        if (id >= 0 && r < lo.rpad)
-            *(f32x4 *)(lo.mid + ((int64_t)z * T + t) * lo.rpad + r) = v;
+    for (int s = 1; s < NW; ++s)
+        v += red[s * kStep + 64 * w + l];
+    *(u32x2 *)(lo.mid + (int64_t)t * lo.rpad + r0 + 16 * w + 4 * (l >> 4)) =
+        (u32x2){pack16<BF16>(v[0], v[1]), pack16<BF16>(v[2], v[3])};
+}
+
+// One token a block while all blocks together read at most this much of the
+// adapters (about 6 us from L2).
+constexpr int64_t kShrinkBytes = 64 << 20;
+
+hipError_t launch_lora_shrink(bool bf16, const uint16_t *x, int64_t ldx, uint32_t xbytes, int64_t T, int K,
+                              const LoraArgs &l, hipStream_t s)
+{
+    const unsigned chunks = (unsigned)(l.rpad / 32);
+    if (T * l.rank * K * 2 <= kShrinkBytes) {
+        const dim3 grid((unsigned)T, chunks);
+        if (bf16)
+            lora_shrink_kernel<true, 8><<<grid, 512, 0, s>>>(x, ldx, xbytes, (int)T, K, 1, l);
+        else
+            lora_shrink_kernel<false, 8><<<grid, 512, 0, s>>>(x, ldx, xbytes, (int)T, K, 1, l);
+    } else {
+        const dim3 grid((unsigned)((T + 15) / 16), chunks);
+        if (bf16)
+            lora_shrink_kernel<true, 4><<<grid, 256, 0, s>>>(x, ldx, xbytes, (int)T, K, 16, l);
+        else
+            lora_shrink_kernel<false, 4><<<grid, 256, 0, s>>>(x, ldx, xbytes, (int)T, K, 16, l);
     }
-}
-
-template <bool BF16>
-static void shrink(const uint16_t *x, int64_t ldx, int T, int K, int tpf, const LoraArgs &l, hipStream_t s)
-{
-    const unsigned nb = (unsigned)((T + tpf - 1) / tpf), nz = (unsigned)l.splits;
-    if (l.rpad <= 32)
-        lora_shrink_kernel<BF16, 2><<<dim3(nb, nz), 64 * kShrinkWaves, 0, s>>>(x, ldx, T, K, tpf, l);
-    else if (l.rpad <= 64)
-        lora_shrink_kernel<BF16, 4><<<dim3(nb, nz), 64 * kShrinkWaves, 0, s>>>(x, ldx, T, K, tpf, l);
-    else
-        lora_shrink_kernel<BF16, 8><<<dim3(nb, nz, (l.rpad + 127) / 128), 64 * kShrinkWaves, 0, s>>>(x, ldx, T, K, tpf,
-                                                                                                   l);
-}
-
-hipError_t launch_lora_shrink(bool bf16, const uint16_t *x, int64_t ldx, int64_t T, int K, const LoraArgs &l,
-                              hipStream_t s)
-{
-    const int tpf = T <= kLoraTokenBlocks ? 1 : 16;
-    if (bf16)
-        shrink<true>(x, ldx, (int)T, K, tpf, l, s);
-    else
-        shrink<false>(x, ldx, (int)T, K, tpf, l, s);
     return hipGetLastError();
 }
 
