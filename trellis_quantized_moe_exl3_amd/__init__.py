@@ -207,10 +207,26 @@ def status(workspace) -> int:
     return int(workspace.view(torch.uint8)[STATUS_OFFSET:STATUS_OFFSET + 4].cpu().view(torch.int32).item())
 
 
+_torch_mod = _raw_stream = None
+
+
+def _torch():
+    """torch, and its lookup of the current stream's handle (building a Stream
+    object costs as much as a launch; used where torch has no such lookup)."""
+    global _torch_mod, _raw_stream
+    if _torch_mod is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda device: torch.cuda.current_stream(device).cuda_stream)
+        _torch_mod = torch
+    return _torch_mod
+
+
 def _stream(stream) -> int:
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    device = _torch().cuda.current_device()
+    return _raw_stream(device)
 
 
 def layer(desc: Desc, weights: Weights, x, out, workspace, stream=None) -> None:
@@ -336,15 +352,14 @@ def lora_workspace_size(desc: LoraDesc, max_tokens: int) -> int:
     return _size("moe_exl3_lora_workspace_size", desc, max_tokens)
 
 
-_dense_types = None
+_dense_types = {}
 
 
 def _dense_dtypes(act_dtype: int):
     """Tensor dtypes accepted for a 16-bit argument (its own, or raw int16)."""
-    global _dense_types
-    if _dense_types is None:
-        import torch
-        _dense_types = {DT_BF16: (torch.bfloat16, torch.int16), DT_F16: (torch.float16, torch.int16)}
+    if not _dense_types:
+        torch = _torch()
+        _dense_types.update({DT_BF16: (torch.bfloat16, torch.int16), DT_F16: (torch.float16, torch.int16)})
     if act_dtype not in _dense_types:
         raise ValueError(f"act_dtype {act_dtype} is neither DT_F16 nor DT_BF16")
     return _dense_types[act_dtype]
@@ -374,12 +389,11 @@ def _whole(t, shape, types, device, what: str):
 def _dense_device(x, workspace, what: str):
     """The device of a call: that of x, which must be the current one, and of
     the workspace."""
-    import torch
     d = x.device
     if d.type != "cuda":
         raise ValueError(f"{what}: tensors must be on the GPU, got {d}")
-    if d.index != torch.cuda.current_device():
-        raise ValueError(f"{what}: tensors on {d}, the current device is {torch.cuda.current_device()}")
+    if d.index != _torch().cuda.current_device():
+        raise ValueError(f"{what}: tensors on {d}, the current device is {_torch().cuda.current_device()}")
     if workspace is None or workspace.device != d or not workspace.is_contiguous():
         raise ValueError(f"{what}: workspace must be a contiguous tensor on {d}")
     return d
@@ -395,8 +409,7 @@ def glu(desc: GluDesc, x, w_gate, w_up, out, workspace, pre=None, stream=None) -
     _whole(w_gate, (I, H), types, d, "glu: w_gate")
     _whole(w_up, (I, H), types, d, "glu: w_up")
     if pre is not None:
-        import torch
-        _whole(pre, (2, T, I), (torch.float32,), d, "glu: pre")
+        _whole(pre, (2, T, I), (_torch().float32,), d, "glu: pre")
     _check(lib().moe_exl3_glu(C.byref(desc), x.data_ptr(), ldx, w_gate.data_ptr(), w_up.data_ptr(), T,
                               out.data_ptr(), ldo, _ptr(pre), workspace.data_ptr(), workspace.nbytes,
                               _stream(stream)), "moe_exl3_glu")
@@ -406,11 +419,10 @@ def glu_backward(desc: GluDesc, x, w_gate, w_up, pre, dout, workspace, dx=None, 
                  stream=None) -> None:
     """Gradients of glu() from dout and its `pre` (moe_exl3_glu_backward): dx
     [T][hidden] and / or dw_gate and dw_up [inter][hidden], written."""
-    import torch
     d = _dense_device(x, workspace, "glu_backward")
     types, T, H, I = _dense_dtypes(desc.act_dtype), x.shape[0], desc.hidden, desc.inter
     ldx, lddo = _rows(x, T, H, types, d, "glu_backward: x"), _rows(dout, T, I, types, d, "glu_backward: dout")
-    _whole(pre, (2, T, I), (torch.float32,), d, "glu_backward: pre")
+    _whole(pre, (2, T, I), (_torch().float32,), d, "glu_backward: pre")
     lddx = H
     if dx is not None:
         lddx = _rows(dx, T, H, types, d, "glu_backward: dx")
@@ -431,7 +443,7 @@ def lora_linear(desc: LoraDesc, x, w, lora_a, lora_b, ids, out, workspace, base=
     [n_adapters][n_out][rank]; ids int32 [T]; base [T][n_out] or None, may be
     out; scales fp32 and ranks int32 [n_adapters] or None.  status(workspace)
     reports ids and ranks out of range."""
-    import torch
+    torch = _torch()
     d = _dense_device(x, workspace, "lora_linear")
     types, T = _dense_dtypes(desc.act_dtype), x.shape[0]
     K, N, n, r = desc.n_in, desc.n_out, desc.n_adapters, desc.rank

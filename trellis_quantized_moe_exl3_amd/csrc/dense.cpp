@@ -3,6 +3,7 @@
 #include "dense.h"
 
 #include <algorithm>
+#include <stdlib.h>
 
 using namespace moe;
 
@@ -11,7 +12,6 @@ namespace {
 constexpr size_t kAlign = 256;
 constexpr int64_t kMaxSize = 65536;
 constexpr int64_t kMaxLd = 1 << 20;
-constexpr int kMaxRank = 256;
 constexpr int64_t kSpanLimit = (int64_t)1 << 31;
 
 // k splits: a launch of fewer tiles than this leaves CUs idle, so its k range
@@ -133,6 +133,13 @@ Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K)
     t.bm = tiles_of(mode, M, N, kDenseLarge) >= kLargeTiles ? kDenseLarge : kDenseSmall;
     t.mt = (mode == DENSE_DW ? 2 : 1) * cdiv(M, t.bm);
     t.nt = cdiv(N, tile_cols(mode, t.bm));
+    if (getenv("DT") ? atoi(getenv("DT")) && t.bm == kDenseSmall : t.bm == kDenseSmall && t.mt * t.nt < kFullTiles) {
+        t.bm = kDenseTile;
+        t.mt = (mode == DENSE_DW ? 2 : 1) * cdiv(M, t.bm);
+        t.nt = cdiv(N, tile_cols(mode, t.bm));
+        t.splits = t.per = 1;
+        return t;
+    }
     const int64_t tiles = t.mt * t.nt, stages = stages_of(mode, K);
     int64_t s = 1;
     if (t.bm == kDenseSmall && tiles < kFullTiles)

@@ -10,13 +10,17 @@
 
 namespace moe {
 
-// Rows and columns of the two output tiles (a GLU tile's columns are half gate,
+// Rows and columns of the output tiles (a GLU tile's columns are half gate,
 // half up), and the k extent of one pipeline stage.
+constexpr int kDenseTile = 64;   // wavefronts cut k (dense_stream.h)
 constexpr int kDenseSmall = 128;
 constexpr int kDenseLarge = 256;
 constexpr int kDenseBK = 32;
 // Tokens up to which the forward operators take the few-token kernel.
 constexpr int64_t kSkinnyTokens = 64;
+// Largest rank of an adapter.
+constexpr int kMaxRank = 256;
+
 // What a tile launch computes, D[m][n] = sum_k P[m][k] Q[n][k]:
 //   GLU  P = x [T][H], Q = gate and up rows: h = act(g) * u, pre = (g, u)
 //   DX   P = dg | du [T][I], Q = Wg | Wu [I][H] read along their rows (k is
@@ -47,7 +51,7 @@ struct DenseArgs {
     int64_t ldo;
     float *pre;              // GLU: fp32 [2][T][I] or NULL
     int act;
-    int bm;                  // tile: kDenseSmall or kDenseLarge
+    int bm;                  // tile: kDenseTile, kDenseSmall or kDenseLarge
     int mt, nt;              // tiles (DW: mt counts both tensors')
     int splits, per;         // k splits and stages of each
     float *part;             // splits > 1: partial tiles, fragment order

@@ -11,14 +11,16 @@
 //
 // An operand's layout in memory decides its LDS image:
 //   KC  k contiguous ([row][k]): 64-byte rows of four 16-byte pieces, piece p
-//       of row r in slot p ^ ((r >> 2) & 3), so that the 16 rows a fragment
-//       reads at one piece hit 16 distinct 4-bank groups (of 64 banks)
+//       of row r in slot p ^ 2 (r / 8 % 2).  A 16-byte LDS read serves the lanes
+//       {0-3, 12-15, 20-27}, {4-11, 16-19, 28-31} and the same of the upper half
+//       together (measured: which lane pairs count bank conflicts); with this
+//       order each such group of a fragment's lanes hits 16 distinct 4-bank
+//       groups (of 64 banks).  Slots p ^ (r / 4 % 4), right for 16 lanes in a
+//       row, cost twice the clocks.
 //   KS  k strided ([k][row]): one LDS row per k, its 16-row chunks of 32 bytes
 //       in slot c ^ f(k), f(k) = k % 4 + 4 (k / 8 % 2): the eight k rows
 //       32 lanes read at once hit distinct 8-bank groups.  The fragment comes
-//       out of the transposing LDS read: in a group of 16 lanes, lane i passes
-//       the address of row i / 4, 8 bytes i % 4, and receives column i of
-//       those four rows (layout checked on the card).
+//       out of the transposing LDS read.
 #pragma once
 
 #include "common.h"
@@ -53,6 +55,13 @@ MOE_DEV uint32_t pack16(float lo, float hi)
         return f32_to_f16_bits(lo) | ((uint32_t)f32_to_f16_bits(hi) << 16);
 }
 
+// The transposing LDS read: in a group of 16 lanes, lane i passes the address of
+// 8 bytes, part i % 4 of row i / 4, and receives column i of the four rows.
+MOE_DEV u32x2 tr_read(const LDS_AS char *at)
+{
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS i16x4 *)const_cast<LDS_AS char *>(at)));
+}
+
 // One operand of R tile rows, loaded by NW wavefronts.
 template <int R, int LAYOUT, int NW>
 struct Operand {
@@ -63,7 +72,7 @@ struct Operand {
 
     // Tile row of the lane's piece of load j (KC), and its source piece.
     MOE_DEV static int kc_row(int w, int l, int j) { return 16 * (w + NW * j) + (l >> 2); }
-    MOE_DEV static int kc_piece(int l) { return (l & 3) ^ ((l >> 4) & 3); }
+    MOE_DEV static int kc_piece(int l) { return (l & 3) ^ ((l >> 4) & 2); }
 
     // KC: `row(r)` is the memory row of tile row r
     template <class F>
@@ -104,7 +113,7 @@ struct Operand {
     MOE_DEV static uint32_t frag_base(int l, int r0)
     {
         if constexpr (LAYOUT == KC)
-            return (uint32_t)((r0 + (l & 15)) * 64 + (((l >> 4) ^ ((l >> 2) & 3)) << 4));
+            return (uint32_t)((r0 + (l & 15)) * 64 + (((l >> 4) ^ ((l >> 2) & 2)) << 4));
         const int i = l & 15, g = l >> 4, k = 8 * g + (i >> 2);
         const int f = (k & 3) | ((k >> 1) & 4);
         return (uint32_t)(k * 2 * R + (((r0 >> 4) ^ f) << 5) + (i & 3) * 8);
@@ -114,11 +123,8 @@ struct Operand {
         if constexpr (LAYOUT == KC)
             return *(const LDS_AS u32x4 *)((const LDS_AS char *)lds + base + 1024 * i);
         const uint32_t o = base ^ (uint32_t)(i << 5);   // r0 is a multiple of 16 x the blocks read
-        auto at = [&](uint32_t b) {
-            return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                 (LDS_AS i16x4 *)((LDS_AS char *)const_cast<LDS_AS uint16_t *>(lds) + b)));
-        };
-        const u32x2 lo = at(o), hi = at(o + 4 * 2 * R);
+        const LDS_AS char *at = (const LDS_AS char *)lds;
+        const u32x2 lo = tr_read(at + o), hi = tr_read(at + o + 4 * 2 * R);
         return (u32x4){lo[0], lo[1], hi[0], hi[1]};
     }
 };

@@ -158,7 +158,7 @@ struct DenseTile {
     // barrier every wavefront's have, and every wavefront has read slot `cur`,
     // which stage s + 4 refills.
     MOE_DEV void stage(int s, LDS_AS uint16_t *cur, const LDS_AS uint16_t *next, const Frags &f, Frags &fn,
-                       f32x4 (&acc)[S::NI][S::NJ])
+                       f32x4 (&acc)[NI][NJ])
     {
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
@@ -168,20 +168,43 @@ struct DenseTile {
         load(s + 4, cur);
         read(next, fn);
 #pragma unroll
-        for (int i = 0; i < S::NI; ++i)
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int j = 0; j < S::NJ; ++j)
+            for (int j = 0; j < NJ; ++j)
                 acc[i][j] = dense_mfma<BF16>(f.q[j], f.p[i], acc[i][j]);
+        if constexpr (TR::kPL == KC && TR::kQL == KC) {
+            // the next fragments' reads and the loads spread over the MFMAs,
+            // early enough that the wait at the next barrier finds them done
+            // (7168 tokens, 4096 x 2048: 213 -> 207 us).  The transposing
+            // reads' two halves a fragment leave no registers for it: there
+            // the same order spills and halves the rate.
+            constexpr int kPer = NI * NJ / (NI + NJ + kLoads);
+#pragma unroll
+            for (int r = 0; r < NI + NJ; ++r) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
+            }
+#pragma unroll
+            for (int r = 0; r < kLoads; ++r) {
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
+            }
+        }
     }
+    // `meanwhile` runs once, while the first loads are on their way.
+    template <class F>
     MOE_DEV void run(int s0, LDS_AS uint16_t *r0, LDS_AS uint16_t *r1, LDS_AS uint16_t *r2, LDS_AS uint16_t *r3,
-                     f32x4 (&acc)[S::NI][S::NJ])
+                     f32x4 (&acc)[NI][NJ], F meanwhile)
     {
-        if (s0 >= send)
+        if (s0 >= send) {
+            meanwhile();
             return;
+        }
         load(s0, r0);
         load(s0 + 1, r1);
         load(s0 + 2, r2);
         load(s0 + 3, r3);
+        meanwhile();
         __builtin_amdgcn_sched_barrier(0);
         wait_vmcnt<3 * kLoads>();
         __builtin_amdgcn_s_barrier();
@@ -197,59 +220,95 @@ struct DenseTile {
     }
 };
 
-// The adapters of a tile's tokens, each in turn with its k stages.
-template <int BM>
-struct AdapterList {
-    static constexpr int kGroups = BM / 64;
-    int id[kGroups];           // of token 64 g + l, -1: none
-    uint64_t left[kGroups];    // tokens whose adapter is still to come
-    int e, k0, rk;             // current adapter, first k of its stage, its rank (e < 0: past the last)
+// B_a's rows for 32 ranks from k0 on, without what follows the adapter's own
+// rank inside an octet (whole octets past it were read as zeros).
+template <int NJ>
+MOE_DEV void lora_cut(int rk, int k0, int l, u32x4 (&q)[NJ])
+{
+    if (k0 + 32 <= rk || !(rk & 7))
+        return;
+    const int k = k0 + 8 * (l >> 4);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            q[j][d] &= (k + 2 * d < rk ? 0xFFFFu : 0u) | (k + 2 * d + 1 < rk ? 0xFFFF0000u : 0u);
+}
 
-    MOE_DEV void next_adapter(const LoraArgs &lo)
-    {
-        e = -1;
+// An adapter's products, q = B_a's rows, p = s_a x A_a^T of 16 tokens, taken
+// into the sums of its own tokens (hit) only: another token's sum never meets
+// them, not even times zero, so one adapter's infinities stay with its own
+// tokens.
+template <bool BF16, int NJ>
+MOE_DEV void lora_products(bool hit, u32x4 p, const u32x4 (&q)[NJ], f32x4 (&acc)[NJ])
+{
 #pragma unroll
-        for (int g = kGroups - 1; g >= 0; --g)
-            if (left[g])
-                e = __builtin_amdgcn_readlane(id[g], __ffsll((unsigned long long)left[g]) - 1);
-        k0 = 0;
-        rk = 0;
-        if (e < 0)
-            return;
-        rk = lo.ranks ? min(max(lo.ranks[e], 0), lo.rank) : lo.rank;
+    for (int j = 0; j < NJ; ++j) {
+        const f32x4 y = dense_mfma<BF16>(q[j], p, acc[j]);
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-            left[g] &= ~__ballot(id[g] == e);
+        for (int r = 0; r < 4; ++r)
+            acc[j][r] = hit ? y[r] : acc[j][r];
     }
-    MOE_DEV void next(const LoraArgs &lo)
+}
+
+// The adapters of a tile's tokens as a list of stages of 32 ranks.
+template <int BM>
+struct AdapterJobs {
+    int id[BM];                         // adapter of each token, -1: none
+    int count;
+    uint32_t job[BM * (kMaxRank / 32)]; // adapter | stage << 16 | its rank << 20
+
+    // The tokens' ids, by all threads.
+    MOE_DEV void ids_of(const LoraArgs &lo, int m0, int T, int tid)
     {
-        k0 += kDenseBK;
-        while (e >= 0 && k0 >= rk)   // adapters of rank 0 have no stage
-            next_adapter(lo);
-    }
-    MOE_DEV void start(const LoraArgs &lo, const LDS_AS int *ids, int l)
-    {
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            id[g] = ids[64 * g + l];
-            left[g] = __ballot(id[g] >= 0);
+        if (tid < BM) {
+            const int t = m0 + tid, e = t < T ? lo.ids[t] : -1;
+            id[tid] = e >= 0 && e < lo.n ? e : -1;
         }
-        e = 0;
-        rk = 0;
-        k0 = 0;
-        next(lo);
+    }
+    // One wavefront, the ids being visible: the list, adapters in the order of
+    // their first tokens.
+    MOE_DEV void build(const LoraArgs &lo, int l)
+    {
+        int n = 0;
+        uint64_t left[BM / 64];
+        int mine[BM / 64], rank[BM / 64];
+#pragma unroll
+        for (int g = 0; g < BM / 64; ++g) {
+            mine[g] = id[64 * g + l];
+            left[g] = __ballot(mine[g] >= 0);
+            rank[g] = lo.rank;
+        }
+        if (lo.ranks)
+#pragma unroll
+            for (int g = 0; g < BM / 64; ++g)
+                rank[g] = min(max(lo.ranks[max(mine[g], 0)], 0), lo.rank);
+#pragma unroll
+        for (int g = 0; g < BM / 64; ++g)
+            while (left[g]) {
+                const int at = __ffsll((unsigned long long)left[g]) - 1;
+                const int e = __builtin_amdgcn_readlane(mine[g], at), rk = __builtin_amdgcn_readlane(rank[g], at);
+#pragma unroll
+                for (int h = g; h < BM / 64; ++h)
+                    left[h] &= ~__ballot(mine[h] == e);
+                const int stages = (rk + 31) / 32;
+                if (l < stages)
+                    job[n + l] = (uint32_t)e | (uint32_t)l << 16 | (uint32_t)rk << 20;
+                n += stages;
+            }
+        if (l == 0)
+            count = n;
     }
 };
 
 // The adapters' share of a tile, added to its accumulators: stages like those
 // of the k loop, one for every 32 ranks of every adapter that a token of the
 // tile names, P = the tokens' s_a x A_a^T, Q = B_a's rows, through the same
-// ring.  A stage's products are added to the sums of its adapter's tokens
-// only: another token's sum never meets them, not even times zero, so one
-// adapter's infinities stay with its own tokens.
+// ring.
 template <bool BF16, class S>
-MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, LDS_AS int *ids, LDS_AS uint16_t *r0,
-                         LDS_AS uint16_t *r1, LDS_AS uint16_t *r2, LDS_AS uint16_t *r3, f32x4 (&acc)[S::NI][S::NJ])
+MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const AdapterJobs<S::BM> &jobs,
+                         LDS_AS uint16_t *r0, LDS_AS uint16_t *r1, LDS_AS uint16_t *r2, LDS_AS uint16_t *r3,
+                         f32x4 (&acc)[S::NI][S::NJ])
 {
     using OP = Operand<S::BM, KC, S::NW>;
     using OQ = Operand<S::BN, KC, S::NW>;
@@ -257,16 +316,10 @@ MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, LDS_AS int
     const LoraArgs &lo = a.lora;
     const int l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = w / S::WN, wn = w % S::WN;
-    if (tid < S::BM) {
-        const int id = m0 + tid < a.M ? lo.ids[m0 + tid] : -1;
-        ids[tid] = id >= 0 && id < lo.n ? id : -1;
-    }
-    __syncthreads();   // ids, and the end of the k loop's reads of the ring
-    AdapterList<S::BM> ahead, now;
-    now.start(lo, ids, l);
-    if (now.e < 0)
+    __syncthreads();   // the list, and the end of the k loop's reads of the ring
+    const int count = __builtin_amdgcn_readfirstlane(jobs.count);
+    if (count == 0)
         return;
-    ahead = now;
     OP po;
     OQ qo;
     po.init_kc(w, l, lo.rpad, [&](int r) { return (int64_t)(m0 + r); });
@@ -274,77 +327,50 @@ MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, LDS_AS int
     const __amdgpu_buffer_rsrc_t pr = buf_rsrc(lo.mid, (uint32_t)((int64_t)a.M * lo.rpad * 2));
     const uint32_t bbytes = (uint32_t)((int64_t)a.N * lo.rank * 2);
     const uint32_t pbase = OP::frag_base(l, wm * S::TM), qbase = OQ::frag_base(l, wn * S::TN);
-    int id[S::NI];
-#pragma unroll
-    for (int i = 0; i < S::NI; ++i)
-        id[i] = ids[wm * S::TM + 16 * i + (l & 15)];
+    const int *ids = jobs.id + wm * S::TM + (l & 15);
 
-    auto load = [&](LDS_AS uint16_t *ring) __attribute__((always_inline)) {
-        const int e = max(ahead.e, 0);
-        const __amdgpu_buffer_rsrc_t qr = buf_rsrc(lo.b + (int64_t)e * a.N * lo.rank, bbytes);
-        po.issue(pr, ring, w, ahead.k0, ahead.rk, 2);
-        qo.issue(qr, ring + S::BM * kDenseBK, w, ahead.k0, ahead.rk, 2);
-        if (ahead.e >= 0)
-            ahead.next(lo);
+    auto job_of = [&](int t) __attribute__((always_inline)) {
+        return (uint32_t)__builtin_amdgcn_readfirstlane((int)jobs.job[min(t, count - 1)]);
     };
-    auto stage = [&](const LDS_AS uint16_t *cur, LDS_AS uint16_t *refill) __attribute__((always_inline)) {
+    auto load = [&](int t, LDS_AS uint16_t *ring) __attribute__((always_inline)) {
+        const uint32_t job = job_of(t);
+        const int e = job & 0xFFFF, k0 = 32 * ((job >> 16) & 15), rk = t < count ? (int)(job >> 20) : 0;
+        po.issue(pr, ring, w, k0, rk, 2);
+        qo.issue(buf_rsrc(lo.b + (int64_t)e * a.N * lo.rank, bbytes), ring + S::BM * kDenseBK, w, k0, rk, 2);
+    };
+    auto stage = [&](int t, const LDS_AS uint16_t *cur, LDS_AS uint16_t *refill) __attribute__((always_inline)) {
         __builtin_amdgcn_sched_barrier(0);
         wait_vmcnt<2 * kLoads>();   // stages t + 1 and t + 2 stay in flight
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        load(refill);
+        load(t + 3, refill);
+        const uint32_t job = job_of(t);
+        const int e = job & 0xFFFF;
         u32x4 q[S::NJ];
 #pragma unroll
         for (int j = 0; j < S::NJ; ++j)
             q[j] = OQ::frag(cur + S::BM * kDenseBK, qbase, j);
-        if (now.rk & 7) {
-            // an octet that the rank ends in: what follows in it is not part
-            // of the adapter (whole octets read zeros)
-            const int k = now.k0 + 8 * (l >> 4);
+        lora_cut(job >> 20, 32 * ((job >> 16) & 15), l, q);
 #pragma unroll
-            for (int j = 0; j < S::NJ; ++j)
-#pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    q[j][d] &= (k + 2 * d < now.rk ? 0xFFFFu : 0u) | (k + 2 * d + 1 < now.rk ? 0xFFFF0000u : 0u);
+        for (int i = 0; i < S::NI; i += 2) {
+            const u32x4 p0 = OP::frag(cur, pbase, i), p1 = OP::frag(cur, pbase, i + 1);
+            lora_products<BF16>(ids[16 * i] == e, p0, q, acc[i]);
+            lora_products<BF16>(ids[16 * i + 16] == e, p1, q, acc[i + 1]);
+            __builtin_amdgcn_sched_barrier(0);   // fragments of two blocks at a time: registers
         }
-#pragma unroll
-        for (int i = 0; i < S::NI; ++i) {
-            const bool hit = id[i] == now.e;
-            const uint64_t any = __ballot(hit);
-            if (!any)
-                continue;
-            const u32x4 p = OP::frag(cur, pbase, i);
-            if (any == ~(uint64_t)0) {
-#pragma unroll
-                for (int j = 0; j < S::NJ; ++j)
-                    acc[i][j] = dense_mfma<BF16>(q[j], p, acc[i][j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < S::NJ; ++j) {
-                    const f32x4 y = dense_mfma<BF16>(q[j], p, (f32x4){});
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[i][j][r] = hit ? acc[i][j][r] + y[r] : acc[i][j][r];
-                }
-            }
-        }
-        now.next(lo);
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): reads done before the next barrier
     };
-    load(r0);
-    load(r1);
-    load(r2);
-    while (now.e >= 0) {
-        stage(r0, r3);
-        if (now.e < 0)
-            break;
-        stage(r1, r0);
-        if (now.e < 0)
-            break;
-        stage(r2, r1);
-        if (now.e < 0)
-            break;
-        stage(r3, r2);
+    load(0, r0);
+    load(1, r1);
+    load(2, r2);
+#pragma unroll 1
+    for (int t = 0; t < count; ++t) {
+        stage(t, r0, r3);
+        LDS_AS uint16_t *r = r0;
+        r0 = r1;
+        r1 = r2;
+        r2 = r3;
+        r3 = r;
     }
     wait_vmcnt<0>();   // the loads past the end still write LDS
 }
@@ -409,16 +435,26 @@ __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
 #pragma unroll
         for (int j = 0; j < S::NJ; ++j)
             acc[i][j] = (f32x4){};
-    t.run(s0, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1, (LDS_AS uint16_t *)ring2, (LDS_AS uint16_t *)ring3,
-          acc);
-
-    // the adapters' share goes with the first k split
     if constexpr (MODE == DENSE_LIN) {
-        __shared__ int ids[S::BM];
+        // the adapters' share goes with the first k split
+        __shared__ AdapterJobs<S::BM> jobs;
+        t.run(s0, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1, (LDS_AS uint16_t *)ring2,
+              (LDS_AS uint16_t *)ring3, acc, [&]() __attribute__((always_inline)) {
+                  if (split == 0) {
+                      jobs.ids_of(a.lora, m0, a.M, tid);
+                      __syncthreads();
+                      if (w == 0)
+                          jobs.build(a.lora, l);
+                  }
+              });
         if (split == 0)
-            lora_expand<BF16, S>(a, m0, n0, tid, (LDS_AS int *)ids, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1,
+            lora_expand<BF16, S>(a, m0, n0, tid, jobs, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1,
                                  (LDS_AS uint16_t *)ring2, (LDS_AS uint16_t *)ring3, acc);
+    } else {
+        t.run(s0, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1, (LDS_AS uint16_t *)ring2,
+              (LDS_AS uint16_t *)ring3, acc, [] {});
     }
+
     if (a.splits > 1) {
         f32x4 *part = (f32x4 *)a.part + ((int64_t)blockIdx.x * S::NI * S::NJ) * (64 * S::NW) + tid;
 #pragma unroll

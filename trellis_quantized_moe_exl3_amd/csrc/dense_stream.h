@@ -14,38 +14,56 @@
 namespace moe {
 
 // D[m][n] over NI x NJ blocks of 16 x 16; the block's wavefronts take k shares
-// of 64 in turn (share `first`, first + stride, ..), RING shares in flight
-// each.  The first NJ loads of Q (8 rows each) go through q[0], the rest
-// through q[1].
+// of 64 in turn, RING shares in flight each.  The first NJ loads of a KC operand
+// Q (8 rows each) go through q[0], the rest through q[1] (GLU: gate, up).
 //
-// LDS image of a share: 128-byte rows of eight 16-byte pieces, piece p of row r
-// in slot p ^ ((r >> 1) & 7): the 16 rows a fragment reads at one piece hit 16
-// distinct 4-bank groups.
-template <bool BF16, int NI, int NJ, int RING>
+// LDS image of an operand's share:
+//   KC  128-byte rows of eight 16-byte pieces, piece p of row r in slot
+//       p ^ ((r >> 1) & 7): the lanes that a 16-byte LDS read serves together
+//       (see dense_gemm.h) hit 16 distinct 4-bank groups
+//   KS  one 128-byte row of 64 tile rows for each k, the 32-byte chunk c in slot
+//       c ^ g(k), g(k) = k / 2 % 2 + 2 (k / 8 % 2): the eight k that 32 lanes
+//       of the transposing read touch hit distinct 8-bank groups
+template <bool BF16, int NI, int NJ, int RING, int PL = KC, int QL = KC>
 struct Stream {
     static constexpr int kLoads = 2 * (NI + NJ);
     static constexpr int kHalves = 16 * (NI + NJ) * 64;   // of one share
+    static_assert((PL == KC || NI == 4) && (QL == KC || NJ == 4), "KS rows are 128 bytes");
     __amdgpu_buffer_rsrc_t p, q[2];
     uint32_t off[kLoads];   // byte offset of the lane's 16 bytes at k = 0
+    uint32_t pstep, qstep;  // bytes from one k to the next
     int l, kend;
 
-    // Row of load j (P: j < 2 NI, Q: j - 2 NI) that lane l fetches, and its
-    // first k.
+    // KC: the row of load j that lane l fetches, and its first k; KS: its k
     MOE_DEV static int row(int l, int j) { return 8 * j + (l >> 3); }
     MOE_DEV static int first_k(int l, int j) { return 8 * ((l & 7) ^ ((4 * j + (l >> 4)) & 7)); }
+    MOE_DEV static int ks_chunk(int k) { return ((k >> 1) & 1) | ((k >> 2) & 2); }
 
-    // prow(r), qrow(r): memory rows of the tile rows
+    // prow, qrow: memory row of tile row r (KC), or memory column of tile row 0
+    // (KS, called with 0)
+    template <int L, int N, class F>
+    MOE_DEV static void offsets(uint32_t *o, int l, int64_t ld, F row_of)
+    {
+#pragma unroll
+        for (int j = 0; j < 2 * N; ++j) {
+            if constexpr (L == KC) {
+                o[j] = (uint32_t)((row_of(row(l, j)) * ld + first_k(l, j)) * 2);
+            } else {
+                const int k = row(l, j);
+                const int c = 16 * (((l & 7) >> 1) ^ ks_chunk(k)) + 8 * (l & 1);
+                o[j] = (uint32_t)((k * ld + row_of(0) + c) * 2);
+            }
+        }
+    }
     template <class FP, class FQ>
     MOE_DEV void init(int lane, int K, int64_t ldp, int64_t ldq, FP prow, FQ qrow)
     {
         l = lane;
         kend = K;
-#pragma unroll
-        for (int j = 0; j < 2 * NI; ++j)
-            off[j] = (uint32_t)((prow(row(l, j)) * ldp + first_k(l, j)) * 2);
-#pragma unroll
-        for (int j = 0; j < 2 * NJ; ++j)
-            off[2 * NI + j] = (uint32_t)((qrow(row(l, j)) * ldq + first_k(l, j)) * 2);
+        pstep = PL == KC ? 2u : (uint32_t)(2 * ldp);
+        qstep = QL == KC ? 2u : (uint32_t)(2 * ldq);
+        offsets<PL, NI>(off, l, ldp, prow);
+        offsets<QL, NJ>(off + 2 * NI, l, ldq, qrow);
     }
     MOE_DEV void load(int share, LDS_AS uint16_t *lds)
     {
@@ -54,9 +72,39 @@ struct Stream {
         for (int j = 0; j < kLoads; ++j) {
             const bool isq = j >= 2 * NI;
             const int jj = isq ? j - 2 * NI : j;
-            const uint32_t o = k0 + first_k(l, jj) < kend ? off[j] + 2u * (uint32_t)k0 : kOutOfRange;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(!isq ? p : jj < NJ ? q[0] : q[1], (LDS_AS void *)(lds + 512 * j),
-                                                     16, o, 0, 0, 0);
+            const int k = k0 + ((isq ? QL : PL) == KC ? first_k(l, jj) : row(l, jj));
+            const uint32_t o = k < kend ? off[j] + (uint32_t)k0 * (isq ? qstep : pstep) : kOutOfRange;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(!isq ? p : QL == KS || jj < NJ ? q[0] : q[1],
+                                                     (LDS_AS void *)(lds + 512 * j), 16, o, 0, 0, 0);
+        }
+    }
+    // Fragments of the half h (32 k) of a share: N blocks of 16 tile rows.
+    template <int L, int N>
+    MOE_DEV static void read(const LDS_AS uint16_t *lds, int l, int h, u32x4 (&f)[N])
+    {
+        const LDS_AS char *at = (const LDS_AS char *)lds;
+        if constexpr (L == KC) {
+            const uint32_t base = (uint32_t)((l & 15) * 128 + (((l >> 4) ^ ((l & 15) >> 1)) << 4)) ^ (64u * h);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                f[i] = *(const LDS_AS u32x4 *)(at + base + 2048 * i);
+        } else {
+            const int k = 32 * h + 8 * (l >> 4) + ((l & 15) >> 2);
+            const uint32_t base = (uint32_t)(k * 128 + (ks_chunk(k) << 5) + (l & 3) * 8);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const u32x2 lo = tr_read(at + (base ^ (uint32_t)(i << 5)));
+                const u32x2 hi = tr_read(at + (base ^ (uint32_t)(i << 5)) + 512);
+                f[i] = (u32x4){lo[0], lo[1], hi[0], hi[1]};
+            }
+        }
+    }
+    MOE_DEV static void fragments(const LDS_AS uint16_t *cur, int l, u32x4 (&pf)[2][NI], u32x4 (&qf)[2][NJ])
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            read<PL, NI>(cur, l, h, pf[h]);
+            read<QL, NJ>(cur + 1024 * NI, l, h, qf[h]);
         }
     }
     // Wait for the share in `cur` (the RING - 1 shares after it stay in
@@ -65,18 +113,8 @@ struct Stream {
     {
         __builtin_amdgcn_sched_barrier(0);
         wait_vmcnt<(RING - 1) * kLoads>();
-        const uint32_t base = (uint32_t)((l & 15) * 128 + (((l >> 4) ^ ((l & 15) >> 1)) << 4));
         u32x4 pf[2][NI], qf[2][NJ];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const LDS_AS char *at = (const LDS_AS char *)cur + (base ^ (64u * h));
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                pf[h][i] = *(const LDS_AS u32x4 *)(at + 2048 * i);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                qf[h][j] = *(const LDS_AS u32x4 *)(at + 2048 * (NI + j));
-        }
+        fragments(cur, l, pf, qf);
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the slot is free
         __builtin_amdgcn_sched_barrier(0);
         load(refill, cur);
@@ -88,23 +126,26 @@ struct Stream {
                 for (int j = 0; j < NJ; ++j)
                     acc[i][j] = dense_mfma<BF16>(qf[h][j], pf[h][i], acc[i][j]);
     }
+    // Shares first, first + stride, .. of the operands.
     MOE_DEV void run(int first, int stride, LDS_AS uint16_t *r0, LDS_AS uint16_t *r1, LDS_AS uint16_t *r2,
                      LDS_AS uint16_t *r3, f32x4 (&acc)[NI][NJ])
     {
-        static_assert(RING == 3 || RING == 4, "ring arrays");
+        static_assert(RING >= 2 && RING <= 4, "ring arrays");
         const int shares = (kend + 63) / 64;
         if (first >= shares)
             return;
         load(first, r0);
         load(first + stride, r1);
-        load(first + 2 * stride, r2);
-        if constexpr (RING == 4)
+        if constexpr (RING >= 3)
+            load(first + 2 * stride, r2);
+        if constexpr (RING >= 4)
             load(first + 3 * stride, r3);
         for (int s = first; s < shares; s += RING * stride) {
             step(s + RING * stride, r0, acc);
             step(s + (RING + 1) * stride, r1, acc);
-            step(s + (RING + 2) * stride, r2, acc);
-            if constexpr (RING == 4)
+            if constexpr (RING >= 3)
+                step(s + (RING + 2) * stride, r2, acc);
+            if constexpr (RING >= 4)
                 step(s + (RING + 3) * stride, r3, acc);
         }
         wait_vmcnt<0>();   // the loads past the end still write LDS
@@ -236,6 +277,133 @@ hipError_t launch_skinny(const DenseArgs &a, hipStream_t s)
     else
         dense_skinny_kernel<MODE, BF16, 4, 4, 3, XW><<<grid, 64 * (4 + XW), 0, s>>>(a);
     return hipGetLastError();
+}
+
+// ---- 64 x 64 tiles: all modes, where larger tiles would leave CUs idle
+
+// The adapters' share of a 64 x 64 tile: the adapters that its tokens name are
+// dealt to the NW wavefronts by their number (so that a token's sum is taken in
+// the same order whatever its neighbours), each adding B_a's rows against the
+// tokens' s_a x A_a^T to its own part of the sums.
+template <bool BF16, int NW, class S>
+MOE_DEV void tile_expand(const DenseArgs &a, int m0, int n0, int w, int l, LDS_AS uint16_t *r0, LDS_AS uint16_t *r1,
+                         f32x4 (&acc)[4][4])
+{
+    const LoraArgs &lo = a.lora;
+    int mine = m0 + l < a.M ? lo.ids[m0 + l] : -1;   // of token m0 + l
+    if (mine < 0 || mine >= lo.n)
+        mine = -1;
+    uint64_t left = __ballot(mine >= 0);
+    if (!left)
+        return;
+    int id[4];   // of the tokens of this lane's columns
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        id[i] = __shfl(mine, 16 * i + (l & 15));
+    S st;
+    st.p = buf_rsrc(lo.mid, (uint32_t)((int64_t)a.M * lo.rpad * 2));
+    st.init(l, 0, lo.rpad, lo.rank, [&](int r) { return (int64_t)(m0 + r); },
+            [&](int r) { return (int64_t)(n0 + r); });
+    while (left) {
+        const int e = __builtin_amdgcn_readlane(mine, __ffsll((unsigned long long)left) - 1);
+        left &= ~__ballot(mine == e);
+        if (e % NW != w)
+            continue;
+        const int rk = lo.ranks ? min(max(lo.ranks[e], 0), lo.rank) : lo.rank;
+        st.kend = rk;
+        st.q[0] = buf_rsrc(lo.b + (int64_t)e * a.N * lo.rank, (uint32_t)((int64_t)a.N * lo.rank * 2));
+        st.q[1] = st.q[0];
+        for (int k0 = 0; k0 < rk; k0 += 64) {
+            LDS_AS uint16_t *cur = (k0 & 64) ? r1 : r0;
+            st.load(k0 / 64, cur);
+            wait_vmcnt<0>();
+            u32x4 pf[2][4], qf[2][4];
+            S::fragments(cur, l, pf, qf);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                lora_cut(rk, k0 + 32 * h, l, qf[h]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    lora_products<BF16>(id[i] == e, pf[h][i], qf[h], acc[i]);
+            }
+        }
+    }
+}
+
+template <int MODE, bool BF16, int NW>
+__global__ __launch_bounds__(64 * NW) void dense_tile_kernel(DenseArgs a)
+{
+    using TR = DenseTraits<MODE>;
+    using S = Stream<BF16, 4, 4, 2, TR::kPL, TR::kQL>;
+    __shared__ __align__(1024) uint16_t ring0[NW * S::kHalves], ring1[NW * S::kHalves];
+    const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    constexpr int kCols = MODE == DENSE_GLU ? 32 : 64;
+    int m, n;
+    dense_tile(blockIdx.x, a.mt * a.nt, a.mt, a.nt, m, n);
+    const int half = MODE == DENSE_DW ? a.mt / 2 : a.mt;
+    const int z = m >= half ? 1 : 0;
+    const int m0 = (m - z * half) * 64, n0 = n * kCols;
+    S st;
+    st.p = buf_rsrc(a.p[MODE == DENSE_DW ? z : 0], a.pbytes);
+    st.q[0] = buf_rsrc(a.q[0], a.qbytes);
+    st.q[1] = MODE == DENSE_GLU ? buf_rsrc(a.q[1], a.qbytes) : st.q[0];
+    st.init(l, a.K, a.ldp, a.ldq, [&](int r) { return (int64_t)(m0 + r); },
+            [&](int r) { return (int64_t)(n0 + (MODE == DENSE_GLU ? r & 31 : r)); });
+    f32x4 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[i][j] = (f32x4){};
+    LDS_AS uint16_t *r0 = (LDS_AS uint16_t *)ring0 + w * S::kHalves, *r1 = (LDS_AS uint16_t *)ring1 + w * S::kHalves;
+    st.run(w, NW, r0, r1, nullptr, nullptr, acc);
+    if constexpr (MODE == DENSE_DX) {
+        st.p = buf_rsrc(a.p[1], a.pbytes);
+        st.q[0] = buf_rsrc(a.q[1], a.qbytes);
+        st.run(w, NW, r0, r1, nullptr, nullptr, acc);
+    }
+    if constexpr (MODE == DENSE_LIN)
+        tile_expand<BF16, NW, S>(a, m0, n0, w, l, r0, r1, acc);
+    // every wavefront's sums in its own part of the first ring array
+    LDS_AS f32x4 *red = (LDS_AS f32x4 *)((LDS_AS uint16_t *)ring0);
+    constexpr int kStep = S::kHalves / 8;
+    static_assert(kStep >= 16 * 64, "sums fit the first ring array");
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            red[w * kStep + (4 * i + j) * 64 + l] = acc[i][j];
+    __syncthreads();
+    for (int i = w; i < 4; i += NW) {
+        f32x4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = red[(4 * i + j) * 64 + l];
+#pragma unroll
+            for (int s = 1; s < NW; ++s)
+                v[j] += red[s * kStep + (4 * i + j) * 64 + l];
+        }
+        dense_store<MODE, BF16, 4>(a, z, m0 + 16 * i, n0, l, v);
+    }
+}
+
+template <int MODE, bool BF16>
+hipError_t launch_tile(const DenseArgs &a, hipStream_t s)
+{
+    const unsigned grid = (unsigned)(a.mt * a.nt);
+    if (grid <= 256)
+        dense_tile_kernel<MODE, BF16, 4><<<grid, 256, 0, s>>>(a);
+    else
+        dense_tile_kernel<MODE, BF16, 2><<<grid, 128, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int MODE>
+hipError_t launch_any(bool bf16, const DenseArgs &a, hipStream_t s)
+{
+    if (a.bm != kDenseTile)
+        return launch_dense_mode<MODE>(bf16, a, s);
+    return bf16 ? launch_tile<MODE, true>(a, s) : launch_tile<MODE, false>(a, s);
 }
 
 }  // namespace moe

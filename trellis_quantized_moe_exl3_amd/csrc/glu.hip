@@ -56,9 +56,9 @@ hipError_t launch_skinny_lin(bool bf16, const DenseArgs &a, hipStream_t s);
 hipError_t launch_dense(int mode, bool bf16, const DenseArgs &a, hipStream_t s)
 {
     switch (mode) {
-    case DENSE_GLU: return launch_dense_mode<DENSE_GLU>(bf16, a, s);
-    case DENSE_DX: return launch_dense_mode<DENSE_DX>(bf16, a, s);
-    case DENSE_DW: return launch_dense_mode<DENSE_DW>(bf16, a, s);
+    case DENSE_GLU: return launch_any<DENSE_GLU>(bf16, a, s);
+    case DENSE_DX: return launch_any<DENSE_DX>(bf16, a, s);
+    case DENSE_DW: return launch_any<DENSE_DW>(bf16, a, s);
     default: return launch_dense_lin(bf16, a, s);
     }
 }

@@ -26,10 +26,23 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(const uint16_t *x,
     if (f == 0 && r0 == 0) {
         // the call's status word: ids and ranks outside their ranges
         int bad = 0;
-        for (int t = tid; t < T; t += 64 * NW)
+        constexpr int kBatch = 4;   // 16-byte loads in flight a thread
+        const int quads = T / 4, threads = 64 * NW;
+        for (int t = tid; t < quads; t += kBatch * threads) {
+            u32x4 v[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                v[b] = ((const u32x4 *)lo.ids)[min(t + b * threads, quads - 1)];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    bad |= ((int)v[b][d] < -1 || (int)v[b][d] >= lo.n) ? 1 : 0;
+        }
+        for (int t = 4 * quads + tid; t < T; t += threads)
             bad |= (lo.ids[t] < -1 || lo.ids[t] >= lo.n) ? 1 : 0;
         if (lo.ranks)
-            for (int e = tid; e < lo.n; e += 64 * NW)
+            for (int e = tid; e < lo.n; e += threads)
                 bad |= (lo.ranks[e] < 0 || lo.ranks[e] > lo.rank) ? 2 : 0;
         const int index = __syncthreads_or(bad & 1), width = __syncthreads_or(bad & 2);
         if (tid == 0)
@@ -109,7 +122,7 @@ hipError_t launch_lora_shrink(bool bf16, const uint16_t *x, int64_t ldx, uint32_
 
 hipError_t launch_dense_lin(bool bf16, const DenseArgs &a, hipStream_t s)
 {
-    return launch_dense_mode<DENSE_LIN>(bf16, a, s);
+    return launch_any<DENSE_LIN>(bf16, a, s);
 }
 
 hipError_t launch_skinny_lin(bool bf16, const DenseArgs &a, hipStream_t s)
