@@ -3,7 +3,6 @@
 #include "dense.h"
 
 #include <algorithm>
-#include <stdlib.h>
 
 using namespace moe;
 
@@ -14,12 +13,8 @@ constexpr int64_t kMaxSize = 65536;
 constexpr int64_t kMaxLd = 1 << 20;
 constexpr int64_t kSpanLimit = (int64_t)1 << 31;
 
-// k splits: a launch of fewer tiles than this leaves CUs idle, so its k range
-// is cut until about kSplitBlocks blocks run (two per CU), each with at least
-// kSplitStages stages (256 k) to do.
-constexpr int64_t kFullTiles = 192;
-// Large tiles from this many on.
-constexpr int64_t kLargeTiles = 192;
+// k splits of the 128-tile: at most this many blocks, each with at least this
+// many stages (256 k).
 constexpr int64_t kSplitBlocks = 512;
 constexpr int64_t kSplitStages = 8;
 
@@ -113,38 +108,66 @@ int check_desc(const moe_exl3_lora_desc *d)
 // T tokens of contiguous rows of this length must be addressable.
 bool rows_fit(int64_t T, int64_t cols) { return T < kSpanLimit && T * cols * 2 < kSpanLimit; }
 
-int64_t tile_cols(int mode, int64_t b) { return mode == DENSE_GLU ? b / 2 : b; }
+// Columns of a tile of `bm` rows.
+int64_t tile_cols(int mode, int64_t bm)
+{
+    const int64_t bn = bm == kDenseLow ? kDenseLarge : bm;
+    return mode == DENSE_GLU ? bn / 2 : bn;
+}
+
+int64_t stages_of(int mode, int64_t K) { return (mode == DENSE_DX ? 2 : 1) * cdiv(K, kDenseBK); }
+
+int64_t tiles_of(int mode, int64_t M, int64_t N, int64_t bm)
+{
+    return (mode == DENSE_DW ? 2 : 1) * cdiv(M, bm) * cdiv(N, tile_cols(mode, bm));
+}
 
 // Tiles and k splits of a launch.
 struct Tiles {
     int64_t bm, mt, nt, splits, per;
 };
 
-int64_t stages_of(int mode, int64_t K) { return (mode == DENSE_DX ? 2 : 1) * cdiv(K, kDenseBK); }
-
-int64_t tiles_of(int mode, int64_t M, int64_t N, int64_t b)
-{
-    return (mode == DENSE_DW ? 2 : 1) * cdiv(M, b) * cdiv(N, tile_cols(mode, b));
-}
-
+// The tile of a launch: the one whose rounds over the 256 CUs are estimated to
+// take the least time.  A round costs a fixed part (launch, first loads,
+// epilogue) and a part per stage of 32 k, in us as measured on the block's
+// forward pass, 96 to 10000 tokens, hidden 1024 and 4096, inter 512 to 4096:
+//   64 x 64     5 + 0.08 a stage up to 256 tiles, else 5.4 + 0.17 a round of 512
+//               (333 tokens, 4096 x 2048: 25 us; 128 x 128 takes 29)
+//   128 x 128   4 + 0.24 (1024 tokens: 35; 64 x 64 takes 50, 256 x 256 71)
+//   224 x 256   9.5 + 0.62 (7168 tokens: 178; 256 x 256 takes 184, 128 x 128 224)
+//   256 x 256   10 + 0.70 (4096 tokens: 100; 128 x 128 takes 128)
+// Few tiles with a long k are cut along k, at the price of partial tiles and a
+// second launch: 18 + 0.24 a stage (96 tokens of the gradient for x, hidden 1024,
+// inter 4096: 27 us, the uncut 128 x 128 tile takes 80; 100 tokens, 8192 x 256:
+// 20, 64 x 64 takes 22).
 Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K)
 {
+    const int64_t stages = stages_of(mode, K);
+    const double s = (double)stages;
+    int64_t bm = 0, cuts = 1;
+    double least = 0;
+    auto offer = [&](int64_t b, int64_t c, double us) {
+        if (bm == 0 || us < least) {
+            bm = b;
+            cuts = c;
+            least = us;
+        }
+    };
+    auto rounds = [&](int64_t tiles, int64_t at_once) { return (double)cdiv(tiles, at_once); };
+    const int64_t t64 = tiles_of(mode, M, N, kDenseTile), t128 = tiles_of(mode, M, N, kDenseSmall);
+    offer(kDenseLarge, 1, rounds(tiles_of(mode, M, N, kDenseLarge), 256) * (10 + 0.70 * s));
+    if (mode != DENSE_DW)
+        offer(kDenseLow, 1, rounds(tiles_of(mode, M, N, kDenseLow), 256) * (9.5 + 0.62 * s));
+    offer(kDenseSmall, 1, rounds(t128, 256) * (4 + 0.24 * s));
+    offer(kDenseTile, 1, t64 <= 256 ? 5 + 0.08 * s : rounds(t64, 512) * (5.4 + 0.17 * s));
+    const int64_t c = std::min(kSplitBlocks / t128, stages / kSplitStages);
+    if (c > 1)
+        offer(kDenseSmall, c, 18 + 0.24 * (double)cdiv(stages, c));
     Tiles t{};
-    t.bm = tiles_of(mode, M, N, kDenseLarge) >= kLargeTiles ? kDenseLarge : kDenseSmall;
-    t.mt = (mode == DENSE_DW ? 2 : 1) * cdiv(M, t.bm);
-    t.nt = cdiv(N, tile_cols(mode, t.bm));
-    if (getenv("DT") ? atoi(getenv("DT")) && t.bm == kDenseSmall : t.bm == kDenseSmall && t.mt * t.nt < kFullTiles) {
-        t.bm = kDenseTile;
-        t.mt = (mode == DENSE_DW ? 2 : 1) * cdiv(M, t.bm);
-        t.nt = cdiv(N, tile_cols(mode, t.bm));
-        t.splits = t.per = 1;
-        return t;
-    }
-    const int64_t tiles = t.mt * t.nt, stages = stages_of(mode, K);
-    int64_t s = 1;
-    if (t.bm == kDenseSmall && tiles < kFullTiles)
-        s = std::max<int64_t>(1, std::min(kSplitBlocks / std::max<int64_t>(1, tiles), stages / kSplitStages));
-    t.per = std::max<int64_t>(1, cdiv(stages, s));
+    t.bm = bm;
+    t.mt = (mode == DENSE_DW ? 2 : 1) * cdiv(M, bm);
+    t.nt = cdiv(N, tile_cols(mode, bm));
+    t.per = std::max<int64_t>(1, cdiv(stages, cuts));
     t.splits = std::max<int64_t>(1, cdiv(stages, t.per));
     return t;
 }

@@ -46,11 +46,14 @@ struct DenseTraits {
 template <int BM_, int BN_, int WM_, int WN_>
 struct DenseShape {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NW = WM * WN;
+    static constexpr int RM = (BM + 127) / 128 * 128;   // rows of P in LDS (whole loads)
     static constexpr int TM = BM / WM, TN = BN / WN, NI = TM / 16, NJ = TN / 16;
     static_assert(TN == 64 && NW % 4 == 0, "GLU column interleave");
+    static_assert(RM % 64 == 0 && 64 * NW >= RM, "a thread for each row");
 };
 using SmallTile = DenseShape<kDenseSmall, kDenseSmall, 2, 2>;
 using LargeTile = DenseShape<kDenseLarge, kDenseLarge, 2, 4>;
+using LowTile = DenseShape<kDenseLow, kDenseLarge, 2, 4>;
 
 // Result columns n0 + .. of a tile: GLU tiles hold BN / 2 columns of both
 // projections, interleaved by 32 (tile rows 64 s + 0..31 of Q are gate columns
@@ -90,27 +93,66 @@ MOE_DEV void lin_store(const DenseArgs &a, int m, int n, f32x4 y)
     *(u32x2 *)(a.out[0] + (int64_t)m * a.ldo + n) = (u32x2){pack16<BF16>(y[0], y[1]), pack16<BF16>(y[2], y[3])};
 }
 
-// Epilogue of the 16 rows m0 .. of a wavefront's NJ column blocks from n0 on
-// (GLU: n0 is the first of its NJ / 2 x 16 intermediate columns).
-template <int MODE, bool BF16, int NJ>
-MOE_DEV void dense_store(const DenseArgs &a, int z, int m0, int n0, int l, f32x4 (&v)[NJ])
+// Eight consecutive values in 16 bits.
+template <bool BF16>
+MOE_DEV u32x4 pack8(f32x4 a, f32x4 b)
 {
-    const int m = m0 + (l & 15), nl = 4 * (l >> 4);
-    if (m >= a.M)
-        return;
-    constexpr int kBlocks = MODE == DENSE_GLU ? NJ / 2 : NJ;
+    return (u32x4){pack16<BF16>(a[0], a[1]), pack16<BF16>(a[2], a[3]), pack16<BF16>(b[0], b[1]),
+                   pack16<BF16>(b[2], b[3])};
+}
+
+// Epilogue of the 16 rows m0 .. of a wavefront's 64 tile columns (n0: the first
+// result column; GLU: of its 32).  The accumulators hold four columns of row
+// l % 16: stored as they are, neighbouring lanes would write to different rows
+// and every lane be a memory transaction of its own.  They pass through 4 KiB
+// of LDS that only this wavefront uses (16-byte unit c of row r in place
+// c ^ r), so that eight lanes write the 128 bytes of a row (GLU: four lanes 64)
+// (2048 tokens, adapters alone, 4096 columns: 25.0 -> BESIDE us).
+template <int MODE, bool BF16>
+MOE_DEV void dense_store(const DenseArgs &a, int z, int m0, int n0, int l, const f32x4 (&v)[4], LDS_AS f32x4 *lds)
+{
+    const int r = l & 15;
 #pragma unroll
-    for (int j = 0; j < kBlocks; ++j) {
-        const int n = n0 + 16 * j + nl;
-        if (n >= a.N)
-            continue;
-        if constexpr (MODE == DENSE_GLU)
-            glu_store<BF16>(a, m, n, v[j], v[j + kBlocks]);
-        else if constexpr (MODE == DENSE_LIN)
-            lin_store<BF16>(a, m, n, v[j]);
-        else
-            *(u32x2 *)(a.out[MODE == DENSE_DW ? z : 0] + (int64_t)m * a.ldo + n) =
-                (u32x2){pack16<BF16>(v[j][0], v[j][1]), pack16<BF16>(v[j][2], v[j][3])};
+    for (int j = 0; j < 4; ++j)
+        lds[16 * r + ((4 * j + (l >> 4)) ^ r)] = v[j];
+    auto at = [&](int row, int unit) { return lds[16 * row + (unit ^ row)]; };
+    if constexpr (MODE == DENSE_GLU) {
+        const int row = l >> 2, c = 2 * (l & 3), m = m0 + row, n = n0 + 4 * c;
+        const f32x4 g[2] = {at(row, c), at(row, c + 1)}, u[2] = {at(row, 8 + c), at(row, 9 + c)};
+        if (m >= a.M || n >= a.N)
+            return;
+        f32x4 h[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                h[q][d] = act_value(a.act, g[q][d]) * u[q][d];
+        *(u32x4 *)(a.out[0] + (int64_t)m * a.ldo + n) = pack8<BF16>(h[0], h[1]);
+        if (a.pre) {
+            f32x4 *p = (f32x4 *)(a.pre + (int64_t)m * a.N + n), *pu = (f32x4 *)((float *)p + (int64_t)a.M * a.N);
+            p[0] = g[0];
+            p[1] = g[1];
+            pu[0] = u[0];
+            pu[1] = u[1];
+        }
+    } else {
+        uint16_t *out = a.out[MODE == DENSE_DW ? z : 0];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = 8 * h + (l >> 3), c = 2 * (l & 7), m = m0 + row, n = n0 + 4 * c;
+            f32x4 y[2] = {at(row, c), at(row, c + 1)};
+            if (m >= a.M || n >= a.N)
+                continue;
+            if constexpr (MODE == DENSE_LIN) {
+                if (a.base) {
+                    const u32x4 b = *(const u32x4 *)(a.base + (int64_t)m * a.ldbase + n);
+#pragma unroll
+                    for (int d = 0; d < 8; ++d)
+                        y[d >> 2][d & 3] += act_to_f32<BF16>((uint16_t)(b[d >> 1] >> (16 * (d & 1))));
+                }
+            }
+            *(u32x4 *)(out + (int64_t)m * a.ldo + n) = pack8<BF16>(y[0], y[1]);
+        }
     }
 }
 
@@ -125,7 +167,7 @@ struct DenseTile {
     static constexpr int NI = S::NI, NJ = S::NJ;
     using Frags = DenseFrags<S>;
     using TR = DenseTraits<MODE>;
-    using OP = Operand<S::BM, TR::kPL, S::NW>;
+    using OP = Operand<S::RM, TR::kPL, S::NW>;
     using OQ = Operand<S::BN, TR::kQL, S::NW>;
     static constexpr int kLoads = OP::kLoads + OQ::kLoads;
     OP po;
@@ -141,7 +183,7 @@ struct DenseTile {
         const int k0 = kDenseBK * (second ? s - nsk : s);
         const int end = s < send ? kend : 0;
         po.issue(second ? pr[1] : pr[0], ring, w, k0, end, pstep);
-        qo.issue(second ? qr[1] : qr[0], ring + S::BM * kDenseBK, w, k0, end, qstep);
+        qo.issue(second ? qr[1] : qr[0], ring + S::RM * kDenseBK, w, k0, end, qstep);
     }
     MOE_DEV void read(const LDS_AS uint16_t *ring, Frags &f)
     {
@@ -150,7 +192,7 @@ struct DenseTile {
             f.p[i] = OP::frag(ring, pbase, i);
 #pragma unroll
         for (int j = 0; j < S::NJ; ++j)
-            f.q[j] = OQ::frag(ring + S::BM * kDenseBK, qbase, j);
+            f.q[j] = OQ::frag(ring + S::RM * kDenseBK, qbase, j);
     }
     // Stage s in ring slot `cur`, whose fragments `f` were read during stage
     // s - 1.  "At most 2 loads' worth outstanding" (stages s + 2 and s + 3)
@@ -259,10 +301,10 @@ struct AdapterJobs {
     uint32_t job[BM * (kMaxRank / 32)]; // adapter | stage << 16 | its rank << 20
 
     // The tokens' ids, by all threads.
-    MOE_DEV void ids_of(const LoraArgs &lo, int m0, int T, int tid)
+    MOE_DEV void ids_of(const LoraArgs &lo, int m0, int rows, int T, int tid)
     {
         if (tid < BM) {
-            const int t = m0 + tid, e = t < T ? lo.ids[t] : -1;
+            const int t = m0 + tid, e = tid < rows && t < T ? lo.ids[t] : -1;
             id[tid] = e >= 0 && e < lo.n ? e : -1;
         }
     }
@@ -306,11 +348,11 @@ struct AdapterJobs {
 // tile names, P = the tokens' s_a x A_a^T, Q = B_a's rows, through the same
 // ring.
 template <bool BF16, class S>
-MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const AdapterJobs<S::BM> &jobs,
+MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const AdapterJobs<S::RM> &jobs,
                          LDS_AS uint16_t *r0, LDS_AS uint16_t *r1, LDS_AS uint16_t *r2, LDS_AS uint16_t *r3,
                          f32x4 (&acc)[S::NI][S::NJ])
 {
-    using OP = Operand<S::BM, KC, S::NW>;
+    using OP = Operand<S::RM, KC, S::NW>;
     using OQ = Operand<S::BN, KC, S::NW>;
     constexpr int kLoads = OP::kLoads + OQ::kLoads;
     const LoraArgs &lo = a.lora;
@@ -322,7 +364,7 @@ MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const Adap
         return;
     OP po;
     OQ qo;
-    po.init_kc(w, l, lo.rpad, [&](int r) { return (int64_t)(m0 + r); });
+    po.init_kc(w, l, lo.rpad, [&](int r) { return (int64_t)(r < S::BM ? m0 + r : a.M); });
     qo.init_kc(w, l, lo.rank, [&](int r) { return (int64_t)(n0 + r); });
     const __amdgpu_buffer_rsrc_t pr = buf_rsrc(lo.mid, (uint32_t)((int64_t)a.M * lo.rpad * 2));
     const uint32_t bbytes = (uint32_t)((int64_t)a.N * lo.rank * 2);
@@ -336,7 +378,7 @@ MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const Adap
         const uint32_t job = job_of(t);
         const int e = job & 0xFFFF, k0 = 32 * ((job >> 16) & 15), rk = t < count ? (int)(job >> 20) : 0;
         po.issue(pr, ring, w, k0, rk, 2);
-        qo.issue(buf_rsrc(lo.b + (int64_t)e * a.N * lo.rank, bbytes), ring + S::BM * kDenseBK, w, k0, rk, 2);
+        qo.issue(buf_rsrc(lo.b + (int64_t)e * a.N * lo.rank, bbytes), ring + S::RM * kDenseBK, w, k0, rk, 2);
     };
     auto stage = [&](int t, const LDS_AS uint16_t *cur, LDS_AS uint16_t *refill) __attribute__((always_inline)) {
         __builtin_amdgcn_sched_barrier(0);
@@ -349,13 +391,15 @@ MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const Adap
         u32x4 q[S::NJ];
 #pragma unroll
         for (int j = 0; j < S::NJ; ++j)
-            q[j] = OQ::frag(cur + S::BM * kDenseBK, qbase, j);
+            q[j] = OQ::frag(cur + S::RM * kDenseBK, qbase, j);
         lora_cut(job >> 20, 32 * ((job >> 16) & 15), l, q);
 #pragma unroll
         for (int i = 0; i < S::NI; i += 2) {
-            const u32x4 p0 = OP::frag(cur, pbase, i), p1 = OP::frag(cur, pbase, i + 1);
+            constexpr int kLast = S::NI - 1;
+            const u32x4 p0 = OP::frag(cur, pbase, i), p1 = OP::frag(cur, pbase, min(i + 1, kLast));
             lora_products<BF16>(ids[16 * i] == e, p0, q, acc[i]);
-            lora_products<BF16>(ids[16 * i + 16] == e, p1, q, acc[i + 1]);
+            if (i < kLast)
+                lora_products<BF16>(ids[16 * i + 16] == e, p1, q, acc[min(i + 1, kLast)]);
             __builtin_amdgcn_sched_barrier(0);   // fragments of two blocks at a time: registers
         }
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): reads done before the next barrier
@@ -379,7 +423,7 @@ template <int MODE, bool BF16, class S>
 __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
 {
     using T = DenseTile<MODE, BF16, S>;
-    constexpr int kHalves = (S::BM + S::BN) * kDenseBK;
+    constexpr int kHalves = (S::RM + S::BN) * kDenseBK;
     __shared__ __align__(1024) uint16_t ring0[kHalves], ring1[kHalves], ring2[kHalves], ring3[kHalves];
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = w / S::WN, wn = w % S::WN;
@@ -411,7 +455,8 @@ __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
         t.qr[1] = MODE == DENSE_DX ? buf_rsrc(a.q[1], a.qbytes) : t.qr[0];
     }
     if constexpr (T::TR::kPL == KC) {
-        t.po.init_kc(w, l, a.ldp, [&](int r) { return (int64_t)(m0 + r); });
+        // rows past the tile's own read zeros
+        t.po.init_kc(w, l, a.ldp, [&](int r) { return (int64_t)(r < S::BM ? m0 + r : a.M); });
         t.pstep = 2;
     } else {
         t.po.init_ks(w, l, a.ldp, m0);
@@ -437,11 +482,11 @@ __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
             acc[i][j] = (f32x4){};
     if constexpr (MODE == DENSE_LIN) {
         // the adapters' share goes with the first k split
-        __shared__ AdapterJobs<S::BM> jobs;
+        __shared__ AdapterJobs<S::RM> jobs;
         t.run(s0, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1, (LDS_AS uint16_t *)ring2,
               (LDS_AS uint16_t *)ring3, acc, [&]() __attribute__((always_inline)) {
                   if (split == 0) {
-                      jobs.ids_of(a.lora, m0, a.M, tid);
+                      jobs.ids_of(a.lora, m0, S::BM, a.M, tid);
                       __syncthreads();
                       if (w == 0)
                           jobs.build(a.lora, l);
@@ -465,9 +510,12 @@ __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
         return;
     }
     const int mw = m0 + wm * S::TM, nw = n0 + wn * ((kDenseCols<MODE, S>) / S::WN);
+    __syncthreads();   // the ring is free
+    LDS_AS f32x4 *lds = (LDS_AS f32x4 *)(LDS_AS uint16_t *)ring0 + 256 * w;
+    static_assert(S::NW * 4096 <= kHalves * 2, "a wavefront's share of the first ring array");
 #pragma unroll
     for (int i = 0; i < S::NI; ++i)
-        dense_store<MODE, BF16, S::NJ>(a, z, mw + 16 * i, nw, l, acc[i]);
+        dense_store<MODE, BF16>(a, z, mw + 16 * i, nw, l, acc[i], lds);
 }
 
 // Sum of the k splits' partial tiles, in split order, and the epilogue: block
@@ -495,7 +543,8 @@ __global__ __launch_bounds__(64 * S::NW) void dense_finish_kernel(DenseArgs a)
         for (int j = 0; j < S::NJ; ++j)
             acc[0][j] += part[k * step + j * (64 * S::NW)];
     const int mw = m0 + wm * S::TM + 16 * i, nw = n0 + wn * ((kDenseCols<MODE, S>) / S::WN);
-    dense_store<MODE, BF16, S::NJ>(a, z, mw, nw, l, acc[0]);
+    __shared__ f32x4 lds[S::NW * 256];
+    dense_store<MODE, BF16>(a, z, mw, nw, l, acc[0], (LDS_AS f32x4 *)lds + 256 * w);
 }
 
 template <int MODE, bool BF16, class S>
@@ -510,6 +559,9 @@ hipError_t launch_dense_shape(const DenseArgs &a, hipStream_t s)
 template <int MODE>
 hipError_t launch_dense_mode(bool bf16, const DenseArgs &a, hipStream_t s)
 {
+    if constexpr (DenseTraits<MODE>::kPL == KC)
+        if (a.bm == kDenseLow)
+            return bf16 ? launch_dense_shape<MODE, true, LowTile>(a, s) : launch_dense_shape<MODE, false, LowTile>(a, s);
     if (a.bm == kDenseLarge)
         return bf16 ? launch_dense_shape<MODE, true, LargeTile>(a, s) : launch_dense_shape<MODE, false, LargeTile>(a, s);
     return bf16 ? launch_dense_shape<MODE, true, SmallTile>(a, s) : launch_dense_shape<MODE, false, SmallTile>(a, s);

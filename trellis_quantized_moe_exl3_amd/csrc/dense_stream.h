@@ -383,7 +383,7 @@ __global__ __launch_bounds__(64 * NW) void dense_tile_kernel(DenseArgs a)
             for (int s = 1; s < NW; ++s)
                 v[j] += red[s * kStep + (4 * i + j) * 64 + l];
         }
-        dense_store<MODE, BF16, 4>(a, z, m0 + 16 * i, n0, l, v);
+        dense_store<MODE, BF16>(a, z, m0 + 16 * i, n0, l, v, (LDS_AS f32x4 *)(LDS_AS uint16_t *)ring1 + 256 * w);
     }
 }
 
