@@ -46,13 +46,15 @@ MOE_DEV f32x4 dense_mfma(u32x4 q, u32x4 p, f32x4 c)
                                                        0, 0, 0);
 }
 
+// Two fp32 rounded to nearest even (one instruction for bf16).
 template <bool BF16>
 MOE_DEV uint32_t pack16(float lo, float hi)
 {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
     if constexpr (BF16)
-        return f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){lo, hi}, bf16x2));
     else
-        return f32_to_f16_bits(lo) | ((uint32_t)f32_to_f16_bits(hi) << 16);
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){lo, hi}, f16x2));
 }
 
 // The transposing LDS read: in a group of 16 lanes, lane i passes the address of

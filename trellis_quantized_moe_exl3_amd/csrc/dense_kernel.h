@@ -13,11 +13,13 @@ MOE_DEV float logistic(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)
 constexpr float kGeluK = 0.7978845608028654f;   // sqrt(2 / pi)
 constexpr float kGeluC = 0.044715f;
 
-MOE_DEV float act_value(int act, float g)
+template <int ACT>
+MOE_DEV float act_value(float g)
 {
-    if (act == MOE_EXL3_ACT_SILU)
+    if constexpr (ACT == MOE_EXL3_ACT_SILU)
         return silu_f(g);
-    return g * logistic(2.0f * kGeluK * (g + kGeluC * g * g * g));
+    else
+        return g * logistic(2.0f * kGeluK * (g + kGeluC * g * g * g));
 }
 
 MOE_DEV void act_value_slope(int act, float g, float &v, float &d)
@@ -70,7 +72,8 @@ MOE_DEV void glu_store(const DenseArgs &a, int m, int n, f32x4 g, f32x4 u)
     float h[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-        h[r] = act_value(a.act, g[r]) * u[r];
+        h[r] = (a.act == MOE_EXL3_ACT_SILU ? act_value<MOE_EXL3_ACT_SILU>(g[r])
+                                           : act_value<MOE_EXL3_ACT_GELU_TANH>(g[r])) * u[r];
     *(u32x2 *)(a.out[0] + (int64_t)m * a.ldo + n) = (u32x2){pack16<BF16>(h[0], h[1]), pack16<BF16>(h[2], h[3])};
     if (a.pre) {
         float *p = a.pre + (int64_t)m * a.N + n;
@@ -102,13 +105,14 @@ MOE_DEV u32x4 pack8(f32x4 a, f32x4 b)
 }
 
 // Epilogue of the 16 rows m0 .. of a wavefront's 64 tile columns (n0: the first
-// result column; GLU: of its 32).  The accumulators hold four columns of row
-// l % 16: stored as they are, neighbouring lanes would write to different rows
-// and every lane be a memory transaction of its own.  They pass through 4 KiB
-// of LDS that only this wavefront uses (16-byte unit c of row r in place
-// c ^ r), so that eight lanes write the 128 bytes of a row (GLU: four lanes 64)
-// (2048 tokens, adapters alone, 4096 columns: 25.0 -> BESIDE us).
-template <int MODE, bool BF16>
+// result column; GLU: of its 32; ACT: its activation).  The accumulators hold
+// four columns of row l % 16: stored as they are, neighbouring lanes would
+// write to different rows and every lane be a memory transaction of its own.
+// They pass through 4 KiB of LDS that only this wavefront uses (16-byte unit c
+// of row r in place c ^ r), so that eight lanes write the 128 bytes of a row
+// (GLU: four lanes 64) (2048 tokens, adapters alone, 4096 columns: tile kernel
+// 14.2 -> 12.2 us).
+template <int MODE, bool BF16, int ACT>
 MOE_DEV void dense_store(const DenseArgs &a, int z, int m0, int n0, int l, const f32x4 (&v)[4], LDS_AS f32x4 *lds)
 {
     const int r = l & 15;
@@ -116,43 +120,63 @@ MOE_DEV void dense_store(const DenseArgs &a, int z, int m0, int n0, int l, const
     for (int j = 0; j < 4; ++j)
         lds[16 * r + ((4 * j + (l >> 4)) ^ r)] = v[j];
     auto at = [&](int row, int unit) { return lds[16 * row + (unit ^ row)]; };
+    // one 64-bit address for the 16 rows, 32-bit offsets in them
+    uint16_t *out = a.out[MODE == DENSE_DW ? z : 0] + (int64_t)m0 * a.ldo + n0;
+    const int left = a.M - m0, ldo = (int)a.ldo;
     if constexpr (MODE == DENSE_GLU) {
-        const int row = l >> 2, c = 2 * (l & 3), m = m0 + row, n = n0 + 4 * c;
+        const int row = l >> 2, c = 2 * (l & 3);
         const f32x4 g[2] = {at(row, c), at(row, c + 1)}, u[2] = {at(row, 8 + c), at(row, 9 + c)};
-        if (m >= a.M || n >= a.N)
+        if (row >= left || n0 + 4 * c >= a.N)
             return;
         f32x4 h[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int d = 0; d < 4; ++d)
-                h[q][d] = act_value(a.act, g[q][d]) * u[q][d];
-        *(u32x4 *)(a.out[0] + (int64_t)m * a.ldo + n) = pack8<BF16>(h[0], h[1]);
+                h[q][d] = act_value<ACT>(g[q][d]) * u[q][d];
+        *(u32x4 *)(out + (uint32_t)(row * ldo + 4 * c)) = pack8<BF16>(h[0], h[1]);
         if (a.pre) {
-            f32x4 *p = (f32x4 *)(a.pre + (int64_t)m * a.N + n), *pu = (f32x4 *)((float *)p + (int64_t)a.M * a.N);
-            p[0] = g[0];
-            p[1] = g[1];
-            pu[0] = u[0];
-            pu[1] = u[1];
+            float *pg = a.pre + (int64_t)m0 * a.N + n0, *pu = pg + (int64_t)a.M * a.N;
+            const uint32_t o = (uint32_t)(row * a.N + 4 * c);
+            *(f32x4 *)(pg + o) = g[0];
+            *(f32x4 *)(pg + o + 4) = g[1];
+            *(f32x4 *)(pu + o) = u[0];
+            *(f32x4 *)(pu + o + 4) = u[1];
         }
     } else {
-        uint16_t *out = a.out[MODE == DENSE_DW ? z : 0];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int row = 8 * h + (l >> 3), c = 2 * (l & 7), m = m0 + row, n = n0 + 4 * c;
+            const int row = 8 * h + (l >> 3), c = 2 * (l & 7);
             f32x4 y[2] = {at(row, c), at(row, c + 1)};
-            if (m >= a.M || n >= a.N)
+            if (row >= left || n0 + 4 * c >= a.N)
                 continue;
             if constexpr (MODE == DENSE_LIN) {
                 if (a.base) {
-                    const u32x4 b = *(const u32x4 *)(a.base + (int64_t)m * a.ldbase + n);
+                    const uint16_t *base = a.base + (int64_t)m0 * a.ldbase + n0;
+                    const u32x4 b = *(const u32x4 *)(base + (uint32_t)(row * (int)a.ldbase + 4 * c));
 #pragma unroll
                     for (int d = 0; d < 8; ++d)
                         y[d >> 2][d & 3] += act_to_f32<BF16>((uint16_t)(b[d >> 1] >> (16 * (d & 1))));
                 }
             }
-            *(u32x4 *)(out + (int64_t)m * a.ldo + n) = pack8<BF16>(y[0], y[1]);
+            *(u32x4 *)(out + (uint32_t)(row * ldo + 4 * c)) = pack8<BF16>(y[0], y[1]);
         }
+    }
+}
+
+// The same for N blocks of 16 rows.
+template <int MODE, bool BF16, int N>
+MOE_DEV void dense_store_all(const DenseArgs &a, int z, int m0, int n0, int l, const f32x4 (&v)[N][4],
+                             LDS_AS f32x4 *lds)
+{
+    if (MODE != DENSE_GLU || a.act == MOE_EXL3_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            dense_store<MODE, BF16, MOE_EXL3_ACT_SILU>(a, z, m0 + 16 * i, n0, l, v[i], lds);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            dense_store<MODE, BF16, MOE_EXL3_ACT_GELU_TANH>(a, z, m0 + 16 * i, n0, l, v[i], lds);
     }
 }
 
@@ -513,9 +537,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
     __syncthreads();   // the ring is free
     LDS_AS f32x4 *lds = (LDS_AS f32x4 *)(LDS_AS uint16_t *)ring0 + 256 * w;
     static_assert(S::NW * 4096 <= kHalves * 2, "a wavefront's share of the first ring array");
-#pragma unroll
-    for (int i = 0; i < S::NI; ++i)
-        dense_store<MODE, BF16>(a, z, mw + 16 * i, nw, l, acc[i], lds);
+    dense_store_all<MODE, BF16>(a, z, mw, nw, l, acc, lds);
 }
 
 // Sum of the k splits' partial tiles, in split order, and the epilogue: block
@@ -544,7 +566,7 @@ __global__ __launch_bounds__(64 * S::NW) void dense_finish_kernel(DenseArgs a)
             acc[0][j] += part[k * step + j * (64 * S::NW)];
     const int mw = m0 + wm * S::TM + 16 * i, nw = n0 + wn * ((kDenseCols<MODE, S>) / S::WN);
     __shared__ f32x4 lds[S::NW * 256];
-    dense_store<MODE, BF16>(a, z, mw, nw, l, acc[0], (LDS_AS f32x4 *)lds + 256 * w);
+    dense_store_all<MODE, BF16>(a, z, mw, nw, l, acc, (LDS_AS f32x4 *)lds + 256 * w);
 }
 
 template <int MODE, bool BF16, class S>

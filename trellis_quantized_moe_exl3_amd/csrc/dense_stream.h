@@ -152,55 +152,95 @@ struct Stream {
     }
 };
 
+// ---- adapters: x A^T
+
+// The adapter and the rank of token t: -1 and 0 for none.
+MOE_DEV void token_adapter(const LoraArgs &lo, int t, int T, int &id, int &rk)
+{
+    id = t < T ? lo.ids[t] : -1;
+    if (id < 0 || id >= lo.n)
+        id = -1;
+    rk = id < 0 ? 0 : lo.ranks ? min(max(lo.ranks[id], 0), lo.rank) : lo.rank;
+}
+
+// sum += this wavefront's k share of scales[e] x[t] A_e^T, rows r0 .. r0 + 16 NR
+// of A_e, for the 16 tokens of the lanes (lane l: token l % 16 with adapter id
+// and rank, -1: none); once per adapter that they name.
+template <bool BF16, int NR, int RING, class F>
+MOE_DEV void lora_rows(const LoraArgs &lo, int id, int rank, int r0, int l, int w, int nw, int K, int64_t ldx,
+                       __amdgpu_buffer_rsrc_t xr, F row, LDS_AS uint16_t *ring0, LDS_AS uint16_t *ring1,
+                       LDS_AS uint16_t *ring2, LDS_AS uint16_t *ring3, f32x4 (&sum)[NR])
+{
+    Stream<BF16, 1, NR, RING> st;
+    st.p = xr;
+    st.init(l, K, ldx, K, row, [&](int r) { return (int64_t)(r0 + r); });
+    uint64_t left = __ballot(rank > r0);   // without rows here there is nothing to add
+    while (left) {
+        const int at = __ffsll((unsigned long long)left) - 1;
+        const int e = __builtin_amdgcn_readlane(id, at), rk = __builtin_amdgcn_readlane(rank, at);
+        const bool mine = id == e;
+        left &= ~__ballot(mine);
+        const float sc = lo.scales ? lo.scales[e] : 1.0f;
+        // rows from the adapter's own rank on lie past its buffer: zeros
+        st.q[0] = buf_rsrc(lo.a + (int64_t)e * lo.rank * K, (uint32_t)rk * (uint32_t)K * 2u);
+        st.q[1] = st.q[0];
+        f32x4 acc[1][NR] = {};
+        st.run(w, nw, ring0, ring1, ring2, ring3, acc);
+        if (mine)
+#pragma unroll
+            for (int j = 0; j < NR; ++j)
+                sum[j] = acc[0][j] * sc;
+    }
+}
+
 // ---- the block and the projection for few tokens
 
-// delta[t][16 columns]: the adapters' rows of tokens t = w, w + XW, .. , four
-// at a time: lane l takes column l / 4 and the k octets l % 4 + 0, 4, .. of the
-// token's adapter (four lanes to 64 bytes of a row of B), summed in fp32.
-template <bool BF16, int XW>
+// delta[t][16 columns]: the adapters' rows of tokens t = w, w + XW, .. , kBatch
+// at a time with all their loads in flight: lane l takes column l / 4 and the k
+// octets l % 4 + 0, 4, .. of the token's adapter (four lanes to 64 bytes of a
+// row of B), summed in fp32.
+template <bool BF16, int NI, int XW>
 MOE_DEV void skinny_expand(const DenseArgs &a, int n0, int w, int l, float (*delta)[16])
 {
     const LoraArgs &lo = a.lora;
+    int mine, rank;   // of token l
+    token_adapter(lo, l, a.M, mine, rank);
     const int c = l >> 2, n = min(n0 + c, a.N - 1);
-    constexpr int kBatch = 4;
-    for (int t0 = w; t0 < a.M; t0 += kBatch * XW) {
-        int rk[kBatch], most = 0;
-        const uint16_t *bp[kBatch], *up[kBatch];
+    constexpr int kBatch = 16 * NI / XW;   // tokens of a wavefront
+    int rk[kBatch], most = 0;
+    const uint16_t *bp[kBatch], *up[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+        const int t = w + b * XW;   // below 16 NI <= 64
+        rk[b] = __builtin_amdgcn_readlane(rank, t);
+        most = max(most, rk[b]);
+        const int e = max(__builtin_amdgcn_readlane(mine, t), 0);
+        bp[b] = lo.b + ((int64_t)e * a.N + n) * lo.rank;
+        up[b] = lo.mid + (int64_t)min(t, a.M - 1) * lo.rpad;
+    }
+    float sum[kBatch] = {};
+    for (int k = 8 * (l & 3); k < most; k += 32) {
+        u32x4 bv[kBatch], uv[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int t = min(t0 + b * XW, a.M - 1);
-            const int id = lo.ids[t];
-            const bool on = id >= 0 && id < lo.n;
-            const int e = on ? id : 0;
-            rk[b] = on ? (lo.ranks ? min(max(lo.ranks[e], 0), lo.rank) : lo.rank) : 0;
-            most = max(most, rk[b]);
-            bp[b] = lo.b + ((int64_t)e * a.N + n) * lo.rank;
-            up[b] = lo.mid + (int64_t)t * lo.rpad;
+            bv[b] = *(const u32x4 *)(bp[b] + min(k, lo.rank - 8));
+            uv[b] = *(const u32x4 *)(up[b] + k);
         }
-        float sum[kBatch] = {};
-        for (int k = 8 * (l & 3); k < most; k += 32) {
-            u32x4 bv[kBatch], uv[kBatch];
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                bv[b] = *(const u32x4 *)(bp[b] + min(k, lo.rank - 8));
-                uv[b] = *(const u32x4 *)(up[b] + k);
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+                const float y = act_to_f32<BF16>((uint16_t)(bv[b][d >> 1] >> (16 * (d & 1)))) *
+                                act_to_f32<BF16>((uint16_t)(uv[b][d >> 1] >> (16 * (d & 1))));
+                sum[b] += k + d < rk[b] ? y : 0.0f;
             }
+    }
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-                for (int d = 0; d < 8; ++d) {
-                    const float y = act_to_f32<BF16>((uint16_t)(bv[b][d >> 1] >> (16 * (d & 1)))) *
-                                    act_to_f32<BF16>((uint16_t)(uv[b][d >> 1] >> (16 * (d & 1))));
-                    sum[b] += k + d < rk[b] ? y : 0.0f;
-                }
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            sum[b] += __shfl_xor(sum[b], 1);
-            sum[b] += __shfl_xor(sum[b], 2);
-            if ((l & 3) == 0 && t0 + b * XW < a.M)
-                delta[t0 + b * XW][c] = sum[b];
-        }
+    for (int b = 0; b < kBatch; ++b) {
+        sum[b] += __shfl_xor(sum[b], 1);
+        sum[b] += __shfl_xor(sum[b], 2);
+        if ((l & 3) == 0)
+            delta[w + b * XW][c] = sum[b];
     }
 }
 
@@ -241,7 +281,8 @@ __global__ __launch_bounds__(64 * (NW + XW)) void dense_skinny_kernel(DenseArgs 
         for (int i = 0; i < NI; ++i)
             red[w * kStep + 64 * i + l] = acc[i][0];
     } else {
-        skinny_expand<BF16, XW>(a, n0, w - NW, l, delta);
+        if constexpr (XW > 0)
+            skinny_expand<BF16, NI, XW>(a, n0, w - NW, l, delta);
     }
     __syncthreads();
     if (w >= NI)
@@ -268,14 +309,15 @@ __global__ __launch_bounds__(64 * (NW + XW)) void dense_skinny_kernel(DenseArgs 
 template <int MODE, bool BF16>
 hipError_t launch_skinny(const DenseArgs &a, hipStream_t s)
 {
-    constexpr int kCols = MODE == DENSE_GLU ? 8 : 16, XW = MODE == DENSE_LIN ? 4 : 0;
+    constexpr int kCols = MODE == DENSE_GLU ? 8 : 16;
+    constexpr bool kLin = MODE == DENSE_LIN;
     const unsigned grid = (unsigned)((a.N + kCols - 1) / kCols);
     if (a.M <= 16)
-        dense_skinny_kernel<MODE, BF16, 1, 8, 4, XW><<<grid, 64 * (8 + XW), 0, s>>>(a);
+        dense_skinny_kernel<MODE, BF16, 1, 8, 4, kLin ? 4 : 0><<<grid, 64 * (kLin ? 12 : 8), 0, s>>>(a);
     else if (a.M <= 32)
-        dense_skinny_kernel<MODE, BF16, 2, 8, 3, XW><<<grid, 64 * (8 + XW), 0, s>>>(a);
+        dense_skinny_kernel<MODE, BF16, 2, 8, 3, kLin ? 8 : 0><<<grid, 64 * (kLin ? 16 : 8), 0, s>>>(a);
     else
-        dense_skinny_kernel<MODE, BF16, 4, 4, 3, XW><<<grid, 64 * (4 + XW), 0, s>>>(a);
+        dense_skinny_kernel<MODE, BF16, 4, 4, 3, kLin ? 8 : 0><<<grid, 64 * (kLin ? 12 : 4), 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -285,14 +327,12 @@ hipError_t launch_skinny(const DenseArgs &a, hipStream_t s)
 // dealt to the NW wavefronts by their number (so that a token's sum is taken in
 // the same order whatever its neighbours), each adding B_a's rows against the
 // tokens' s_a x A_a^T to its own part of the sums.
+// mine, rank: the adapter of token m0 + l.
 template <bool BF16, int NW, class S>
-MOE_DEV void tile_expand(const DenseArgs &a, int m0, int n0, int w, int l, LDS_AS uint16_t *r0, LDS_AS uint16_t *r1,
-                         f32x4 (&acc)[4][4])
+MOE_DEV void tile_expand(const DenseArgs &a, int mine, int rank, int m0, int n0, int w, int l, LDS_AS uint16_t *r0,
+                         LDS_AS uint16_t *r1, f32x4 (&acc)[4][4])
 {
     const LoraArgs &lo = a.lora;
-    int mine = m0 + l < a.M ? lo.ids[m0 + l] : -1;   // of token m0 + l
-    if (mine < 0 || mine >= lo.n)
-        mine = -1;
     uint64_t left = __ballot(mine >= 0);
     if (!left)
         return;
@@ -305,11 +345,11 @@ MOE_DEV void tile_expand(const DenseArgs &a, int m0, int n0, int w, int l, LDS_A
     st.init(l, 0, lo.rpad, lo.rank, [&](int r) { return (int64_t)(m0 + r); },
             [&](int r) { return (int64_t)(n0 + r); });
     while (left) {
-        const int e = __builtin_amdgcn_readlane(mine, __ffsll((unsigned long long)left) - 1);
+        const int at = __ffsll((unsigned long long)left) - 1;
+        const int e = __builtin_amdgcn_readlane(mine, at), rk = __builtin_amdgcn_readlane(rank, at);
         left &= ~__ballot(mine == e);
         if (e % NW != w)
             continue;
-        const int rk = lo.ranks ? min(max(lo.ranks[e], 0), lo.rank) : lo.rank;
         st.kend = rk;
         st.q[0] = buf_rsrc(lo.b + (int64_t)e * a.N * lo.rank, (uint32_t)((int64_t)a.N * lo.rank * 2));
         st.q[1] = st.q[0];
@@ -356,6 +396,9 @@ __global__ __launch_bounds__(64 * NW) void dense_tile_kernel(DenseArgs a)
         for (int j = 0; j < 4; ++j)
             acc[i][j] = (f32x4){};
     LDS_AS uint16_t *r0 = (LDS_AS uint16_t *)ring0 + w * S::kHalves, *r1 = (LDS_AS uint16_t *)ring1 + w * S::kHalves;
+    int mine = -1, rank = 0;
+    if constexpr (MODE == DENSE_LIN)
+        token_adapter(a.lora, m0 + l, a.M, mine, rank);
     st.run(w, NW, r0, r1, nullptr, nullptr, acc);
     if constexpr (MODE == DENSE_DX) {
         st.p = buf_rsrc(a.p[1], a.pbytes);
@@ -363,7 +406,7 @@ __global__ __launch_bounds__(64 * NW) void dense_tile_kernel(DenseArgs a)
         st.run(w, NW, r0, r1, nullptr, nullptr, acc);
     }
     if constexpr (MODE == DENSE_LIN)
-        tile_expand<BF16, NW, S>(a, m0, n0, w, l, r0, r1, acc);
+        tile_expand<BF16, NW, S>(a, mine, rank, m0, n0, w, l, r0, r1, acc);
     // every wavefront's sums in its own part of the first ring array
     LDS_AS f32x4 *red = (LDS_AS f32x4 *)((LDS_AS uint16_t *)ring0);
     constexpr int kStep = S::kHalves / 8;
@@ -375,15 +418,15 @@ __global__ __launch_bounds__(64 * NW) void dense_tile_kernel(DenseArgs a)
             red[w * kStep + (4 * i + j) * 64 + l] = acc[i][j];
     __syncthreads();
     for (int i = w; i < 4; i += NW) {
-        f32x4 v[4];
+        f32x4 v[1][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            v[j] = red[(4 * i + j) * 64 + l];
+            v[0][j] = red[(4 * i + j) * 64 + l];
 #pragma unroll
             for (int s = 1; s < NW; ++s)
-                v[j] += red[s * kStep + (4 * i + j) * 64 + l];
+                v[0][j] += red[s * kStep + (4 * i + j) * 64 + l];
         }
-        dense_store<MODE, BF16>(a, z, m0 + 16 * i, n0, l, v, (LDS_AS f32x4 *)(LDS_AS uint16_t *)ring1 + 256 * w);
+        dense_store_all<MODE, BF16>(a, z, m0 + 16 * i, n0, l, v, (LDS_AS f32x4 *)(LDS_AS uint16_t *)ring1 + 256 * w);
     }
 }
 

@@ -4,89 +4,77 @@
 
 namespace moe {
 
+// The call's status word: ids and ranks outside their ranges.
+template <int THREADS>
+MOE_DEV void check_adapters(const LoraArgs &lo, int T, int tid)
+{
+    int bad = 0;
+    constexpr int kBatch = 4;   // 16-byte loads in flight a thread
+    const int quads = T / 4;
+    for (int t = tid; t < quads; t += kBatch * THREADS) {
+        u32x4 v[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            v[b] = ((const u32x4 *)lo.ids)[min(t + b * THREADS, quads - 1)];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                bad |= ((int)v[b][d] < -1 || (int)v[b][d] >= lo.n) ? 1 : 0;
+    }
+    for (int t = 4 * quads + tid; t < T; t += THREADS)
+        bad |= (lo.ids[t] < -1 || lo.ids[t] >= lo.n) ? 1 : 0;
+    if (lo.ranks)
+        for (int e = tid; e < lo.n; e += THREADS)
+            bad |= (lo.ranks[e] < 0 || lo.ranks[e] > lo.rank) ? 2 : 0;
+    const int index = __syncthreads_or(bad & 1), width = __syncthreads_or(bad & 2);
+    if (tid == 0)
+        *lo.status = (index ? (int)MOE_EXL3_STATUS_BAD_INDEX : 0) | (width ? (int)MOE_EXL3_STATUS_BAD_WIDTH : 0);
+}
+
 // mid[t][0..rpad) = scales[e] x[t] A_e^T, e = ids[t], in 16 bits for the second
 // product; zeros from the adapter's own rank on.  Tokens without an adapter are
 // not written.
 //
-// Block (f, r): `tpf` tokens (1 or 16) against 32 rows of their adapters, k cut
-// over the NW wavefronts.  Tokens are the matrix instruction's columns, so a
-// 16-token block that names several adapters runs once per adapter and each
+// Block (f, r): `tpf` tokens (1 or 16) against 16 NR rows of their adapters, k
+// cut over the NW wavefronts.  Tokens are the matrix instruction's columns, so
+// a 16-token block that names several adapters runs once per adapter and each
 // token keeps its own result.  One token a block lets all the adapters of a
 // decode step stream at once, at the price of reading an adapter once per
 // token; 16 tokens a block read it once where a request's tokens stand together.
-template <bool BF16, int NW>
+template <bool BF16, int NW, int NR, int RING>
 __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(const uint16_t *x, int64_t ldx, uint32_t xbytes, int T,
                                                               int K, int tpf, LoraArgs lo)
 {
-    using S = Stream<BF16, 1, 2, 3>;
-    __shared__ __align__(1024) uint16_t ring0[NW * S::kHalves], ring1[NW * S::kHalves], ring2[NW * S::kHalves];
+    using S = Stream<BF16, 1, NR, RING>;
+    __shared__ __align__(1024) uint16_t ring0[NW * S::kHalves], ring1[NW * S::kHalves], ring2[NW * S::kHalves],
+        ring3[RING == 4 ? NW * S::kHalves : 8];
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int f = blockIdx.x, r0 = 32 * blockIdx.y, c = l & 15;
-
-    if (f == 0 && r0 == 0) {
-        // the call's status word: ids and ranks outside their ranges
-        int bad = 0;
-        constexpr int kBatch = 4;   // 16-byte loads in flight a thread
-        const int quads = T / 4, threads = 64 * NW;
-        for (int t = tid; t < quads; t += kBatch * threads) {
-            u32x4 v[kBatch];
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b)
-                v[b] = ((const u32x4 *)lo.ids)[min(t + b * threads, quads - 1)];
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    bad |= ((int)v[b][d] < -1 || (int)v[b][d] >= lo.n) ? 1 : 0;
-        }
-        for (int t = 4 * quads + tid; t < T; t += threads)
-            bad |= (lo.ids[t] < -1 || lo.ids[t] >= lo.n) ? 1 : 0;
-        if (lo.ranks)
-            for (int e = tid; e < lo.n; e += threads)
-                bad |= (lo.ranks[e] < 0 || lo.ranks[e] > lo.rank) ? 2 : 0;
-        const int index = __syncthreads_or(bad & 1), width = __syncthreads_or(bad & 2);
-        if (tid == 0)
-            *lo.status = (index ? (int)MOE_EXL3_STATUS_BAD_INDEX : 0) | (width ? (int)MOE_EXL3_STATUS_BAD_WIDTH : 0);
+    const int f = blockIdx.x, r0 = 16 * NR * blockIdx.y, c = l & 15;
+    if (f * tpf >= T) {   // the last block
+        if (r0 == 0)
+            check_adapters<64 * NW>(lo, T, tid);
+        return;
     }
-
     const int t = f * tpf + c;
-    int id = c < tpf && t < T ? lo.ids[t] : -1;
-    if (id >= lo.n)
-        id = -1;
-    S st;
-    st.p = buf_rsrc(x, xbytes);
-    // rows past the block's tokens read zeros
-    st.init(l, K, ldx, K, [&](int r) { return (int64_t)(r < tpf ? f * tpf + r : T); },
-            [&](int r) { return (int64_t)(r0 + r); });
-    f32x4 sum[2] = {};
-    bool left = id >= 0;
-    for (;;) {
-        const uint64_t any = __ballot(left);
-        if (!any)
-            break;
-        const int e = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)any) - 1);
-        const int rk = lo.ranks ? min(max(lo.ranks[e], 0), lo.rank) : lo.rank;
-        const float sc = lo.scales ? lo.scales[e] : 1.0f;
-        // rows from the adapter's own rank on lie past its buffer: zeros
-        st.q[0] = buf_rsrc(lo.a + (int64_t)e * lo.rank * K, (uint32_t)rk * (uint32_t)K * 2u);
-        st.q[1] = st.q[0];
-        f32x4 acc[1][2] = {};
-        const int at = w * S::kHalves;
-        st.run(w, NW, (LDS_AS uint16_t *)ring0 + at, (LDS_AS uint16_t *)ring1 + at, (LDS_AS uint16_t *)ring2 + at,
-               nullptr, acc);
-        if (id == e) {
-            sum[0] = acc[0][0] * sc;
-            sum[1] = acc[0][1] * sc;
-            left = false;
-        }
-    }
+    int id, rank;   // of this lane's token
+    token_adapter(lo, c < tpf ? t : T, T, id, rank);
+    const int at = w * S::kHalves;
+    f32x4 sum[NR] = {};
+    lora_rows<BF16, NR, RING>(
+        lo, id, rank, r0, l, w, NW, K, ldx, buf_rsrc(x, xbytes),
+        // rows past the block's tokens read zeros
+        [&](int r) { return (int64_t)(r < tpf ? f * tpf + r : T); }, (LDS_AS uint16_t *)ring0 + at,
+        (LDS_AS uint16_t *)ring1 + at, (LDS_AS uint16_t *)ring2 + at, (LDS_AS uint16_t *)ring3 + (RING == 4 ? at : 0),
+        sum);
     // the wavefronts' sums, each in its own part of the first ring array
     LDS_AS f32x4 *red = (LDS_AS f32x4 *)((LDS_AS uint16_t *)ring0);
     constexpr int kStep = S::kHalves / 8;
-    red[w * kStep + l] = sum[0];
-    red[w * kStep + 64 + l] = sum[1];
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+        red[w * kStep + 64 * j + l] = sum[j];
     __syncthreads();
-    if (w >= 2 || id < 0)
+    if (w >= NR || id < 0)
         return;
     f32x4 v = red[64 * w + l];
 #pragma unroll
@@ -100,23 +88,35 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(const uint16_t *x,
 // adapters (about 6 us from L2).
 constexpr int64_t kShrinkBytes = 64 << 20;
 
+template <bool BF16>
+static void shrink(const uint16_t *x, int64_t ldx, uint32_t xbytes, int T, int K, const LoraArgs &l, hipStream_t s)
+{
+    if ((int64_t)T * l.rank * K * 2 <= kShrinkBytes) {
+        // one block more, for the status word; every wavefront of a 2048-k
+        // token has all its shares in flight
+        const dim3 grid((unsigned)(T + 1), (unsigned)(l.rpad / 16));
+        if ((int64_t)T * grid.y <= 512)
+            lora_shrink_kernel<BF16, 8, 1, 4><<<grid, 512, 0, s>>>(x, ldx, xbytes, T, K, 1, l);
+        else
+            lora_shrink_kernel<BF16, 4, 1, 4><<<grid, 256, 0, s>>>(x, ldx, xbytes, T, K, 1, l);
+    } else {
+        const dim3 grid((unsigned)((T + 15) / 16 + 1), (unsigned)(l.rpad / 32));
+        // eight wavefronts a block while that is one block a CU (144 KiB of
+        // LDS), four and two blocks beyond
+        if ((int64_t)(grid.x - 1) * grid.y <= 256)
+            lora_shrink_kernel<BF16, 8, 2, 3><<<grid, 512, 0, s>>>(x, ldx, xbytes, T, K, 16, l);
+        else
+            lora_shrink_kernel<BF16, 4, 2, 3><<<grid, 256, 0, s>>>(x, ldx, xbytes, T, K, 16, l);
+    }
+}
+
 hipError_t launch_lora_shrink(bool bf16, const uint16_t *x, int64_t ldx, uint32_t xbytes, int64_t T, int K,
                               const LoraArgs &l, hipStream_t s)
 {
-    const unsigned chunks = (unsigned)(l.rpad / 32);
-    if (T * l.rank * K * 2 <= kShrinkBytes) {
-        const dim3 grid((unsigned)T, chunks);
-        if (bf16)
-            lora_shrink_kernel<true, 8><<<grid, 512, 0, s>>>(x, ldx, xbytes, (int)T, K, 1, l);
-        else
-            lora_shrink_kernel<false, 8><<<grid, 512, 0, s>>>(x, ldx, xbytes, (int)T, K, 1, l);
-    } else {
-        const dim3 grid((unsigned)((T + 15) / 16), chunks);
-        if (bf16)
-            lora_shrink_kernel<true, 4><<<grid, 256, 0, s>>>(x, ldx, xbytes, (int)T, K, 16, l);
-        else
-            lora_shrink_kernel<false, 4><<<grid, 256, 0, s>>>(x, ldx, xbytes, (int)T, K, 16, l);
-    }
+    if (bf16)
+        shrink<true>(x, ldx, xbytes, (int)T, K, l, s);
+    else
+        shrink<false>(x, ldx, xbytes, (int)T, K, l, s);
     return hipGetLastError();
 }
 
