@@ -13,9 +13,9 @@ constexpr int64_t kMaxSize = 65536;
 constexpr int64_t kMaxLd = 1 << 20;
 constexpr int64_t kSpanLimit = (int64_t)1 << 31;
 
-// k splits of the 128-tile: at most this many blocks, each with at least this
-// many stages (256 k).
-constexpr int64_t kSplitBlocks = 512;
+// k splits of the 128-tile: at most this many blocks (one a CU), each with at
+// least this many stages (256 k).
+constexpr int64_t kSplitBlocks = 256;
 constexpr int64_t kSplitStages = 8;
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
@@ -470,7 +470,10 @@ int moe_exl3_lora_linear(const moe_exl3_lora_desc *desc, const void *x, int64_t 
     l.n = (int)n;
     l.rank = (int)r;
     l.rpad = p.rpad;
-    if (launch_lora_shrink(bf16, (const uint16_t *)x, ldx, (uint32_t)mx.span(), T, (int)K, l, s) != hipSuccess)
+    l.k = (int)K;
+    l.fused = T == 1 && r <= kFusedRank && r * K * 2 <= kFusedBytes && N <= kFusedCols;
+    if (!l.fused &&
+        launch_lora_shrink(bf16, (const uint16_t *)x, ldx, (uint32_t)mx.span(), T, (int)K, l, s) != hipSuccess)
         return MOE_EXL3_ERR_HIP;
     a.p[0] = (const uint16_t *)x;
     a.q[0] = (const uint16_t *)w;

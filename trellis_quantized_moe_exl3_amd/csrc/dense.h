@@ -19,6 +19,15 @@ constexpr int kDenseLow = 224;   // rows of a large tile where they fill the rou
 constexpr int kDenseBK = 32;
 // Tokens up to which the forward operators take the few-token kernel.
 constexpr int64_t kSkinnyTokens = 64;
+// Largest rank, bytes of A and columns up to which the few-token kernel computes
+// one token's x A^T itself, in every block.  Up to 4096 columns that is one
+// block a CU (2048 x 4096, rank 16: 11.8 -> 9.2 us a call; 4096 x 2048, rank 32:
+// 12.1 -> 10.8; but 8192 x 8192, rank 16: 34.9 -> 42.7).  Two tokens' adapters,
+// one after the other, take longer than the launch they save (4096 x 4096, rank
+// 8: 12.2 -> 14.7).
+constexpr int kFusedRank = 32;
+constexpr int64_t kFusedBytes = 256 << 10;
+constexpr int64_t kFusedCols = 4096;
 // Largest rank of an adapter.
 constexpr int kMaxRank = 256;
 
@@ -41,6 +50,8 @@ struct LoraArgs {
     int32_t *status;         // status word of the call
     uint16_t *mid;           // [T][rpad] s_a x A_a^T in 16 bits, zeros from the adapter's rank on
     int n, rank, rpad;       // rpad: rank rounded up to 32
+    int k;                   // columns of x and of A's rows
+    bool fused;              // one token: x A^T in the same launch, mid is not used
 };
 
 struct DenseArgs {

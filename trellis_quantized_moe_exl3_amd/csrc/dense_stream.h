@@ -244,16 +244,75 @@ MOE_DEV void skinny_expand(const DenseArgs &a, int n0, int w, int l, float (*del
     }
 }
 
+// skinny_expand of one token of rank at most 32 with x A^T computed here, by the
+// XW wavefronts of the block that do not stream weights (one barrier of the
+// whole block between the two products).
+template <bool BF16, int XW>
+MOE_DEV void fused_expand(const DenseArgs &a, int n0, int w, int l, float (*delta)[16])
+{
+    using S = Stream<BF16, 1, 2, 3>;
+    __shared__ __align__(1024) uint16_t ring0[XW * S::kHalves], ring1[XW * S::kHalves], ring2[XW * S::kHalves];
+    const LoraArgs &lo = a.lora;
+    int id, rank;   // of token l % 16: the one in lanes 0, 16, ..
+    token_adapter(lo, l & 15, a.M, id, rank);
+    if (blockIdx.x == 0 && w == 0) {
+        // the call's status word
+        bool wide = false;
+        if (lo.ranks)
+            for (int e = l; e < lo.n; e += 64)
+                wide |= lo.ranks[e] < 0 || lo.ranks[e] > lo.rank;
+        const bool width = __ballot(wide), index = lo.ids[0] < -1 || lo.ids[0] >= lo.n;
+        if (l == 0)
+            *lo.status = (index ? (int)MOE_EXL3_STATUS_BAD_INDEX : 0) | (width ? (int)MOE_EXL3_STATUS_BAD_WIDTH : 0);
+    }
+    // B's rows for the second product: lane l takes column l / 4, ranks k .. k + 7
+    const int c = l >> 2, n = min(n0 + c, a.N - 1), k = 8 * (l & 3);
+    const int e = max(__builtin_amdgcn_readfirstlane(id), 0), rk = __builtin_amdgcn_readfirstlane(rank);
+    u32x4 bv = {};
+    if (k < rk)
+        bv = *(const u32x4 *)(lo.b + ((int64_t)e * a.N + n) * lo.rank + k);
+    f32x4 sum[2] = {};
+    const int at = w * S::kHalves;
+    lora_rows<BF16, 2, 3>(lo, id, rank, 0, l, w, XW, lo.k, a.ldp, buf_rsrc(a.p[0], a.pbytes),
+                          [](int r) { return (int64_t)r; }, (LDS_AS uint16_t *)ring0 + at,
+                          (LDS_AS uint16_t *)ring1 + at, (LDS_AS uint16_t *)ring2 + at, nullptr, sum);
+    LDS_AS f32x4 *red = (LDS_AS f32x4 *)((LDS_AS uint16_t *)ring0);
+    constexpr int kStep = S::kHalves / 8;
+    red[w * kStep + l] = sum[0];
+    red[w * kStep + 64 + l] = sum[1];
+    __syncthreads();
+    if (w > 0)
+        return;
+    // ranks k .. k + 3 of token 0 are lane 4 (k % 16)'s of block k / 16, the next
+    // four lane 4 (k % 16) + 16's
+    f32x4 u0 = {}, u1 = {};
+#pragma unroll
+    for (int s = 0; s < XW; ++s) {
+        u0 += red[s * kStep + 64 * (k >> 4) + 4 * (k & 15)];
+        u1 += red[s * kStep + 64 * (k >> 4) + 4 * (k & 15) + 16];
+    }
+    float y = 0.0f;
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+        const float v = act_to_f32<BF16>((uint16_t)(bv[d >> 1] >> (16 * (d & 1)))) * (d < 4 ? u0[d & 3] : u1[d & 3]);
+        y += k + d < rk ? v : 0.0f;
+    }
+    y += __shfl_xor(y, 1);
+    y += __shfl_xor(y, 2);
+    if ((l & 3) == 0)
+        delta[0][c] = y;
+}
+
 // A block owns 16 weight rows (GLU: 8 gate and the same 8 up columns, so that
 // a 2048-column block still makes 256 blocks) and all tokens.  NW wavefronts
 // stream the weights; LIN blocks have XW more, which work on the adapters
-// meanwhile.
-template <int MODE, bool BF16, int NI, int NW, int RING, int XW>
+// meanwhile.  FUSED: with one token's x A^T too (see kFusedRank).
+template <int MODE, bool BF16, int NI, int NW, int RING, int XW, bool FUSED = false>
 __global__ __launch_bounds__(64 * (NW + XW)) void dense_skinny_kernel(DenseArgs a)
 {
     using S = Stream<BF16, NI, 1, RING>;
-    __shared__ __align__(1024) uint16_t ring0[NW * S::kHalves], ring1[NW * S::kHalves], ring2[NW * S::kHalves],
-        ring3[RING == 4 ? NW * S::kHalves : 8];
+    __shared__ __align__(1024) uint16_t ring0[NW * S::kHalves], ring1[NW * S::kHalves],
+        ring2[RING >= 3 ? NW * S::kHalves : 8], ring3[RING == 4 ? NW * S::kHalves : 8];
     __shared__ __align__(16) float delta[MODE == DENSE_LIN ? 16 * NI : 1][16];
     static_assert(NI <= NW && NI * 1024 <= S::kHalves * 2, "sums fit the first ring array");
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -273,16 +332,19 @@ __global__ __launch_bounds__(64 * (NW + XW)) void dense_skinny_kernel(DenseArgs 
         for (int i = 0; i < NI; ++i)
             acc[i][0] = (f32x4){};
         const int at = w * S::kHalves;
-        st.run(w, NW, (LDS_AS uint16_t *)ring0 + at, (LDS_AS uint16_t *)ring1 + at, (LDS_AS uint16_t *)ring2 + at,
-               (LDS_AS uint16_t *)ring3 + (RING == 4 ? at : 0), acc);
+        st.run(w, NW, (LDS_AS uint16_t *)ring0 + at, (LDS_AS uint16_t *)ring1 + at,
+               (LDS_AS uint16_t *)ring2 + (RING >= 3 ? at : 0), (LDS_AS uint16_t *)ring3 + (RING == 4 ? at : 0), acc);
         // the sums of a wavefront in its own part of the first ring array, which
         // only it has used
 #pragma unroll
         for (int i = 0; i < NI; ++i)
             red[w * kStep + 64 * i + l] = acc[i][0];
-    } else {
-        if constexpr (XW > 0)
-            skinny_expand<BF16, NI, XW>(a, n0, w - NW, l, delta);
+        if constexpr (FUSED)
+            __syncthreads();
+    } else if constexpr (FUSED) {
+        fused_expand<BF16, XW>(a, n0, w - NW, l, delta);
+    } else if constexpr (XW > 0) {
+        skinny_expand<BF16, NI, XW>(a, n0, w - NW, l, delta);
     }
     __syncthreads();
     if (w >= NI)
@@ -312,7 +374,9 @@ hipError_t launch_skinny(const DenseArgs &a, hipStream_t s)
     constexpr int kCols = MODE == DENSE_GLU ? 8 : 16;
     constexpr bool kLin = MODE == DENSE_LIN;
     const unsigned grid = (unsigned)((a.N + kCols - 1) / kCols);
-    if (a.M <= 16)
+    if (kLin && a.lora.fused)
+        dense_skinny_kernel<DENSE_LIN, BF16, 1, 8, 2, 4, true><<<grid, 64 * 12, 0, s>>>(a);
+    else if (a.M <= 16)
         dense_skinny_kernel<MODE, BF16, 1, 8, 4, kLin ? 4 : 0><<<grid, 64 * (kLin ? 12 : 8), 0, s>>>(a);
     else if (a.M <= 32)
         dense_skinny_kernel<MODE, BF16, 2, 8, 3, kLin ? 8 : 0><<<grid, 64 * (kLin ? 16 : 8), 0, s>>>(a);
@@ -344,30 +408,59 @@ MOE_DEV void tile_expand(const DenseArgs &a, int mine, int rank, int m0, int n0,
     st.p = buf_rsrc(lo.mid, (uint32_t)((int64_t)a.M * lo.rpad * 2));
     st.init(l, 0, lo.rpad, lo.rank, [&](int r) { return (int64_t)(m0 + r); },
             [&](int r) { return (int64_t)(n0 + r); });
-    while (left) {
-        const int at = __ffsll((unsigned long long)left) - 1;
-        const int e = __builtin_amdgcn_readlane(mine, at), rk = __builtin_amdgcn_readlane(rank, at);
-        left &= ~__ballot(mine == e);
-        if (e % NW != w)
-            continue;
-        st.kend = rk;
-        st.q[0] = buf_rsrc(lo.b + (int64_t)e * a.N * lo.rank, (uint32_t)((int64_t)a.N * lo.rank * 2));
-        st.q[1] = st.q[0];
-        for (int k0 = 0; k0 < rk; k0 += 64) {
-            LDS_AS uint16_t *cur = (k0 & 64) ? r1 : r0;
-            st.load(k0 / 64, cur);
-            wait_vmcnt<0>();
-            u32x4 pf[2][4], qf[2][4];
-            S::fragments(cur, l, pf, qf);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                lora_cut(rk, k0 + 32 * h, l, qf[h]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    lora_products<BF16>(id[i] == e, pf[h][i], qf[h], acc[i]);
+    // (e, k0): this wavefront's shares of 64 ranks, one after the other; e < 0
+    // past the last
+    int e = -1, rk = 0, k0 = 0;
+    auto next = [&]() __attribute__((always_inline)) {
+        k0 += 64;
+        if (k0 < rk)
+            return;
+        k0 = 0;
+        rk = 0;
+        e = -1;
+        while (left && rk == 0) {
+            const int at = __ffsll((unsigned long long)left) - 1;
+            const int id0 = __builtin_amdgcn_readlane(mine, at);
+            left &= ~__ballot(mine == id0);
+            if (id0 % NW == w) {
+                e = id0;
+                rk = __builtin_amdgcn_readlane(rank, at);
             }
         }
+    };
+    auto load = [&](LDS_AS uint16_t *slot) __attribute__((always_inline)) {
+        st.kend = rk;   // 0 past the last: the loads read zeros
+        st.q[0] = buf_rsrc(lo.b + (int64_t)max(e, 0) * a.N * lo.rank, (uint32_t)((int64_t)a.N * lo.rank * 2));
+        st.q[1] = st.q[0];
+        st.load(k0 / 64, slot);
+    };
+    next();
+    load(r0);
+    // the share in `slot` while the one after it loads into `other`
+    auto step = [&](LDS_AS uint16_t *slot, LDS_AS uint16_t *other) __attribute__((always_inline)) {
+        const int ce = e, crk = rk, ck = k0;
+        next();
+        load(other);
+        __builtin_amdgcn_sched_barrier(0);
+        wait_vmcnt<S::kLoads>();
+        u32x4 pf[2][4], qf[2][4];
+        S::fragments(slot, l, pf, qf);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            lora_cut(crk, ck + 32 * h, l, qf[h]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                lora_products<BF16>(id[i] == ce, pf[h][i], qf[h], acc[i]);
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the slot is free
+    };
+    while (e >= 0) {
+        step(r0, r1);
+        if (e < 0)
+            break;
+        step(r1, r0);
     }
+    wait_vmcnt<0>();   // the loads past the end still write LDS
 }
 
 template <int MODE, bool BF16, int NW>

@@ -85,8 +85,8 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(const uint16_t *x,
 }
 
 // One token a block while all blocks together read at most this much of the
-// adapters (about 6 us from L2).
-constexpr int64_t kShrinkBytes = 64 << 20;
+// adapters (about 15 us from L2).
+constexpr int64_t kShrinkBytes = 192 << 20;
 
 template <bool BF16>
 static void shrink(const uint16_t *x, int64_t ldx, uint32_t xbytes, int T, int K, const LoraArgs &l, hipStream_t s)
