@@ -125,6 +125,7 @@ int64_t tiles_of(int mode, int64_t M, int64_t N, int64_t bm)
 // Tiles and k splits of a launch.
 struct Tiles {
     int64_t bm, mt, nt, splits, per;
+    double us;   // estimate
 };
 
 // The tile of a launch: the one whose rounds over the 256 CUs are estimated to
@@ -160,7 +161,7 @@ Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K)
         offer(kDenseLow, 1, rounds(tiles_of(mode, M, N, kDenseLow), 256) * (9.5 + 0.62 * s));
     offer(kDenseSmall, 1, rounds(t128, 256) * (4 + 0.24 * s));
     offer(kDenseTile, 1, t64 <= 256 ? 5 + 0.08 * s : rounds(t64, 512) * (5.4 + 0.17 * s));
-    const int64_t c = std::min(kSplitBlocks / t128, stages / kSplitStages);
+    const int64_t c = t128 > 0 ? std::min(kSplitBlocks / t128, stages / kSplitStages) : 0;
     if (c > 1)
         offer(kDenseSmall, c, 18 + 0.24 * (double)cdiv(stages, c));
     Tiles t{};
@@ -169,6 +170,21 @@ Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K)
     t.nt = cdiv(N, tile_cols(mode, bm));
     t.per = std::max<int64_t>(1, cdiv(stages, cuts));
     t.splits = std::max<int64_t>(1, cdiv(stages, t.per));
+    t.us = least;
+    return t;
+}
+
+// The same in 64 x 64 tiles whatever they cost; us: what its blocks take of the
+// GPU, one on each of the 256 CUs at a time.
+Tiles plan_small_tiles(int mode, int64_t M, int64_t N, int64_t K)
+{
+    Tiles t{};
+    t.bm = kDenseTile;
+    t.mt = (mode == DENSE_DW ? 2 : 1) * cdiv(M, t.bm);
+    t.nt = cdiv(N, tile_cols(mode, t.bm));
+    t.per = std::max<int64_t>(1, stages_of(mode, K));
+    t.splits = 1;
+    t.us = (double)(t.mt * t.nt) / 256 * (5 + 0.08 * (double)t.per);
     return t;
 }
 
@@ -388,38 +404,53 @@ int moe_exl3_glu_backward(const moe_exl3_glu_desc *desc, const void *x, int64_t 
     uint16_t *dg = at<uint16_t>(workspace, p.dg), *du = at<uint16_t>(workspace, p.du);
     if (T > 0 && launch_glu_grad(bf16, desc->act, pre, (const uint16_t *)dout, lddo, T, (int)I, dg, du, s) != hipSuccess)
         return MOE_EXL3_ERR_HIP;
-    DenseArgs a{};
-    a.p[0] = dg;
-    a.p[1] = du;
-    a.ldp = I;
-    a.pbytes = (uint32_t)(T * I * 2);
-    a.ldq = H;
-    if (dx && T > 0) {
-        a.q[0] = (const uint16_t *)w_gate;
-        a.q[1] = (const uint16_t *)w_up;
-        a.qbytes = (uint32_t)mg.span();
-        a.M = (int)T;
-        a.N = (int)H;
-        a.K = (int)I;
-        a.out[0] = (uint16_t *)dx;
-        a.ldo = lddx;
-        set_tiles(a, plan_tiles(DENSE_DX, T, H, I), at<float>(workspace, p.part));
-        if (launch_dense(DENSE_DX, bf16, a, s) != hipSuccess)
+    DenseArgs ax{}, aw{};
+    ax.p[0] = aw.p[0] = dg;
+    ax.p[1] = aw.p[1] = du;
+    ax.ldp = aw.ldp = I;
+    ax.pbytes = aw.pbytes = (uint32_t)(T * I * 2);
+    ax.q[0] = (const uint16_t *)w_gate;
+    ax.q[1] = (const uint16_t *)w_up;
+    ax.ldq = H;
+    ax.qbytes = (uint32_t)mg.span();
+    ax.M = (int)T;
+    ax.N = (int)H;
+    ax.K = (int)I;
+    ax.out[0] = (uint16_t *)dx;
+    ax.ldo = lddx;
+    aw.q[0] = (const uint16_t *)x;
+    aw.ldq = ldx;
+    aw.qbytes = (uint32_t)mx.span();
+    aw.M = (int)I;
+    aw.N = (int)H;
+    aw.K = (int)T;
+    aw.out[0] = (uint16_t *)dw_gate;
+    aw.out[1] = (uint16_t *)dw_up;
+    aw.ldo = H;
+    float *part = at<float>(workspace, p.part);
+    const bool want_dx = dx && T > 0, want_dw = dw_gate;
+    // Small gradients leave CUs idle on their own: their tiles share one launch
+    // (509 tokens, 776 x 1304: 17.7 and 8.5 us apart, 23 together).  The
+    // choice is the same where only one is wanted, and so are its bits.
+    Tiles tx = plan_tiles(DENSE_DX, T, H, I), tw = plan_tiles(DENSE_DW, I, H, T);
+    const Tiles sx = plan_small_tiles(DENSE_DX, T, H, I), sw = plan_small_tiles(DENSE_DW, I, H, T);
+    if (T > 0 && sx.us + sw.us < tx.us + tw.us) {
+        set_tiles(ax, sx, part);
+        set_tiles(aw, sw, part);
+        if (!want_dx)
+            ax.mt = 0;
+        if (!want_dw)
+            aw.mt = 0;
+        return launch_dense_grads(bf16, ax, aw, s) == hipSuccess ? MOE_EXL3_OK : MOE_EXL3_ERR_HIP;
+    }
+    if (want_dx) {
+        set_tiles(ax, tx, part);
+        if (launch_dense(DENSE_DX, bf16, ax, s) != hipSuccess)
             return MOE_EXL3_ERR_HIP;
     }
-    if (dw_gate) {
-        a.q[0] = (const uint16_t *)x;
-        a.q[1] = nullptr;
-        a.ldq = ldx;
-        a.qbytes = (uint32_t)mx.span();
-        a.M = (int)I;
-        a.N = (int)H;
-        a.K = (int)T;
-        a.out[0] = (uint16_t *)dw_gate;
-        a.out[1] = (uint16_t *)dw_up;
-        a.ldo = H;
-        set_tiles(a, plan_tiles(DENSE_DW, I, H, T), at<float>(workspace, p.part));
-        if (launch_dense(DENSE_DW, bf16, a, s) != hipSuccess)
+    if (want_dw) {
+        set_tiles(aw, tw, part);
+        if (launch_dense(DENSE_DW, bf16, aw, s) != hipSuccess)
             return MOE_EXL3_ERR_HIP;
     }
     return MOE_EXL3_OK;

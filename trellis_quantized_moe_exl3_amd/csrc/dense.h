@@ -73,6 +73,8 @@ struct DenseArgs {
 };
 
 hipError_t launch_dense(int mode, bool bf16, const DenseArgs &a, hipStream_t s);
+// DX and DW, both in 64 x 64 tiles, in one launch.
+hipError_t launch_dense_grads(bool bf16, const DenseArgs &dx, const DenseArgs &dw, hipStream_t s);
 // GLU or LIN of at most kSkinnyTokens tokens.
 hipError_t launch_dense_skinny(int mode, bool bf16, const DenseArgs &a, hipStream_t s);
 hipError_t launch_glu_grad(bool bf16, int act, const float *pre, const uint16_t *dh, int64_t lddh, int64_t T, int I,

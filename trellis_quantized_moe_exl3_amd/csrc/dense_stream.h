@@ -463,16 +463,19 @@ MOE_DEV void tile_expand(const DenseArgs &a, int mine, int rank, int m0, int n0,
     wait_vmcnt<0>();   // the loads past the end still write LDS
 }
 
+// Tile `block` of a launch of NW wavefronts a block; ring0, ring1: its LDS.
+constexpr int kTileHalves = 16 * 8 * 64;   // of one share of both operands
+
 template <int MODE, bool BF16, int NW>
-__global__ __launch_bounds__(64 * NW) void dense_tile_kernel(DenseArgs a)
+MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *ring0, LDS_AS uint16_t *ring1)
 {
     using TR = DenseTraits<MODE>;
     using S = Stream<BF16, 4, 4, 2, TR::kPL, TR::kQL>;
-    __shared__ __align__(1024) uint16_t ring0[NW * S::kHalves], ring1[NW * S::kHalves];
+    static_assert(S::kHalves == kTileHalves, "ring size");
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     constexpr int kCols = MODE == DENSE_GLU ? 32 : 64;
     int m, n;
-    dense_tile(blockIdx.x, a.mt * a.nt, a.mt, a.nt, m, n);
+    dense_tile(block, a.mt * a.nt, a.mt, a.nt, m, n);
     const int half = MODE == DENSE_DW ? a.mt / 2 : a.mt;
     const int z = m >= half ? 1 : 0;
     const int m0 = (m - z * half) * 64, n0 = n * kCols;
@@ -488,7 +491,7 @@ __global__ __launch_bounds__(64 * NW) void dense_tile_kernel(DenseArgs a)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             acc[i][j] = (f32x4){};
-    LDS_AS uint16_t *r0 = (LDS_AS uint16_t *)ring0 + w * S::kHalves, *r1 = (LDS_AS uint16_t *)ring1 + w * S::kHalves;
+    LDS_AS uint16_t *r0 = ring0 + w * S::kHalves, *r1 = ring1 + w * S::kHalves;
     int mine = -1, rank = 0;
     if constexpr (MODE == DENSE_LIN)
         token_adapter(a.lora, m0 + l, a.M, mine, rank);
@@ -501,7 +504,7 @@ __global__ __launch_bounds__(64 * NW) void dense_tile_kernel(DenseArgs a)
     if constexpr (MODE == DENSE_LIN)
         tile_expand<BF16, NW, S>(a, mine, rank, m0, n0, w, l, r0, r1, acc);
     // every wavefront's sums in its own part of the first ring array
-    LDS_AS f32x4 *red = (LDS_AS f32x4 *)((LDS_AS uint16_t *)ring0);
+    LDS_AS f32x4 *red = (LDS_AS f32x4 *)ring0;
     constexpr int kStep = S::kHalves / 8;
     static_assert(kStep >= 16 * 64, "sums fit the first ring array");
 #pragma unroll
@@ -519,13 +522,35 @@ __global__ __launch_bounds__(64 * NW) void dense_tile_kernel(DenseArgs a)
             for (int s = 1; s < NW; ++s)
                 v[0][j] += red[s * kStep + (4 * i + j) * 64 + l];
         }
-        dense_store_all<MODE, BF16>(a, z, m0 + 16 * i, n0, l, v, (LDS_AS f32x4 *)(LDS_AS uint16_t *)ring1 + 256 * w);
+        dense_store_all<MODE, BF16>(a, z, m0 + 16 * i, n0, l, v, (LDS_AS f32x4 *)ring1 + 256 * w);
     }
+}
+
+template <int MODE, bool BF16, int NW>
+__global__ __launch_bounds__(64 * NW) void dense_tile_kernel(DenseArgs a)
+{
+    __shared__ __align__(1024) uint16_t ring0[NW * kTileHalves], ring1[NW * kTileHalves];
+    tile_block<MODE, BF16, NW>(a, blockIdx.x, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1);
+}
+
+// Both gradients in one launch: the tiles of dx first (a longer k each), then
+// those of dw.
+template <bool BF16>
+__global__ __launch_bounds__(256) void dense_grads_kernel(DenseArgs dx, DenseArgs dw)
+{
+    __shared__ __align__(1024) uint16_t ring0[4 * kTileHalves], ring1[4 * kTileHalves];
+    const int block = blockIdx.x, first = dx.mt * dx.nt;
+    if (block < first)
+        tile_block<DENSE_DX, BF16, 4>(dx, block, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1);
+    else
+        tile_block<DENSE_DW, BF16, 4>(dw, block - first, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1);
 }
 
 template <int MODE, bool BF16>
 hipError_t launch_tile(const DenseArgs &a, hipStream_t s)
 {
+    // four wavefronts and 128 KiB of LDS while that is one block a CU, two
+    // blocks of two wavefronts beyond
     const unsigned grid = (unsigned)(a.mt * a.nt);
     if (grid <= 256)
         dense_tile_kernel<MODE, BF16, 4><<<grid, 256, 0, s>>>(a);
