@@ -109,11 +109,7 @@ int check_desc(const moe_exl3_lora_desc *d)
 bool rows_fit(int64_t T, int64_t cols) { return T < kSpanLimit && T * cols * 2 < kSpanLimit; }
 
 // Columns of a tile of `bm` rows.
-int64_t tile_cols(int mode, int64_t bm)
-{
-    const int64_t bn = bm == kDenseLow ? kDenseLarge : bm;
-    return mode == DENSE_GLU ? bn / 2 : bn;
-}
+int64_t tile_cols(int mode, int64_t bm) { return mode == DENSE_GLU ? bm / 2 : bm; }
 
 int64_t stages_of(int mode, int64_t K) { return (mode == DENSE_DX ? 2 : 1) * cdiv(K, kDenseBK); }
 
@@ -135,7 +131,6 @@ struct Tiles {
 //   64 x 64     5 + 0.08 a stage up to 256 tiles, else 5.4 + 0.17 a round of 512
 //               (333 tokens, 4096 x 2048: 25 us; 128 x 128 takes 29)
 //   128 x 128   4 + 0.24 (1024 tokens: 35; 64 x 64 takes 50, 256 x 256 71)
-//   224 x 256   9.5 + 0.62 (7168 tokens: 178; 256 x 256 takes 184, 128 x 128 224)
 //   256 x 256   10 + 0.70 (4096 tokens: 100; 128 x 128 takes 128)
 // Few tiles with a long k are cut along k, at the price of partial tiles and a
 // second launch: 18 + 0.24 a stage (96 tokens of the gradient for x, hidden 1024,
@@ -157,8 +152,6 @@ Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K)
     auto rounds = [&](int64_t tiles, int64_t at_once) { return (double)cdiv(tiles, at_once); };
     const int64_t t64 = tiles_of(mode, M, N, kDenseTile), t128 = tiles_of(mode, M, N, kDenseSmall);
     offer(kDenseLarge, 1, rounds(tiles_of(mode, M, N, kDenseLarge), 256) * (10 + 0.70 * s));
-    if (mode != DENSE_DW)
-        offer(kDenseLow, 1, rounds(tiles_of(mode, M, N, kDenseLow), 256) * (9.5 + 0.62 * s));
     offer(kDenseSmall, 1, rounds(t128, 256) * (4 + 0.24 * s));
     offer(kDenseTile, 1, t64 <= 256 ? 5 + 0.08 * s : rounds(t64, 512) * (5.4 + 0.17 * s));
     const int64_t c = t128 > 0 ? std::min(kSplitBlocks / t128, stages / kSplitStages) : 0;

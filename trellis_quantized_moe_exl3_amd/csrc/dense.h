@@ -15,7 +15,6 @@ namespace moe {
 constexpr int kDenseTile = 64;   // wavefronts cut k (dense_stream.h)
 constexpr int kDenseSmall = 128;
 constexpr int kDenseLarge = 256;
-constexpr int kDenseLow = 224;   // rows of a large tile where they fill the rounds better
 constexpr int kDenseBK = 32;
 // Tokens up to which the forward operators take the few-token kernel.
 constexpr int64_t kSkinnyTokens = 64;
@@ -63,7 +62,7 @@ struct DenseArgs {
     int64_t ldo;
     float *pre;              // GLU: fp32 [2][T][I] or NULL
     int act;
-    int bm;                  // tile: kDenseTile, kDenseSmall, kDenseLow or kDenseLarge
+    int bm;                  // tile: kDenseTile, kDenseSmall or kDenseLarge
     int mt, nt;              // tiles (DW: mt counts both tensors')
     int splits, per;         // k splits and stages of each
     float *part;             // splits > 1: partial tiles, fragment order

@@ -48,14 +48,12 @@ struct DenseTraits {
 template <int BM_, int BN_, int WM_, int WN_>
 struct DenseShape {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NW = WM * WN;
-    static constexpr int RM = (BM + 127) / 128 * 128;   // rows of P in LDS (whole loads)
     static constexpr int TM = BM / WM, TN = BN / WN, NI = TM / 16, NJ = TN / 16;
     static_assert(TN == 64 && NW % 4 == 0, "GLU column interleave");
-    static_assert(RM % 64 == 0 && 64 * NW >= RM, "a thread for each row");
+    static_assert(BM % 64 == 0 && 64 * NW >= BM, "a thread for each row");
 };
 using SmallTile = DenseShape<kDenseSmall, kDenseSmall, 2, 2>;
 using LargeTile = DenseShape<kDenseLarge, kDenseLarge, 2, 4>;
-using LowTile = DenseShape<kDenseLow, kDenseLarge, 2, 4>;
 
 // Result columns n0 + .. of a tile: GLU tiles hold BN / 2 columns of both
 // projections, interleaved by 32 (tile rows 64 s + 0..31 of Q are gate columns
@@ -204,7 +202,7 @@ struct DenseTile {
     static constexpr int NI = S::NI, NJ = S::NJ;
     using Frags = DenseFrags<S>;
     using TR = DenseTraits<MODE>;
-    using OP = Operand<S::RM, TR::kPL, S::NW>;
+    using OP = Operand<S::BM, TR::kPL, S::NW>;
     using OQ = Operand<S::BN, TR::kQL, S::NW>;
     static constexpr int kLoads = OP::kLoads + OQ::kLoads;
     OP po;
@@ -220,7 +218,7 @@ struct DenseTile {
         const int k0 = kDenseBK * (second ? s - nsk : s);
         const int end = s < send ? kend : 0;
         po.issue(second ? pr[1] : pr[0], ring, w, k0, end, pstep);
-        qo.issue(second ? qr[1] : qr[0], ring + S::RM * kDenseBK, w, k0, end, qstep);
+        qo.issue(second ? qr[1] : qr[0], ring + S::BM * kDenseBK, w, k0, end, qstep);
     }
     MOE_DEV void read(const LDS_AS uint16_t *ring, Frags &f)
     {
@@ -229,7 +227,7 @@ struct DenseTile {
             f.p[i] = OP::frag(ring, pbase, i);
 #pragma unroll
         for (int j = 0; j < S::NJ; ++j)
-            f.q[j] = OQ::frag(ring + S::RM * kDenseBK, qbase, j);
+            f.q[j] = OQ::frag(ring + S::BM * kDenseBK, qbase, j);
     }
     // Stage s in ring slot `cur`, whose fragments `f` were read during stage
     // s - 1.  "At most 2 loads' worth outstanding" (stages s + 2 and s + 3)
@@ -338,10 +336,10 @@ struct AdapterJobs {
     uint32_t job[BM * (kMaxRank / 32)]; // adapter | stage << 16 | its rank << 20
 
     // The tokens' ids, by all threads.
-    MOE_DEV void ids_of(const LoraArgs &lo, int m0, int rows, int T, int tid)
+    MOE_DEV void ids_of(const LoraArgs &lo, int m0, int T, int tid)
     {
         if (tid < BM) {
-            const int t = m0 + tid, e = tid < rows && t < T ? lo.ids[t] : -1;
+            const int t = m0 + tid, e = t < T ? lo.ids[t] : -1;
             id[tid] = e >= 0 && e < lo.n ? e : -1;
         }
     }
@@ -385,11 +383,11 @@ struct AdapterJobs {
 // tile names, P = the tokens' s_a x A_a^T, Q = B_a's rows, through the same
 // ring.
 template <bool BF16, class S>
-MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const AdapterJobs<S::RM> &jobs,
+MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const AdapterJobs<S::BM> &jobs,
                          LDS_AS uint16_t *r0, LDS_AS uint16_t *r1, LDS_AS uint16_t *r2, LDS_AS uint16_t *r3,
                          f32x4 (&acc)[S::NI][S::NJ])
 {
-    using OP = Operand<S::RM, KC, S::NW>;
+    using OP = Operand<S::BM, KC, S::NW>;
     using OQ = Operand<S::BN, KC, S::NW>;
     constexpr int kLoads = OP::kLoads + OQ::kLoads;
     const LoraArgs &lo = a.lora;
@@ -401,7 +399,7 @@ MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const Adap
         return;
     OP po;
     OQ qo;
-    po.init_kc(w, l, lo.rpad, [&](int r) { return (int64_t)(r < S::BM ? m0 + r : a.M); });
+    po.init_kc(w, l, lo.rpad, [&](int r) { return (int64_t)(m0 + r); });
     qo.init_kc(w, l, lo.rank, [&](int r) { return (int64_t)(n0 + r); });
     const __amdgpu_buffer_rsrc_t pr = buf_rsrc(lo.mid, (uint32_t)((int64_t)a.M * lo.rpad * 2));
     const uint32_t bbytes = (uint32_t)((int64_t)a.N * lo.rank * 2);
@@ -415,7 +413,7 @@ MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const Adap
         const uint32_t job = job_of(t);
         const int e = job & 0xFFFF, k0 = 32 * ((job >> 16) & 15), rk = t < count ? (int)(job >> 20) : 0;
         po.issue(pr, ring, w, k0, rk, 2);
-        qo.issue(buf_rsrc(lo.b + (int64_t)e * a.N * lo.rank, bbytes), ring + S::RM * kDenseBK, w, k0, rk, 2);
+        qo.issue(buf_rsrc(lo.b + (int64_t)e * a.N * lo.rank, bbytes), ring + S::BM * kDenseBK, w, k0, rk, 2);
     };
     auto stage = [&](int t, const LDS_AS uint16_t *cur, LDS_AS uint16_t *refill) __attribute__((always_inline)) {
         __builtin_amdgcn_sched_barrier(0);
@@ -428,15 +426,13 @@ MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const Adap
         u32x4 q[S::NJ];
 #pragma unroll
         for (int j = 0; j < S::NJ; ++j)
-            q[j] = OQ::frag(cur + S::RM * kDenseBK, qbase, j);
+            q[j] = OQ::frag(cur + S::BM * kDenseBK, qbase, j);
         lora_cut(job >> 20, 32 * ((job >> 16) & 15), l, q);
 #pragma unroll
         for (int i = 0; i < S::NI; i += 2) {
-            constexpr int kLast = S::NI - 1;
-            const u32x4 p0 = OP::frag(cur, pbase, i), p1 = OP::frag(cur, pbase, min(i + 1, kLast));
+            const u32x4 p0 = OP::frag(cur, pbase, i), p1 = OP::frag(cur, pbase, i + 1);
             lora_products<BF16>(ids[16 * i] == e, p0, q, acc[i]);
-            if (i < kLast)
-                lora_products<BF16>(ids[16 * i + 16] == e, p1, q, acc[min(i + 1, kLast)]);
+            lora_products<BF16>(ids[16 * i + 16] == e, p1, q, acc[i + 1]);
             __builtin_amdgcn_sched_barrier(0);   // fragments of two blocks at a time: registers
         }
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): reads done before the next barrier
@@ -460,7 +456,7 @@ template <int MODE, bool BF16, class S>
 __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
 {
     using T = DenseTile<MODE, BF16, S>;
-    constexpr int kHalves = (S::RM + S::BN) * kDenseBK;
+    constexpr int kHalves = (S::BM + S::BN) * kDenseBK;
     __shared__ __align__(1024) uint16_t ring0[kHalves], ring1[kHalves], ring2[kHalves], ring3[kHalves];
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = w / S::WN, wn = w % S::WN;
@@ -492,8 +488,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
         t.qr[1] = MODE == DENSE_DX ? buf_rsrc(a.q[1], a.qbytes) : t.qr[0];
     }
     if constexpr (T::TR::kPL == KC) {
-        // rows past the tile's own read zeros
-        t.po.init_kc(w, l, a.ldp, [&](int r) { return (int64_t)(r < S::BM ? m0 + r : a.M); });
+        t.po.init_kc(w, l, a.ldp, [&](int r) { return (int64_t)(m0 + r); });
         t.pstep = 2;
     } else {
         t.po.init_ks(w, l, a.ldp, m0);
@@ -519,11 +514,11 @@ __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
             acc[i][j] = (f32x4){};
     if constexpr (MODE == DENSE_LIN) {
         // the adapters' share goes with the first k split
-        __shared__ AdapterJobs<S::RM> jobs;
+        __shared__ AdapterJobs<S::BM> jobs;
         t.run(s0, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1, (LDS_AS uint16_t *)ring2,
               (LDS_AS uint16_t *)ring3, acc, [&]() __attribute__((always_inline)) {
                   if (split == 0) {
-                      jobs.ids_of(a.lora, m0, S::BM, a.M, tid);
+                      jobs.ids_of(a.lora, m0, a.M, tid);
                       __syncthreads();
                       if (w == 0)
                           jobs.build(a.lora, l);
@@ -594,9 +589,6 @@ hipError_t launch_dense_shape(const DenseArgs &a, hipStream_t s)
 template <int MODE>
 hipError_t launch_dense_mode(bool bf16, const DenseArgs &a, hipStream_t s)
 {
-    if constexpr (DenseTraits<MODE>::kPL == KC)
-        if (a.bm == kDenseLow)
-            return bf16 ? launch_dense_shape<MODE, true, LowTile>(a, s) : launch_dense_shape<MODE, false, LowTile>(a, s);
     if (a.bm == kDenseLarge)
         return bf16 ? launch_dense_shape<MODE, true, LargeTile>(a, s) : launch_dense_shape<MODE, false, LargeTile>(a, s);
     return bf16 ? launch_dense_shape<MODE, true, SmallTile>(a, s) : launch_dense_shape<MODE, false, SmallTile>(a, s);
