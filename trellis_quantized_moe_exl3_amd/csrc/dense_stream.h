@@ -195,6 +195,11 @@ MOE_DEV void lora_rows(const LoraArgs &lo, int id, int rank, int r0, int l, int 
 
 // ---- the block and the projection for few tokens
 
+// Result columns of a block with 16 NJ weight rows.
+template <int MODE>
+constexpr int skinny_cols(int nj) { return MODE == DENSE_GLU ? 8 * nj : 16 * nj; }
+
+
 // delta[t][16 columns]: the adapters' rows of tokens t = w, w + XW, .. , kBatch
 // at a time with all their loads in flight: lane l takes column l / 4 and the k
 // octets l % 4 + 0, 4, .. of the token's adapter (four lanes to 64 bytes of a
@@ -303,20 +308,26 @@ MOE_DEV void fused_expand(const DenseArgs &a, int n0, int w, int l, float (*delt
         delta[0][c] = y;
 }
 
-// A block owns 16 weight rows (GLU: 8 gate and the same 8 up columns, so that
-// a 2048-column block still makes 256 blocks) and all tokens.  NW wavefronts
-// stream the weights; LIN blocks have XW more, which work on the adapters
-// meanwhile.  FUSED: with one token's x A^T too (see kFusedRank).
-template <int MODE, bool BF16, int NI, int NW, int RING, int XW, bool FUSED = false>
+// A block owns 16 NJ weight rows (GLU: half of them gate, half the up rows of
+// the same columns) and all tokens.  NW wavefronts stream the weights; LIN
+// blocks have XW more, which work on the adapters meanwhile.  FUSED: with one
+// token's x A^T too (see kFusedRank).
+//
+// Every block reads all tokens' rows from L2: with 64 tokens, 16 weight rows a
+// block move five times the weights' bytes (4096 x 2048: 13.2 us), 32 three times
+// (12.4; inter 4096: 26 -> 16.7), where that leaves a block for every other CU.
+// A LIN block's adapters are the longer part, and stay with 16 rows (64 tokens,
+// 32 adapters of up to 64: 18.0 us, 20.0 with 32).
+template <int MODE, bool BF16, int NI, int NJ, int NW, int RING, int XW, bool FUSED = false>
 __global__ __launch_bounds__(64 * (NW + XW)) void dense_skinny_kernel(DenseArgs a)
 {
-    using S = Stream<BF16, NI, 1, RING>;
+    using S = Stream<BF16, NI, NJ, RING>;
     __shared__ __align__(1024) uint16_t ring0[NW * S::kHalves], ring1[NW * S::kHalves],
         ring2[RING >= 3 ? NW * S::kHalves : 8], ring3[RING == 4 ? NW * S::kHalves : 8];
     __shared__ __align__(16) float delta[MODE == DENSE_LIN ? 16 * NI : 1][16];
-    static_assert(NI <= NW && NI * 1024 <= S::kHalves * 2, "sums fit the first ring array");
+    static_assert(NI <= NW && NI * NJ * 1024 <= S::kHalves * 2, "sums fit the first ring array");
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    constexpr int kCols = MODE == DENSE_GLU ? 8 : 16;
+    constexpr int kCols = skinny_cols<MODE>(NJ);
     const int n0 = blockIdx.x * kCols;
     LDS_AS f32x4 *red = (LDS_AS f32x4 *)((LDS_AS uint16_t *)ring0);
     constexpr int kStep = S::kHalves / 8;   // f32x4 between the wavefronts' parts
@@ -326,11 +337,13 @@ __global__ __launch_bounds__(64 * (NW + XW)) void dense_skinny_kernel(DenseArgs 
         st.q[0] = buf_rsrc(a.q[0], a.qbytes);
         st.q[1] = MODE == DENSE_GLU ? buf_rsrc(a.q[1], a.qbytes) : st.q[0];
         st.init(l, a.K, a.ldp, a.ldq, [](int r) { return (int64_t)r; },
-                [&](int r) { return (int64_t)(n0 + (MODE == DENSE_GLU ? r & 7 : r)); });
-        f32x4 acc[NI][1];
+                [&](int r) { return (int64_t)(n0 + (MODE == DENSE_GLU ? r & (kCols - 1) : r)); });
+        f32x4 acc[NI][NJ];
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-            acc[i][0] = (f32x4){};
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                acc[i][j] = (f32x4){};
         const int at = w * S::kHalves;
         st.run(w, NW, (LDS_AS uint16_t *)ring0 + at, (LDS_AS uint16_t *)ring1 + at,
                (LDS_AS uint16_t *)ring2 + (RING >= 3 ? at : 0), (LDS_AS uint16_t *)ring3 + (RING == 4 ? at : 0), acc);
@@ -338,7 +351,9 @@ __global__ __launch_bounds__(64 * (NW + XW)) void dense_skinny_kernel(DenseArgs 
         // only it has used
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-            red[w * kStep + 64 * i + l] = acc[i][0];
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                red[w * kStep + 64 * (NJ * i + j) + l] = acc[i][j];
         if constexpr (FUSED)
             __syncthreads();
     } else if constexpr (FUSED) {
@@ -347,41 +362,46 @@ __global__ __launch_bounds__(64 * (NW + XW)) void dense_skinny_kernel(DenseArgs 
         skinny_expand<BF16, NI, XW>(a, n0, w - NW, l, delta);
     }
     __syncthreads();
-    if (w >= NI)
+    const int m = 16 * w + (l & 15), c = 4 * (l >> 4);
+    if (w >= NI || m >= a.M)
         return;
-    const int m = 16 * w + (l & 15);
-    auto total = [&](int lane) {
-        f32x4 v = red[64 * w + lane];
+    auto total = [&](int j, int lane) {
+        f32x4 v = red[64 * (NJ * w + j) + lane];
 #pragma unroll
         for (int s = 1; s < NW; ++s)
-            v += red[s * kStep + 64 * w + lane];
+            v += red[s * kStep + 64 * (NJ * w + j) + lane];
         return v;
     };
-    if constexpr (MODE == DENSE_GLU) {
+    if constexpr (MODE == DENSE_GLU && NJ == 1) {
         // lanes 0..31 hold gate columns 4 (l / 16) + 0..3, lanes 32..63 the same
         // columns of up
-        if (l < 32 && m < a.M)
-            glu_store<BF16>(a, m, n0 + 4 * (l >> 4), total(l), total(l + 32));
-    } else if (m < a.M && n0 + 4 * (l >> 4) < a.N) {
-        const f32x4 d = *(const f32x4 *)&delta[m][4 * (l >> 4)];
-        lin_store<BF16>(a, m, n0 + 4 * (l >> 4), total(l) + d);
+        if (l < 32)
+            glu_store<BF16>(a, m, n0 + c, total(0, l), total(0, l + 32));
+    } else if constexpr (MODE == DENSE_GLU) {
+        if (n0 + c < a.N)
+            glu_store<BF16>(a, m, n0 + c, total(0, l), total(1, l));
+    } else {
+        static_assert(NJ == 1, "delta holds 16 columns");
+        if (n0 + c < a.N)
+            lin_store<BF16>(a, m, n0 + c, total(0, l) + *(const f32x4 *)&delta[m][c]);
     }
 }
 
 template <int MODE, bool BF16>
 hipError_t launch_skinny(const DenseArgs &a, hipStream_t s)
 {
-    constexpr int kCols = MODE == DENSE_GLU ? 8 : 16;
     constexpr bool kLin = MODE == DENSE_LIN;
-    const unsigned grid = (unsigned)((a.N + kCols - 1) / kCols);
+    const unsigned narrow = (unsigned)((a.N + skinny_cols<MODE>(1) - 1) / skinny_cols<MODE>(1));   // blocks
     if (kLin && a.lora.fused)
-        dense_skinny_kernel<DENSE_LIN, BF16, 1, 8, 2, 4, true><<<grid, 64 * 12, 0, s>>>(a);
+        dense_skinny_kernel<DENSE_LIN, BF16, 1, 1, 8, 2, 4, true><<<narrow, 64 * 12, 0, s>>>(a);
     else if (a.M <= 16)
-        dense_skinny_kernel<MODE, BF16, 1, 8, 4, kLin ? 4 : 0><<<grid, 64 * (kLin ? 12 : 8), 0, s>>>(a);
+        dense_skinny_kernel<MODE, BF16, 1, 1, 8, 4, kLin ? 4 : 0><<<narrow, 64 * (kLin ? 12 : 8), 0, s>>>(a);
     else if (a.M <= 32)
-        dense_skinny_kernel<MODE, BF16, 2, 8, 3, kLin ? 8 : 0><<<grid, 64 * (kLin ? 16 : 8), 0, s>>>(a);
+        dense_skinny_kernel<MODE, BF16, 2, 1, 8, 3, kLin ? 8 : 0><<<narrow, 64 * (kLin ? 16 : 8), 0, s>>>(a);
+    else if (kLin || narrow < 256)
+        dense_skinny_kernel<MODE, BF16, 4, 1, 4, 3, kLin ? 8 : 0><<<narrow, 64 * (kLin ? 12 : 4), 0, s>>>(a);
     else
-        dense_skinny_kernel<MODE, BF16, 4, 4, 3, kLin ? 8 : 0><<<grid, 64 * (kLin ? 12 : 4), 0, s>>>(a);
+        dense_skinny_kernel<DENSE_GLU, BF16, 4, 2, 4, 3, 0><<<(narrow + 1) / 2, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
