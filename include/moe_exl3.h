@@ -395,10 +395,12 @@ int moe_exl3_glu(const moe_exl3_glu_desc *desc, const void *x, int64_t ldx, cons
  *   dg = dout * up * act'(gate), du = dout * act(gate)
  *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
  * dx: device [T][H] or NULL; dw_gate, dw_up: device [I][H], both or neither
- * NULL.  Outputs are written, not added to.  dg and du are rounded to the
- * 16-bit type before the products, every output once more.  With T = 0 the
- * weights' gradients are set to zero and x, pre and dout are not read (NULL
- * is allowed).
+ * NULL; the weights are read for dx alone (NULL without it).  Outputs are
+ * written, not added to.  dg and du are rounded to the 16-bit type before the
+ * products, every output once more: in F16 values of magnitude 65520 or more
+ * become infinite there, and those below 2^-24 vanish (scale the loss).  With
+ * T = 0 the weights' gradients are set to zero and x, pre and dout are not
+ * read (NULL is allowed).
  */
 int moe_exl3_glu_backward(const moe_exl3_glu_desc *desc, const void *x, int64_t ldx, const void *w_gate,
                           const void *w_up, const float *pre, const void *dout, int64_t lddo, int64_t T, void *dx,

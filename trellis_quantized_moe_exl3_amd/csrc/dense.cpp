@@ -367,7 +367,8 @@ int moe_exl3_glu_backward(const moe_exl3_glu_desc *desc, const void *x, int64_t 
     if (T < 0 || !dw_gate != !dw_up || (!dx && !dw_gate))
         return MOE_EXL3_ERR_INVALID_ARG;
     const int64_t H = desc->hidden, I = desc->inter;
-    const Mat mx{x, T, H, ldx}, mg{w_gate, I, H, H}, mu{w_up, I, H, H}, mo{dout, T, I, lddo};
+    const int64_t wrows = dx ? I : 0;   // the weights are read for dx alone
+    const Mat mx{x, T, H, ldx}, mg{w_gate, wrows, H, H}, mu{w_up, wrows, H, H}, mo{dout, T, I, lddo};
     const Mat mdx{dx, dx ? T : 0, H, lddx}, mdg{dw_gate, dw_gate ? I : 0, H, H}, mdu{dw_up, dw_up ? I : 0, H, H};
     for (const Mat &m : {mx, mg, mu, mo, mdx, mdg, mdu})
         if ((rc = check_mat(m)))
@@ -475,7 +476,8 @@ int moe_exl3_lora_linear(const moe_exl3_lora_desc *desc, const void *x, int64_t 
             return MOE_EXL3_ERR_MISALIGNED;
     if (overlap(my, mx) || overlap(my, mw) || (overlap(my, mb) && !(base == y && ldbase == ldy)) ||
         spans_meet(y, my.span(), adapters->a, 2 * n * r * K) || spans_meet(y, my.span(), adapters->b, 2 * n * r * N) ||
-        spans_meet(y, my.span(), ids, 4 * T))
+        spans_meet(y, my.span(), ids, 4 * T) || spans_meet(y, my.span(), adapters->scales, adapters->scales ? 4 * n : 0) ||
+        spans_meet(y, my.span(), adapters->ranks, adapters->ranks ? 4 * n : 0))
         return MOE_EXL3_ERR_INVALID_ARG;
     const LoraPlan p = plan_lora(*desc, T);
     if ((rc = check_ws(workspace, ws_bytes, p.total)))

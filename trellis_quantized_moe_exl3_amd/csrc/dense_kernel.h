@@ -123,6 +123,19 @@ MOE_DEV void dense_store(const DenseArgs &a, int z, int m0, int n0, int l, const
     uint16_t *out = a.out[MODE == DENSE_DW ? z : 0] + (int64_t)m0 * a.ldo + n0;
     const int left = a.M - m0, ldo = (int)a.ldo;
     if constexpr (MODE == DENSE_GLU) {
+        if (a.pre) {
+            // eight lanes to the 128 bytes of a row of 32 columns
+            float *pg = a.pre + (int64_t)m0 * a.N + n0, *pu = pg + (int64_t)a.M * a.N;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = 8 * h + (l >> 3), c = l & 7;
+                const f32x4 g = at(row, c), u = at(row, 8 + c);
+                if (row < left && n0 + 4 * c < a.N) {
+                    *(f32x4 *)(pg + (uint32_t)(row * a.N + 4 * c)) = g;
+                    *(f32x4 *)(pu + (uint32_t)(row * a.N + 4 * c)) = u;
+                }
+            }
+        }
         const int row = l >> 2, c = 2 * (l & 3);
         const f32x4 g[2] = {at(row, c), at(row, c + 1)}, u[2] = {at(row, 8 + c), at(row, 9 + c)};
         if (row >= left || n0 + 4 * c >= a.N)
@@ -134,14 +147,6 @@ MOE_DEV void dense_store(const DenseArgs &a, int z, int m0, int n0, int l, const
             for (int d = 0; d < 4; ++d)
                 h[q][d] = act_value<ACT>(g[q][d]) * u[q][d];
         *(u32x4 *)(out + (uint32_t)(row * ldo + 4 * c)) = pack8<BF16>(h[0], h[1]);
-        if (a.pre) {
-            float *pg = a.pre + (int64_t)m0 * a.N + n0, *pu = pg + (int64_t)a.M * a.N;
-            const uint32_t o = (uint32_t)(row * a.N + 4 * c);
-            *(f32x4 *)(pg + o) = g[0];
-            *(f32x4 *)(pg + o + 4) = g[1];
-            *(f32x4 *)(pu + o) = u[0];
-            *(f32x4 *)(pu + o + 4) = u[1];
-        }
     } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

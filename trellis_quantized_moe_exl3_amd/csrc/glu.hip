@@ -17,7 +17,10 @@ __global__ __launch_bounds__(256) void glu_grad_kernel(int act, const float *pre
         return;
     const int64_t t = i / I, c = i - t * I;
     const f32x4 *gp = (const f32x4 *)(pre + i), *up = (const f32x4 *)(pre + T * I + i);
-    const f32x4 g[2] = {gp[0], gp[1]}, u[2] = {up[0], up[1]};
+    // pre is read once: past the caches, which keep dg and du for the products
+    // (16384 x 2048: 92 -> 79 us)
+    const f32x4 g[2] = {__builtin_nontemporal_load(gp), __builtin_nontemporal_load(gp + 1)};
+    const f32x4 u[2] = {__builtin_nontemporal_load(up), __builtin_nontemporal_load(up + 1)};
     const u32x4 d = *(const u32x4 *)(dh + t * lddh + c);
     u32x4 og, ou;
 #pragma unroll
