@@ -16,7 +16,11 @@ ACTS = [M.ACT_SILU, M.ACT_GELU_TANH]
 SHAPES = [(1, 256, 128), (1, 8, 8), (2, 264, 40), (7, 520, 136), (8, 4096, 2048), (15, 40, 72), (16, 1032, 200),
           (17, 256, 264), (31, 72, 1000), (33, 1032, 1384), (63, 512, 64), (64, 2048, 512), (65, 136, 128),
           (127, 776, 1304), (128, 512, 256), (129, 24, 520), (257, 1000, 328), (300, 4096, 136), (515, 640, 1032),
-          (1100, 264, 2056)]
+          (1100, 264, 2056),
+          # 32 weight rows a block, the 64-row tiles of two wavefronts, k cut over
+          # blocks (forward, dx, dw), the 256-row tiles (forward, dx, dw)
+          (40, 136, 2056), (64, 264, 2048), (333, 1032, 1384), (70, 16384, 128), (70, 128, 8192), (20000, 128, 64),
+          (4000, 264, 2040), (3990, 4088, 264), (260, 2056, 2040)]
 
 
 def _gen(seed):
@@ -132,6 +136,18 @@ def test_backward_of_no_tokens_zeroes_the_weights_gradients():
     assert (dwg == 0).all() and (dwu == 0).all()
     out = torch.empty_like(dh)
     M.glu(d, x, w, w, out, R.poisoned(M.glu_workspace_size(d, 0)))
+
+
+@pytest.mark.parametrize("T", [9, 400])
+def test_weights_gradients_need_no_weights(T):
+    g = _gen(T)
+    d = M.make_glu_desc(264, 136, M.DT_BF16)
+    x, dh = R.gauss(g, (T, 264), 1.0, torch.bfloat16), R.gauss(g, (T, 136), 0.5, torch.bfloat16)
+    wg, wu = (R.gauss(g, (136, 264), 0.06, torch.bfloat16) for _ in range(2))
+    _, pre = _forward(d, x, wg, wu)
+    _, dwg, dwu = _backward(d, x, wg, wu, pre, dh, want_dx=False)
+    got = _backward(d, x, None, None, pre, dh, want_dx=False)
+    assert torch.equal(got[1], dwg) and torch.equal(got[2], dwu)
 
 
 @pytest.mark.parametrize("a", ACTS)

@@ -14,7 +14,11 @@ TYPES = [torch.bfloat16, torch.float16]
 SHAPES = [(1, 256, 128, 1, 8), (1, 2048, 4096, 8, 16), (2, 8, 8, 3, 8), (7, 520, 136, 4, 24), (16, 1032, 200, 16, 32),
           (17, 264, 72, 5, 40), (33, 1032, 1384, 40, 16), (64, 2048, 512, 64, 64), (65, 136, 128, 3, 128),
           (100, 512, 1000, 7, 256), (128, 776, 264, 33, 16), (129, 512, 256, 2, 8), (257, 1000, 328, 300, 16),
-          (300, 40, 520, 9, 72), (515, 1384, 1032, 12, 32), (1100, 264, 2056, 6, 136)]
+          (300, 40, 520, 9, 72), (515, 1384, 1032, 12, 32), (1100, 264, 2056, 6, 136),
+          # 64-row tiles of two wavefronts, k cut over blocks, 256-row tiles and
+          # 16 tokens a shrink block, one token of rank 32 and of more than that
+          (333, 1384, 4096, 5, 24), (70, 16384, 128, 30, 64), (3900, 264, 4096, 6, 24), (1, 4096, 2048, 4, 32),
+          (1, 1032, 136, 4, 40)]
 
 
 def _gen(seed):
