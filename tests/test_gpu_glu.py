@@ -20,7 +20,9 @@ SHAPES = [(1, 256, 128), (1, 8, 8), (2, 264, 40), (7, 520, 136), (8, 4096, 2048)
           # 32 weight rows a block, the 64-row tiles of two wavefronts, k cut over
           # blocks (forward, dx, dw), the 256-row tiles (forward, dx, dw)
           (40, 136, 2056), (64, 264, 2048), (333, 1032, 1384), (70, 16384, 128), (70, 128, 8192), (20000, 128, 64),
-          (4000, 264, 2040), (3990, 4088, 264), (260, 2056, 2040)]
+          (4000, 264, 2040), (3990, 4088, 264), (260, 2056, 2040),
+          # dw and dx in 64-row tiles of their own launch
+          (1000, 4096, 64), (1000, 4096, 136), (320, 4096, 1024)]
 
 
 def _gen(seed):

@@ -167,8 +167,7 @@ Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K)
     return t;
 }
 
-// The same in 64 x 64 tiles whatever they cost; us: what its blocks take of the
-// GPU, one on each of the 256 CUs at a time.
+// The same in 64 x 64 tiles whatever they cost; us: one block.
 Tiles plan_small_tiles(int mode, int64_t M, int64_t N, int64_t K)
 {
     Tiles t{};
@@ -177,8 +176,15 @@ Tiles plan_small_tiles(int mode, int64_t M, int64_t N, int64_t K)
     t.nt = cdiv(N, tile_cols(mode, t.bm));
     t.per = std::max<int64_t>(1, stages_of(mode, K));
     t.splits = 1;
-    t.us = (double)(t.mt * t.nt) / 256 * (5 + 0.08 * (double)t.per);
+    t.us = 5 + 0.08 * (double)t.per;
     return t;
+}
+
+// Both kinds of such blocks in one launch, one on each of the 256 CUs at a time:
+// their sum over the CUs, at least the longer block.
+double small_tiles_us(const Tiles &a, const Tiles &b)
+{
+    return std::max(std::max(a.us, b.us), ((double)(a.mt * a.nt) * a.us + (double)(b.mt * b.nt) * b.us) / 256);
 }
 
 // Bytes of partial tiles that any launch of at most this size can need
@@ -428,7 +434,7 @@ int moe_exl3_glu_backward(const moe_exl3_glu_desc *desc, const void *x, int64_t 
     // choice is the same where only one is wanted, and so are its bits.
     Tiles tx = plan_tiles(DENSE_DX, T, H, I), tw = plan_tiles(DENSE_DW, I, H, T);
     const Tiles sx = plan_small_tiles(DENSE_DX, T, H, I), sw = plan_small_tiles(DENSE_DW, I, H, T);
-    if (T > 0 && sx.us + sw.us < tx.us + tw.us) {
+    if (T > 0 && small_tiles_us(sx, sw) < tx.us + tw.us) {
         set_tiles(ax, sx, part);
         set_tiles(aw, sw, part);
         if (!want_dx)
