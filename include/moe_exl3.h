@@ -437,8 +437,9 @@ int moe_exl3_lora_workspace_size(const moe_exl3_lora_desc *desc, int64_t max_tok
  * depends on its own adapter only: another adapter's infinities or NaNs do
  * not reach it.  T = 0 is a no-op.
  *
- * The status word (see MOE_EXL3_STATUS_OFFSET) reports BAD_INDEX for an id outside [-1, n_adapters) (the token then has no
- * adapter) and BAD_WIDTH for a rank outside [0, desc.rank] (clamped).
+ * The status word (see MOE_EXL3_STATUS_OFFSET) reports BAD_INDEX for an id
+ * outside [-1, n_adapters) (the token then has no adapter) and BAD_WIDTH for a
+ * named adapter's rank outside [0, desc.rank] (clamped).
  */
 int moe_exl3_lora_linear(const moe_exl3_lora_desc *desc, const void *x, int64_t ldx, const void *w,
                          const moe_exl3_lora_adapters *adapters, const int32_t *ids, const void *base, int64_t ldbase,

@@ -165,6 +165,29 @@ def test_bad_ids_and_ranks_are_reported_and_left_out(T):
     assert torch.equal(y, _run(d, x, w, a, b, ids, None, None, held, dtype))
 
 
+@pytest.mark.parametrize("T", [1, 3, 70, 300, 5000])
+def test_ranks_of_adapters_without_tokens_are_not_read(T):
+    # a stack of many adapters costs what its named ones cost: a rank that no
+    # token asks for is no fault, the last token's is
+    g = _gen(T + 7)
+    K, N, n, r = 72, 64, 3000, 8
+    d = M.make_lora_desc(K, N, n, r, M.DT_F16)
+    half = torch.float16
+    x, w = R.gauss(g, (T, K), 1.0, half), R.gauss(g, (N, K), 0.1, half)
+    a, b = R.gauss(g, (n, r, K), 0.1, half), R.gauss(g, (n, N, r), 0.3, half)
+    ids = torch.randint(0, 50, (T,), generator=g, device="cuda").to(torch.int32)
+    ids[-1] = n - 1
+    ranks = torch.full((n,), -5, dtype=torch.int32, device="cuda")
+    ranks[:50], ranks[n - 1] = 5, 8
+    y, ws = torch.empty(T, N, dtype=half, device="cuda"), R.poisoned(M.lora_workspace_size(d, T))
+    M.lora_linear(d, x, w, a, b, ids, y, ws, ranks=ranks)
+    assert M.status(ws) == 0
+    ranks[n - 1] = 9
+    z = torch.empty_like(y)
+    M.lora_linear(d, x, w, a, b, ids, z, ws, ranks=ranks)
+    assert M.status(ws) == M.STATUS_BAD_WIDTH and torch.equal(y, z)
+
+
 @pytest.mark.parametrize("T", [1, 48, 200, 900])
 def test_a_tokens_row_does_not_depend_on_its_neighbours(T):
     # the same token and adapter among other tokens and ids: the same bits

@@ -163,6 +163,17 @@ MOE_DEV void token_adapter(const LoraArgs &lo, int t, int T, int &id, int &rk)
     rk = id < 0 ? 0 : lo.ranks ? min(max(lo.ranks[id], 0), lo.rank) : lo.rank;
 }
 
+// The status bits of one token's id and its adapter's rank.
+MOE_DEV int id_faults(const LoraArgs &lo, int id)
+{
+    if (id < 0 || id >= lo.n)
+        return id == -1 ? 0 : (int)MOE_EXL3_STATUS_BAD_INDEX;
+    if (!lo.ranks)
+        return 0;
+    const int rank = lo.ranks[id];
+    return rank < 0 || rank > lo.rank ? (int)MOE_EXL3_STATUS_BAD_WIDTH : 0;
+}
+
 // sum += this wavefront's k share of scales[e] x[t] A_e^T, rows r0 .. r0 + 16 NR
 // of A_e, for the 16 tokens of the lanes (lane l: token l % 16 with adapter id
 // and rank, -1: none); once per adapter that they name.
@@ -198,7 +209,6 @@ MOE_DEV void lora_rows(const LoraArgs &lo, int id, int rank, int r0, int l, int 
 // Result columns of a block with 16 NJ weight rows.
 template <int MODE>
 constexpr int skinny_cols(int nj) { return MODE == DENSE_GLU ? 8 * nj : 16 * nj; }
-
 
 // delta[t][16 columns]: the adapters' rows of tokens t = w, w + XW, .. , kBatch
 // at a time with all their loads in flight: lane l takes column l / 4 and the k
@@ -260,16 +270,8 @@ MOE_DEV void fused_expand(const DenseArgs &a, int n0, int w, int l, float (*delt
     const LoraArgs &lo = a.lora;
     int id, rank;   // of token l % 16: the one in lanes 0, 16, ..
     token_adapter(lo, l & 15, a.M, id, rank);
-    if (blockIdx.x == 0 && w == 0) {
-        // the call's status word
-        bool wide = false;
-        if (lo.ranks)
-            for (int e = l; e < lo.n; e += 64)
-                wide |= lo.ranks[e] < 0 || lo.ranks[e] > lo.rank;
-        const bool width = __ballot(wide), index = lo.ids[0] < -1 || lo.ids[0] >= lo.n;
-        if (l == 0)
-            *lo.status = (index ? (int)MOE_EXL3_STATUS_BAD_INDEX : 0) | (width ? (int)MOE_EXL3_STATUS_BAD_WIDTH : 0);
-    }
+    if (blockIdx.x == 0 && w == 0 && l == 0)
+        *lo.status = id_faults(lo, lo.ids[0]);
     // B's rows for the second product: lane l takes column l / 4, ranks k .. k + 7
     const int c = l >> 2, n = min(n0 + c, a.N - 1), k = 8 * (l & 3);
     const int e = max(__builtin_amdgcn_readfirstlane(id), 0), rk = __builtin_amdgcn_readfirstlane(rank);

@@ -4,7 +4,8 @@
 
 namespace moe {
 
-// The call's status word: ids and ranks outside their ranges.
+// The call's status word: ids outside their range, and ranks of the adapters
+// that they name.
 template <int THREADS>
 MOE_DEV void check_adapters(const LoraArgs &lo, int T, int tid)
 {
@@ -20,14 +21,12 @@ MOE_DEV void check_adapters(const LoraArgs &lo, int T, int tid)
         for (int b = 0; b < kBatch; ++b)
 #pragma unroll
             for (int d = 0; d < 4; ++d)
-                bad |= ((int)v[b][d] < -1 || (int)v[b][d] >= lo.n) ? 1 : 0;
+                bad |= id_faults(lo, (int)v[b][d]);
     }
     for (int t = 4 * quads + tid; t < T; t += THREADS)
-        bad |= (lo.ids[t] < -1 || lo.ids[t] >= lo.n) ? 1 : 0;
-    if (lo.ranks)
-        for (int e = tid; e < lo.n; e += THREADS)
-            bad |= (lo.ranks[e] < 0 || lo.ranks[e] > lo.rank) ? 2 : 0;
-    const int index = __syncthreads_or(bad & 1), width = __syncthreads_or(bad & 2);
+        bad |= id_faults(lo, lo.ids[t]);
+    const int index = __syncthreads_or(bad & (int)MOE_EXL3_STATUS_BAD_INDEX);
+    const int width = __syncthreads_or(bad & (int)MOE_EXL3_STATUS_BAD_WIDTH);
     if (tid == 0)
         *lo.status = (index ? (int)MOE_EXL3_STATUS_BAD_INDEX : 0) | (width ? (int)MOE_EXL3_STATUS_BAD_WIDTH : 0);
 }
