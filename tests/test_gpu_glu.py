@@ -205,6 +205,26 @@ def test_extreme_values(T):
     R.assert_close(out[4:], h, bound, "clean rows")
 
 
+@pytest.mark.parametrize("a", ACTS)
+def test_slope_of_huge_gates(a):
+    # gates far past where the activation is straight: slope 1 or 0, no
+    # overflow of their squares; a NaN gate stays one
+    H, I = 8, 16
+    d = M.make_glu_desc(H, I, M.DT_BF16, a)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    gate = torch.tensor([1e4, 1e13, 1e19, 1e25, 3e38, -1e4, -1e13, -1e19, -1e25, -3e38, 20.0, -200.0, 16.0, 0.0, 90.0,
+                         float("nan")], device="cuda")
+    pre = torch.stack((gate, torch.ones_like(gate)))[:, None].contiguous()
+    x, dout = torch.ones(1, H, **bf), torch.ones(1, I, **bf)
+    dwg, dwu = torch.empty(I, H, **bf), torch.empty(I, H, **bf)
+    M.glu_backward(d, x, None, None, pre, dout, R.poisoned(M.glu_backward_workspace_size(d, 1)), dw_gate=dwg, dw_up=dwu)
+    slope = (gate > 0).float()
+    slope[13] = 0.5
+    assert torch.equal(dwg[:15].float(), slope[:15, None].expand(15, H))
+    assert torch.equal(dwu[:15].float(), gate[:15].clamp(min=0).bfloat16().float()[:, None].expand(15, H))
+    assert torch.isnan(dwg[15]).all() and torch.isnan(dwu[15]).all()
+
+
 @pytest.mark.parametrize("T,H,I", [(1, 4096, 2048), (40, 512, 256), (300, 1032, 1384), (2100, 520, 512)])
 def test_same_bits_every_time(T, H, I):
     g = _gen(1)
@@ -264,6 +284,10 @@ def test_binding_refuses():
         a.update(kw)
         with pytest.raises(ValueError):
             M.glu(d, a["x"], a["w"], w, a["out"], a["ws"], pre=a["pre"])
+    class Elsewhere:   # a stream of another GPU
+        device, cuda_stream = torch.device("cuda", 7), 0
+    with pytest.raises(ValueError):
+        M.glu(d, x, w, w, out, ws, stream=Elsewhere())
     with pytest.raises(M.MoeError) as e:
         M.glu(d, x, w, w, out, ws[:16])
     assert e.value.code == M.ERR_WORKSPACE

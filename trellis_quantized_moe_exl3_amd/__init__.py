@@ -386,9 +386,9 @@ def _whole(t, shape, types, device, what: str):
                          f"{t.dtype} on {t.device}")
 
 
-def _dense_device(x, workspace, what: str):
-    """The device of a call: that of x, which must be the current one, and of
-    the workspace."""
+def _dense_device(x, workspace, stream, what: str):
+    """The device of a call: that of x, which must be the current one, of the
+    workspace and of the stream."""
     d = x.device
     if d.type != "cuda":
         raise ValueError(f"{what}: tensors must be on the GPU, got {d}")
@@ -396,6 +396,8 @@ def _dense_device(x, workspace, what: str):
         raise ValueError(f"{what}: tensors on {d}, the current device is {_torch().cuda.current_device()}")
     if workspace is None or workspace.device != d or not workspace.is_contiguous():
         raise ValueError(f"{what}: workspace must be a contiguous tensor on {d}")
+    if stream is not None and stream.device != d:
+        raise ValueError(f"{what}: a stream of {stream.device}, tensors on {d}")
     return d
 
 
@@ -403,7 +405,7 @@ def glu(desc: GluDesc, x, w_gate, w_up, out, workspace, pre=None, stream=None) -
     """out = act(x w_gate^T) * (x w_up^T) (moe_exl3_glu).  x [T][hidden], out
     [T][inter], weights [inter][hidden]; pre: optional fp32 [2][T][inter] that
     receives the two products for glu_backward()."""
-    d = _dense_device(x, workspace, "glu")
+    d = _dense_device(x, workspace, stream, "glu")
     types, T, H, I = _dense_dtypes(desc.act_dtype), x.shape[0], desc.hidden, desc.inter
     ldx, ldo = _rows(x, T, H, types, d, "glu: x"), _rows(out, T, I, types, d, "glu: out")
     _whole(w_gate, (I, H), types, d, "glu: w_gate")
@@ -419,7 +421,7 @@ def glu_backward(desc: GluDesc, x, w_gate, w_up, pre, dout, workspace, dx=None, 
                  stream=None) -> None:
     """Gradients of glu() from dout and its `pre` (moe_exl3_glu_backward): dx
     [T][hidden] and / or dw_gate and dw_up [inter][hidden], written."""
-    d = _dense_device(x, workspace, "glu_backward")
+    d = _dense_device(x, workspace, stream, "glu_backward")
     types, T, H, I = _dense_dtypes(desc.act_dtype), x.shape[0], desc.hidden, desc.inter
     ldx, lddo = _rows(x, T, H, types, d, "glu_backward: x"), _rows(dout, T, I, types, d, "glu_backward: dout")
     _whole(pre, (2, T, I), (_torch().float32,), d, "glu_backward: pre")
@@ -444,7 +446,7 @@ def lora_linear(desc: LoraDesc, x, w, lora_a, lora_b, ids, out, workspace, base=
     out; scales fp32 and ranks int32 [n_adapters] or None.  status(workspace)
     reports ids and ranks out of range."""
     torch = _torch()
-    d = _dense_device(x, workspace, "lora_linear")
+    d = _dense_device(x, workspace, stream, "lora_linear")
     types, T = _dense_dtypes(desc.act_dtype), x.shape[0]
     K, N, n, r = desc.n_in, desc.n_out, desc.n_adapters, desc.rank
     ldx, ldy = _rows(x, T, K, types, d, "lora_linear: x"), _rows(out, T, N, types, d, "lora_linear: out")

@@ -29,9 +29,12 @@ MOE_DEV void act_value_slope(int act, float g, float &v, float &d)
         v = g * p;
         d = p * (1.0f + g * (1.0f - p));
     } else {
-        const float p = logistic(2.0f * kGeluK * (g + kGeluC * g * g * g));
+        // past 16 the logistic is 0 or 1 and the slope no longer moves: the cube
+        // of a larger gate would overflow against that zero
+        const float z = g > 16.0f ? 16.0f : g < -16.0f ? -16.0f : g;
+        const float p = logistic(2.0f * kGeluK * (z + kGeluC * z * z * z));
         v = g * p;
-        d = p + 2.0f * g * p * (1.0f - p) * kGeluK * (1.0f + 3.0f * kGeluC * g * g);
+        d = p + 2.0f * z * p * (1.0f - p) * kGeluK * (1.0f + 3.0f * kGeluC * z * z);
     }
 }
 
