@@ -222,10 +222,13 @@ def _torch():
     return _torch_mod
 
 
-def _stream(stream) -> int:
+def _stream(stream, device: Optional[int] = None) -> int:
+    """Handle of a stream; None: the current one (of `device`, if it is known
+    to be the current GPU)."""
     if stream is not None:
         return stream.cuda_stream
-    device = _torch().cuda.current_device()
+    if device is None:
+        device = _torch().cuda.current_device()
     return _raw_stream(device)
 
 
@@ -365,12 +368,12 @@ def _dense_dtypes(act_dtype: int):
     return _dense_types[act_dtype]
 
 
-def _rows(t, rows: int, cols: int, types, device, what: str) -> int:
-    """Row stride of a [rows][cols] activation (unit column stride, rows apart
-    by any stride; a single row has none)."""
-    if t.shape != (rows, cols) or t.dtype not in types or t.device != device:
-        raise ValueError(f"{what}: expected [{rows}][{cols}] {types[0]} on {device}, got {tuple(t.shape)} {t.dtype} "
-                         f"on {t.device}")
+def _rows(t, rows: int, cols: int, types, device: int, what: str) -> int:
+    """Row stride of a [rows][cols] activation on a GPU (unit column stride,
+    rows apart by any stride; a single row has none)."""
+    if t.shape != (rows, cols) or t.dtype not in types or t.get_device() != device:
+        raise ValueError(f"{what}: expected [{rows}][{cols}] {types[0]} on GPU {device}, got {tuple(t.shape)} "
+                         f"{t.dtype} on {t.device}")
     ld, step = t.stride()
     if rows <= 1:
         ld = cols
@@ -379,25 +382,23 @@ def _rows(t, rows: int, cols: int, types, device, what: str) -> int:
     return ld
 
 
-def _whole(t, shape, types, device, what: str):
+def _whole(t, shape, types, device: int, what: str):
     """A contiguous tensor of exactly this shape."""
-    if t.shape != shape or t.dtype not in types or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous {shape} {types[0]} on {device}, got {tuple(t.shape)} "
+    if t.shape != shape or t.dtype not in types or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {shape} {types[0]} on GPU {device}, got {tuple(t.shape)} "
                          f"{t.dtype} on {t.device}")
 
 
-def _dense_device(x, workspace, stream, what: str):
-    """The device of a call: that of x, which must be the current one, of the
+def _dense_device(x, workspace, stream, what: str) -> int:
+    """The GPU of a call: that of x, which must be the current one, of the
     workspace and of the stream."""
-    d = x.device
-    if d.type != "cuda":
-        raise ValueError(f"{what}: tensors must be on the GPU, got {d}")
-    if d.index != _torch().cuda.current_device():
-        raise ValueError(f"{what}: tensors on {d}, the current device is {_torch().cuda.current_device()}")
-    if workspace is None or workspace.device != d or not workspace.is_contiguous():
-        raise ValueError(f"{what}: workspace must be a contiguous tensor on {d}")
-    if stream is not None and stream.device != d:
-        raise ValueError(f"{what}: a stream of {stream.device}, tensors on {d}")
+    d = x.get_device()   # below 0: not on a GPU
+    if d < 0 or d != _torch().cuda.current_device():
+        raise ValueError(f"{what}: tensors must be on the current GPU, got {x.device}")
+    if workspace is None or workspace.get_device() != d or not workspace.is_contiguous():
+        raise ValueError(f"{what}: workspace must be a contiguous tensor on GPU {d}")
+    if stream is not None and stream.device != x.device:
+        raise ValueError(f"{what}: a stream of {stream.device}, tensors on {x.device}")
     return d
 
 
@@ -414,7 +415,7 @@ def glu(desc: GluDesc, x, w_gate, w_up, out, workspace, pre=None, stream=None) -
         _whole(pre, (2, T, I), (_torch().float32,), d, "glu: pre")
     _check(lib().moe_exl3_glu(C.byref(desc), x.data_ptr(), ldx, w_gate.data_ptr(), w_up.data_ptr(), T,
                               out.data_ptr(), ldo, _ptr(pre), workspace.data_ptr(), workspace.nbytes,
-                              _stream(stream)), "moe_exl3_glu")
+                              _stream(stream, d)), "moe_exl3_glu")
 
 
 def glu_backward(desc: GluDesc, x, w_gate, w_up, pre, dout, workspace, dx=None, dw_gate=None, dw_up=None,
@@ -433,7 +434,7 @@ def glu_backward(desc: GluDesc, x, w_gate, w_up, pre, dout, workspace, dx=None, 
             _whole(t, (I, H), types, d, "glu_backward: " + what)
     _check(lib().moe_exl3_glu_backward(C.byref(desc), x.data_ptr(), ldx, _ptr(w_gate), _ptr(w_up), pre.data_ptr(),
                                        dout.data_ptr(), lddo, T, _ptr(dx), lddx, _ptr(dw_gate), _ptr(dw_up),
-                                       workspace.data_ptr(), workspace.nbytes, _stream(stream)),
+                                       workspace.data_ptr(), workspace.nbytes, _stream(stream, d)),
            "moe_exl3_glu_backward")
 
 
@@ -465,4 +466,4 @@ def lora_linear(desc: LoraDesc, x, w, lora_a, lora_b, ids, out, workspace, base=
     ad = LoraAdapters(lora_a.data_ptr(), lora_b.data_ptr(), _ptr(scales), _ptr(ranks))
     _check(lib().moe_exl3_lora_linear(C.byref(desc), x.data_ptr(), ldx, _ptr(w), C.byref(ad), ids.data_ptr(),
                                       _ptr(base), ldb, T, out.data_ptr(), ldy, workspace.data_ptr(),
-                                      workspace.nbytes, _stream(stream)), "moe_exl3_lora_linear")
+                                      workspace.nbytes, _stream(stream, d)), "moe_exl3_lora_linear")
