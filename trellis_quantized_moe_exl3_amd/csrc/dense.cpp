@@ -167,22 +167,22 @@ Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K)
     return t;
 }
 
-// The same in 64 x 64 tiles whatever they cost; us: one block.
-Tiles plan_small_tiles(int mode, int64_t M, int64_t N, int64_t K)
+// The same in tiles of one size, whatever they cost, k uncut; us: one block.
+Tiles plan_fixed(int mode, int64_t M, int64_t N, int64_t K, int64_t bm)
 {
     Tiles t{};
-    t.bm = kDenseTile;
-    t.mt = (mode == DENSE_DW ? 2 : 1) * cdiv(M, t.bm);
-    t.nt = cdiv(N, tile_cols(mode, t.bm));
+    t.bm = bm;
+    t.mt = (mode == DENSE_DW ? 2 : 1) * cdiv(M, bm);
+    t.nt = cdiv(N, tile_cols(mode, bm));
     t.per = std::max<int64_t>(1, stages_of(mode, K));
     t.splits = 1;
-    t.us = 5 + 0.08 * (double)t.per;
+    t.us = bm == kDenseTile ? 5 + 0.08 * (double)t.per : 4 + 0.24 * (double)t.per;
     return t;
 }
 
 // Both kinds of such blocks in one launch, one on each of the 256 CUs at a time:
 // their sum over the CUs, at least the longer block.
-double small_tiles_us(const Tiles &a, const Tiles &b)
+double merged_us(const Tiles &a, const Tiles &b)
 {
     return std::max(std::max(a.us, b.us), ((double)(a.mt * a.nt) * a.us + (double)(b.mt * b.nt) * b.us) / 256);
 }
@@ -429,12 +429,17 @@ int moe_exl3_glu_backward(const moe_exl3_glu_desc *desc, const void *x, int64_t 
     aw.ldo = H;
     float *part = at<float>(workspace, p.part);
     const bool want_dx = dx && T > 0, want_dw = dw_gate;
-    // Small gradients leave CUs idle on their own: their tiles share one launch
-    // (509 tokens, 776 x 1304: 17.7 and 8.5 us apart, 23 together).  The
-    // choice is the same where only one is wanted, and so are its bits.
-    Tiles tx = plan_tiles(DENSE_DX, T, H, I), tw = plan_tiles(DENSE_DW, I, H, T);
-    const Tiles sx = plan_small_tiles(DENSE_DX, T, H, I), sw = plan_small_tiles(DENSE_DW, I, H, T);
-    if (T > 0 && small_tiles_us(sx, sw) < tx.us + tw.us) {
+    // Small gradients leave CUs idle on their own: their tiles share one launch,
+    // dx in 64 x 64 ones, dw in the better of two (509 tokens, 776 x 1304: 17.7
+    // and 8.5 us apart, 23 together in 64 x 64 tiles, TODO with 128 x 128 for dw).
+    // The choice is the same where only one is wanted, and so are its bits.
+    const Tiles tx = plan_tiles(DENSE_DX, T, H, I), tw = plan_tiles(DENSE_DW, I, H, T);
+    const Tiles sx = plan_fixed(DENSE_DX, T, H, I, kDenseTile);
+    Tiles sw = plan_fixed(DENSE_DW, I, H, T, kDenseTile);
+    const Tiles lw = plan_fixed(DENSE_DW, I, H, T, kDenseSmall);
+    if (merged_us(sx, lw) < merged_us(sx, sw))
+        sw = lw;
+    if (T > 0 && merged_us(sx, sw) < tx.us + tw.us) {
         set_tiles(ax, sx, part);
         set_tiles(aw, sw, part);
         if (!want_dx)

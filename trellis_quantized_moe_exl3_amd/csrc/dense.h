@@ -72,7 +72,7 @@ struct DenseArgs {
 };
 
 hipError_t launch_dense(int mode, bool bf16, const DenseArgs &a, hipStream_t s);
-// DX and DW, both in 64 x 64 tiles, in one launch.
+// DX in 64 x 64 tiles and DW in 64 x 64 or 128 x 128 ones, in one launch.
 hipError_t launch_dense_grads(bool bf16, const DenseArgs &dx, const DenseArgs &dw, hipStream_t s);
 // GLU or LIN of at most kSkinnyTokens tokens.
 hipError_t launch_dense_skinny(int mode, bool bf16, const DenseArgs &a, hipStream_t s);

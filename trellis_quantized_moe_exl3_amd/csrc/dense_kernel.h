@@ -460,18 +460,22 @@ MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const Adap
     wait_vmcnt<0>();   // the loads past the end still write LDS
 }
 
+// Halves of a ring array: one stage of both operands.
+template <class S>
+constexpr int kDenseHalves = (S::BM + S::BN) * kDenseBK;
+
+// Tile `block` of a launch; r0 .. r3: its LDS ring.
 template <int MODE, bool BF16, class S>
-__global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
+MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *r0, LDS_AS uint16_t *r1,
+                         LDS_AS uint16_t *r2, LDS_AS uint16_t *r3)
 {
     using T = DenseTile<MODE, BF16, S>;
-    constexpr int kHalves = (S::BM + S::BN) * kDenseBK;
-    __shared__ __align__(1024) uint16_t ring0[kHalves], ring1[kHalves], ring2[kHalves], ring3[kHalves];
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = w / S::WN, wn = w % S::WN;
     const int tiles = a.mt * a.nt;
-    const int split = blockIdx.x / tiles;
+    const int split = block / tiles;
     int m, n;
-    dense_tile(blockIdx.x - split * tiles, tiles, a.mt, a.nt, m, n);
+    dense_tile(block - split * tiles, tiles, a.mt, a.nt, m, n);
     // DW: the row tiles of the second tensor follow those of the first
     const int half = MODE == DENSE_DW ? a.mt / 2 : a.mt;
     const int z = m >= half ? 1 : 0;
@@ -523,25 +527,22 @@ __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
     if constexpr (MODE == DENSE_LIN) {
         // the adapters' share goes with the first k split
         __shared__ AdapterJobs<S::BM> jobs;
-        t.run(s0, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1, (LDS_AS uint16_t *)ring2,
-              (LDS_AS uint16_t *)ring3, acc, [&]() __attribute__((always_inline)) {
-                  if (split == 0) {
-                      jobs.ids_of(a.lora, m0, a.M, tid);
-                      __syncthreads();
-                      if (w == 0)
-                          jobs.build(a.lora, l);
-                  }
-              });
+        t.run(s0, r0, r1, r2, r3, acc, [&]() __attribute__((always_inline)) {
+            if (split == 0) {
+                jobs.ids_of(a.lora, m0, a.M, tid);
+                __syncthreads();
+                if (w == 0)
+                    jobs.build(a.lora, l);
+            }
+        });
         if (split == 0)
-            lora_expand<BF16, S>(a, m0, n0, tid, jobs, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1,
-                                 (LDS_AS uint16_t *)ring2, (LDS_AS uint16_t *)ring3, acc);
+            lora_expand<BF16, S>(a, m0, n0, tid, jobs, r0, r1, r2, r3, acc);
     } else {
-        t.run(s0, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1, (LDS_AS uint16_t *)ring2,
-              (LDS_AS uint16_t *)ring3, acc, [] {});
+        t.run(s0, r0, r1, r2, r3, acc, [] {});
     }
 
     if (a.splits > 1) {
-        f32x4 *part = (f32x4 *)a.part + ((int64_t)blockIdx.x * S::NI * S::NJ) * (64 * S::NW) + tid;
+        f32x4 *part = (f32x4 *)a.part + ((int64_t)block * S::NI * S::NJ) * (64 * S::NW) + tid;
 #pragma unroll
         for (int i = 0; i < S::NI; ++i)
 #pragma unroll
@@ -551,9 +552,17 @@ __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
     }
     const int mw = m0 + wm * S::TM, nw = n0 + wn * ((kDenseCols<MODE, S>) / S::WN);
     __syncthreads();   // the ring is free
-    LDS_AS f32x4 *lds = (LDS_AS f32x4 *)(LDS_AS uint16_t *)ring0 + 256 * w;
-    static_assert(S::NW * 4096 <= kHalves * 2, "a wavefront's share of the first ring array");
-    dense_store_all<MODE, BF16>(a, z, mw, nw, l, acc, lds);
+    static_assert(S::NW * 4096 <= kDenseHalves<S> * 2, "a wavefront's share of the first ring array");
+    dense_store_all<MODE, BF16>(a, z, mw, nw, l, acc, (LDS_AS f32x4 *)r0 + 256 * w);
+}
+
+template <int MODE, bool BF16, class S>
+__global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
+{
+    __shared__ __align__(1024) uint16_t ring0[kDenseHalves<S>], ring1[kDenseHalves<S>], ring2[kDenseHalves<S>],
+        ring3[kDenseHalves<S>];
+    dense_block<MODE, BF16, S>(a, blockIdx.x, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1,
+                               (LDS_AS uint16_t *)ring2, (LDS_AS uint16_t *)ring3);
 }
 
 // Sum of the k splits' partial tiles, in split order, and the epilogue: block

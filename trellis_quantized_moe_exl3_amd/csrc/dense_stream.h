@@ -485,11 +485,14 @@ MOE_DEV void tile_expand(const DenseArgs &a, int mine, int rank, int m0, int n0,
     wait_vmcnt<0>();   // the loads past the end still write LDS
 }
 
-// Tile `block` of a launch of NW wavefronts a block; ring0, ring1: its LDS.
+// Tile `block` of a launch of NW wavefronts a block.  Its LDS: the first slot of
+// the lower half's rings in lo0, of the upper half's in hi0, the second slots in
+// lo1 and hi1.
 constexpr int kTileHalves = 16 * 8 * 64;   // of one share of both operands
 
 template <int MODE, bool BF16, int NW>
-MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *ring0, LDS_AS uint16_t *ring1)
+MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *lo0, LDS_AS uint16_t *hi0,
+                        LDS_AS uint16_t *lo1, LDS_AS uint16_t *hi1)
 {
     using TR = DenseTraits<MODE>;
     using S = Stream<BF16, 4, 4, 2, TR::kPL, TR::kQL>;
@@ -513,7 +516,10 @@ MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *ring0, L
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             acc[i][j] = (f32x4){};
-    LDS_AS uint16_t *r0 = ring0 + w * S::kHalves, *r1 = ring1 + w * S::kHalves;
+    constexpr int kLow = NW / 2;
+    const bool low = w < kLow;
+    LDS_AS uint16_t *r0 = low ? lo0 + w * S::kHalves : hi0 + (w - kLow) * S::kHalves;
+    LDS_AS uint16_t *r1 = low ? lo1 + w * S::kHalves : hi1 + (w - kLow) * S::kHalves;
     int mine = -1, rank = 0;
     if constexpr (MODE == DENSE_LIN)
         token_adapter(a.lora, m0 + l, a.M, mine, rank);
@@ -525,26 +531,26 @@ MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *ring0, L
     }
     if constexpr (MODE == DENSE_LIN)
         tile_expand<BF16, NW, S>(a, mine, rank, m0, n0, w, l, r0, r1, acc);
-    // every wavefront's sums in its own part of the first ring array
-    LDS_AS f32x4 *red = (LDS_AS f32x4 *)ring0;
+    // every wavefront's sums in its own first slot
     constexpr int kStep = S::kHalves / 8;
-    static_assert(kStep >= 16 * 64, "sums fit the first ring array");
+    static_assert(kStep >= 16 * 64, "sums fit a slot");
+    auto sums = [&](int s) { return (LDS_AS f32x4 *)(s < kLow ? lo0 : hi0) + (s % kLow) * kStep; };
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            red[w * kStep + (4 * i + j) * 64 + l] = acc[i][j];
+            ((LDS_AS f32x4 *)r0)[(4 * i + j) * 64 + l] = acc[i][j];
     __syncthreads();
     for (int i = w; i < 4; i += NW) {
         f32x4 v[1][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            v[0][j] = red[(4 * i + j) * 64 + l];
+            v[0][j] = sums(0)[(4 * i + j) * 64 + l];
 #pragma unroll
             for (int s = 1; s < NW; ++s)
-                v[0][j] += red[s * kStep + (4 * i + j) * 64 + l];
+                v[0][j] += sums(s)[(4 * i + j) * 64 + l];
         }
-        dense_store_all<MODE, BF16>(a, z, m0 + 16 * i, n0, l, v, (LDS_AS f32x4 *)ring1 + 256 * w);
+        dense_store_all<MODE, BF16>(a, z, m0 + 16 * i, n0, l, v, (LDS_AS f32x4 *)r1);
     }
 }
 
@@ -552,20 +558,29 @@ template <int MODE, bool BF16, int NW>
 __global__ __launch_bounds__(64 * NW) void dense_tile_kernel(DenseArgs a)
 {
     __shared__ __align__(1024) uint16_t ring0[NW * kTileHalves], ring1[NW * kTileHalves];
-    tile_block<MODE, BF16, NW>(a, blockIdx.x, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1);
+    LDS_AS uint16_t *r0 = (LDS_AS uint16_t *)ring0, *r1 = (LDS_AS uint16_t *)ring1;
+    constexpr int kHalf = NW / 2 * kTileHalves;
+    tile_block<MODE, BF16, NW>(a, blockIdx.x, r0, r0 + kHalf, r1, r1 + kHalf);
 }
 
-// Both gradients in one launch: the tiles of dx first (a longer k each), then
-// those of dw.
-template <bool BF16>
+// Both gradients in one launch: the tiles of dx first (64 x 64, a longer k
+// each), then those of dw, 64 x 64 or (WIDE) 128 x 128.  One block a CU.
+template <bool BF16, bool WIDE>
 __global__ __launch_bounds__(256) void dense_grads_kernel(DenseArgs dx, DenseArgs dw)
 {
-    __shared__ __align__(1024) uint16_t ring0[4 * kTileHalves], ring1[4 * kTileHalves];
+    constexpr int kPart = 2 * kTileHalves;   // two wavefronts' rings
+    __shared__ __align__(1024) uint16_t a0[kPart], a1[kPart], b0[kPart], b1[kPart];
+    LDS_AS uint16_t *r[4] = {(LDS_AS uint16_t *)a0, (LDS_AS uint16_t *)a1, (LDS_AS uint16_t *)b0,
+                             (LDS_AS uint16_t *)b1};
     const int block = blockIdx.x, first = dx.mt * dx.nt;
-    if (block < first)
-        tile_block<DENSE_DX, BF16, 4>(dx, block, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1);
-    else
-        tile_block<DENSE_DW, BF16, 4>(dw, block - first, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1);
+    if (block < first) {
+        tile_block<DENSE_DX, BF16, 4>(dx, block, r[0], r[1], r[2], r[3]);
+    } else if constexpr (WIDE) {
+        static_assert(SmallTile::NW == 4 && kDenseHalves<SmallTile> <= kPart, "the same threads and LDS");
+        dense_block<DENSE_DW, BF16, SmallTile>(dw, block - first, r[0], r[1], r[2], r[3]);
+    } else {
+        tile_block<DENSE_DW, BF16, 4>(dw, block - first, r[0], r[1], r[2], r[3]);
+    }
 }
 
 template <int MODE, bool BF16>

@@ -69,10 +69,12 @@ hipError_t launch_dense(int mode, bool bf16, const DenseArgs &a, hipStream_t s)
 hipError_t launch_dense_grads(bool bf16, const DenseArgs &dx, const DenseArgs &dw, hipStream_t s)
 {
     const unsigned grid = (unsigned)(dx.mt * dx.nt + dw.mt * dw.nt);
-    if (bf16)
-        dense_grads_kernel<true><<<grid, 256, 0, s>>>(dx, dw);
+    if (dw.bm == kDenseSmall)
+        bf16 ? dense_grads_kernel<true, true><<<grid, 256, 0, s>>>(dx, dw)
+             : dense_grads_kernel<false, true><<<grid, 256, 0, s>>>(dx, dw);
     else
-        dense_grads_kernel<false><<<grid, 256, 0, s>>>(dx, dw);
+        bf16 ? dense_grads_kernel<true, false><<<grid, 256, 0, s>>>(dx, dw)
+             : dense_grads_kernel<false, false><<<grid, 256, 0, s>>>(dx, dw);
     return hipGetLastError();
 }
 
