@@ -15,7 +15,8 @@ namespace moe {
 
 // D[m][n] over NI x NJ blocks of 16 x 16; the block's wavefronts take k shares
 // of 64 in turn, RING shares in flight each.  The first NJ loads of a KC operand
-// Q (8 rows each) go through q[0], the rest through q[1] (GLU: gate, up).
+// Q (8 rows each) go through q[0], the rest through q[1] (GLU: gate, up).  TWO: a
+// second pair of tensors p2, q2 follows along k (DX).
 //
 // LDS image of an operand's share:
 //   KC  128-byte rows of eight 16-byte pieces, piece p of row r in slot
@@ -24,12 +25,12 @@ namespace moe {
 //   KS  one 128-byte row of 64 tile rows for each k, the 32-byte chunk c in slot
 //       c ^ g(k), g(k) = k / 2 % 2 + 2 (k / 8 % 2): the eight k that 32 lanes
 //       of the transposing read touch hit distinct 8-bank groups
-template <bool BF16, int NI, int NJ, int RING, int PL = KC, int QL = KC>
+template <bool BF16, int NI, int NJ, int RING, int PL = KC, int QL = KC, bool TWO = false>
 struct Stream {
     static constexpr int kLoads = 2 * (NI + NJ);
     static constexpr int kHalves = 16 * (NI + NJ) * 64;   // of one share
     static_assert((PL == KC || NI == 4) && (QL == KC || NJ == 4), "KS rows are 128 bytes");
-    __amdgpu_buffer_rsrc_t p, q[2];
+    __amdgpu_buffer_rsrc_t p, q[2], p2, q2;
     uint32_t off[kLoads];   // byte offset of the lane's 16 bytes at k = 0
     uint32_t pstep, qstep;  // bytes from one k to the next
     int l, kend;
@@ -67,14 +68,19 @@ struct Stream {
     }
     MOE_DEV void load(int share, LDS_AS uint16_t *lds)
     {
-        const int k0 = 64 * share;
+        const int most = (kend + 63) / 64;
+        const bool second = TWO && share >= most;
+        const int k0 = 64 * (second ? share - most : share);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const bool isq = j >= 2 * NI;
             const int jj = isq ? j - 2 * NI : j;
             const int k = k0 + ((isq ? QL : PL) == KC ? first_k(l, jj) : row(l, jj));
             const uint32_t o = k < kend ? off[j] + (uint32_t)k0 * (isq ? qstep : pstep) : kOutOfRange;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(!isq ? p : QL == KS || jj < NJ ? q[0] : q[1],
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(!isq ? (second ? p2 : p)
+                                                     : second                ? q2
+                                                     : QL == KS || jj < NJ   ? q[0]
+                                                                             : q[1],
                                                      (LDS_AS void *)(lds + 512 * j), 16, o, 0, 0, 0);
         }
     }
@@ -131,7 +137,7 @@ struct Stream {
                      LDS_AS uint16_t *r3, f32x4 (&acc)[NI][NJ])
     {
         static_assert(RING >= 2 && RING <= 4, "ring arrays");
-        const int shares = (kend + 63) / 64;
+        const int shares = (TWO ? 2 : 1) * ((kend + 63) / 64);
         if (first >= shares)
             return;
         load(first, r0);
@@ -495,7 +501,7 @@ MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *lo0, LDS
                         LDS_AS uint16_t *lo1, LDS_AS uint16_t *hi1)
 {
     using TR = DenseTraits<MODE>;
-    using S = Stream<BF16, 4, 4, 2, TR::kPL, TR::kQL>;
+    using S = Stream<BF16, 4, 4, 2, TR::kPL, TR::kQL, MODE == DENSE_DX>;
     static_assert(S::kHalves == kTileHalves, "ring size");
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     constexpr int kCols = MODE == DENSE_GLU ? 32 : 64;
@@ -523,12 +529,11 @@ MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *lo0, LDS
     int mine = -1, rank = 0;
     if constexpr (MODE == DENSE_LIN)
         token_adapter(a.lora, m0 + l, a.M, mine, rank);
-    st.run(w, NW, r0, r1, nullptr, nullptr, acc);
     if constexpr (MODE == DENSE_DX) {
-        st.p = buf_rsrc(a.p[1], a.pbytes);
-        st.q[0] = buf_rsrc(a.q[1], a.qbytes);
-        st.run(w, NW, r0, r1, nullptr, nullptr, acc);
+        st.p2 = buf_rsrc(a.p[1], a.pbytes);
+        st.q2 = buf_rsrc(a.q[1], a.qbytes);
     }
+    st.run(w, NW, r0, r1, nullptr, nullptr, acc);
     if constexpr (MODE == DENSE_LIN)
         tile_expand<BF16, NW, S>(a, mine, rank, m0, n0, w, l, r0, r1, acc);
     // every wavefront's sums in its own first slot
