@@ -156,7 +156,7 @@ Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K)
     offer(kDenseTile, 1, t64 <= 256 ? 5 + 0.08 * s : rounds(t64, 512) * (5.4 + 0.17 * s));
     const int64_t c = t128 > 0 ? std::min(kSplitBlocks / t128, stages / kSplitStages) : 0;
     if (c > 1)
-        offer(kDenseSmall, c, 18 + 0.24 * (double)cdiv(stages, c));
+        offer(kDenseSmall, c, 12 + 0.24 * (double)cdiv(stages, c));
     Tiles t{};
     t.bm = bm;
     t.mt = (mode == DENSE_DW ? 2 : 1) * cdiv(M, bm);
@@ -446,7 +446,7 @@ int moe_exl3_glu_backward(const moe_exl3_glu_desc *desc, const void *x, int64_t 
             ax.mt = 0;
         if (!want_dw)
             aw.mt = 0;
-        return launch_dense_grads(bf16, ax, aw, s) == hipSuccess ? MOE_EXL3_OK : MOE_EXL3_ERR_HIP;
+        return launch_dense_grads(bf16, ax, aw, sw.us > sx.us, s) == hipSuccess ? MOE_EXL3_OK : MOE_EXL3_ERR_HIP;
     }
     if (want_dx) {
         set_tiles(ax, tx, part);

@@ -72,8 +72,9 @@ struct DenseArgs {
 };
 
 hipError_t launch_dense(int mode, bool bf16, const DenseArgs &a, hipStream_t s);
-// DX in 64 x 64 tiles and DW in 64 x 64 or 128 x 128 ones, in one launch.
-hipError_t launch_dense_grads(bool bf16, const DenseArgs &dx, const DenseArgs &dw, hipStream_t s);
+// DX in 64 x 64 tiles and DW in 64 x 64 or 128 x 128 ones, in one launch, DW's
+// blocks before or behind DX's.
+hipError_t launch_dense_grads(bool bf16, const DenseArgs &dx, const DenseArgs &dw, bool dw_first, hipStream_t s);
 // GLU or LIN of at most kSkinnyTokens tokens.
 hipError_t launch_dense_skinny(int mode, bool bf16, const DenseArgs &a, hipStream_t s);
 hipError_t launch_glu_grad(bool bf16, int act, const float *pre, const uint16_t *dh, int64_t lddh, int64_t T, int I,

@@ -460,6 +460,10 @@ MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const Adap
     wait_vmcnt<0>();   // the loads past the end still write LDS
 }
 
+// Whether k may be cut over blocks: a grid of few tiles takes the small ones.
+template <class S>
+constexpr bool kDenseSplits = S::BM == kDenseSmall;
+
 // Halves of a ring array: one stage of both operands.
 template <class S>
 constexpr int kDenseHalves = (S::BM + S::BN) * kDenseBK;
@@ -473,7 +477,7 @@ MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *r0, LDS
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = w / S::WN, wn = w % S::WN;
     const int tiles = a.mt * a.nt;
-    const int split = block / tiles;
+    const int split = kDenseSplits<S> ? block / tiles : 0;
     int m, n;
     dense_tile(block - split * tiles, tiles, a.mt, a.nt, m, n);
     // DW: the row tiles of the second tensor follow those of the first
@@ -541,7 +545,7 @@ MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *r0, LDS
         t.run(s0, r0, r1, r2, r3, acc, [] {});
     }
 
-    if (a.splits > 1) {
+    if (kDenseSplits<S> && a.splits > 1) {
         f32x4 *part = (f32x4 *)a.part + ((int64_t)block * S::NI * S::NJ) * (64 * S::NW) + tid;
 #pragma unroll
         for (int i = 0; i < S::NI; ++i)
@@ -566,40 +570,49 @@ __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
 }
 
 // Sum of the k splits' partial tiles, in split order, and the epilogue: block
-// (tile, i) finishes the 16-row blocks i of the tile's wavefronts.
+// (tile, w, i) finishes the 16-row block i of the tile's wavefront w.  Bound by
+// what one CU draws of the partial tiles, which come from behind the other XCDs'
+// L2: hence small blocks, many of them (32 splits of 4 tiles: FINISH).
 template <int MODE, bool BF16, class S>
-__global__ __launch_bounds__(64 * S::NW) void dense_finish_kernel(DenseArgs a)
+__global__ __launch_bounds__(64) void dense_finish_kernel(DenseArgs a)
 {
-    const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int l = threadIdx.x, i = blockIdx.x % S::NI, w = blockIdx.x / S::NI % S::NW;
     const int wm = w / S::WN, wn = w % S::WN;
-    const int tiles = a.mt * a.nt;
-    const int L = blockIdx.x / S::NI, i = blockIdx.x % S::NI;
+    const int tiles = a.mt * a.nt, L = blockIdx.x / (S::NI * S::NW);
     int m, n;
     dense_tile(L, tiles, a.mt, a.nt, m, n);
     const int half = MODE == DENSE_DW ? a.mt / 2 : a.mt;
     const int z = m >= half ? 1 : 0;
     const int m0 = (m - z * half) * S::BM, n0 = n * (kDenseCols<MODE, S>);
-    const f32x4 *part = (const f32x4 *)a.part + ((int64_t)L * S::NI + i) * S::NJ * (64 * S::NW) + tid;
+    const f32x4 *part = (const f32x4 *)a.part + ((int64_t)L * S::NI + i) * S::NJ * (64 * S::NW) + 64 * w + l;
     const int64_t step = (int64_t)tiles * S::NI * S::NJ * (64 * S::NW);
-    f32x4 acc[1][S::NJ];
+    f32x4 acc[1][S::NJ] = {};
+    constexpr int kBatch = 8;   // splits in flight
+    for (int k = 0; k < a.splits; k += kBatch) {
+        f32x4 v[kBatch][S::NJ];
 #pragma unroll
-    for (int j = 0; j < S::NJ; ++j)
-        acc[0][j] = part[j * (64 * S::NW)];
-    for (int k = 1; k < a.splits; ++k)
+        for (int b = 0; b < kBatch; ++b)
 #pragma unroll
-        for (int j = 0; j < S::NJ; ++j)
-            acc[0][j] += part[k * step + j * (64 * S::NW)];
+            for (int j = 0; j < S::NJ; ++j)
+                v[b][j] = part[min(k + b, a.splits - 1) * step + j * (64 * S::NW)];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int j = 0; j < S::NJ; ++j)
+                acc[0][j] += k + b < a.splits ? v[b][j] : (f32x4){};
+    }
     const int mw = m0 + wm * S::TM + 16 * i, nw = n0 + wn * ((kDenseCols<MODE, S>) / S::WN);
-    __shared__ f32x4 lds[S::NW * 256];
-    dense_store_all<MODE, BF16>(a, z, mw, nw, l, acc, (LDS_AS f32x4 *)lds + 256 * w);
+    __shared__ f32x4 lds[256];
+    dense_store_all<MODE, BF16>(a, z, mw, nw, l, acc, (LDS_AS f32x4 *)lds);
 }
 
 template <int MODE, bool BF16, class S>
 hipError_t launch_dense_shape(const DenseArgs &a, hipStream_t s)
 {
     dense_kernel<MODE, BF16, S><<<(unsigned)(a.mt * a.nt * a.splits), 64 * S::NW, 0, s>>>(a);
-    if (a.splits > 1)
-        dense_finish_kernel<MODE, BF16, S><<<(unsigned)(a.mt * a.nt * S::NI), 64 * S::NW, 0, s>>>(a);
+    if constexpr (kDenseSplits<S>)
+        if (a.splits > 1)
+            dense_finish_kernel<MODE, BF16, S><<<(unsigned)(a.mt * a.nt * S::NW * S::NI), 64, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -66,15 +66,15 @@ hipError_t launch_dense(int mode, bool bf16, const DenseArgs &a, hipStream_t s)
     }
 }
 
-hipError_t launch_dense_grads(bool bf16, const DenseArgs &dx, const DenseArgs &dw, hipStream_t s)
+hipError_t launch_dense_grads(bool bf16, const DenseArgs &dx, const DenseArgs &dw, bool dw_first, hipStream_t s)
 {
     const unsigned grid = (unsigned)(dx.mt * dx.nt + dw.mt * dw.nt);
     if (dw.bm == kDenseSmall)
-        bf16 ? dense_grads_kernel<true, true><<<grid, 256, 0, s>>>(dx, dw)
-             : dense_grads_kernel<false, true><<<grid, 256, 0, s>>>(dx, dw);
+        bf16 ? dense_grads_kernel<true, true><<<grid, 256, 0, s>>>(dx, dw, dw_first)
+             : dense_grads_kernel<false, true><<<grid, 256, 0, s>>>(dx, dw, dw_first);
     else
-        bf16 ? dense_grads_kernel<true, false><<<grid, 256, 0, s>>>(dx, dw)
-             : dense_grads_kernel<false, false><<<grid, 256, 0, s>>>(dx, dw);
+        bf16 ? dense_grads_kernel<true, false><<<grid, 256, 0, s>>>(dx, dw, dw_first)
+             : dense_grads_kernel<false, false><<<grid, 256, 0, s>>>(dx, dw, dw_first);
     return hipGetLastError();
 }
 
