@@ -22,7 +22,10 @@ SHAPES = [(1, 256, 128), (1, 8, 8), (2, 264, 40), (7, 520, 136), (8, 4096, 2048)
           (40, 136, 2056), (64, 264, 2048), (333, 1032, 1384), (70, 16384, 128), (70, 128, 8192), (20000, 128, 64),
           (4000, 264, 2040), (3990, 4088, 264), (260, 2056, 2040),
           # dw and dx in 64-row tiles of their own launch
-          (1000, 4096, 64), (1000, 4096, 136), (320, 4096, 1024)]
+          (1000, 4096, 64), (1000, 4096, 136), (320, 4096, 1024),
+          # dx in 64-row tiles of four and of two wavefronts with dw in 128- and
+          # 256-row ones, both in 64-row tiles of one launch, the longer dw first
+          (2000, 512, 1024), (333, 4096, 2048), (1000, 256, 256), (3000, 264, 136)]
 
 
 def _gen(seed):

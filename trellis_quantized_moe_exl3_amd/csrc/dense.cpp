@@ -133,9 +133,9 @@ struct Tiles {
 //   128 x 128   4 + 0.24 (1024 tokens: 35; 64 x 64 takes 50, 256 x 256 71)
 //   256 x 256   10 + 0.70 (4096 tokens: 100; 128 x 128 takes 128)
 // Few tiles with a long k are cut along k, at the price of partial tiles and a
-// second launch: 18 + 0.24 a stage (96 tokens of the gradient for x, hidden 1024,
-// inter 4096: 27 us, the uncut 128 x 128 tile takes 80; 100 tokens, 8192 x 256:
-// 20, 64 x 64 takes 22).
+// second launch: 12 + 0.24 a stage (a call of 100 tokens, 8192 x 256: 13.6 us,
+// 64 x 64 takes 22; 4096 x 512: 11.6, 13.7; but 200 tokens, 4096 x 1024: 14.8,
+// 13.9 in 64 x 64).
 Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K)
 {
     const int64_t stages = stages_of(mode, K);
@@ -181,10 +181,16 @@ Tiles plan_fixed(int mode, int64_t M, int64_t N, int64_t K, int64_t bm)
 }
 
 // Both kinds of such blocks in one launch, one on each of the 256 CUs at a time:
-// their sum over the CUs, at least the longer block.
+// the longest block or the sum over the CUs, and a fifth of the other for the
+// last blocks' uneven ends.  Whole steps, in one launch and in two, in us: 250
+// tokens, 2048 x 2048: 34.6, 41.7; 4000, 512 x 512: 41.5, 45.1; 1, 4096 x 2048:
+// 34.1, 40.7; but 8000, 256 x 1024: 88.3, 85.8; 128, 1536 x 4096: 45.6, 41.4;
+// 16000, 256 x 256: 75.3, 53.8.
 double merged_us(const Tiles &a, const Tiles &b)
 {
-    return std::max(std::max(a.us, b.us), ((double)(a.mt * a.nt) * a.us + (double)(b.mt * b.nt) * b.us) / 256);
+    const double longest = std::max(a.us, b.us);
+    const double sum = ((double)(a.mt * a.nt) * a.us + (double)(b.mt * b.nt) * b.us) / 256;
+    return std::max(longest, sum) + 0.2 * std::min(longest, sum);
 }
 
 // Bytes of partial tiles that any launch of at most this size can need
@@ -430,8 +436,8 @@ int moe_exl3_glu_backward(const moe_exl3_glu_desc *desc, const void *x, int64_t 
     float *part = at<float>(workspace, p.part);
     const bool want_dx = dx && T > 0, want_dw = dw_gate;
     // Small gradients leave CUs idle on their own: their tiles share one launch,
-    // dx in 64 x 64 ones, dw in the better of two (509 tokens, 776 x 1304: 17.7
-    // and 8.5 us apart, 23 together in 64 x 64 tiles, TODO with 128 x 128 for dw).
+    // dx in 64 x 64 ones, dw in the better of two (509 tokens, 776 x 1304: 22.9 us
+    // with 64 x 64 tiles for both, 18.2 with 128 x 128 for dw).
     // The choice is the same where only one is wanted, and so are its bits.
     const Tiles tx = plan_tiles(DENSE_DX, T, H, I), tw = plan_tiles(DENSE_DW, I, H, T);
     const Tiles sx = plan_fixed(DENSE_DX, T, H, I, kDenseTile);

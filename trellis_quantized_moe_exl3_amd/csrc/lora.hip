@@ -41,6 +41,8 @@ MOE_DEV void check_adapters(const LoraArgs &lo, int T, int tid)
 // token keeps its own result.  One token a block lets all the adapters of a
 // decode step stream at once, at the price of reading an adapter once per
 // token; 16 tokens a block read it once where a request's tokens stand together.
+// Bound by latency: 64 tokens, 2048 k, rank 64: 5.2 us (4 MB of A); 7168 tokens,
+// 2048 k, rank 32: 10 us for 30 MB of x.
 template <bool BF16, int NW, int NR, int RING>
 __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(const uint16_t *x, int64_t ldx, uint32_t xbytes, int T,
                                                               int K, int tpf, LoraArgs lo)
