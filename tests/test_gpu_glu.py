@@ -25,7 +25,9 @@ SHAPES = [(1, 256, 128), (1, 8, 8), (2, 264, 40), (7, 520, 136), (8, 4096, 2048)
           (1000, 4096, 64), (1000, 4096, 136), (320, 4096, 1024),
           # dx in 64-row tiles of four and of two wavefronts with dw in 128- and
           # 256-row ones, both in 64-row tiles of one launch, the longer dw first
-          (2000, 512, 1024), (333, 4096, 2048), (1000, 256, 256), (3000, 264, 136)]
+          (2000, 512, 1024), (333, 4096, 2048), (1000, 256, 256), (3000, 264, 136),
+          # dx in 128-row tiles, two on a CU
+          (2300, 2056, 264)]
 
 
 def _gen(seed):

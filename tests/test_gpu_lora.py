@@ -18,7 +18,10 @@ SHAPES = [(1, 256, 128, 1, 8), (1, 2048, 4096, 8, 16), (2, 8, 8, 3, 8), (7, 520,
           # 64-row tiles of two wavefronts, k cut over blocks, 256-row tiles and
           # 16 tokens a shrink block, one token of rank 32 and of more than that
           (333, 1384, 4096, 5, 24), (70, 16384, 128, 30, 64), (3900, 264, 4096, 6, 24), (1, 4096, 2048, 4, 32),
-          (1, 1032, 136, 4, 40)]
+          (1, 1032, 136, 4, 40),
+          # 128-row tiles, two on a CU; adapters dealt to the k splits; many of them
+          # in a tile without much of a projection
+          (1300, 264, 4096, 6, 104), (89, 5008, 1008, 12, 96), (116, 40, 1984, 62, 32)]
 
 
 def _gen(seed):
@@ -188,13 +191,13 @@ def test_ranks_of_adapters_without_tokens_are_not_read(T):
     assert M.status(ws) == M.STATUS_BAD_WIDTH and torch.equal(y, z)
 
 
-@pytest.mark.parametrize("T", [1, 48, 200, 900])
-def test_a_tokens_row_does_not_depend_on_its_neighbours(T):
+@pytest.mark.parametrize("T,K,N", [(1, 1032, 264), (48, 1032, 264), (200, 1032, 264), (900, 1032, 264), (100, 8200, 264)])
+def test_a_tokens_row_does_not_depend_on_its_neighbours(T, K, N):
     # the same token and adapter among other tokens and ids: the same bits
     # (the calls take the same number of tokens, hence the same kernels)
     g = _gen(T + 3)
     dtype = torch.bfloat16
-    K, N, n, r = 1032, 264, 9, 24
+    n, r = 9, 24
     d = M.make_lora_desc(K, N, n, r, M.DT_BF16)
     x, w = R.gauss(g, (T, K), 1.0, dtype), R.gauss(g, (N, K), 0.03, dtype)
     a, b = R.gauss(g, (n, r, K), 0.03, dtype), R.gauss(g, (n, N, r), 0.3, dtype)

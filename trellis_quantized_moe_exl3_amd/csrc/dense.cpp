@@ -3,6 +3,7 @@
 #include "dense.h"
 
 #include <algorithm>
+#include <cmath>
 
 using namespace moe;
 
@@ -16,7 +17,7 @@ constexpr int64_t kSpanLimit = (int64_t)1 << 31;
 // k splits of the 128-tile: at most this many blocks (one a CU), each with at
 // least this many stages (256 k).
 constexpr int64_t kSplitBlocks = 256;
-constexpr int64_t kSplitStages = 8;
+constexpr int64_t kSplitStages = 4;
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -111,7 +112,7 @@ bool rows_fit(int64_t T, int64_t cols) { return T < kSpanLimit && T * cols * 2 <
 // Columns of a tile of `bm` rows.
 int64_t tile_cols(int mode, int64_t bm) { return mode == DENSE_GLU ? bm / 2 : bm; }
 
-int64_t stages_of(int mode, int64_t K) { return (mode == DENSE_DX ? 2 : 1) * cdiv(K, kDenseBK); }
+int64_t stages_of(int mode, int64_t K) { return (mode == DENSE_DX ? 2 : 1) * cdiv(K, kDenseK); }
 
 int64_t tiles_of(int mode, int64_t M, int64_t N, int64_t bm)
 {
@@ -126,17 +127,26 @@ struct Tiles {
 
 // The tile of a launch: the one whose rounds over the 256 CUs are estimated to
 // take the least time.  A round costs a fixed part (launch, first loads,
-// epilogue) and a part per stage of 32 k, in us as measured on the block's
-// forward pass, 96 to 10000 tokens, hidden 1024 and 4096, inter 512 to 4096:
-//   64 x 64     5 + 0.08 a stage up to 256 tiles, else 5.4 + 0.17 a round of 512
-//               (333 tokens, 4096 x 2048: 25 us; 128 x 128 takes 29)
-//   128 x 128   4 + 0.24 (1024 tokens: 35; 64 x 64 takes 50, 256 x 256 71)
-//   256 x 256   10 + 0.70 (4096 tokens: 100; 128 x 128 takes 128)
+// epilogue) and a part per 64 k, in us as measured on the block's forward pass,
+// 96 to 16384 tokens, hidden 512 to 8192, inter 256 to 8192 (calls one after the
+// other):
+//   64 x 64     5 + 0.16 for 64 k up to 256 tiles, else 5.4 + 0.34 a round of 512
+//               (333 tokens, 1032 x 1384: 11.0; 128 x 128 takes 15.2)
+//   128 x 128   4 + 0.48 (1024 tokens, 4096 x 2048: 35.7; 64 x 64 takes 52,
+//               256 x 256 73)
+//   256 x 256   10 + 1.40 (4096 tokens, 4096 x 2048: 104; 128 x 128 takes 114)
 // Few tiles with a long k are cut along k, at the price of partial tiles and a
-// second launch: 12 + 0.24 a stage (a call of 100 tokens, 8192 x 256: 13.6 us,
-// 64 x 64 takes 22; 4096 x 512: 11.6, 13.7; but 200 tokens, 4096 x 1024: 14.8,
-// 13.9 in 64 x 64).
-Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K)
+// second launch: 12 + 0.48 for 64 k + 0.1 a split, into as many as make that
+// least (100 tokens, 8192 x 256: 13.6, 64 x 64 takes 22; but 200 tokens, 2048 x
+// 1024: 18.0, 10.1 in 64 x 64).
+//
+// An adapter that a tile's tokens name costs 0.6 us for 64 ranks in a 128 x 128
+// tile, twice that in a 256 x 256 one; the splits share them, and so do the
+// wavefronts of a 64 x 64 tile (116 tokens, 62 adapters of 32, 1984 columns and no
+// projection: a call of 53 us in 128 x 128, 24 in 64 x 64).  Of n adapters a tile of bm
+// tokens is taken to name n bm / T and one more, the tokens of a request standing
+// together.
+Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K, int64_t n = 0, int64_t rank = 0)
 {
     const int64_t stages = stages_of(mode, K);
     const double s = (double)stages;
@@ -150,13 +160,18 @@ Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K)
         }
     };
     auto rounds = [&](int64_t tiles, int64_t at_once) { return (double)cdiv(tiles, at_once); };
+    auto adapters = [&](int64_t b) {
+        return n == 0 || M == 0 ? 0.0 : 0.6 * (double)(std::min({n, b, cdiv(n * b, M) + 1}) * cdiv(rank, 64));
+    };
+    const double l64 = adapters(kDenseTile), l128 = adapters(kDenseSmall), l256 = 2 * adapters(kDenseLarge);
     const int64_t t64 = tiles_of(mode, M, N, kDenseTile), t128 = tiles_of(mode, M, N, kDenseSmall);
-    offer(kDenseLarge, 1, rounds(tiles_of(mode, M, N, kDenseLarge), 256) * (10 + 0.70 * s));
-    offer(kDenseSmall, 1, rounds(t128, 256) * (4 + 0.24 * s));
-    offer(kDenseTile, 1, t64 <= 256 ? 5 + 0.08 * s : rounds(t64, 512) * (5.4 + 0.17 * s));
-    const int64_t c = t128 > 0 ? std::min(kSplitBlocks / t128, stages / kSplitStages) : 0;
+    offer(kDenseLarge, 1, rounds(tiles_of(mode, M, N, kDenseLarge), 256) * (10 + 1.40 * s + l256));
+    offer(kDenseSmall, 1, rounds(t128, 256) * (4 + 0.48 * s + l128));
+    offer(kDenseTile, 1, t64 <= 256 ? 5 + 0.16 * s + l64 / 4 : rounds(t64, 512) * (5.4 + 0.34 * s + l64 / 2));
+    const int64_t most = t128 > 0 ? std::min(kSplitBlocks / t128, stages / kSplitStages) : 0;
+    const int64_t c = std::min(most, std::max<int64_t>(2, (int64_t)std::sqrt((0.48 * s + l128) / 0.1)));
     if (c > 1)
-        offer(kDenseSmall, c, 12 + 0.24 * (double)cdiv(stages, c));
+        offer(kDenseSmall, c, 12 + 0.48 * (double)cdiv(stages, c) + l128 / (double)c + 0.1 * (double)c);
     Tiles t{};
     t.bm = bm;
     t.mt = (mode == DENSE_DW ? 2 : 1) * cdiv(M, bm);
@@ -176,21 +191,28 @@ Tiles plan_fixed(int mode, int64_t M, int64_t N, int64_t K, int64_t bm)
     t.nt = cdiv(N, tile_cols(mode, bm));
     t.per = std::max<int64_t>(1, stages_of(mode, K));
     t.splits = 1;
-    t.us = bm == kDenseTile ? 5 + 0.08 * (double)t.per : 4 + 0.24 * (double)t.per;
+    t.us = bm == kDenseTile ? 5 + 0.16 * (double)t.per : 4 + 0.48 * (double)t.per;
     return t;
+}
+
+// Both kinds' blocks over the 256 CUs.
+double merged_sum(const Tiles &a, const Tiles &b)
+{
+    return ((double)(a.mt * a.nt) * a.us + (double)(b.mt * b.nt) * b.us) / 256;
 }
 
 // Both kinds of such blocks in one launch, one on each of the 256 CUs at a time:
 // the longest block or the sum over the CUs, and a fifth of the other for the
 // last blocks' uneven ends.  Whole steps, in one launch and in two, in us: 250
-// tokens, 2048 x 2048: 34.6, 41.7; 4000, 512 x 512: 41.5, 45.1; 1, 4096 x 2048:
-// 34.1, 40.7; but 8000, 256 x 1024: 88.3, 85.8; 128, 1536 x 4096: 45.6, 41.4;
-// 16000, 256 x 256: 75.3, 53.8.
-double merged_us(const Tiles &a, const Tiles &b)
+// tokens, 2048 x 2048: 37.1, 42.1; 4000, 512 x 512: 42.3, 46.0; 1, 4096 x 2048:
+// 39.5, 41.3; but 8000, 256 x 1024: 88.3, 85.8; 16000, 256 x 256: 75.3, 53.8.
+// Beyond a sum of 25 us (the rounds are many, and each gradient fills the CUs by
+// itself) one launch has only lost: 500, 2056 x 2056: 75.6, 72.4; 4542, 1408 x
+// 1560: 225, 191.
+bool merge_pays(const Tiles &a, const Tiles &b, double apart)
 {
-    const double longest = std::max(a.us, b.us);
-    const double sum = ((double)(a.mt * a.nt) * a.us + (double)(b.mt * b.nt) * b.us) / 256;
-    return std::max(longest, sum) + 0.2 * std::min(longest, sum);
+    const double longest = std::max(a.us, b.us), sum = merged_sum(a, b);
+    return sum <= 25 && std::max(longest, sum) + 0.2 * std::min(longest, sum) < apart;
 }
 
 // Bytes of partial tiles that any launch of at most this size can need
@@ -222,7 +244,7 @@ int launch_forward(int mode, int dtype, DenseArgs &a, float *part, void *stream)
     if (a.M <= kSkinnyTokens) {
         e = launch_dense_skinny(mode, bf16, a, (hipStream_t)stream);
     } else {
-        set_tiles(a, plan_tiles(mode, a.M, a.N, a.K), part);
+        set_tiles(a, plan_tiles(mode, a.M, a.N, a.K, a.lora.n, a.lora.rank), part);
         e = launch_dense(mode, bf16, a, (hipStream_t)stream);
     }
     return e == hipSuccess ? MOE_EXL3_OK : MOE_EXL3_ERR_HIP;
@@ -443,9 +465,9 @@ int moe_exl3_glu_backward(const moe_exl3_glu_desc *desc, const void *x, int64_t 
     const Tiles sx = plan_fixed(DENSE_DX, T, H, I, kDenseTile);
     Tiles sw = plan_fixed(DENSE_DW, I, H, T, kDenseTile);
     const Tiles lw = plan_fixed(DENSE_DW, I, H, T, kDenseSmall);
-    if (merged_us(sx, lw) < merged_us(sx, sw))
+    if (std::max(lw.us, merged_sum(sx, lw)) < std::max(sw.us, merged_sum(sx, sw)))
         sw = lw;
-    if (T > 0 && merged_us(sx, sw) < tx.us + tw.us) {
+    if (T > 0 && merge_pays(sx, sw, tx.us + tw.us)) {
         set_tiles(ax, sx, part);
         set_tiles(aw, sw, part);
         if (!want_dx)

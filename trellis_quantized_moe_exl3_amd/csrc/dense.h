@@ -11,11 +11,11 @@
 namespace moe {
 
 // Rows and columns of the output tiles (a GLU tile's columns are half gate,
-// half up), and the k extent of one pipeline stage.
+// half up), and the k that their launch plans count in.
 constexpr int kDenseTile = 64;   // wavefronts cut k (dense_stream.h)
 constexpr int kDenseSmall = 128;
 constexpr int kDenseLarge = 256;
-constexpr int kDenseBK = 32;
+constexpr int kDenseK = 64;
 // Tokens up to which the forward operators take the few-token kernel.
 constexpr int64_t kSkinnyTokens = 64;
 // Largest rank, bytes of A and columns up to which the few-token kernel computes

@@ -46,17 +46,19 @@ struct DenseTraits {
     static constexpr int kQL = (MODE == DENSE_DX || MODE == DENSE_DW) ? KS : KC;
 };
 
-// Tile shapes: WM x WN wavefronts of TM x TN outputs each.  TN = 64 in all of
-// them (see kDenseCols).
-template <int BM_, int BN_, int WM_, int WN_>
+// Tile shapes: WM x WN wavefronts of TM x TN outputs each, RING stages of BK k in
+// LDS.  TN = 64 in all of them (see kDenseCols).
+template <int BM_, int BN_, int WM_, int WN_, int BK_, int RING_>
 struct DenseShape {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NW = WM * WN;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NW = WM * WN, BK = BK_, RING = RING_;
+    static constexpr int kHalves = (BM + BN) * BK;   // of a stage of both operands
     static constexpr int TM = BM / WM, TN = BN / WN, NI = TM / 16, NJ = TN / 16;
     static_assert(TN == 64 && NW % 4 == 0, "GLU column interleave");
     static_assert(BM % 64 == 0 && 64 * NW >= BM, "a thread for each row");
 };
-using SmallTile = DenseShape<kDenseSmall, kDenseSmall, 2, 2>;
-using LargeTile = DenseShape<kDenseLarge, kDenseLarge, 2, 4>;
+using SmallTile = DenseShape<kDenseSmall, kDenseSmall, 2, 2, 64, 2>;   // two on a CU
+using AloneTile = DenseShape<kDenseSmall, kDenseSmall, 2, 2, 64, 4>;   // one on a CU
+using LargeTile = DenseShape<kDenseLarge, kDenseLarge, 2, 4, 32, 4>;
 
 // Result columns n0 + .. of a tile: GLU tiles hold BN / 2 columns of both
 // projections, interleaved by 32 (tile rows 64 s + 0..31 of Q are gate columns
@@ -199,7 +201,7 @@ MOE_DEV void dense_store_all(const DenseArgs &a, int z, int m0, int n0, int l, c
     }
 }
 
-// Fragments of one stage: NI row blocks of P and NJ of Q.
+// Fragments of 32 k: NI row blocks of P and NJ of Q.
 template <class S>
 struct DenseFrags {
     u32x4 p[S::NI], q[S::NJ];
@@ -210,8 +212,8 @@ struct DenseTile {
     static constexpr int NI = S::NI, NJ = S::NJ;
     using Frags = DenseFrags<S>;
     using TR = DenseTraits<MODE>;
-    using OP = Operand<S::BM, TR::kPL, S::NW>;
-    using OQ = Operand<S::BN, TR::kQL, S::NW>;
+    using OP = Operand<S::BM, TR::kPL, S::NW, S::BK>;
+    using OQ = Operand<S::BN, TR::kQL, S::NW, S::BK>;
     static constexpr int kLoads = OP::kLoads + OQ::kLoads;
     OP po;
     OQ qo;
@@ -223,84 +225,98 @@ struct DenseTile {
     MOE_DEV void load(int s, LDS_AS uint16_t *ring)
     {
         const bool second = MODE == DENSE_DX && s >= nsk;
-        const int k0 = kDenseBK * (second ? s - nsk : s);
+        const int k0 = S::BK * (second ? s - nsk : s);
         const int end = s < send ? kend : 0;
         po.issue(second ? pr[1] : pr[0], ring, w, k0, end, pstep);
-        qo.issue(second ? qr[1] : qr[0], ring + S::BM * kDenseBK, w, k0, end, qstep);
+        qo.issue(second ? qr[1] : qr[0], ring + S::BM * S::BK, w, k0, end, qstep);
     }
-    MOE_DEV void read(const LDS_AS uint16_t *ring, Frags &f)
+    MOE_DEV void read(const LDS_AS uint16_t *ring, int h, Frags &f)
     {
 #pragma unroll
         for (int i = 0; i < S::NI; ++i)
-            f.p[i] = OP::frag(ring, pbase, i);
+            f.p[i] = OP::frag(ring, pbase, i, h);
 #pragma unroll
         for (int j = 0; j < S::NJ; ++j)
-            f.q[j] = OQ::frag(ring + S::BM * kDenseBK, qbase, j);
+            f.q[j] = OQ::frag(ring + S::BM * S::BK, qbase, j, h);
     }
-    // Stage s in ring slot `cur`, whose fragments `f` were read during stage
-    // s - 1.  "At most 2 loads' worth outstanding" (stages s + 2 and s + 3)
-    // proves that this wavefront's loads of stage s + 1 have landed; past the
-    // barrier every wavefront's have, and every wavefront has read slot `cur`,
-    // which stage s + 4 refills.
-    MOE_DEV void stage(int s, LDS_AS uint16_t *cur, const LDS_AS uint16_t *next, const Frags &f, Frags &fn,
-                       f32x4 (&acc)[NI][NJ])
+    MOE_DEV void multiply(const Frags &f, f32x4 (&acc)[NI][NJ])
     {
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-        wait_vmcnt<2 * kLoads>();
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        load(s + 4, cur);
-        read(next, fn);
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
                 acc[i][j] = dense_mfma<BF16>(f.q[j], f.p[i], acc[i][j]);
+    }
+    // The order of 32 k: the next fragments' reads and L loads spread over the
+    // MFMAs, early enough that the next wait finds them done (7168 tokens, 4096 x
+    // 2048: 213 -> 207 us).  The transposing reads' two halves a fragment leave
+    // no registers for it: there the same order spills and halves the rate.
+    template <int L>
+    MOE_DEV static void spread()
+    {
         if constexpr (TR::kPL == KC && TR::kQL == KC) {
-            // the next fragments' reads and the loads spread over the MFMAs,
-            // early enough that the wait at the next barrier finds them done
-            // (7168 tokens, 4096 x 2048: 213 -> 207 us).  The transposing
-            // reads' two halves a fragment leave no registers for it: there
-            // the same order spills and halves the rate.
-            constexpr int kPer = NI * NJ / (NI + NJ + kLoads);
+            constexpr int kPer = NI * NJ / (NI + NJ + L);
 #pragma unroll
             for (int r = 0; r < NI + NJ; ++r) {
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
             }
 #pragma unroll
-            for (int r = 0; r < kLoads; ++r) {
+            for (int r = 0; r < L; ++r) {
                 __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
             }
         }
     }
+    // Stage s in ring slot `cur`, whose first fragments f0 were read during stage
+    // s - 1; f0 and f1 change places from one 32 k to the next.  "At most RING - 2
+    // stages' loads outstanding" (s + 2 .. s + RING - 1) proves that this
+    // wavefront's loads of stage s + 1 have landed; past the barrier every
+    // wavefront's have, and every wavefront has read slot `cur`, which stage s +
+    // RING refills.
+    MOE_DEV void stage(int s, LDS_AS uint16_t *cur, const LDS_AS uint16_t *next, Frags &f0, Frags &f1,
+                       f32x4 (&acc)[NI][NJ])
+    {
+        if constexpr (S::BK == 64) {
+            read(cur, 1, f1);
+            multiply(f0, acc);
+            spread<0>();
+        }
+        Frags &last = S::BK == 64 ? f1 : f0, &first = S::BK == 64 ? f0 : f1;
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+        wait_vmcnt<(S::RING - 2) * kLoads>();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        load(s + S::RING, cur);
+        read(next, 0, first);
+        multiply(last, acc);
+        spread<kLoads>();
+    }
     // `meanwhile` runs once, while the first loads are on their way.
     template <class F>
-    MOE_DEV void run(int s0, LDS_AS uint16_t *r0, LDS_AS uint16_t *r1, LDS_AS uint16_t *r2, LDS_AS uint16_t *r3,
-                     f32x4 (&acc)[NI][NJ], F meanwhile)
+    MOE_DEV void run(int s0, LDS_AS uint16_t *const (&ring)[S::RING], f32x4 (&acc)[NI][NJ], F meanwhile)
     {
         if (s0 >= send) {
             meanwhile();
             return;
         }
-        load(s0, r0);
-        load(s0 + 1, r1);
-        load(s0 + 2, r2);
-        load(s0 + 3, r3);
+#pragma unroll
+        for (int r = 0; r < S::RING; ++r)
+            load(s0 + r, ring[r]);
         meanwhile();
         __builtin_amdgcn_sched_barrier(0);
-        wait_vmcnt<3 * kLoads>();
+        wait_vmcnt<(S::RING - 1) * kLoads>();
         __builtin_amdgcn_s_barrier();
         Frags f0, f1;
-        read(r0, f0);
-        for (int s = s0; s < send; s += 4) {
-            stage(s, r0, r1, f0, f1, acc);
-            stage(s + 1, r1, r2, f1, f0, acc);
-            stage(s + 2, r2, r3, f0, f1, acc);
-            stage(s + 3, r3, r0, f1, f0, acc);
-        }
+        read(ring[0], 0, f0);
+        constexpr bool kSwap = S::BK == 32;
+        for (int s = s0; s < send; s += S::RING)
+#pragma unroll
+            for (int r = 0; r < S::RING; r += 2) {
+                stage(s + r, ring[r], ring[r + 1], f0, f1, acc);
+                stage(s + r + 1, ring[r + 1], ring[(r + 2) % S::RING], kSwap ? f1 : f0, kSwap ? f0 : f1, acc);
+            }
         wait_vmcnt<0>();   // the loads past the end still write LDS
     }
 };
@@ -336,12 +352,12 @@ MOE_DEV void lora_products(bool hit, u32x4 p, const u32x4 (&q)[NJ], f32x4 (&acc)
     }
 }
 
-// The adapters of a tile's tokens as a list of stages of 32 ranks.
-template <int BM>
+// The adapters of a tile's tokens as a list of stages of BK ranks.
+template <int BM, int BK>
 struct AdapterJobs {
     int id[BM];                         // adapter of each token, -1: none
     int count;
-    uint32_t job[BM * (kMaxRank / 32)]; // adapter | stage << 16 | its rank << 20
+    uint32_t job[BM * (kMaxRank / BK)]; // adapter | stage << 16 | its rank << 20
 
     // The tokens' ids, by all threads.
     MOE_DEV void ids_of(const LoraArgs &lo, int m0, int T, int tid)
@@ -351,9 +367,11 @@ struct AdapterJobs {
             id[tid] = e >= 0 && e < lo.n ? e : -1;
         }
     }
-    // One wavefront, the ids being visible: the list, adapters in the order of
-    // their first tokens.
-    MOE_DEV void build(const LoraArgs &lo, int l)
+    // One wavefront, the ids being visible: the list of this k split's share,
+    // adapters in the order of their first tokens.  Adapters go to the splits by
+    // their number, so that a token's sum is taken in the same order whatever its
+    // neighbours.
+    MOE_DEV void build(const LoraArgs &lo, int split, int splits, int l)
     {
         int n = 0;
         uint64_t left[BM / 64];
@@ -376,7 +394,7 @@ struct AdapterJobs {
 #pragma unroll
                 for (int h = g; h < BM / 64; ++h)
                     left[h] &= ~__ballot(mine[h] == e);
-                const int stages = (rk + 31) / 32;
+                const int stages = e % splits == split ? (rk + BK - 1) / BK : 0;
                 if (l < stages)
                     job[n + l] = (uint32_t)e | (uint32_t)l << 16 | (uint32_t)rk << 20;
                 n += stages;
@@ -387,16 +405,15 @@ struct AdapterJobs {
 };
 
 // The adapters' share of a tile, added to its accumulators: stages like those
-// of the k loop, one for every 32 ranks of every adapter that a token of the
+// of the k loop, one for every BK ranks of every adapter that a token of the
 // tile names, P = the tokens' s_a x A_a^T, Q = B_a's rows, through the same
 // ring.
 template <bool BF16, class S>
-MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const AdapterJobs<S::BM> &jobs,
-                         LDS_AS uint16_t *r0, LDS_AS uint16_t *r1, LDS_AS uint16_t *r2, LDS_AS uint16_t *r3,
-                         f32x4 (&acc)[S::NI][S::NJ])
+MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const AdapterJobs<S::BM, S::BK> &jobs,
+                         LDS_AS uint16_t *const (&ring)[S::RING], f32x4 (&acc)[S::NI][S::NJ])
 {
-    using OP = Operand<S::BM, KC, S::NW>;
-    using OQ = Operand<S::BN, KC, S::NW>;
+    using OP = Operand<S::BM, KC, S::NW, S::BK>;
+    using OQ = Operand<S::BN, KC, S::NW, S::BK>;
     constexpr int kLoads = OP::kLoads + OQ::kLoads;
     const LoraArgs &lo = a.lora;
     const int l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -417,61 +434,66 @@ MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const Adap
     auto job_of = [&](int t) __attribute__((always_inline)) {
         return (uint32_t)__builtin_amdgcn_readfirstlane((int)jobs.job[min(t, count - 1)]);
     };
-    auto load = [&](int t, LDS_AS uint16_t *ring) __attribute__((always_inline)) {
+    auto load = [&](int t, LDS_AS uint16_t *slot) __attribute__((always_inline)) {
         const uint32_t job = job_of(t);
-        const int e = job & 0xFFFF, k0 = 32 * ((job >> 16) & 15), rk = t < count ? (int)(job >> 20) : 0;
-        po.issue(pr, ring, w, k0, rk, 2);
-        qo.issue(buf_rsrc(lo.b + (int64_t)e * a.N * lo.rank, bbytes), ring + S::BM * kDenseBK, w, k0, rk, 2);
+        const int e = job & 0xFFFF, k0 = S::BK * ((job >> 16) & 15), rk = t < count ? (int)(job >> 20) : 0;
+        po.issue(pr, slot, w, k0, rk, 2);
+        qo.issue(buf_rsrc(lo.b + (int64_t)e * a.N * lo.rank, bbytes), slot + S::BM * S::BK, w, k0, rk, 2);
     };
     auto stage = [&](int t, const LDS_AS uint16_t *cur, LDS_AS uint16_t *refill) __attribute__((always_inline)) {
         __builtin_amdgcn_sched_barrier(0);
-        wait_vmcnt<2 * kLoads>();   // stages t + 1 and t + 2 stay in flight
+        wait_vmcnt<(S::RING - 2) * kLoads>();   // the stages after t stay in flight
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        load(t + 3, refill);
+        load(t + S::RING - 1, refill);
         const uint32_t job = job_of(t);
-        const int e = job & 0xFFFF;
-        u32x4 q[S::NJ];
+        const int e = job & 0xFFFF, k0 = S::BK * ((job >> 16) & 15), rk = job >> 20;
 #pragma unroll
-        for (int j = 0; j < S::NJ; ++j)
-            q[j] = OQ::frag(cur + S::BM * kDenseBK, qbase, j);
-        lora_cut(job >> 20, 32 * ((job >> 16) & 15), l, q);
+        for (int h = 0; h < S::BK / 32; ++h) {
+            if (k0 + 32 * h >= rk)
+                break;
+            u32x4 q[S::NJ];
 #pragma unroll
-        for (int i = 0; i < S::NI; i += 2) {
-            const u32x4 p0 = OP::frag(cur, pbase, i), p1 = OP::frag(cur, pbase, i + 1);
-            lora_products<BF16>(ids[16 * i] == e, p0, q, acc[i]);
-            lora_products<BF16>(ids[16 * i + 16] == e, p1, q, acc[i + 1]);
-            __builtin_amdgcn_sched_barrier(0);   // fragments of two blocks at a time: registers
+            for (int j = 0; j < S::NJ; ++j)
+                q[j] = OQ::frag(cur + S::BM * S::BK, qbase, j, h);
+            lora_cut(rk, k0 + 32 * h, l, q);
+#pragma unroll
+            for (int i = 0; i < S::NI; i += 2) {
+                const u32x4 p0 = OP::frag(cur, pbase, i, h), p1 = OP::frag(cur, pbase, i + 1, h);
+                lora_products<BF16>(ids[16 * i] == e, p0, q, acc[i]);
+                lora_products<BF16>(ids[16 * i + 16] == e, p1, q, acc[i + 1]);
+                __builtin_amdgcn_sched_barrier(0);   // fragments of two blocks at a time: registers
+            }
         }
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): reads done before the next barrier
     };
-    load(0, r0);
-    load(1, r1);
-    load(2, r2);
+    LDS_AS uint16_t *slot[S::RING];
+#pragma unroll
+    for (int r = 0; r < S::RING; ++r) {
+        slot[r] = ring[r];
+        if (r < S::RING - 1)
+            load(r, slot[r]);
+    }
 #pragma unroll 1
     for (int t = 0; t < count; ++t) {
-        stage(t, r0, r3);
-        LDS_AS uint16_t *r = r0;
-        r0 = r1;
-        r1 = r2;
-        r2 = r3;
-        r3 = r;
+        stage(t, slot[0], slot[S::RING - 1]);
+        LDS_AS uint16_t *first = slot[0];
+#pragma unroll
+        for (int r = 0; r < S::RING - 1; ++r)
+            slot[r] = slot[r + 1];
+        slot[S::RING - 1] = first;
     }
     wait_vmcnt<0>();   // the loads past the end still write LDS
 }
 
 // Whether k may be cut over blocks: a grid of few tiles takes the small ones.
 template <class S>
-constexpr bool kDenseSplits = S::BM == kDenseSmall;
+constexpr bool kDenseSplits = S::BM == kDenseSmall && S::RING == 4;
 
-// Halves of a ring array: one stage of both operands.
-template <class S>
-constexpr int kDenseHalves = (S::BM + S::BN) * kDenseBK;
-
-// Tile `block` of a launch; r0 .. r3: its LDS ring.
+// Tile `block` of a launch.  The ring's slots are arrays apart: of loads into one
+// array the compiler waits for all before it reads any.
 template <int MODE, bool BF16, class S>
-MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *r0, LDS_AS uint16_t *r1,
-                         LDS_AS uint16_t *r2, LDS_AS uint16_t *r3)
+MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *const (&ring)[S::RING])
 {
     using T = DenseTile<MODE, BF16, S>;
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -488,16 +510,18 @@ MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *r0, LDS
     T t;
     t.w = w;
     t.kend = a.K;
-    t.nsk = (a.K + kDenseBK - 1) / kDenseBK;
-    const int s0 = split * a.per;
-    t.send = min(s0 + a.per, MODE == DENSE_DX ? 2 * t.nsk : t.nsk);
+    t.nsk = (a.K + S::BK - 1) / S::BK;
+    const int most = MODE == DENSE_DX ? 2 * t.nsk : t.nsk;
+    const int s0 = kDenseSplits<S> ? split * a.per : 0;
+    t.send = kDenseSplits<S> ? min(s0 + a.per, most) : most;
     const int ztensor = MODE == DENSE_DW ? z : 0;
     t.pr[0] = buf_rsrc(a.p[ztensor], a.pbytes);
     t.pr[1] = MODE == DENSE_DX ? buf_rsrc(a.p[1], a.pbytes) : t.pr[0];
     if constexpr (MODE == DENSE_GLU) {
-        // a wavefront's loads (16 tile rows each) all lie in one projection
-        static_assert(S::NW % 4 == 0, "projection of a wavefront's loads");
-        t.qr[0] = buf_rsrc(a.q[(w >> 1) & 1], a.qbytes);
+        // a wavefront's loads all lie in one projection: 32 rows next to each
+        // other, or 16 rows and those 16 NW further on
+        static_assert(S::BK == 64 ? 8 * T::OQ::kLoads == 32 : S::NW % 4 == 0, "projection of a wavefront's loads");
+        t.qr[0] = buf_rsrc(a.q[S::BK == 64 ? w & 1 : (w >> 1) & 1], a.qbytes);
         t.qr[1] = t.qr[0];
     } else {
         t.qr[0] = buf_rsrc(a.q[0], a.qbytes);
@@ -529,20 +553,16 @@ MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *r0, LDS
         for (int j = 0; j < S::NJ; ++j)
             acc[i][j] = (f32x4){};
     if constexpr (MODE == DENSE_LIN) {
-        // the adapters' share goes with the first k split
-        __shared__ AdapterJobs<S::BM> jobs;
-        t.run(s0, r0, r1, r2, r3, acc, [&]() __attribute__((always_inline)) {
-            if (split == 0) {
-                jobs.ids_of(a.lora, m0, a.M, tid);
-                __syncthreads();
-                if (w == 0)
-                    jobs.build(a.lora, l);
-            }
+        __shared__ AdapterJobs<S::BM, S::BK> jobs;
+        t.run(s0, ring, acc, [&]() __attribute__((always_inline)) {
+            jobs.ids_of(a.lora, m0, a.M, tid);
+            __syncthreads();
+            if (w == 0)
+                jobs.build(a.lora, split, a.splits, l);
         });
-        if (split == 0)
-            lora_expand<BF16, S>(a, m0, n0, tid, jobs, r0, r1, r2, r3, acc);
+        lora_expand<BF16, S>(a, m0, n0, tid, jobs, ring, acc);
     } else {
-        t.run(s0, r0, r1, r2, r3, acc, [] {});
+        t.run(s0, ring, acc, [] {});
     }
 
     if (kDenseSplits<S> && a.splits > 1) {
@@ -556,26 +576,37 @@ MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *r0, LDS
     }
     const int mw = m0 + wm * S::TM, nw = n0 + wn * ((kDenseCols<MODE, S>) / S::WN);
     __syncthreads();   // the ring is free
-    static_assert(S::NW * 4096 <= kDenseHalves<S> * 2, "a wavefront's share of the first ring array");
-    dense_store_all<MODE, BF16>(a, z, mw, nw, l, acc, (LDS_AS f32x4 *)r0 + 256 * w);
+    static_assert(S::NW * 4096 <= S::kHalves * 2, "a wavefront's share of the first ring array");
+    dense_store_all<MODE, BF16>(a, z, mw, nw, l, acc, (LDS_AS f32x4 *)ring[0] + 256 * w);
 }
 
 // The large products.  A tile of BM x BN reads BM + BN rows of each k for BM x BN
 // multiply-adds, so the larger the tile the less it asks of L2 and LDS: 256 x 256
-// (eight wavefronts of 128 x 64, 128 KiB of LDS, one block a CU) where they fill
-// the CUs, 128 x 128 (four of 64 x 64, two blocks a CU) below that.  Bound by the
-// matrix cores at the clock that their power allows (they are busy 57 to 71% of
-// the time; a loop of nothing else reaches 1.93 to 2.05 PFLOP/s on random data):
-// 4096 x 2048 bf16, forward 7168 tokens 199 us alone, 212 one after the other
-// (1.13 - 1.21 PFLOP/s); 16384 tokens with pre 474 us (1.16), dx 455 (1.21), dw
-// 400 (1.37); a library product of 8192^3: 1.55.
+// (eight wavefronts of 128 x 64, four stages of 32 k) where they fill the CUs, 128
+// x 128 (four of 64 x 64) below that, with four stages of 64 k where it has a CU to
+// itself and two where two share one.  A load of a 64-k stage takes eight whole
+// 128-byte pieces of rows; those of 32 k are twice as many, and where rows do not
+// begin on a 128-byte line they touch up to two lines each (198 tokens, 7528 x
+// 6144, 128 x 128 tiles: 130 us in four stages of 32 k, 95 in four of 64; 1024
+// tokens, 4096 x 2048: 37.5, 35.3).  256 x 256 tiles have no room for that: in two
+// stages of 64 k they wait for the loads (7168 tokens, 4096 x 2048: 197 -> 304).
+//
+// Bound by the matrix cores at the clock that their power allows (they are busy 57
+// to 71% of the time; a loop of nothing else reaches 1.93 to 2.05 PFLOP/s on
+// random data): 4096 x 2048 bf16, forward 7168 tokens 197 us alone, 212 one after
+// the other (1.13 - 1.22 PFLOP/s; 4104 x 2048: 257); 16384 tokens with pre 474 us
+// (1.16), dx 455 (1.21), dw 400 (1.37); a library product of 8192^3: 1.55.
 template <int MODE, bool BF16, class S>
 __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
 {
-    __shared__ __align__(1024) uint16_t ring0[kDenseHalves<S>], ring1[kDenseHalves<S>], ring2[kDenseHalves<S>],
-        ring3[kDenseHalves<S>];
-    dense_block<MODE, BF16, S>(a, blockIdx.x, (LDS_AS uint16_t *)ring0, (LDS_AS uint16_t *)ring1,
-                               (LDS_AS uint16_t *)ring2, (LDS_AS uint16_t *)ring3);
+    __shared__ __align__(1024) uint16_t r0[S::kHalves], r1[S::kHalves];
+    if constexpr (S::RING == 2) {
+        dense_block<MODE, BF16, S>(a, blockIdx.x, {(LDS_AS uint16_t *)r0, (LDS_AS uint16_t *)r1});
+    } else {
+        __shared__ __align__(1024) uint16_t r2[S::kHalves], r3[S::kHalves];
+        dense_block<MODE, BF16, S>(a, blockIdx.x, {(LDS_AS uint16_t *)r0, (LDS_AS uint16_t *)r1, (LDS_AS uint16_t *)r2,
+                                                   (LDS_AS uint16_t *)r3});
+    }
 }
 
 // Sum of the k splits' partial tiles, in split order, and the epilogue: block
@@ -632,6 +663,8 @@ hipError_t launch_dense_mode(bool bf16, const DenseArgs &a, hipStream_t s)
 {
     if (a.bm == kDenseLarge)
         return bf16 ? launch_dense_shape<MODE, true, LargeTile>(a, s) : launch_dense_shape<MODE, false, LargeTile>(a, s);
+    if (a.mt * a.nt * a.splits <= 256)
+        return bf16 ? launch_dense_shape<MODE, true, AloneTile>(a, s) : launch_dense_shape<MODE, false, AloneTile>(a, s);
     return bf16 ? launch_dense_shape<MODE, true, SmallTile>(a, s) : launch_dense_shape<MODE, false, SmallTile>(a, s);
 }
 

@@ -586,7 +586,7 @@ __global__ __launch_bounds__(256) void dense_grads_kernel(DenseArgs dx, DenseArg
 {
     constexpr int kPart = 2 * kTileHalves;   // two wavefronts' rings
     __shared__ __align__(1024) uint16_t a0[kPart], a1[kPart], b0[kPart], b1[kPart];
-    LDS_AS uint16_t *r[4] = {(LDS_AS uint16_t *)a0, (LDS_AS uint16_t *)a1, (LDS_AS uint16_t *)b0,
+    LDS_AS uint16_t *const r[4] = {(LDS_AS uint16_t *)a0, (LDS_AS uint16_t *)a1, (LDS_AS uint16_t *)b0,
                              (LDS_AS uint16_t *)b1};
     const int nx = dx.mt * dx.nt, nw = dw.mt * dw.nt, at = blockIdx.x;
     const bool is_dx = dw_first ? at >= nw : at < nx;
@@ -594,8 +594,8 @@ __global__ __launch_bounds__(256) void dense_grads_kernel(DenseArgs dx, DenseArg
     if (is_dx) {
         tile_block<DENSE_DX, BF16, 4>(dx, block, r[0], r[1], r[2], r[3]);
     } else if constexpr (WIDE) {
-        static_assert(SmallTile::NW == 4 && kDenseHalves<SmallTile> <= kPart, "the same threads and LDS");
-        dense_block<DENSE_DW, BF16, SmallTile>(dw, block, r[0], r[1], r[2], r[3]);
+        static_assert(AloneTile::NW == 4 && AloneTile::kHalves <= kPart, "the same threads and LDS");
+        dense_block<DENSE_DW, BF16, AloneTile>(dw, block, r);
     } else {
         tile_block<DENSE_DW, BF16, 4>(dw, block, r[0], r[1], r[2], r[3]);
     }
