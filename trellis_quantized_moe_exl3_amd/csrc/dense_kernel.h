@@ -114,7 +114,7 @@ MOE_DEV u32x4 pack8(f32x4 a, f32x4 b)
 // They pass through 4 KiB of LDS that only this wavefront uses (16-byte unit c
 // of row r in place c ^ r), so that eight lanes write the 128 bytes of a row
 // (GLU: four lanes 64) (2048 tokens, adapters alone, 4096 columns: tile kernel
-// 14.2 -> 12.2 us).
+// 14.2 -> 12.2 us; 10.6 since its stages are 64 ranks).
 template <int MODE, bool BF16, int ACT>
 MOE_DEV void dense_store(const DenseArgs &a, int z, int m0, int n0, int l, const f32x4 (&v)[4],
                          const u32x4 (&base)[2], LDS_AS f32x4 *lds)
@@ -591,11 +591,13 @@ MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *const (
 // tokens, 4096 x 2048: 37.5, 35.3).  256 x 256 tiles have no room for that: in two
 // stages of 64 k they wait for the loads (7168 tokens, 4096 x 2048: 197 -> 304).
 //
-// Bound by the matrix cores at the clock that their power allows (they are busy 57
-// to 71% of the time; a loop of nothing else reaches 1.93 to 2.05 PFLOP/s on
-// random data): 4096 x 2048 bf16, forward 7168 tokens 197 us alone, 212 one after
-// the other (1.13 - 1.22 PFLOP/s; 4104 x 2048: 257); 16384 tokens with pre 474 us
-// (1.16), dx 455 (1.21), dw 400 (1.37); a library product of 8192^3: 1.55.
+// The matrix cores are busy 62 to 71% of the CUs' time; the rest are waits at the
+// stages' barriers, first loads and epilogues, which no other block covers, and
+// rounds that do not come out even (448 tiles on 256 CUs: 1.75 as 2).  4096 x 2048
+// bf16, forward 7168 tokens 197 us alone, 212 one after the other (1.13 - 1.22
+// PFLOP/s; 4104 x 2048: 257); 16384 tokens with pre 470 us (1.17), dx 455 (1.21),
+// dw 405 (1.36).  The library's bare products of these sizes: 193, 367, 446 and
+// 490 us, and 1.55 PFLOP/s for 8192^3.
 template <int MODE, bool BF16, class S>
 __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
 {
