@@ -135,8 +135,8 @@ def test_glu_backward_refused(kw, code):
     (dict(x=None), M.ERR_INVALID_ARG), (dict(a=None), M.ERR_INVALID_ARG), (dict(b=None), M.ERR_INVALID_ARG),
     (dict(ids=None), M.ERR_INVALID_ARG), (dict(y=None), M.ERR_INVALID_ARG), (dict(null=True), M.ERR_INVALID_ARG),
     (dict(T=-1), M.ERR_INVALID_ARG), (dict(ldy=248), M.ERR_INVALID_ARG), (dict(base=DX, ldb=0), M.ERR_INVALID_ARG),
-    (dict(ids=PRE + 4), M.ERR_MISALIGNED), (dict(a=WU + 2), M.ERR_MISALIGNED), (dict(scales=DX + 4), M.ERR_MISALIGNED),
-    (dict(ranks=DX + 4), M.ERR_MISALIGNED), (dict(w=WG + 8), M.ERR_MISALIGNED), (dict(ldx=514), M.ERR_MISALIGNED),
+    (dict(ids=PRE + 2), M.ERR_MISALIGNED), (dict(a=WU + 2), M.ERR_MISALIGNED), (dict(scales=DX + 2), M.ERR_MISALIGNED),
+    (dict(ranks=DX + 1), M.ERR_MISALIGNED), (dict(w=WG + 8), M.ERR_MISALIGNED), (dict(ldx=514), M.ERR_MISALIGNED),
     (dict(ws=WS + 128), M.ERR_MISALIGNED), (dict(n=256), M.ERR_WORKSPACE), (dict(T=1 << 22), M.ERR_UNSUPPORTED),
     (dict(y=X), M.ERR_INVALID_ARG), (dict(y=WG), M.ERR_INVALID_ARG), (dict(y=WU + 64), M.ERR_INVALID_ARG),
     (dict(y=DWG), M.ERR_INVALID_ARG), (dict(y=PRE), M.ERR_INVALID_ARG),

@@ -208,6 +208,25 @@ def test_a_tokens_row_does_not_depend_on_its_neighbours(T, K, N):
     assert torch.equal(second, first[perm])
 
 
+@pytest.mark.parametrize("T", [1, 50, 333, 3000])
+def test_ids_scales_and_ranks_inside_longer_arrays(T):
+    # a chunk of a batch, one layer's rows of a table: any 4-byte alignment, and
+    # what stands around them takes no part
+    g = _gen(T + 11)
+    half = torch.float16
+    K, N, n, r = 72, 64, 5, 16
+    d = M.make_lora_desc(K, N, n, r, M.DT_F16)
+    x, w = R.gauss(g, (T, K), 1.0, half), R.gauss(g, (N, K), 0.1, half)
+    a, b = R.gauss(g, (n, r, K), 0.1, half), R.gauss(g, (n, N, r), 0.3, half)
+    ids, scales = _ids(g, T, n, "mixed"), torch.rand(n, generator=g, device="cuda") + 0.5
+    ranks = torch.randint(1, r + 1, (n,), generator=g, device="cuda").to(torch.int32)
+    want = _run(d, x, w, a, b, ids, None, scales, ranks, half)
+    for shift in (1, 2, 3):
+        inner = [torch.full((t.numel() + 8,), 2 ** 30, dtype=t.dtype, device="cuda")[shift:shift + t.numel()].copy_(t)
+                 for t in (ids, scales, ranks)]
+        assert torch.equal(_run(d, x, w, a, b, inner[0], None, inner[1], inner[2], half), want)
+
+
 def test_zero_tokens_and_workspace_reuse():
     g = _gen(5)
     dtype = torch.float16

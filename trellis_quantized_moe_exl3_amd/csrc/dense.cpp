@@ -509,9 +509,10 @@ int moe_exl3_lora_linear(const moe_exl3_lora_desc *desc, const void *x, int64_t 
             return rc;
     if (!rows_fit(T, K) || !rows_fit(T, N) || !rows_fit(T, kMaxRank))
         return MOE_EXL3_ERR_UNSUPPORTED;
-    for (const void *q : {adapters->a, adapters->b, (const void *)adapters->scales, (const void *)adapters->ranks,
-                          (const void *)ids})
-        if (!aligned16(q))
+    if (!aligned16(adapters->a) || !aligned16(adapters->b))
+        return MOE_EXL3_ERR_MISALIGNED;
+    for (const void *q : {(const void *)adapters->scales, (const void *)adapters->ranks, (const void *)ids})
+        if ((uintptr_t)q & 3u)
             return MOE_EXL3_ERR_MISALIGNED;
     if (overlap(my, mx) || overlap(my, mw) || (overlap(my, mb) && !(base == y && ldbase == ldy)) ||
         spans_meet(y, my.span(), adapters->a, 2 * n * r * K) || spans_meet(y, my.span(), adapters->b, 2 * n * r * N) ||

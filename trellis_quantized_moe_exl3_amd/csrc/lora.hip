@@ -10,21 +10,16 @@ template <int THREADS>
 MOE_DEV void check_adapters(const LoraArgs &lo, int T, int tid)
 {
     int bad = 0;
-    constexpr int kBatch = 4;   // 16-byte loads in flight a thread
-    const int quads = T / 4;
-    for (int t = tid; t < quads; t += kBatch * THREADS) {
-        u32x4 v[kBatch];
+    constexpr int kBatch = 8;   // loads in flight a thread
+    for (int t = tid; t < T; t += kBatch * THREADS) {
+        int id[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
-            v[b] = ((const u32x4 *)lo.ids)[min(t + b * THREADS, quads - 1)];
+            id[b] = lo.ids[min(t + b * THREADS, T - 1)];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-            for (int d = 0; d < 4; ++d)
-                bad |= id_faults(lo, (int)v[b][d]);
+            bad |= id_faults(lo, id[b]);
     }
-    for (int t = 4 * quads + tid; t < T; t += THREADS)
-        bad |= id_faults(lo, lo.ids[t]);
     const int index = __syncthreads_or(bad & (int)MOE_EXL3_STATUS_BAD_INDEX);
     const int width = __syncthreads_or(bad & (int)MOE_EXL3_STATUS_BAD_WIDTH);
     if (tid == 0)
