@@ -136,19 +136,21 @@ struct Stream {
     MOE_DEV void run(int first, int stride, LDS_AS uint16_t *r0, LDS_AS uint16_t *r1, LDS_AS uint16_t *r2,
                      LDS_AS uint16_t *r3, f32x4 (&acc)[NI][NJ])
     {
-        static_assert(RING >= 2 && RING <= 4, "ring arrays");
+        static_assert(RING >= 1 && RING <= 4, "ring arrays");
         const int shares = (TWO ? 2 : 1) * ((kend + 63) / 64);
         if (first >= shares)
             return;
         load(first, r0);
-        load(first + stride, r1);
+        if constexpr (RING >= 2)
+            load(first + stride, r1);
         if constexpr (RING >= 3)
             load(first + 2 * stride, r2);
         if constexpr (RING >= 4)
             load(first + 3 * stride, r3);
         for (int s = first; s < shares; s += RING * stride) {
             step(s + RING * stride, r0, acc);
-            step(s + (RING + 1) * stride, r1, acc);
+            if constexpr (RING >= 2)
+                step(s + (RING + 1) * stride, r1, acc);
             if constexpr (RING >= 3)
                 step(s + (RING + 2) * stride, r2, acc);
             if constexpr (RING >= 4)
@@ -425,8 +427,8 @@ hipError_t launch_skinny(const DenseArgs &a, hipStream_t s)
 // tokens' s_a x A_a^T to its own part of the sums.
 // mine, rank: the adapter of token m0 + l.
 template <bool BF16, int NW, class S>
-MOE_DEV void tile_expand(const DenseArgs &a, int mine, int rank, int m0, int n0, int w, int l, LDS_AS uint16_t *r0,
-                         LDS_AS uint16_t *r1, f32x4 (&acc)[4][4])
+MOE_DEV void tile_expand(const DenseArgs &a, int mine, int rank, int m0, int n0, int w, int l, LDS_AS uint16_t *slot,
+                         f32x4 (&acc)[4][4])
 {
     const LoraArgs &lo = a.lora;
     uint64_t left = __ballot(mine >= 0);
@@ -460,23 +462,24 @@ MOE_DEV void tile_expand(const DenseArgs &a, int mine, int rank, int m0, int n0,
             }
         }
     };
-    auto load = [&](LDS_AS uint16_t *slot) __attribute__((always_inline)) {
+    auto load = [&]() __attribute__((always_inline)) {
         st.kend = rk;   // 0 past the last: the loads read zeros
         st.q[0] = buf_rsrc(lo.b + (int64_t)max(e, 0) * a.N * lo.rank, (uint32_t)((int64_t)a.N * lo.rank * 2));
         st.q[1] = st.q[0];
         st.load(k0 / 64, slot);
     };
     next();
-    load(r0);
-    // the share in `slot` while the one after it loads into `other`
-    auto step = [&](LDS_AS uint16_t *slot, LDS_AS uint16_t *other) __attribute__((always_inline)) {
+    load();
+    while (e >= 0) {
         const int ce = e, crk = rk, ck = k0;
-        next();
-        load(other);
         __builtin_amdgcn_sched_barrier(0);
-        wait_vmcnt<S::kLoads>();
+        wait_vmcnt<0>();
         u32x4 pf[2][4], qf[2][4];
         S::fragments(slot, l, pf, qf);
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the slot is free
+        __builtin_amdgcn_sched_barrier(0);
+        next();
+        load();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             lora_cut(crk, ck + 32 * h, l, qf[h]);
@@ -484,28 +487,21 @@ MOE_DEV void tile_expand(const DenseArgs &a, int mine, int rank, int m0, int n0,
             for (int i = 0; i < 4; ++i)
                 lora_products<BF16>(id[i] == ce, pf[h][i], qf[h], acc[i]);
         }
-        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the slot is free
-    };
-    while (e >= 0) {
-        step(r0, r1);
-        if (e < 0)
-            break;
-        step(r1, r0);
     }
     wait_vmcnt<0>();   // the loads past the end still write LDS
 }
 
-// Tile `block` of a launch of NW wavefronts a block.  Its LDS: the first slot of
-// the lower half's rings in lo0, of the upper half's in hi0, the second slots in
-// lo1 and hi1.
+// Tile `block` of a launch of NW wavefronts a block; lo, hi: a slot of kTileHalves
+// for each of the lower and of the upper half of them, which holds one share at a
+// time: a share's fragments are all read before its products, which cover the
+// next one's loads.
 constexpr int kTileHalves = 16 * 8 * 64;   // of one share of both operands
 
 template <int MODE, bool BF16, int NW>
-MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *lo0, LDS_AS uint16_t *hi0,
-                        LDS_AS uint16_t *lo1, LDS_AS uint16_t *hi1)
+MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *lo, LDS_AS uint16_t *hi)
 {
     using TR = DenseTraits<MODE>;
-    using S = Stream<BF16, 4, 4, 2, TR::kPL, TR::kQL, MODE == DENSE_DX>;
+    using S = Stream<BF16, 4, 4, 1, TR::kPL, TR::kQL, MODE == DENSE_DX>;
     static_assert(S::kHalves == kTileHalves, "ring size");
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     constexpr int kCols = MODE == DENSE_GLU ? 32 : 64;
@@ -526,10 +522,7 @@ MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *lo0, LDS
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             acc[i][j] = (f32x4){};
-    constexpr int kLow = NW / 2;
-    const bool low = w < kLow;
-    LDS_AS uint16_t *r0 = low ? lo0 + w * S::kHalves : hi0 + (w - kLow) * S::kHalves;
-    LDS_AS uint16_t *r1 = low ? lo1 + w * S::kHalves : hi1 + (w - kLow) * S::kHalves;
+    LDS_AS uint16_t *slot = w < NW / 2 ? lo + w * S::kHalves : hi + (w - NW / 2) * S::kHalves;
     int mine = -1, rank = 0;
     if constexpr (MODE == DENSE_LIN)
         token_adapter(a.lora, m0 + l, a.M, mine, rank);
@@ -537,30 +530,34 @@ MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *lo0, LDS
         st.p2 = buf_rsrc(a.p[1], a.pbytes);
         st.q2 = buf_rsrc(a.q[1], a.qbytes);
     }
-    st.run(w, NW, r0, r1, nullptr, nullptr, acc);
+    st.run(w, NW, slot, nullptr, nullptr, nullptr, acc);
     if constexpr (MODE == DENSE_LIN)
-        tile_expand<BF16, NW, S>(a, mine, rank, m0, n0, w, l, r0, r1, acc);
-    // every wavefront's sums in its own first slot
+        tile_expand<BF16, NW, S>(a, mine, rank, m0, n0, w, l, slot, acc);
+    // every wavefront's sums in its own slot
     constexpr int kStep = S::kHalves / 8;
     static_assert(kStep >= 16 * 64, "sums fit a slot");
-    auto sums = [&](int s) { return (LDS_AS f32x4 *)(s < kLow ? lo0 : hi0) + (s % kLow) * kStep; };
+    auto sums = [&](int s) {
+        return s < NW / 2 ? (LDS_AS f32x4 *)lo + s * kStep : (LDS_AS f32x4 *)hi + (s - NW / 2) * kStep;
+    };
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            ((LDS_AS f32x4 *)r0)[(4 * i + j) * 64 + l] = acc[i][j];
+            ((LDS_AS f32x4 *)slot)[(4 * i + j) * 64 + l] = acc[i][j];
     __syncthreads();
-    for (int i = w; i < 4; i += NW) {
-        f32x4 v[1][4];
+    if (w >= 4)
+        return;
+    // wavefront i takes the rows i, and its scratch where only it has read
+    static_assert(NW >= 4, "a wavefront for each 16 rows");
+    f32x4 v[1][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[0][j] = sums(0)[(4 * i + j) * 64 + l];
+    for (int j = 0; j < 4; ++j) {
+        v[0][j] = sums(0)[(4 * w + j) * 64 + l];
 #pragma unroll
-            for (int s = 1; s < NW; ++s)
-                v[0][j] += sums(s)[(4 * i + j) * 64 + l];
-        }
-        dense_store_all<MODE, BF16>(a, z, m0 + 16 * i, n0, l, v, (LDS_AS f32x4 *)r1);
+        for (int s = 1; s < NW; ++s)
+            v[0][j] += sums(s)[(4 * w + j) * 64 + l];
     }
+    dense_store_all<MODE, BF16>(a, z, m0 + 16 * w, n0, l, v, sums(0) + 256 * w);
 }
 
 // Grids that 128 x 128 tiles would not fill.  The k of a 64 x 64 tile is cut over
@@ -569,12 +566,10 @@ MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *lo0, LDS
 // which bounds it (64 KiB into LDS and out of it for each 256 k).  333 tokens,
 // 1032 x 1384: 11 us (174 TFLOP/s); 512 tokens, 4096 x 2048: 25.5 us (674).
 template <int MODE, bool BF16, int NW>
-__global__ __launch_bounds__(64 * NW) void dense_tile_kernel(DenseArgs a)
+__global__ __launch_bounds__(64 * NW, 2) void dense_tile_kernel(DenseArgs a)
 {
-    __shared__ __align__(1024) uint16_t ring0[NW * kTileHalves], ring1[NW * kTileHalves];
-    LDS_AS uint16_t *r0 = (LDS_AS uint16_t *)ring0, *r1 = (LDS_AS uint16_t *)ring1;
-    constexpr int kHalf = NW / 2 * kTileHalves;
-    tile_block<MODE, BF16, NW>(a, blockIdx.x, r0, r0 + kHalf, r1, r1 + kHalf);
+    __shared__ __align__(1024) uint16_t lds[NW * kTileHalves];
+    tile_block<MODE, BF16, NW>(a, blockIdx.x, (LDS_AS uint16_t *)lds, (LDS_AS uint16_t *)lds + NW / 2 * kTileHalves);
 }
 
 // Both gradients in one launch: the tiles of dx (64 x 64) and those of dw, 64 x 64
@@ -582,22 +577,21 @@ __global__ __launch_bounds__(64 * NW) void dense_tile_kernel(DenseArgs a)
 // shorter ones fill what they leave (4000 tokens, 512 x 512, dw's twice as long:
 // 31.3 us behind dx's, 25.9 before them).
 template <bool BF16, bool WIDE>
-__global__ __launch_bounds__(256) void dense_grads_kernel(DenseArgs dx, DenseArgs dw, bool dw_first)
+__global__ __launch_bounds__(256, 2) void dense_grads_kernel(DenseArgs dx, DenseArgs dw, bool dw_first)
 {
-    constexpr int kPart = 2 * kTileHalves;   // two wavefronts' rings
-    __shared__ __align__(1024) uint16_t a0[kPart], a1[kPart], b0[kPart], b1[kPart];
-    LDS_AS uint16_t *const r[4] = {(LDS_AS uint16_t *)a0, (LDS_AS uint16_t *)a1, (LDS_AS uint16_t *)b0,
-                             (LDS_AS uint16_t *)b1};
+    static_assert(SmallTile::NW == 4 && SmallTile::RING == 2 && SmallTile::kHalves == 2 * kTileHalves,
+                  "the same threads and LDS");
+    __shared__ __align__(1024) uint16_t lds0[SmallTile::kHalves], lds1[SmallTile::kHalves];
+    LDS_AS uint16_t *r0 = (LDS_AS uint16_t *)lds0, *r1 = (LDS_AS uint16_t *)lds1;
     const int nx = dx.mt * dx.nt, nw = dw.mt * dw.nt, at = blockIdx.x;
     const bool is_dx = dw_first ? at >= nw : at < nx;
     const int block = dw_first == is_dx ? at - (is_dx ? nw : nx) : at;
     if (is_dx) {
-        tile_block<DENSE_DX, BF16, 4>(dx, block, r[0], r[1], r[2], r[3]);
+        tile_block<DENSE_DX, BF16, 4>(dx, block, r0, r1);
     } else if constexpr (WIDE) {
-        static_assert(AloneTile::NW == 4 && AloneTile::kHalves <= kPart, "the same threads and LDS");
-        dense_block<DENSE_DW, BF16, AloneTile>(dw, block, r);
+        dense_block<DENSE_DW, BF16, SmallTile>(dw, block, {r0, r1});
     } else {
-        tile_block<DENSE_DW, BF16, 4>(dw, block, r[0], r[1], r[2], r[3]);
+        tile_block<DENSE_DW, BF16, 4>(dw, block, r0, r1);
     }
 }
 
@@ -608,9 +602,9 @@ hipError_t launch_tile(const DenseArgs &a, hipStream_t s)
     // blocks of two wavefronts beyond
     const unsigned grid = (unsigned)(a.mt * a.nt);
     if (grid <= 256)
-        dense_tile_kernel<MODE, BF16, 4><<<grid, 256, 0, s>>>(a);
+        dense_tile_kernel<MODE, BF16, 8><<<grid, 512, 0, s>>>(a);
     else
-        dense_tile_kernel<MODE, BF16, 2><<<grid, 128, 0, s>>>(a);
+        dense_tile_kernel<MODE, BF16, 4><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
