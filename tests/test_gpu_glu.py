@@ -26,8 +26,9 @@ SHAPES = [(1, 256, 128), (1, 8, 8), (2, 264, 40), (7, 520, 136), (8, 4096, 2048)
           # dx in 64-row tiles of four and of two wavefronts with dw in 128- and
           # 256-row ones, both in 64-row tiles of one launch, the longer dw first
           (2000, 512, 1024), (333, 4096, 2048), (1000, 256, 256), (3000, 264, 136),
-          # dx in 128-row tiles, two on a CU
-          (2300, 2056, 264)]
+          # launches of their own: 128-row tiles of dx and dw, two on a CU; 64-row ones
+          # of dx with 256-row ones of dw
+          (2600, 2056, 1032), (100, 16384, 2048)]
 
 
 def _gen(seed):

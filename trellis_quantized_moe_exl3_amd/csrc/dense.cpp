@@ -201,18 +201,17 @@ double merged_sum(const Tiles &a, const Tiles &b)
     return ((double)(a.mt * a.nt) * a.us + (double)(b.mt * b.nt) * b.us) / 256;
 }
 
-// Both kinds of such blocks in one launch, one on each of the 256 CUs at a time:
-// the longest block or the sum over the CUs, and a fifth of the other for the
-// last blocks' uneven ends.  Whole steps, in one launch and in two, in us: 250
-// tokens, 2048 x 2048: 37.1, 42.1; 4000, 512 x 512: 42.3, 46.0; 1, 4096 x 2048:
-// 39.5, 41.3; but 8000, 256 x 1024: 88.3, 85.8; 16000, 256 x 256: 75.3, 53.8.
-// Beyond a sum of 25 us (the rounds are many, and each gradient fills the CUs by
-// itself) one launch has only lost: 500, 2056 x 2056: 75.6, 72.4; 4542, 1408 x
-// 1560: 225, 191.
+// Whether both kinds of such blocks take less time in one launch, two blocks on
+// a CU: three quarters of the sum, at least the longest block, which its
+// neighbour slows down.  Whole steps, in one launch and in two, in us: 250 tokens,
+// 2048 x 2048: 33.9, 41.5; 1908, 1000 x 1376: 68.0, 76.3; 30, 8192 x 2048: 55, 67;
+// but with long blocks 128, 1536 x 4096: 45, 43; 60, 1664 x 5816: 65, 57.  Beyond
+// a sum of 80 us each gradient fills the CUs by itself, in larger tiles: 3000
+// tokens, 2056 x 2056: 261, 236; 9000, 1024 x 1024: 200, 190.
 bool merge_pays(const Tiles &a, const Tiles &b, double apart)
 {
-    const double longest = std::max(a.us, b.us), sum = merged_sum(a, b);
-    return sum <= 25 && std::max(longest, sum) + 0.2 * std::min(longest, sum) < apart;
+    const double sum = merged_sum(a, b);
+    return sum <= 80 && std::max(1.3 * std::max(a.us, b.us), 0.75 * sum) < apart;
 }
 
 // Bytes of partial tiles that any launch of at most this size can need
@@ -458,8 +457,7 @@ int moe_exl3_glu_backward(const moe_exl3_glu_desc *desc, const void *x, int64_t 
     float *part = at<float>(workspace, p.part);
     const bool want_dx = dx && T > 0, want_dw = dw_gate;
     // Small gradients leave CUs idle on their own: their tiles share one launch,
-    // dx in 64 x 64 ones, dw in the better of two (509 tokens, 776 x 1304: 22.9 us
-    // with 64 x 64 tiles for both, 18.2 with 128 x 128 for dw).
+    // dx in 64 x 64 ones, dw in the better of two.
     // The choice is the same where only one is wanted, and so are its bits.
     const Tiles tx = plan_tiles(DENSE_DX, T, H, I), tw = plan_tiles(DENSE_DW, I, H, T);
     const Tiles sx = plan_fixed(DENSE_DX, T, H, I, kDenseTile);

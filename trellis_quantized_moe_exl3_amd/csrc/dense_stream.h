@@ -563,8 +563,11 @@ MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *lo, LDS_
 // Grids that 128 x 128 tiles would not fill.  The k of a 64 x 64 tile is cut over
 // the wavefronts, so that a block needs a barrier once and short rows of k still
 // keep every load in flight; the price is twice the LDS and L2 traffic a product,
-// which bounds it (64 KiB into LDS and out of it for each 256 k).  333 tokens,
-// 1032 x 1384: 11 us (174 TFLOP/s); 512 tokens, 4096 x 2048: 25.5 us (674).
+// which bounds it (64 KiB into LDS and out of it for each 256 k).  Eight wavefronts
+// where a block has its CU to itself, four where two share one (half of them with
+// two shares each in flight: 100 tokens, 1032 x 1384: 8.4 us a call, 7.6 like this;
+// 200 tokens, 2048 x 2048, 64 adapters: 50.6, 41.3).  333 tokens, 1032 x 1384: 10.5
+// us (181 TFLOP/s); 4096 x 2048: 24.6 (454).
 template <int MODE, bool BF16, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void dense_tile_kernel(DenseArgs a)
 {
@@ -573,9 +576,10 @@ __global__ __launch_bounds__(64 * NW, 2) void dense_tile_kernel(DenseArgs a)
 }
 
 // Both gradients in one launch: the tiles of dx (64 x 64) and those of dw, 64 x 64
-// or (WIDE) 128 x 128.  One block a CU; the longer blocks go first, so that the
-// shorter ones fill what they leave (4000 tokens, 512 x 512, dw's twice as long:
-// 31.3 us behind dx's, 25.9 before them).
+// or (WIDE) 128 x 128, two blocks on a CU.  The longer blocks go first, so that
+// the shorter ones fill what they leave (4000 tokens, 512 x 512, dw's twice as
+// long: 31.3 us behind dx's, 25.9 before them, when a CU held one).  Bound by
+// their number's uneven end and by L2: 509 tokens, 776 x 1304: 16.7 us.
 template <bool BF16, bool WIDE>
 __global__ __launch_bounds__(256, 2) void dense_grads_kernel(DenseArgs dx, DenseArgs dw, bool dw_first)
 {
@@ -598,8 +602,8 @@ __global__ __launch_bounds__(256, 2) void dense_grads_kernel(DenseArgs dx, Dense
 template <int MODE, bool BF16>
 hipError_t launch_tile(const DenseArgs &a, hipStream_t s)
 {
-    // four wavefronts and 128 KiB of LDS while that is one block a CU, two
-    // blocks of two wavefronts beyond
+    // eight wavefronts and 128 KiB of LDS while that is one block a CU, two
+    // blocks of four wavefronts beyond
     const unsigned grid = (unsigned)(a.mt * a.nt);
     if (grid <= 256)
         dense_tile_kernel<MODE, BF16, 8><<<grid, 512, 0, s>>>(a);
