@@ -14,7 +14,7 @@ constexpr int64_t kMaxSize = 65536;
 constexpr int64_t kMaxLd = 1 << 20;
 constexpr int64_t kSpanLimit = (int64_t)1 << 31;
 
-// k splits of the 128-tile: at most this many blocks (one a CU), each with at
+// k splits of 64 x 64 tiles: at most this many blocks (one a CU), each with at
 // least this many stages (256 k).
 constexpr int64_t kSplitBlocks = 256;
 constexpr int64_t kSplitStages = 4;
@@ -135,17 +135,16 @@ struct Tiles {
 //   128 x 128   4 + 0.48 (1024 tokens, 4096 x 2048: 35.7; 64 x 64 takes 52,
 //               256 x 256 73)
 //   256 x 256   10 + 1.40 (4096 tokens, 4096 x 2048: 104; 128 x 128 takes 114)
-// Few tiles with a long k are cut along k, at the price of partial tiles and a
-// second launch: 12 + 0.48 for 64 k + 0.1 a split, into as many as make that
-// least (100 tokens, 8192 x 256: 13.6, 64 x 64 takes 22; but 200 tokens, 2048 x
-// 1024: 18.0, 10.1 in 64 x 64).
+// Few 64 x 64 tiles with a long k are cut along k, at the price of partial tiles
+// and a second launch: 11 + 0.16 for 64 k + 0.1 a split, into as many as make that
+// least (calls of 100 tokens, 8192 x 256: 12.4, uncut 22; 4096 x 512: 11.4, uncut
+// 14.1; but 200 tokens, 2048 x 1024: 10.1 uncut).
 //
 // An adapter that a tile's tokens name costs 0.6 us for 64 ranks in a 128 x 128
-// tile, twice that in a 256 x 256 one; the splits share them, and so do the
-// wavefronts of a 64 x 64 tile (116 tokens, 62 adapters of 32, 1984 columns and no
-// projection: a call of 53 us in 128 x 128, 24 in 64 x 64).  Of n adapters a tile of bm
-// tokens is taken to name n bm / T and one more, the tokens of a request standing
-// together.
+// tile, twice that in a 256 x 256 one; the wavefronts of a 64 x 64 tile share them,
+// and so do its splits (116 tokens, 62 adapters of 32, 1984 columns, 840 k: a call
+// of 53 us in 128 x 128, 17 in 64 x 64).  Of n adapters a tile of bm tokens is taken
+// to name n bm / T and one more, the tokens of a request standing together.
 Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K, int64_t n = 0, int64_t rank = 0)
 {
     const int64_t stages = stages_of(mode, K);
@@ -168,10 +167,10 @@ Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K, int64_t n = 0, int64
     offer(kDenseLarge, 1, rounds(tiles_of(mode, M, N, kDenseLarge), 256) * (10 + 1.40 * s + l256));
     offer(kDenseSmall, 1, rounds(t128, 256) * (4 + 0.48 * s + l128));
     offer(kDenseTile, 1, t64 <= 256 ? 5 + 0.16 * s + l64 / 4 : rounds(t64, 512) * (5.4 + 0.34 * s + l64 / 2));
-    const int64_t most = t128 > 0 ? std::min(kSplitBlocks / t128, stages / kSplitStages) : 0;
-    const int64_t c = std::min(most, std::max<int64_t>(2, (int64_t)std::sqrt((0.48 * s + l128) / 0.1)));
+    const int64_t most = t64 > 0 ? std::min(kSplitBlocks / t64, stages / kSplitStages) : 0;
+    const int64_t c = std::min(most, std::max<int64_t>(2, (int64_t)std::sqrt((0.16 * s + l64) / 0.1)));
     if (c > 1)
-        offer(kDenseSmall, c, 12 + 0.48 * (double)cdiv(stages, c) + l128 / (double)c + 0.1 * (double)c);
+        offer(kDenseTile, c, 11 + 0.16 * (double)cdiv(stages, c) + l64 / (double)c + 0.1 * (double)c);
     Tiles t{};
     t.bm = bm;
     t.mt = (mode == DENSE_DW ? 2 : 1) * cdiv(M, bm);
@@ -218,11 +217,11 @@ bool merge_pays(const Tiles &a, const Tiles &b, double apart)
 // (tiles x splits never exceeds kSplitBlocks or tiles x stages / kSplitStages).
 size_t part_bound(int mode, int64_t M, int64_t N, int64_t K)
 {
-    const int64_t tiles = tiles_of(mode, M, N, kDenseSmall), most = stages_of(mode, K) / kSplitStages;
+    const int64_t tiles = tiles_of(mode, M, N, kDenseTile), most = stages_of(mode, K) / kSplitStages;
     if (most <= 1 || tiles == 0)
         return 0;
     const int64_t blocks = tiles > kSplitBlocks ? kSplitBlocks : std::min(kSplitBlocks, tiles * most);
-    return (size_t)blocks * kDenseSmall * kDenseSmall * sizeof(float);
+    return (size_t)blocks * kDenseTile * kDenseTile * sizeof(float);
 }
 
 void set_tiles(DenseArgs &a, const Tiles &t, void *part)

@@ -218,7 +218,7 @@ struct DenseTile {
     OP po;
     OQ qo;
     __amdgpu_buffer_rsrc_t pr[2], qr[2];
-    int w, nsk, send, kend;   // stages per segment, first stage past this block's share, K
+    int w, nsk, send, kend;   // stages per segment, all of them, K
     uint32_t pstep, qstep;
     uint32_t pbase, qbase;
 
@@ -295,15 +295,15 @@ struct DenseTile {
     }
     // `meanwhile` runs once, while the first loads are on their way.
     template <class F>
-    MOE_DEV void run(int s0, LDS_AS uint16_t *const (&ring)[S::RING], f32x4 (&acc)[NI][NJ], F meanwhile)
+    MOE_DEV void run(LDS_AS uint16_t *const (&ring)[S::RING], f32x4 (&acc)[NI][NJ], F meanwhile)
     {
-        if (s0 >= send) {
+        if (send == 0) {
             meanwhile();
             return;
         }
 #pragma unroll
         for (int r = 0; r < S::RING; ++r)
-            load(s0 + r, ring[r]);
+            load(r, ring[r]);
         meanwhile();
         __builtin_amdgcn_sched_barrier(0);
         wait_vmcnt<(S::RING - 1) * kLoads>();
@@ -311,7 +311,7 @@ struct DenseTile {
         Frags f0, f1;
         read(ring[0], 0, f0);
         constexpr bool kSwap = S::BK == 32;
-        for (int s = s0; s < send; s += S::RING)
+        for (int s = 0; s < send; s += S::RING)
 #pragma unroll
             for (int r = 0; r < S::RING; r += 2) {
                 stage(s + r, ring[r], ring[r + 1], f0, f1, acc);
@@ -367,11 +367,9 @@ struct AdapterJobs {
             id[tid] = e >= 0 && e < lo.n ? e : -1;
         }
     }
-    // One wavefront, the ids being visible: the list of this k split's share,
-    // adapters in the order of their first tokens.  Adapters go to the splits by
-    // their number, so that a token's sum is taken in the same order whatever its
-    // neighbours.
-    MOE_DEV void build(const LoraArgs &lo, int split, int splits, int l)
+    // One wavefront, the ids being visible: the list, adapters in the order of
+    // their first tokens.
+    MOE_DEV void build(const LoraArgs &lo, int l)
     {
         int n = 0;
         uint64_t left[BM / 64];
@@ -394,7 +392,7 @@ struct AdapterJobs {
 #pragma unroll
                 for (int h = g; h < BM / 64; ++h)
                     left[h] &= ~__ballot(mine[h] == e);
-                const int stages = e % splits == split ? (rk + BK - 1) / BK : 0;
+                const int stages = (rk + BK - 1) / BK;
                 if (l < stages)
                     job[n + l] = (uint32_t)e | (uint32_t)l << 16 | (uint32_t)rk << 20;
                 n += stages;
@@ -486,10 +484,6 @@ MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const Adap
     wait_vmcnt<0>();   // the loads past the end still write LDS
 }
 
-// Whether k may be cut over blocks: a grid of few tiles takes the small ones.
-template <class S>
-constexpr bool kDenseSplits = S::BM == kDenseSmall && S::RING == 4;
-
 // Tile `block` of a launch.  The ring's slots are arrays apart: of loads into one
 // array the compiler waits for all before it reads any.
 template <int MODE, bool BF16, class S>
@@ -498,10 +492,8 @@ MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *const (
     using T = DenseTile<MODE, BF16, S>;
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = w / S::WN, wn = w % S::WN;
-    const int tiles = a.mt * a.nt;
-    const int split = kDenseSplits<S> ? block / tiles : 0;
     int m, n;
-    dense_tile(block - split * tiles, tiles, a.mt, a.nt, m, n);
+    dense_tile(block, a.mt * a.nt, a.mt, a.nt, m, n);
     // DW: the row tiles of the second tensor follow those of the first
     const int half = MODE == DENSE_DW ? a.mt / 2 : a.mt;
     const int z = m >= half ? 1 : 0;
@@ -511,9 +503,7 @@ MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *const (
     t.w = w;
     t.kend = a.K;
     t.nsk = (a.K + S::BK - 1) / S::BK;
-    const int most = MODE == DENSE_DX ? 2 * t.nsk : t.nsk;
-    const int s0 = kDenseSplits<S> ? split * a.per : 0;
-    t.send = kDenseSplits<S> ? min(s0 + a.per, most) : most;
+    t.send = MODE == DENSE_DX ? 2 * t.nsk : t.nsk;
     const int ztensor = MODE == DENSE_DW ? z : 0;
     t.pr[0] = buf_rsrc(a.p[ztensor], a.pbytes);
     t.pr[1] = MODE == DENSE_DX ? buf_rsrc(a.p[1], a.pbytes) : t.pr[0];
@@ -554,26 +544,17 @@ MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *const (
             acc[i][j] = (f32x4){};
     if constexpr (MODE == DENSE_LIN) {
         __shared__ AdapterJobs<S::BM, S::BK> jobs;
-        t.run(s0, ring, acc, [&]() __attribute__((always_inline)) {
+        t.run(ring, acc, [&]() __attribute__((always_inline)) {
             jobs.ids_of(a.lora, m0, a.M, tid);
             __syncthreads();
             if (w == 0)
-                jobs.build(a.lora, split, a.splits, l);
+                jobs.build(a.lora, l);
         });
         lora_expand<BF16, S>(a, m0, n0, tid, jobs, ring, acc);
     } else {
-        t.run(s0, ring, acc, [] {});
+        t.run(ring, acc, [] {});
     }
 
-    if (kDenseSplits<S> && a.splits > 1) {
-        f32x4 *part = (f32x4 *)a.part + ((int64_t)block * S::NI * S::NJ) * (64 * S::NW) + tid;
-#pragma unroll
-        for (int i = 0; i < S::NI; ++i)
-#pragma unroll
-            for (int j = 0; j < S::NJ; ++j)
-                part[(i * S::NJ + j) * (64 * S::NW)] = acc[i][j];
-        return;
-    }
     const int mw = m0 + wm * S::TM, nw = n0 + wn * ((kDenseCols<MODE, S>) / S::WN);
     __syncthreads();   // the ring is free
     static_assert(S::NW * 4096 <= S::kHalves * 2, "a wavefront's share of the first ring array");
@@ -611,52 +592,10 @@ __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
     }
 }
 
-// Sum of the k splits' partial tiles, in split order, and the epilogue: block
-// (tile, w, i) finishes the 16-row block i of the tile's wavefront w.  Bound by
-// what one CU draws of the partial tiles, which come from behind the other XCDs'
-// L2, and by their latency: hence small blocks with eight splits in flight (32
-// splits of 4 tiles: 7.1 us; 13.4 with a block a tile row and one split after the
-// other).
-template <int MODE, bool BF16, class S>
-__global__ __launch_bounds__(64) void dense_finish_kernel(DenseArgs a)
-{
-    const int l = threadIdx.x, i = blockIdx.x % S::NI, w = blockIdx.x / S::NI % S::NW;
-    const int wm = w / S::WN, wn = w % S::WN;
-    const int tiles = a.mt * a.nt, L = blockIdx.x / (S::NI * S::NW);
-    int m, n;
-    dense_tile(L, tiles, a.mt, a.nt, m, n);
-    const int half = MODE == DENSE_DW ? a.mt / 2 : a.mt;
-    const int z = m >= half ? 1 : 0;
-    const int m0 = (m - z * half) * S::BM, n0 = n * (kDenseCols<MODE, S>);
-    const f32x4 *part = (const f32x4 *)a.part + ((int64_t)L * S::NI + i) * S::NJ * (64 * S::NW) + 64 * w + l;
-    const int64_t step = (int64_t)tiles * S::NI * S::NJ * (64 * S::NW);
-    f32x4 acc[1][S::NJ] = {};
-    constexpr int kBatch = 8;   // splits in flight
-    for (int k = 0; k < a.splits; k += kBatch) {
-        f32x4 v[kBatch][S::NJ];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-            for (int j = 0; j < S::NJ; ++j)
-                v[b][j] = part[min(k + b, a.splits - 1) * step + j * (64 * S::NW)];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-            for (int j = 0; j < S::NJ; ++j)
-                acc[0][j] += k + b < a.splits ? v[b][j] : (f32x4){};
-    }
-    const int mw = m0 + wm * S::TM + 16 * i, nw = n0 + wn * ((kDenseCols<MODE, S>) / S::WN);
-    __shared__ f32x4 lds[256];
-    dense_store_all<MODE, BF16>(a, z, mw, nw, l, acc, (LDS_AS f32x4 *)lds);
-}
-
 template <int MODE, bool BF16, class S>
 hipError_t launch_dense_shape(const DenseArgs &a, hipStream_t s)
 {
-    dense_kernel<MODE, BF16, S><<<(unsigned)(a.mt * a.nt * a.splits), 64 * S::NW, 0, s>>>(a);
-    if constexpr (kDenseSplits<S>)
-        if (a.splits > 1)
-            dense_finish_kernel<MODE, BF16, S><<<(unsigned)(a.mt * a.nt * S::NW * S::NI), 64, 0, s>>>(a);
+    dense_kernel<MODE, BF16, S><<<(unsigned)(a.mt * a.nt), 64 * S::NW, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -665,7 +604,7 @@ hipError_t launch_dense_mode(bool bf16, const DenseArgs &a, hipStream_t s)
 {
     if (a.bm == kDenseLarge)
         return bf16 ? launch_dense_shape<MODE, true, LargeTile>(a, s) : launch_dense_shape<MODE, false, LargeTile>(a, s);
-    if (a.mt * a.nt * a.splits <= 256)
+    if (a.mt * a.nt <= 256)
         return bf16 ? launch_dense_shape<MODE, true, AloneTile>(a, s) : launch_dense_shape<MODE, false, AloneTile>(a, s);
     return bf16 ? launch_dense_shape<MODE, true, SmallTile>(a, s) : launch_dense_shape<MODE, false, SmallTile>(a, s);
 }

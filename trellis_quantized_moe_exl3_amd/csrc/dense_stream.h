@@ -132,13 +132,14 @@ struct Stream {
                 for (int j = 0; j < NJ; ++j)
                     acc[i][j] = dense_mfma<BF16>(qf[h][j], pf[h][i], acc[i][j]);
     }
-    // Shares first, first + stride, .. of the operands.
-    MOE_DEV void run(int first, int stride, LDS_AS uint16_t *r0, LDS_AS uint16_t *r1, LDS_AS uint16_t *r2,
+    MOE_DEV int shares() const { return (TWO ? 2 : 1) * ((kend + 63) / 64); }
+    // Shares first, first + stride, .. below end of the operands.  (Loads past the
+    // operands read zeros; those past an earlier end are never multiplied: RING 1.)
+    MOE_DEV void run(int first, int stride, int end, LDS_AS uint16_t *r0, LDS_AS uint16_t *r1, LDS_AS uint16_t *r2,
                      LDS_AS uint16_t *r3, f32x4 (&acc)[NI][NJ])
     {
         static_assert(RING >= 1 && RING <= 4, "ring arrays");
-        const int shares = (TWO ? 2 : 1) * ((kend + 63) / 64);
-        if (first >= shares)
+        if (first >= end)
             return;
         load(first, r0);
         if constexpr (RING >= 2)
@@ -147,7 +148,7 @@ struct Stream {
             load(first + 2 * stride, r2);
         if constexpr (RING >= 4)
             load(first + 3 * stride, r3);
-        for (int s = first; s < shares; s += RING * stride) {
+        for (int s = first; s < end; s += RING * stride) {
             step(s + RING * stride, r0, acc);
             if constexpr (RING >= 2)
                 step(s + (RING + 1) * stride, r1, acc);
@@ -204,7 +205,7 @@ MOE_DEV void lora_rows(const LoraArgs &lo, int id, int rank, int r0, int l, int 
         st.q[0] = buf_rsrc(lo.a + (int64_t)e * lo.rank * K, (uint32_t)rk * (uint32_t)K * 2u);
         st.q[1] = st.q[0];
         f32x4 acc[1][NR] = {};
-        st.run(w, nw, ring0, ring1, ring2, ring3, acc);
+        st.run(w, nw, st.shares(), ring0, ring1, ring2, ring3, acc);
         if (mine)
 #pragma unroll
             for (int j = 0; j < NR; ++j)
@@ -359,7 +360,7 @@ __global__ __launch_bounds__(64 * (NW + XW)) void dense_skinny_kernel(DenseArgs 
             for (int j = 0; j < NJ; ++j)
                 acc[i][j] = (f32x4){};
         const int at = w * S::kHalves;
-        st.run(w, NW, (LDS_AS uint16_t *)ring0 + at, (LDS_AS uint16_t *)ring1 + at,
+        st.run(w, NW, st.shares(), (LDS_AS uint16_t *)ring0 + at, (LDS_AS uint16_t *)ring1 + at,
                (LDS_AS uint16_t *)ring2 + (RING >= 3 ? at : 0), (LDS_AS uint16_t *)ring3 + (RING == 4 ? at : 0), acc);
         // the sums of a wavefront in its own part of the first ring array, which
         // only it has used
@@ -422,13 +423,13 @@ hipError_t launch_skinny(const DenseArgs &a, hipStream_t s)
 // ---- 64 x 64 tiles: all modes, where larger tiles would leave CUs idle
 
 // The adapters' share of a 64 x 64 tile: the adapters that its tokens name are
-// dealt to the NW wavefronts by their number (so that a token's sum is taken in
-// the same order whatever its neighbours), each adding B_a's rows against the
+// dealt to the nw wavefronts of its blocks by their number (so that a token's sum
+// is taken in the same order whatever its neighbours), each adding B_a's rows against the
 // tokens' s_a x A_a^T to its own part of the sums.
 // mine, rank: the adapter of token m0 + l.
-template <bool BF16, int NW, class S>
-MOE_DEV void tile_expand(const DenseArgs &a, int mine, int rank, int m0, int n0, int w, int l, LDS_AS uint16_t *slot,
-                         f32x4 (&acc)[4][4])
+template <bool BF16, class S>
+MOE_DEV void tile_expand(const DenseArgs &a, int mine, int rank, int m0, int n0, int w, int nw, int l,
+                         LDS_AS uint16_t *slot, f32x4 (&acc)[4][4])
 {
     const LoraArgs &lo = a.lora;
     uint64_t left = __ballot(mine >= 0);
@@ -456,7 +457,7 @@ MOE_DEV void tile_expand(const DenseArgs &a, int mine, int rank, int m0, int n0,
             const int at = __ffsll((unsigned long long)left) - 1;
             const int id0 = __builtin_amdgcn_readlane(mine, at);
             left &= ~__ballot(mine == id0);
-            if (id0 % NW == w) {
+            if (id0 % nw == w) {
                 e = id0;
                 rk = __builtin_amdgcn_readlane(rank, at);
             }
@@ -497,6 +498,10 @@ MOE_DEV void tile_expand(const DenseArgs &a, int mine, int rank, int m0, int n0,
 // next one's loads.
 constexpr int kTileHalves = 16 * 8 * 64;   // of one share of both operands
 
+// Result columns of a tile.
+template <int MODE>
+constexpr int kTileCols = MODE == DENSE_GLU ? 32 : 64;
+
 template <int MODE, bool BF16, int NW>
 MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *lo, LDS_AS uint16_t *hi)
 {
@@ -504,12 +509,12 @@ MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *lo, LDS_
     using S = Stream<BF16, 4, 4, 1, TR::kPL, TR::kQL, MODE == DENSE_DX>;
     static_assert(S::kHalves == kTileHalves, "ring size");
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    constexpr int kCols = MODE == DENSE_GLU ? 32 : 64;
+    const int tiles = a.mt * a.nt, split = block / tiles;
     int m, n;
-    dense_tile(block, a.mt * a.nt, a.mt, a.nt, m, n);
+    dense_tile(block - split * tiles, tiles, a.mt, a.nt, m, n);
     const int half = MODE == DENSE_DW ? a.mt / 2 : a.mt;
     const int z = m >= half ? 1 : 0;
-    const int m0 = (m - z * half) * 64, n0 = n * kCols;
+    const int m0 = (m - z * half) * 64, n0 = n * kTileCols<MODE>;
     S st;
     st.p = buf_rsrc(a.p[MODE == DENSE_DW ? z : 0], a.pbytes);
     st.q[0] = buf_rsrc(a.q[0], a.qbytes);
@@ -530,9 +535,9 @@ MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *lo, LDS_
         st.p2 = buf_rsrc(a.p[1], a.pbytes);
         st.q2 = buf_rsrc(a.q[1], a.qbytes);
     }
-    st.run(w, NW, slot, nullptr, nullptr, nullptr, acc);
+    st.run(split * a.per + w, NW, min((split + 1) * a.per, st.shares()), slot, nullptr, nullptr, nullptr, acc);
     if constexpr (MODE == DENSE_LIN)
-        tile_expand<BF16, NW, S>(a, mine, rank, m0, n0, w, l, slot, acc);
+        tile_expand<BF16, S>(a, mine, rank, m0, n0, split * NW + w, a.splits * NW, l, slot, acc);
     // every wavefront's sums in its own slot
     constexpr int kStep = S::kHalves / 8;
     static_assert(kStep >= 16 * 64, "sums fit a slot");
@@ -557,6 +562,13 @@ MOE_DEV void tile_block(const DenseArgs &a, int block, LDS_AS uint16_t *lo, LDS_
         for (int s = 1; s < NW; ++s)
             v[0][j] += sums(s)[(4 * w + j) * 64 + l];
     }
+    if (a.splits > 1) {
+        f32x4 *part = (f32x4 *)a.part + (int64_t)block * (16 * 64) + (4 * w) * 64 + l;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            part[64 * j] = v[0][j];
+        return;
+    }
     dense_store_all<MODE, BF16>(a, z, m0 + 16 * w, n0, l, v, sums(0) + 256 * w);
 }
 
@@ -573,6 +585,40 @@ __global__ __launch_bounds__(64 * NW, 2) void dense_tile_kernel(DenseArgs a)
 {
     __shared__ __align__(1024) uint16_t lds[NW * kTileHalves];
     tile_block<MODE, BF16, NW>(a, blockIdx.x, (LDS_AS uint16_t *)lds, (LDS_AS uint16_t *)lds + NW / 2 * kTileHalves);
+}
+
+// Sum of the k splits' partial tiles, in split order, and the epilogue: block
+// (tile, i) finishes the 16 rows i.  Bound by what one CU draws of the partial
+// tiles, which come from behind the other XCDs' L2, and by their latency: hence
+// small blocks with eight splits in flight (32 splits of 16 tiles: 7.1 us; 13.4
+// with a block for four of these and one split after the other).
+template <int MODE, bool BF16>
+__global__ __launch_bounds__(64) void dense_finish_kernel(DenseArgs a)
+{
+    const int l = threadIdx.x, i = blockIdx.x & 3, tile = blockIdx.x >> 2, tiles = a.mt * a.nt;
+    int m, n;
+    dense_tile(tile, tiles, a.mt, a.nt, m, n);
+    const int half = MODE == DENSE_DW ? a.mt / 2 : a.mt;
+    const int z = m >= half ? 1 : 0;
+    const f32x4 *part = (const f32x4 *)a.part + (int64_t)tile * (16 * 64) + 4 * i * 64 + l;
+    const int64_t step = (int64_t)tiles * (16 * 64);
+    f32x4 acc[1][4] = {};
+    constexpr int kBatch = 8;   // splits in flight
+    for (int k = 0; k < a.splits; k += kBatch) {
+        f32x4 v[kBatch][4];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[b][j] = part[min(k + b, a.splits - 1) * step + 64 * j];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[0][j] += k + b < a.splits ? v[b][j] : (f32x4){};
+    }
+    __shared__ f32x4 lds[256];
+    dense_store_all<MODE, BF16>(a, z, (m - z * half) * 64 + 16 * i, n * kTileCols<MODE>, l, acc, (LDS_AS f32x4 *)lds);
 }
 
 // Both gradients in one launch: the tiles of dx (64 x 64) and those of dw, 64 x 64
@@ -604,11 +650,13 @@ hipError_t launch_tile(const DenseArgs &a, hipStream_t s)
 {
     // eight wavefronts and 128 KiB of LDS while that is one block a CU, two
     // blocks of four wavefronts beyond
-    const unsigned grid = (unsigned)(a.mt * a.nt);
+    const unsigned grid = (unsigned)(a.mt * a.nt * a.splits);
     if (grid <= 256)
         dense_tile_kernel<MODE, BF16, 8><<<grid, 512, 0, s>>>(a);
     else
         dense_tile_kernel<MODE, BF16, 4><<<grid, 256, 0, s>>>(a);
+    if (a.splits > 1)
+        dense_finish_kernel<MODE, BF16><<<4 * (unsigned)(a.mt * a.nt), 64, 0, s>>>(a);
     return hipGetLastError();
 }
 
