@@ -21,7 +21,9 @@ SHAPES = [(1, 256, 128, 1, 8), (1, 2048, 4096, 8, 16), (2, 8, 8, 3, 8), (7, 520,
           (1, 1032, 136, 4, 40),
           # 128-row tiles, two on a CU; adapters dealt to the k splits; many of them
           # in a tile without much of a projection
-          (1300, 264, 4096, 6, 104), (89, 5008, 1008, 12, 96), (116, 40, 1984, 62, 32)]
+          (1300, 264, 4096, 6, 104), (89, 5008, 1008, 12, 96), (116, 40, 1984, 62, 32),
+          # 8 tokens a shrink block
+          (300, 4104, 264, 3, 128)]
 
 
 def _gen(seed):

@@ -30,7 +30,7 @@ MOE_DEV void check_adapters(const LoraArgs &lo, int T, int tid)
 // product; zeros from the adapter's own rank on.  Tokens without an adapter are
 // not written.
 //
-// Block (f, r): `tpf` tokens (1 or 16) against 16 NR rows of their adapters, k
+// Block (f, r): `tpf` tokens (1, 8 or 16) against 16 NR rows of their adapters, k
 // cut over the NW wavefronts.  Tokens are the matrix instruction's columns, so
 // a 16-token block that names several adapters runs once per adapter and each
 // token keeps its own result.  One token a block lets all the adapters of a
@@ -100,13 +100,18 @@ static void shrink(const uint16_t *x, int64_t ldx, uint32_t xbytes, int T, int K
         else
             lora_shrink_kernel<BF16, 4, 1, 4><<<grid, 256, 0, s>>>(x, ldx, xbytes, T, K, 1, l);
     } else {
-        const dim3 grid((unsigned)((T + 15) / 16 + 1), (unsigned)(l.rpad / 32));
+        // 8 tokens a block where 16 would leave most CUs idle (whole calls with 8
+        // and with 16: 300 tokens, 4096 k, 64 adapters of 128: 72 us, 78; 732
+        // tokens, 6696 k, rank 48: 43.5, 47.4; but 1000 tokens, 4096 k, 64 adapters
+        // of 64: 32, 28)
+        const int tpf = (int64_t)((T + 15) / 16) * (l.rpad / 32) <= 96 ? 8 : 16;
+        const dim3 grid((unsigned)((T + tpf - 1) / tpf + 1), (unsigned)(l.rpad / 32));
         // eight wavefronts a block while that is one block a CU (144 KiB of
         // LDS), four and two blocks beyond
         if ((int64_t)(grid.x - 1) * grid.y <= 256)
-            lora_shrink_kernel<BF16, 8, 2, 3><<<grid, 512, 0, s>>>(x, ldx, xbytes, T, K, 16, l);
+            lora_shrink_kernel<BF16, 8, 2, 3><<<grid, 512, 0, s>>>(x, ldx, xbytes, T, K, tpf, l);
         else
-            lora_shrink_kernel<BF16, 4, 2, 3><<<grid, 256, 0, s>>>(x, ldx, xbytes, T, K, 16, l);
+            lora_shrink_kernel<BF16, 4, 2, 3><<<grid, 256, 0, s>>>(x, ldx, xbytes, T, K, tpf, l);
     }
 }
 
