@@ -1,6 +1,8 @@
 // The tile kernel of the dense operators and its epilogues (see DenseMode).
 #pragma once
 
+#include <type_traits>
+
 #include "dense_gemm.h"
 
 namespace moe {
@@ -207,6 +209,38 @@ struct DenseFrags {
     u32x4 p[S::NI], q[S::NJ];
 };
 
+template <bool BF16, class S>
+MOE_DEV void multiply(const DenseFrags<S> &f, f32x4 (&acc)[S::NI][S::NJ])
+{
+#pragma unroll
+    for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+        for (int j = 0; j < S::NJ; ++j)
+            acc[i][j] = dense_mfma<BF16>(f.q[j], f.p[i], acc[i][j]);
+}
+
+// The order of 32 k: the next fragments' reads and L loads spread over the
+// MFMAs, early enough that the next wait finds them done (1024 tokens, 4096 x 2048:
+// see dense_kernel).  The transposing reads' two halves a fragment leave no
+// registers for it: there the same order spills and halves the rate.
+template <int MODE, class S, int L>
+MOE_DEV void spread()
+{
+    if constexpr (DenseTraits<MODE>::kPL == KC && DenseTraits<MODE>::kQL == KC) {
+        constexpr int kPer = S::NI * S::NJ / (S::NI + S::NJ + L);
+#pragma unroll
+        for (int r = 0; r < S::NI + S::NJ; ++r) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
+        }
+#pragma unroll
+        for (int r = 0; r < L; ++r) {
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
+        }
+    }
+}
+
 template <int MODE, bool BF16, class S>
 struct DenseTile {
     static constexpr int NI = S::NI, NJ = S::NJ;
@@ -215,6 +249,7 @@ struct DenseTile {
     using OP = Operand<S::BM, TR::kPL, S::NW, S::BK>;
     using OQ = Operand<S::BN, TR::kQL, S::NW, S::BK>;
     static constexpr int kLoads = OP::kLoads + OQ::kLoads;
+    static constexpr int kRing = S::RING, kStep = S::BK, kPer = 1;
     OP po;
     OQ qo;
     __amdgpu_buffer_rsrc_t pr[2], qr[2];
@@ -239,35 +274,6 @@ struct DenseTile {
         for (int j = 0; j < S::NJ; ++j)
             f.q[j] = OQ::frag(ring + S::BM * S::BK, qbase, j, h);
     }
-    MOE_DEV void multiply(const Frags &f, f32x4 (&acc)[NI][NJ])
-    {
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                acc[i][j] = dense_mfma<BF16>(f.q[j], f.p[i], acc[i][j]);
-    }
-    // The order of 32 k: the next fragments' reads and L loads spread over the
-    // MFMAs, early enough that the next wait finds them done (7168 tokens, 4096 x
-    // 2048: 213 -> 207 us).  The transposing reads' two halves a fragment leave
-    // no registers for it: there the same order spills and halves the rate.
-    template <int L>
-    MOE_DEV static void spread()
-    {
-        if constexpr (TR::kPL == KC && TR::kQL == KC) {
-            constexpr int kPer = NI * NJ / (NI + NJ + L);
-#pragma unroll
-            for (int r = 0; r < NI + NJ; ++r) {
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
-            }
-#pragma unroll
-            for (int r = 0; r < L; ++r) {
-                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
-            }
-        }
-    }
     // Stage s in ring slot `cur`, whose first fragments f0 were read during stage
     // s - 1; f0 and f1 change places from one 32 k to the next.  "At most RING - 2
     // stages' loads outstanding" (s + 2 .. s + RING - 1) proves that this
@@ -279,8 +285,8 @@ struct DenseTile {
     {
         if constexpr (S::BK == 64) {
             read(cur, 1, f1);
-            multiply(f0, acc);
-            spread<0>();
+            multiply<BF16, S>(f0, acc);
+            spread<MODE, S, 0>();
         }
         Frags &last = S::BK == 64 ? f1 : f0, &first = S::BK == 64 ? f0 : f1;
         __builtin_amdgcn_sched_barrier(0);
@@ -290,8 +296,8 @@ struct DenseTile {
         __builtin_amdgcn_sched_barrier(0);
         load(s + S::RING, cur);
         read(next, 0, first);
-        multiply(last, acc);
-        spread<kLoads>();
+        multiply<BF16, S>(last, acc);
+        spread<MODE, S, kLoads>();
     }
     // `meanwhile` runs once, while the first loads are on their way.
     template <class F>
@@ -320,6 +326,113 @@ struct DenseTile {
         wait_vmcnt<0>();   // the loads past the end still write LDS
     }
 };
+
+// The same for 256 x 256 tiles whose P is KC: P in two stages of 64 k (whole
+// lines, see dense_kernel), Q in four of 32.
+template <int MODE, bool BF16, class S>
+struct PairTile {
+    static constexpr int NI = S::NI, NJ = S::NJ, kRing = 6;   // slots: P's two, then Q's four
+    static constexpr int kPHalves = S::BM * 64, kQHalves = S::BN * 32;
+    static constexpr int kStep = 32, kPer = 2;   // k of a stage; stages come in pairs
+    using Frags = DenseFrags<S>;
+    using TR = DenseTraits<MODE>;
+    using OP = Operand<S::BM, KC, S::NW, 64>;
+    using OQ = Operand<S::BN, TR::kQL, S::NW, 32>;
+    OP po;
+    OQ qo;
+    __amdgpu_buffer_rsrc_t pr[2], qr[2];
+    int w, nsk, send, kend;   // stages per segment (even), all of them, K
+    uint32_t pstep, qstep;
+    uint32_t pbase, qbase;
+
+    // Stages s and s + 1, s even, of P; stage s of Q.
+    MOE_DEV void load_p(int s, LDS_AS uint16_t *slot)
+    {
+        const bool second = MODE == DENSE_DX && s >= nsk;
+        po.issue(second ? pr[1] : pr[0], slot, w, 32 * (second ? s - nsk : s), s < send ? kend : 0, pstep);
+    }
+    MOE_DEV void load_q(int s, LDS_AS uint16_t *slot)
+    {
+        const bool second = MODE == DENSE_DX && s >= nsk;
+        qo.issue(second ? qr[1] : qr[0], slot, w, 32 * (second ? s - nsk : s), s < send ? kend : 0, qstep);
+    }
+    MOE_DEV void read(const LDS_AS uint16_t *p, int h, const LDS_AS uint16_t *q, Frags &f)
+    {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            f.p[i] = OP::frag(p, pbase, i, h);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            f.q[j] = OQ::frag(q, qbase, j, 0);
+    }
+    // Stage s, R = s % 4, whose fragments f were read during stage s - 1.  Odd
+    // stages load P for s + 3 and s + 4, every stage then Q for s + 4: younger than
+    // the loads of stage s + 1 are those of Q for s + 2 and s + 3, and in even
+    // stages of P for s + 2.  Past the barrier every wavefront has read stage s:
+    // Q's slot is free, and in odd stages P's.
+    template <int R>
+    MOE_DEV void stage(int s, LDS_AS uint16_t *const (&ring)[kRing], const Frags &f, Frags &fn, f32x4 (&acc)[NI][NJ])
+    {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+        wait_vmcnt<R & 1 ? 2 * OQ::kLoads : OP::kLoads + 2 * OQ::kLoads>();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (R & 1)
+            load_p(s + 3, ring[R / 2 % 2]);
+        load_q(s + 4, ring[2 + R % 4]);
+        read(ring[(R + 1) / 2 % 2], (R + 1) & 1, ring[2 + (R + 1) % 4], fn);
+        multiply<BF16, S>(f, acc);
+        if constexpr (TR::kQL == KC) {
+            // the loads between the first MFMAs, the reads between the others
+            // (7168 tokens, 4096 x 2048: 196.7 -> 193.7 us); reads before loads
+            // leave too many fragments in registers and spill (237)
+#pragma unroll
+            for (int r = 0; r < OQ::kLoads + (R & 1) * OP::kLoads; ++r) {
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            }
+#pragma unroll
+            for (int r = 0; r < NI + NJ; ++r) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+            }
+        }
+    }
+    template <class F>
+    MOE_DEV void run(LDS_AS uint16_t *const (&ring)[kRing], f32x4 (&acc)[NI][NJ], F meanwhile)
+    {
+        if (send == 0) {
+            meanwhile();
+            return;
+        }
+        load_q(0, ring[2]);
+        load_p(0, ring[0]);
+        load_q(1, ring[3]);
+        load_q(2, ring[4]);
+        load_p(2, ring[1]);
+        load_q(3, ring[5]);
+        meanwhile();
+        __builtin_amdgcn_sched_barrier(0);
+        wait_vmcnt<OP::kLoads + 3 * OQ::kLoads>();
+        __builtin_amdgcn_s_barrier();
+        Frags f0, f1;
+        read(ring[0], 0, ring[2], f0);
+        for (int s = 0; s < send; s += 4) {
+            stage<0>(s, ring, f0, f1, acc);
+            stage<1>(s + 1, ring, f1, f0, acc);
+            stage<2>(s + 2, ring, f0, f1, acc);
+            stage<3>(s + 3, ring, f1, f0, acc);
+        }
+        wait_vmcnt<0>();   // the loads past the end still write LDS
+    }
+};
+
+template <int MODE, class S>
+constexpr bool kPairs = S::BM == kDenseLarge && DenseTraits<MODE>::kPL == KC;
+
+template <int MODE, bool BF16, class S>
+using TileOf = std::conditional_t<kPairs<MODE, S>, PairTile<MODE, BF16, S>, DenseTile<MODE, BF16, S>>;
 
 // B_a's rows for 32 ranks from k0 on, without what follows the adapter's own
 // rank inside an octet (whole octets past it were read as zeros).
@@ -406,9 +519,10 @@ struct AdapterJobs {
 // of the k loop, one for every BK ranks of every adapter that a token of the
 // tile names, P = the tokens' s_a x A_a^T, Q = B_a's rows, through the same
 // ring.
-template <bool BF16, class S>
+template <bool BF16, class S, int RING>
 MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const AdapterJobs<S::BM, S::BK> &jobs,
-                         LDS_AS uint16_t *const (&ring)[S::RING], f32x4 (&acc)[S::NI][S::NJ])
+                         LDS_AS uint16_t *const (&pring)[RING], LDS_AS uint16_t *const (&qring)[RING],
+                         f32x4 (&acc)[S::NI][S::NJ])
 {
     using OP = Operand<S::BM, KC, S::NW, S::BK>;
     using OQ = Operand<S::BN, KC, S::NW, S::BK>;
@@ -432,18 +546,27 @@ MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const Adap
     auto job_of = [&](int t) __attribute__((always_inline)) {
         return (uint32_t)__builtin_amdgcn_readfirstlane((int)jobs.job[min(t, count - 1)]);
     };
-    auto load = [&](int t, LDS_AS uint16_t *slot) __attribute__((always_inline)) {
+    auto load = [&](int t, LDS_AS uint16_t *pslot, LDS_AS uint16_t *qslot) __attribute__((always_inline)) {
         const uint32_t job = job_of(t);
         const int e = job & 0xFFFF, k0 = S::BK * ((job >> 16) & 15), rk = t < count ? (int)(job >> 20) : 0;
-        po.issue(pr, slot, w, k0, rk, 2);
-        qo.issue(buf_rsrc(lo.b + (int64_t)e * a.N * lo.rank, bbytes), slot + S::BM * S::BK, w, k0, rk, 2);
+        po.issue(pr, pslot, w, k0, rk, 2);
+        qo.issue(buf_rsrc(lo.b + (int64_t)e * a.N * lo.rank, bbytes), qslot, w, k0, rk, 2);
     };
-    auto stage = [&](int t, const LDS_AS uint16_t *cur, LDS_AS uint16_t *refill) __attribute__((always_inline)) {
+    LDS_AS uint16_t *ps[RING], *qs[RING];   // slots of stages t, t + 1, ..
+#pragma unroll
+    for (int r = 0; r < RING; ++r) {
+        ps[r] = pring[r];
+        qs[r] = qring[r];
+        if (r < RING - 1)
+            load(r, ps[r], qs[r]);
+    }
+#pragma unroll 1
+    for (int t = 0; t < count; ++t) {
         __builtin_amdgcn_sched_barrier(0);
-        wait_vmcnt<(S::RING - 2) * kLoads>();   // the stages after t stay in flight
+        wait_vmcnt<(RING - 2) * kLoads>();   // the stages after t stay in flight
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        load(t + S::RING - 1, refill);
+        load(t + RING - 1, ps[RING - 1], qs[RING - 1]);
         const uint32_t job = job_of(t);
         const int e = job & 0xFFFF, k0 = S::BK * ((job >> 16) & 15), rk = job >> 20;
 #pragma unroll
@@ -453,33 +576,25 @@ MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const Adap
             u32x4 q[S::NJ];
 #pragma unroll
             for (int j = 0; j < S::NJ; ++j)
-                q[j] = OQ::frag(cur + S::BM * S::BK, qbase, j, h);
+                q[j] = OQ::frag(qs[0], qbase, j, h);
             lora_cut(rk, k0 + 32 * h, l, q);
 #pragma unroll
             for (int i = 0; i < S::NI; i += 2) {
-                const u32x4 p0 = OP::frag(cur, pbase, i, h), p1 = OP::frag(cur, pbase, i + 1, h);
+                const u32x4 p0 = OP::frag(ps[0], pbase, i, h), p1 = OP::frag(ps[0], pbase, i + 1, h);
                 lora_products<BF16>(ids[16 * i] == e, p0, q, acc[i]);
                 lora_products<BF16>(ids[16 * i + 16] == e, p1, q, acc[i + 1]);
                 __builtin_amdgcn_sched_barrier(0);   // fragments of two blocks at a time: registers
             }
         }
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): reads done before the next barrier
-    };
-    LDS_AS uint16_t *slot[S::RING];
+        LDS_AS uint16_t *p0 = ps[0], *q0 = qs[0];
 #pragma unroll
-    for (int r = 0; r < S::RING; ++r) {
-        slot[r] = ring[r];
-        if (r < S::RING - 1)
-            load(r, slot[r]);
-    }
-#pragma unroll 1
-    for (int t = 0; t < count; ++t) {
-        stage(t, slot[0], slot[S::RING - 1]);
-        LDS_AS uint16_t *first = slot[0];
-#pragma unroll
-        for (int r = 0; r < S::RING - 1; ++r)
-            slot[r] = slot[r + 1];
-        slot[S::RING - 1] = first;
+        for (int r = 0; r < RING - 1; ++r) {
+            ps[r] = ps[r + 1];
+            qs[r] = qs[r + 1];
+        }
+        ps[RING - 1] = p0;
+        qs[RING - 1] = q0;
     }
     wait_vmcnt<0>();   // the loads past the end still write LDS
 }
@@ -487,9 +602,9 @@ MOE_DEV void lora_expand(const DenseArgs &a, int m0, int n0, int tid, const Adap
 // Tile `block` of a launch.  The ring's slots are arrays apart: of loads into one
 // array the compiler waits for all before it reads any.
 template <int MODE, bool BF16, class S>
-MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *const (&ring)[S::RING])
+MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *const (&ring)[TileOf<MODE, BF16, S>::kRing])
 {
-    using T = DenseTile<MODE, BF16, S>;
+    using T = TileOf<MODE, BF16, S>;
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = w / S::WN, wn = w % S::WN;
     int m, n;
@@ -502,7 +617,7 @@ MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *const (
     T t;
     t.w = w;
     t.kend = a.K;
-    t.nsk = (a.K + S::BK - 1) / S::BK;
+    t.nsk = (a.K + T::kStep * T::kPer - 1) / (T::kStep * T::kPer) * T::kPer;
     t.send = MODE == DENSE_DX ? 2 * t.nsk : t.nsk;
     const int ztensor = MODE == DENSE_DW ? z : 0;
     t.pr[0] = buf_rsrc(a.p[ztensor], a.pbytes);
@@ -550,7 +665,15 @@ MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *const (
             if (w == 0)
                 jobs.build(a.lora, l);
         });
-        lora_expand<BF16, S>(a, m0, n0, tid, jobs, ring, acc);
+        if constexpr (kPairs<MODE, S>) {
+            lora_expand<BF16, S, 2>(a, m0, n0, tid, jobs, {ring[0], ring[1]}, {ring[2], ring[3]}, acc);
+        } else {
+            LDS_AS uint16_t *qring[S::RING];
+#pragma unroll
+            for (int r = 0; r < S::RING; ++r)
+                qring[r] = ring[r] + S::BM * S::BK;
+            lora_expand<BF16, S, S::RING>(a, m0, n0, tid, jobs, ring, qring, acc);
+        }
     } else {
         t.run(ring, acc, [] {});
     }
@@ -563,32 +686,42 @@ MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *const (
 
 // The large products.  A tile of BM x BN reads BM + BN rows of each k for BM x BN
 // multiply-adds, so the larger the tile the less it asks of L2 and LDS: 256 x 256
-// (eight wavefronts of 128 x 64, four stages of 32 k) where they fill the CUs, 128
-// x 128 (four of 64 x 64) below that, with four stages of 64 k where it has a CU to
-// itself and two where two share one.  A load of a 64-k stage takes eight whole
-// 128-byte pieces of rows; those of 32 k are twice as many, and where rows do not
-// begin on a 128-byte line they touch up to two lines each (198 tokens, 7528 x
-// 6144, 128 x 128 tiles: 130 us in four stages of 32 k, 95 in four of 64; 1024
-// tokens, 4096 x 2048: 37.5, 35.3).  256 x 256 tiles have no room for that: in two
-// stages of 64 k they wait for the loads (7168 tokens, 4096 x 2048: 197 -> 304).
+// (eight wavefronts of 128 x 64) where they fill the CUs, 128 x 128 (four of 64 x
+// 64) below that, with four stages of 64 k where it has a CU to itself and two
+// where two share one.  A load of a 64-k stage takes eight whole 128-byte pieces
+// of rows; those of 32 k are twice as many, and where rows do not begin on a
+// 128-byte line they touch up to two lines each (198 tokens, 7528 x 6144, 128 x 128
+// tiles: 130 us in four stages of 32 k, 95 in four of 64; 1024 tokens, 4096 x 2048:
+// 37.5, 35.3).  256 x 256 tiles have room for one operand's: x or dg in two stages
+// of 64 k, the weights in four of 32 (7168 tokens, 4104 x 2048: 255 us with both in
+// 32, 223; 4096 x 2048: 197, 194; with both in two of 64 they wait for the loads:
+// 304).  The gradients of the weights read both operands along their rows.
 //
 // The matrix cores are busy 62 to 71% of the CUs' time; the rest are waits at the
 // stages' barriers, first loads and epilogues, which no other block covers, and
 // rounds that do not come out even (448 tiles on 256 CUs: 1.75 as 2).  4096 x 2048
-// bf16, forward 7168 tokens 197 us alone, 212 one after the other (1.13 - 1.22
-// PFLOP/s; 4104 x 2048: 257); 16384 tokens with pre 470 us (1.17), dx 455 (1.21),
-// dw 405 (1.36).  The library's bare products of these sizes: 193, 367, 446 and
-// 490 us, and 1.55 PFLOP/s for 8192^3.
+// bf16, forward 7168 tokens 194 us (1.24 PFLOP/s; 4104 x 2048: 223); 16384 tokens
+// with pre 460 us (1.20), dx 435 (1.26), dw 400 (1.37).  The library's bare products
+// of these sizes: 193, 367, 446 and 490 us, and 1.55 PFLOP/s for 8192^3.
 template <int MODE, bool BF16, class S>
 __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
 {
-    __shared__ __align__(1024) uint16_t r0[S::kHalves], r1[S::kHalves];
-    if constexpr (S::RING == 2) {
-        dense_block<MODE, BF16, S>(a, blockIdx.x, {(LDS_AS uint16_t *)r0, (LDS_AS uint16_t *)r1});
+    if constexpr (kPairs<MODE, S>) {
+        using T = TileOf<MODE, BF16, S>;
+        __shared__ __align__(1024) uint16_t p0[T::kPHalves], p1[T::kPHalves];
+        __shared__ __align__(1024) uint16_t q0[T::kQHalves], q1[T::kQHalves], q2[T::kQHalves], q3[T::kQHalves];
+        dense_block<MODE, BF16, S>(a, blockIdx.x, {(LDS_AS uint16_t *)p0, (LDS_AS uint16_t *)p1,
+                                                   (LDS_AS uint16_t *)q0, (LDS_AS uint16_t *)q1, (LDS_AS uint16_t *)q2,
+                                                   (LDS_AS uint16_t *)q3});
     } else {
-        __shared__ __align__(1024) uint16_t r2[S::kHalves], r3[S::kHalves];
-        dense_block<MODE, BF16, S>(a, blockIdx.x, {(LDS_AS uint16_t *)r0, (LDS_AS uint16_t *)r1, (LDS_AS uint16_t *)r2,
-                                                   (LDS_AS uint16_t *)r3});
+        __shared__ __align__(1024) uint16_t r0[S::kHalves], r1[S::kHalves];
+        if constexpr (S::RING == 2) {
+            dense_block<MODE, BF16, S>(a, blockIdx.x, {(LDS_AS uint16_t *)r0, (LDS_AS uint16_t *)r1});
+        } else {
+            __shared__ __align__(1024) uint16_t r2[S::kHalves], r3[S::kHalves];
+            dense_block<MODE, BF16, S>(a, blockIdx.x, {(LDS_AS uint16_t *)r0, (LDS_AS uint16_t *)r1,
+                                                       (LDS_AS uint16_t *)r2, (LDS_AS uint16_t *)r3});
+        }
     }
 }
 
