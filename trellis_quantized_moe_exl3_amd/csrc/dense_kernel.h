@@ -219,23 +219,24 @@ MOE_DEV void multiply(const DenseFrags<S> &f, f32x4 (&acc)[S::NI][S::NJ])
             acc[i][j] = dense_mfma<BF16>(f.q[j], f.p[i], acc[i][j]);
 }
 
-// The order of 32 k: the next fragments' reads and L loads spread over the
-// MFMAs, early enough that the next wait finds them done (1024 tokens, 4096 x 2048:
-// see dense_kernel).  The transposing reads' two halves a fragment leave no
-// registers for it: there the same order spills and halves the rate.
+// The order of 32 k: the L loads between the first MFMAs, the next fragments'
+// reads between the others (7168 tokens, 4096 x 2048: 196.7 -> 193.7 us; reads
+// before loads leave too many fragments in registers and spill: 237).  The
+// transposing reads' two halves a fragment leave no registers for any order: they
+// spill and halve the rate.
 template <int MODE, class S, int L>
 MOE_DEV void spread()
 {
     if constexpr (DenseTraits<MODE>::kPL == KC && DenseTraits<MODE>::kQL == KC) {
-        constexpr int kPer = S::NI * S::NJ / (S::NI + S::NJ + L);
-#pragma unroll
-        for (int r = 0; r < S::NI + S::NJ; ++r) {
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
-        }
+        constexpr int kPer = (S::NI * S::NJ - L) / (S::NI + S::NJ);
 #pragma unroll
         for (int r = 0; r < L; ++r) {
             __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }
+#pragma unroll
+        for (int r = 0; r < S::NI + S::NJ; ++r) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
         }
     }
@@ -383,21 +384,7 @@ struct PairTile {
         load_q(s + 4, ring[2 + R % 4]);
         read(ring[(R + 1) / 2 % 2], (R + 1) & 1, ring[2 + (R + 1) % 4], fn);
         multiply<BF16, S>(f, acc);
-        if constexpr (TR::kQL == KC) {
-            // the loads between the first MFMAs, the reads between the others
-            // (7168 tokens, 4096 x 2048: 196.7 -> 193.7 us); reads before loads
-            // leave too many fragments in registers and spill (237)
-#pragma unroll
-            for (int r = 0; r < OQ::kLoads + (R & 1) * OP::kLoads; ++r) {
-                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            }
-#pragma unroll
-            for (int r = 0; r < NI + NJ; ++r) {
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
-            }
-        }
+        spread<MODE, S, OQ::kLoads + (R & 1) * OP::kLoads>();
     }
     template <class F>
     MOE_DEV void run(LDS_AS uint16_t *const (&ring)[kRing], f32x4 (&acc)[NI][NJ], F meanwhile)
