@@ -164,3 +164,45 @@ def test_a_training_step_through_the_block():
         rel = ((got.double() - leaf.grad).norm() / leaf.grad.norm()).item()
         # dh, then dg and du, then the output: three roundings
         assert rel <= 3 * R.half_step(m.dtype)
+
+
+def test_rows_up_to_the_2_gib_limit():
+    # columns of one buffer whose rows lie 2 MiB apart: byte offsets up to 2^31,
+    # and past it for a tile's rows behind the last token
+    T, H, I, ld = 1020, 264, 136, 1 << 20
+    g = torch.Generator(device="cuda").manual_seed(3)
+    dtype = torch.bfloat16
+    big = torch.empty(T, ld, dtype=dtype, device="cuda")
+
+    def far(col, cols, fill=None):
+        v = big[:, col:col + cols]
+        return v if fill is None else v.copy_(fill)
+
+    x, dh, base = (R.gauss(g, (T, n), 1.0, dtype) for n in (H, I, H))
+    wg, wu = (R.gauss(g, (I, H), H ** -0.5, dtype) for _ in range(2))
+    d = M.make_glu_desc(H, I, M.DT_BF16)
+    n = max(M.glu_workspace_size(d, T), M.glu_backward_workspace_size(d, T))
+    ids = torch.randint(-1, 3, (T,), generator=g, device="cuda").to(torch.int32)
+    w, a, b = R.gauss(g, (H, I), 0.1, dtype), R.gauss(g, (3, 16, I), 0.1, dtype), R.gauss(g, (3, H, 16), 0.3, dtype)
+    ld_desc = M.make_lora_desc(I, H, 3, 16, M.DT_BF16)
+
+    def run(x, h, dh, dx, base, y):
+        pre = torch.empty(2, T, I, device="cuda")
+        dwg, dwu = torch.empty_like(wg), torch.empty_like(wu)
+        ws = R.poisoned(n)
+        M.glu(d, x, wg, wu, h, ws, pre=pre)
+        M.glu_backward(d, x, wg, wu, pre, dh, ws, dx=dx, dw_gate=dwg, dw_up=dwu)
+        M.lora_linear(ld_desc, h, w, a, b, ids, y, R.poisoned(M.lora_workspace_size(ld_desc, T)), base=base)
+        return h, dx, dwg, dwu, y
+
+    def near(cols):
+        return torch.empty(T, cols, dtype=dtype, device="cuda")
+
+    want = run(x, near(I), dh, near(H), base, near(H))
+    got = run(far(0, H, x), far(512, I), far(1024, I, dh), far(2048, H), far(ld - 512, H, base), far(4096, H))
+    for a_, b_ in zip(got, want):
+        assert torch.equal(a_, b_)
+    with pytest.raises(M.MoeError) as e:   # one row more no longer spans less than 2 GiB
+        more = torch.empty(1025, ld, dtype=dtype, device="cuda")[:, :H]
+        M.glu(d, more, wg, wu, torch.empty(1025, I, dtype=dtype, device="cuda"), R.poisoned(M.glu_workspace_size(d, 1025)))
+    assert e.value.code == M.ERR_UNSUPPORTED

@@ -229,6 +229,25 @@ def test_ids_scales_and_ranks_inside_longer_arrays(T):
         assert torch.equal(_run(d, x, w, a, b, inner[0], None, inner[1], inner[2], half), want)
 
 
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_stacks_of_more_than_4_gib(T):
+    # the last adapters of a long stack, against the same two in a short one
+    g = _gen(T + 13)
+    half = torch.float16
+    K, N, r, n = 8192, 136, 256, 1100
+    x, w = R.gauss(g, (T, K), 1.0, half), R.gauss(g, (N, K), 0.01, half)
+    a, b = R.gauss(g, (2, r, K), 0.01, half), R.gauss(g, (2, N, r), 0.1, half)
+    ids = torch.randint(0, 2, (T,), generator=g, device="cuda").to(torch.int32)
+    want = _run(M.make_lora_desc(K, N, 2, r, M.DT_F16), x, w, a, b, ids, None, None, None, half)
+    long_a, long_b = torch.empty(n, r, K, dtype=half, device="cuda"), torch.empty(n, N, r, dtype=half, device="cuda")
+    long_a[-2:], long_b[-2:] = a, b
+    got = _run(M.make_lora_desc(K, N, n, r, M.DT_F16), x, w, long_a, long_b, ids + (n - 2), None, None, None, half)
+    # (the stack's length has a part in the choice of tiles: not the same bits)
+    ref, bound = R.lora(x, w, a, b, ids, None, None, None, half)
+    R.assert_close(got, ref, bound, "long")
+    R.assert_close(want, ref, bound, "short")
+
+
 def test_zero_tokens_and_workspace_reuse():
     g = _gen(5)
     dtype = torch.float16
