@@ -399,8 +399,8 @@ int moe_exl3_glu(const moe_exl3_glu_desc *desc, const void *x, int64_t ldx, cons
  * written, not added to.  dg and du are rounded to the 16-bit type before the
  * products, every output once more: in F16 values of magnitude 65520 or more
  * become infinite there, and those below 2^-24 vanish (scale the loss).  With
- * T = 0 the weights' gradients are set to zero and x, pre and dout are not
- * read (NULL is allowed).
+ * T = 0 the weights' gradients are set to zero, and x, pre, dout and dx may be
+ * NULL.
  */
 int moe_exl3_glu_backward(const moe_exl3_glu_desc *desc, const void *x, int64_t ldx, const void *w_gate,
                           const void *w_up, const float *pre, const void *dout, int64_t lddo, int64_t T, void *dx,

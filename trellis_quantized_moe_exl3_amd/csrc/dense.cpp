@@ -396,7 +396,9 @@ int moe_exl3_glu_backward(const moe_exl3_glu_desc *desc, const void *x, int64_t 
     int rc = check_desc(desc);
     if (rc)
         return rc;
-    if (T < 0 || !dw_gate != !dw_up || (!dx && !dw_gate))
+    // (no gradient asked for: a mistake, but for no tokens, whose dx has no
+    // elements and maybe no address)
+    if (T < 0 || !dw_gate != !dw_up || (T > 0 && !dx && !dw_gate))
         return MOE_EXL3_ERR_INVALID_ARG;
     const int64_t H = desc->hidden, I = desc->inter;
     const int64_t wrows = dx ? I : 0;   // the weights are read for dx alone
