@@ -76,7 +76,13 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(const uint16_t *x,
 #pragma unroll
     for (int s = 1; s < NW; ++s)
         v += red[s * kStep + 64 * w + l];
-    *(u32x2 *)(lo.mid + (int64_t)t * lo.rpad + r0 + 16 * w + 4 * (l >> 4)) =
+    // the rows from the adapter's own rank on were read as zeros, which an
+    // infinity in x makes NaNs of
+    const int k = r0 + 16 * w + 4 * (l >> 4);
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+        v[d] = k + d < rank ? v[d] : 0.0f;
+    *(u32x2 *)(lo.mid + (int64_t)t * lo.rpad + k) =
         (u32x2){pack16<BF16>(v[0], v[1]), pack16<BF16>(v[2], v[3])};
 }
 
