@@ -398,9 +398,9 @@ int moe_exl3_glu(const moe_exl3_glu_desc *desc, const void *x, int64_t ldx, cons
  * NULL; the weights are read for dx alone (NULL without it).  Outputs are
  * written, not added to.  dg and du are rounded to the 16-bit type before the
  * products, every output once more: in F16 values of magnitude 65520 or more
- * become infinite there, and those below 2^-24 vanish (scale the loss).  With
- * T = 0 the weights' gradients are set to zero, and x, pre, dout and dx may be
- * NULL.
+ * become infinite there, and those of 2^-25 or less vanish (scale the loss).
+ * With T = 0 the weights' gradients are set to zero, and x, pre, dout and dx may
+ * be NULL.
  */
 int moe_exl3_glu_backward(const moe_exl3_glu_desc *desc, const void *x, int64_t ldx, const void *w_gate,
                           const void *w_up, const float *pre, const void *dout, int64_t lddo, int64_t T, void *dx,
@@ -433,10 +433,11 @@ int moe_exl3_lora_workspace_size(const moe_exl3_lora_desc *desc, int64_t max_tok
  * is computed elsewhere); ids: device int32 [T], in any order (ids, scales and
  * ranks may be parts of longer arrays: 4-byte aligned); base: device
  * [T][N] or NULL, may be y itself (same address and ld); y: device [T][N].
- * scales[e] * a[e] x[t] is rounded to the 16-bit type for the second product
- * where that runs on the matrix cores; y is rounded once.  A token's row
- * depends on its own adapter only: another adapter's infinities or NaNs do
- * not reach it.  T = 0 is a no-op.
+ * scales[e] * a[e] x[t] stays in fp32 in calls of up to 64 tokens and is rounded
+ * to the 16-bit type in larger ones, for the matrix cores: in F16 values of
+ * magnitude 65520 or more become infinite there, and those of 2^-25 or less
+ * vanish.  y is rounded once.  A token's row depends on its own adapter only:
+ * another adapter's infinities or NaNs do not reach it.  T = 0 is a no-op.
  *
  * The status word (see MOE_EXL3_STATUS_OFFSET) reports BAD_INDEX for an id
  * outside [-1, n_adapters) (the token then has no adapter) and BAD_WIDTH for a

@@ -10,6 +10,65 @@ import trellis_quantized_moe_exl3_amd as M
 
 pytestmark = pytest.mark.gpu
 
+TYPES = [torch.bfloat16, torch.float16]
+FEW = [1, 2, 8, 17, 33, 64]   # tokens of the few-token kernel, in all its sizes
+
+
+def _one_rank(T, n, r, dtype, value, times, b):
+    """Adapters whose rank 0 gives times * value for a token of ones and adds b
+    times that to every column; the other ranks are zero."""
+    K, N = 1032, 72
+    bf = dict(dtype=dtype, device="cuda")
+    x, a, bm = torch.ones(T, K, **bf), torch.zeros(n, r, K, **bf), torch.zeros(n, N, r, **bf)
+    a[:, 0, :times] = value
+    bm[:, :, 0] = b
+    ids = (torch.arange(T, device="cuda") % n).to(torch.int32)
+    return M.make_lora_desc(K, N, n, r, R.DT[dtype]), x, a, bm, ids
+
+
+# Sums that need one bit more than the type has: 257 = 2^8 + 1 (bf16), 2049 = 3 x 683
+# (fp16).  Times 1, next to a base of -256 or -2048, 1 is left of them.
+ODD = {torch.bfloat16: (1.0, 257, -256.0), torch.float16: (3.0, 683, -2048.0)}
+
+
+@pytest.mark.parametrize("r", [8, 40])
+@pytest.mark.parametrize("T", FEW)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_few_tokens_keep_the_product_between_in_fp32(T, r, dtype):
+    value, times, base = ODD[dtype]
+    d, x, a, b, ids = _one_rank(T, 3, r, dtype, value, times, 1.0)
+    base = torch.full((T, d.n_out), base, dtype=dtype, device="cuda")
+    y = L._run(d, x, None, a, b, ids, base, None, None, dtype)
+    assert (y == 1.0).all()
+    assert torch.equal(L._run(d, x, torch.zeros(d.n_out, d.n_in, dtype=dtype, device="cuda"), a, b, ids, base, None,
+                              None, dtype), y)
+
+
+@pytest.mark.parametrize("r", [8, 40])
+@pytest.mark.parametrize("T", [65, 300, 1100])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_more_tokens_round_it_once(T, r, dtype):
+    # to even: 256 and 2048
+    value, times, base = ODD[dtype]
+    d, x, a, b, ids = _one_rank(T, 3, r, dtype, value, times, 1.0)
+    base = torch.full((T, d.n_out), base, dtype=dtype, device="cuda")
+    assert (L._run(d, x, None, a, b, ids, base, None, None, dtype) == 0.0).all()
+
+
+@pytest.mark.parametrize("r", [8, 40])
+@pytest.mark.parametrize("T", FEW + [65, 300])
+def test_products_beyond_fp16(T, r):
+    # 70000 = 100 x 700 times 2^-4, and 2^-26 times 2^10 (a scale of 2^-26 on a sum
+    # of 1): finite and not zero for few tokens, infinite and zero where the
+    # product between is rounded
+    d, x, a, b, ids = _one_rank(T, 3, r, torch.float16, 100.0, 700, 2.0 ** -4)
+    y = L._run(d, x, None, a, b, ids, None, None, None, torch.float16)
+    assert (y == (4376.0 if T <= 64 else float("inf"))).all()   # 4375 to a step of 4
+    d, x, a, b, ids = _one_rank(T, 3, r, torch.float16, 1.0, 1, 1024.0)
+    scales = torch.full((3,), 2.0 ** -26, device="cuda")
+    y = L._run(d, x, None, a, b, ids, None, scales, None, torch.float16)
+    assert (y == (2.0 ** -16 if T <= 64 else 0.0)).all()
+
 
 @pytest.mark.parametrize("rank", [1, 4, 8, 13])
 @pytest.mark.parametrize("T", [1, 8, 64, 65, 200, 700, 3900])

@@ -285,7 +285,9 @@ LoraPlan plan_lora(const moe_exl3_lora_desc &d, int64_t T)
     p.rpad = (int)cdiv(d.rank, 32) * 32;
     size_t o = kAlign;
     p.mid = o;
-    o += align_up((size_t)T * p.rpad * 2);
+    // fp32 for the few-token kernel, 16 bits for more tokens: never less than for
+    // fewer of them
+    o += align_up((size_t)p.rpad * (size_t)std::max(4 * std::min(T, kSkinnyTokens), 2 * T));
     p.part = o;
     o += T <= kSkinnyTokens ? 0 : align_up(part_bound(DENSE_LIN, T, d.n_out, d.n_in));
     p.total = o;
@@ -531,7 +533,7 @@ int moe_exl3_lora_linear(const moe_exl3_lora_desc *desc, const void *x, int64_t 
     l.scales = adapters->scales;
     l.ranks = adapters->ranks;
     l.status = at<int32_t>(workspace, MOE_EXL3_STATUS_OFFSET);
-    l.mid = at<uint16_t>(workspace, p.mid);
+    l.mid = at<void>(workspace, p.mid);
     l.n = (int)n;
     l.rank = (int)r;
     l.rpad = p.rpad;

@@ -47,7 +47,8 @@ struct LoraArgs {
     const float *scales;     // [n] or NULL (1)
     const int32_t *ranks;    // [n] or NULL (rank)
     int32_t *status;         // status word of the call
-    uint16_t *mid;           // [T][rpad] s_a x A_a^T in 16 bits, zeros from the adapter's rank on
+    void *mid;               // [T][rpad] s_a x A_a^T, zeros from the adapter's rank on: fp32 for the
+                             // few-token kernel, in 16 bits for the tile kernels
     int n, rank, rpad;       // rpad: rank rounded up to 32
     int k;                   // columns of x and of A's rows
     bool fused;              // one token: x A^T in the same launch, mid is not used

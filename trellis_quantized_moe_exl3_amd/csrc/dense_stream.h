@@ -222,7 +222,10 @@ constexpr int skinny_cols(int nj) { return MODE == DENSE_GLU ? 8 * nj : 16 * nj;
 // delta[t][16 columns]: the adapters' rows of tokens t = w, w + XW, .. , kBatch
 // at a time with all their loads in flight: lane l takes column l / 4 and the k
 // octets l % 4 + 0, 4, .. of the token's adapter (four lanes to 64 bytes of a
-// row of B), summed in fp32.
+// row of B), summed in fp32.  x A^T comes in fp32: 16 bits would round it for
+// nothing, and lose values that fp16 does not hold.  Ranks are masked only in the
+// 32 that an adapter's own rank ends in (64 tokens, 4096 x 4096, 64 adapters of
+// 128: 43.8 us a call with masks everywhere, 39.7).
 template <bool BF16, int NI, int XW>
 MOE_DEV void skinny_expand(const DenseArgs &a, int n0, int w, int l, float (*delta)[16])
 {
@@ -232,7 +235,8 @@ MOE_DEV void skinny_expand(const DenseArgs &a, int n0, int w, int l, float (*del
     const int c = l >> 2, n = min(n0 + c, a.N - 1);
     constexpr int kBatch = 16 * NI / XW;   // tokens of a wavefront
     int rk[kBatch], most = 0;
-    const uint16_t *bp[kBatch], *up[kBatch];
+    const uint16_t *bp[kBatch];
+    const float *up[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
         const int t = w + b * XW;   // below 16 NI <= 64
@@ -240,24 +244,36 @@ MOE_DEV void skinny_expand(const DenseArgs &a, int n0, int w, int l, float (*del
         most = max(most, rk[b]);
         const int e = max(__builtin_amdgcn_readlane(mine, t), 0);
         bp[b] = lo.b + ((int64_t)e * a.N + n) * lo.rank;
-        up[b] = lo.mid + (int64_t)min(t, a.M - 1) * lo.rpad;
+        up[b] = (const float *)lo.mid + (int64_t)min(t, a.M - 1) * lo.rpad;
     }
     float sum[kBatch] = {};
-    for (int k = 8 * (l & 3); k < most; k += 32) {
-        u32x4 bv[kBatch], uv[kBatch];
+    for (int k0 = 0; k0 < most; k0 += 32) {
+        const int k = k0 + 8 * (l & 3);
+        u32x4 bv[kBatch];
+        f32x4 uv[kBatch][2];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             bv[b] = *(const u32x4 *)(bp[b] + min(k, lo.rank - 8));
-            uv[b] = *(const u32x4 *)(up[b] + k);
+            uv[b][0] = *(const f32x4 *)(up[b] + k);
+            uv[b][1] = *(const f32x4 *)(up[b] + k + 4);
         }
+        __builtin_amdgcn_sched_barrier(0);   // all loads first
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
+        for (int b = 0; b < kBatch; ++b) {
+            if (k0 >= rk[b])
+                continue;
+            float y[8];
 #pragma unroll
-            for (int d = 0; d < 8; ++d) {
-                const float y = act_to_f32<BF16>((uint16_t)(bv[b][d >> 1] >> (16 * (d & 1)))) *
-                                act_to_f32<BF16>((uint16_t)(uv[b][d >> 1] >> (16 * (d & 1))));
-                sum[b] += k + d < rk[b] ? y : 0.0f;
-            }
+            for (int d = 0; d < 8; ++d)
+                y[d] = act_to_f32<BF16>((uint16_t)(bv[b][d >> 1] >> (16 * (d & 1)))) * uv[b][d >> 2][d & 3];
+            if (k0 + 32 > rk[b])
+#pragma unroll
+                for (int d = 0; d < 8; ++d)
+                    y[d] = k + d < rk[b] ? y[d] : 0.0f;
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+                sum[b] += y[d];
+        }
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {

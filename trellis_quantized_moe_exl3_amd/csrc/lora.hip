@@ -26,8 +26,9 @@ MOE_DEV void check_adapters(const LoraArgs &lo, int T, int tid)
         *lo.status = (index ? (int)MOE_EXL3_STATUS_BAD_INDEX : 0) | (width ? (int)MOE_EXL3_STATUS_BAD_WIDTH : 0);
 }
 
-// mid[t][0..rpad) = scales[e] x[t] A_e^T, e = ids[t], in 16 bits for the second
-// product; zeros from the adapter's own rank on.  Tokens without an adapter are
+// mid[t][0..rpad) = scales[e] x[t] A_e^T, e = ids[t]: in 16 bits for the matrix
+// cores of the tile kernels, in fp32 for the few-token kernel, which multiplies
+// in fp32; zeros from the adapter's own rank on.  Tokens without an adapter are
 // not written.
 //
 // Block (f, r): `tpf` tokens (1, 8 or 16) against 16 NR rows of their adapters, k
@@ -82,8 +83,11 @@ __global__ __launch_bounds__(64 * NW) void lora_shrink_kernel(const uint16_t *x,
 #pragma unroll
     for (int d = 0; d < 4; ++d)
         v[d] = k + d < rank ? v[d] : 0.0f;
-    *(u32x2 *)(lo.mid + (int64_t)t * lo.rpad + k) =
-        (u32x2){pack16<BF16>(v[0], v[1]), pack16<BF16>(v[2], v[3])};
+    const int64_t o = (int64_t)t * lo.rpad + k;
+    if (T <= (int)kSkinnyTokens)
+        *(f32x4 *)((float *)lo.mid + o) = v;
+    else
+        *(u32x2 *)((uint16_t *)lo.mid + o) = (u32x2){pack16<BF16>(v[0], v[1]), pack16<BF16>(v[2], v[3])};
 }
 
 // One token a block while all blocks together read at most this much of the
