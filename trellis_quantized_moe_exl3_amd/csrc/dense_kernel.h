@@ -122,9 +122,11 @@ MOE_DEV void dense_store(const DenseArgs &a, int z, int m0, int n0, int l, const
                          const u32x4 (&base)[2], LDS_AS f32x4 *lds)
 {
     const int r = l & 15;
+    wave_lds_fence();   // the rows before these, or the sums, are read
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         lds[16 * r + ((4 * j + (l >> 4)) ^ r)] = v[j];
+    wave_lds_fence();
     auto at = [&](int row, int unit) { return lds[16 * row + (unit ^ row)]; };
     // one 64-bit address for the 16 rows, 32-bit offsets in them
     uint16_t *out = a.out[MODE == DENSE_DW ? z : 0] + (int64_t)m0 * a.ldo + n0;

@@ -34,6 +34,15 @@ MOE_DEV void wait_vmcnt()
     __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | 0xF00 | ((N >> 4) << 14));
 }
 
+// Between LDS accesses of a wavefront's lanes to each other's places.  The
+// hardware keeps a wavefront's LDS accesses in order; this keeps the compiler's
+// (which sees each lane on its own), at no instruction.
+MOE_DEV void wave_lds_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // LDS layout of one A stage: row r is 64 bytes = four 16-byte pieces; the
 // piece holding k-offset 8p is stored in slot p ^ ((r >> 2) & 3), which makes
 // the 16-lane reads of an MFMA A fragment (16 consecutive rows, one piece)
