@@ -92,6 +92,22 @@ def test_an_infinite_token_with_ranks_below_the_stacks(T, rank):
         assert torch.equal(y[1:], before[1:])
 
 
+@pytest.mark.parametrize("T", [1, 2, 40, 70, 116, 300, 1024, 4000])
+@pytest.mark.parametrize("K,N,r", [(840, 1984, 32), (264, 4096, 72)])
+def test_appended_adapters_change_no_bits(T, K, N, r):
+    g = L._gen(T + N)
+    dtype = torch.bfloat16
+    n, more = 3, 700
+    x, w = R.gauss(g, (T, K), 1.0, dtype), R.gauss(g, (N, K), K ** -0.5, dtype)
+    a, b = R.gauss(g, (n, r, K), K ** -0.5, dtype), R.gauss(g, (n, N, r), 0.3, dtype)
+    av, bv = (torch.full((more,) + t.shape[1:], float("nan"), dtype=dtype, device="cuda") for t in (a, b))
+    av[:n], bv[:n] = a, b
+    for w_ in (w, None):
+        ids = L._ids(g, T, n, "mixed")
+        want = L._run(M.make_lora_desc(K, N, n, r, M.DT_BF16), x, w_, a, b, ids, None, None, None, dtype)
+        assert torch.equal(L._run(M.make_lora_desc(K, N, more, r, M.DT_BF16), x, w_, av, bv, ids, None, None, None, dtype), want)
+
+
 @pytest.mark.parametrize("want_dx,want_dw", [(True, False), (False, True), (True, True)])
 def test_no_tokens(want_dx, want_dw):
     # torch gives a tensor without elements no address
