@@ -119,3 +119,15 @@ def test_no_tokens(want_dx, want_dw):
     M.glu_backward(d, x, w, w, torch.empty(2, 0, I, device="cuda"), dh, R.poisoned(M.glu_backward_workspace_size(d, 0)),
                    dx=torch.empty_like(x) if want_dx else None, dw_gate=dw[0], dw_up=dw[1])
     assert not want_dw or all((t == 0).all() for t in dw)
+
+
+# The weights' gradients in 256 x 256 tiles of many stages: 400 tokens (12 full
+# stages of 32 and half of one) and 520 (16 and a quarter); both gradients in
+# 64 x 64 tiles of one launch, dx's blocks first; the weights' in eight splits
+GRADIENTS = [(400, 16384, 264), (520, 520, 8192), (500, 256, 1032), (4100, 488, 120)]
+
+
+# 256 x 256 tiles whose adapters take several stages of 32 ranks, the last of them
+# partly; long k in those and in 128 x 128 tiles, alone on a CU and two on one
+PROJECTIONS = [(3900, 264, 4096, 6, 72), (3900, 264, 4096, 3, 256), (3900, 1288, 4096, 3, 72), (1024, 2056, 4096, 6, 40),
+               (2500, 1288, 2056, 4, 40)]
