@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import dense_ref as R
+import test_gpu_glu as G
 import test_gpu_lora as L
 import trellis_quantized_moe_exl3_amd as M
 
@@ -121,13 +122,66 @@ def test_no_tokens(want_dx, want_dw):
     assert not want_dw or all((t == 0).all() for t in dw)
 
 
+@pytest.mark.parametrize("bad", [4, -2, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("K,N,r", [(2048, 4096, 16), (264, 72, 32), (1032, 136, 40)])
+def test_one_token_with_a_bad_id(K, N, r, bad):
+    g = L._gen(K + r)
+    dtype = torch.bfloat16
+    n = 4
+    d = M.make_lora_desc(K, N, n, r, M.DT_BF16)
+    x, w = R.gauss(g, (1, K), 1.0, dtype), R.gauss(g, (N, K), K ** -0.5, dtype)
+    a, b = R.gauss(g, (n, r, K), K ** -0.5, dtype), R.gauss(g, (n, N, r), 0.3, dtype)
+    y, ws = torch.empty(1, N, dtype=dtype, device="cuda"), R.poisoned(M.lora_workspace_size(d, 1))
+    ranks = torch.full((n,), r + 1, dtype=torch.int32, device="cuda")   # not this token's: no fault of theirs
+    M.lora_linear(d, x, w, a, b, torch.tensor([bad], device="cuda").to(torch.int32), y, ws, ranks=ranks)
+    assert M.status(ws) == M.STATUS_BAD_INDEX
+    none = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    assert torch.equal(y, L._run(d, x, w, a, b, none, None, None, None, dtype))
+
+
+@pytest.mark.parametrize("K,N,r", [(2048, 4096, 16), (264, 72, 32), (1032, 136, 40)])
+def test_one_token_and_another_adapters_infinities(K, N, r):
+    g = L._gen(K + N)
+    dtype = torch.float16
+    n = 5
+    d = M.make_lora_desc(K, N, n, r, M.DT_F16)
+    x, w = R.gauss(g, (1, K), 1.0, dtype), R.gauss(g, (N, K), K ** -0.5, dtype)
+    a, b = R.gauss(g, (n, r, K), K ** -0.5, dtype), R.gauss(g, (n, N, r), 0.3, dtype)
+    base = R.gauss(g, (1, N), 1.0, dtype)
+    ranks = torch.tensor([r, r - 3, 5, 8, 0], dtype=torch.int32, device="cuda")
+    for e in range(n):
+        ids = torch.full((1,), e, dtype=torch.int32, device="cuda")
+        av, bv = torch.full_like(a, float("nan")), torch.full_like(b, float("inf"))
+        av[e], bv[e] = a[e], b[e]
+        y = L._run(d, x, w, av, bv, ids, base, None, ranks, dtype)
+        ref, bound = R.lora(x, w, a, b, ids, base, None, ranks, dtype)
+        R.assert_close(y, ref, bound, f"adapter {e}")
+        y = L._run(d, x, w, av, bv, torch.full_like(ids, -1), base, None, ranks, dtype)
+        ref, bound = R.lora(x, w, a, b, torch.full_like(ids, -1), base, None, ranks, dtype)
+        R.assert_close(y, ref, bound, "none")
+
+
 # The weights' gradients in 256 x 256 tiles of many stages: 400 tokens (12 full
 # stages of 32 and half of one) and 520 (16 and a quarter); both gradients in
 # 64 x 64 tiles of one launch, dx's blocks first; the weights' in eight splits
 GRADIENTS = [(400, 16384, 264), (520, 520, 8192), (500, 256, 1032), (4100, 488, 120)]
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,H,I", GRADIENTS)
+def test_gradients_in_long_tiles(T, H, I, dtype):
+    G.test_backward(T, H, I, dtype)
+    G.test_gradients_of_integers_are_exact(T, H, I, dtype)
+
+
 # 256 x 256 tiles whose adapters take several stages of 32 ranks, the last of them
 # partly; long k in those and in 128 x 128 tiles, alone on a CU and two on one
 PROJECTIONS = [(3900, 264, 4096, 6, 72), (3900, 264, 4096, 3, 256), (3900, 1288, 4096, 3, 72), (1024, 2056, 4096, 6, 40),
                (2500, 1288, 2056, 4, 40)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,K,N,n,r", PROJECTIONS)
+def test_projection_in_long_tiles(T, K, N, n, r, dtype):
+    L.test_values(T, K, N, n, r, dtype)
+    L.test_integers_are_exact(T, K, N, n, r, dtype)
