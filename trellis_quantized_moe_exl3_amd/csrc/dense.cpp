@@ -14,8 +14,8 @@ constexpr int64_t kMaxSize = 65536;
 constexpr int64_t kMaxLd = 1 << 20;
 constexpr int64_t kSpanLimit = (int64_t)1 << 31;
 
-// k splits of 64 x 64 tiles: at most this many blocks (one a CU), each with at
-// least this many stages (256 k).
+// k splits of 64 x 64 tiles: at most this many blocks (one a CU), and at most one
+// for each this many stages (256 k; the last split takes what is left).
 constexpr int64_t kSplitBlocks = 256;
 constexpr int64_t kSplitStages = 4;
 // Adapters that a call is taken to name (plan_tiles).

@@ -423,16 +423,21 @@ hipError_t launch_skinny(const DenseArgs &a, hipStream_t s)
 {
     constexpr bool kLin = MODE == DENSE_LIN;
     const unsigned narrow = (unsigned)((a.N + skinny_cols<MODE>(1) - 1) / skinny_cols<MODE>(1));   // blocks
-    if (kLin && a.lora.fused)
-        dense_skinny_kernel<DENSE_LIN, BF16, 1, 1, 8, 2, 4, true><<<narrow, 64 * 12, 0, s>>>(a);
-    else if (a.M <= 16)
+    if constexpr (kLin) {
+        if (a.lora.fused) {
+            dense_skinny_kernel<MODE, BF16, 1, 1, 8, 2, 4, true><<<narrow, 64 * 12, 0, s>>>(a);
+            return hipGetLastError();
+        }
+    } else if (a.M > 32 && narrow >= 256) {
+        dense_skinny_kernel<MODE, BF16, 4, 2, 4, 3, 0><<<(narrow + 1) / 2, 256, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    if (a.M <= 16)
         dense_skinny_kernel<MODE, BF16, 1, 1, 8, 4, kLin ? 4 : 0><<<narrow, 64 * (kLin ? 12 : 8), 0, s>>>(a);
     else if (a.M <= 32)
         dense_skinny_kernel<MODE, BF16, 2, 1, 8, 3, kLin ? 8 : 0><<<narrow, 64 * (kLin ? 16 : 8), 0, s>>>(a);
-    else if (kLin || narrow < 256)
-        dense_skinny_kernel<MODE, BF16, 4, 1, 4, 3, kLin ? 8 : 0><<<narrow, 64 * (kLin ? 12 : 4), 0, s>>>(a);
     else
-        dense_skinny_kernel<DENSE_GLU, BF16, 4, 2, 4, 3, 0><<<(narrow + 1) / 2, 256, 0, s>>>(a);
+        dense_skinny_kernel<MODE, BF16, 4, 1, 4, 3, kLin ? 8 : 0><<<narrow, 64 * (kLin ? 12 : 4), 0, s>>>(a);
     return hipGetLastError();
 }
 
