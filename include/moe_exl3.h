@@ -437,7 +437,9 @@ int moe_exl3_lora_workspace_size(const moe_exl3_lora_desc *desc, int64_t max_tok
  * to the 16-bit type in larger ones, for the matrix cores: in F16 values of
  * magnitude 65520 or more become infinite there, and those of 2^-25 or less
  * vanish.  y is rounded once.  A token's row depends on its own adapter only:
- * another adapter's infinities or NaNs do not reach it.  T = 0 is a no-op.
+ * another adapter's infinities or NaNs do not reach it.  Its last bits may depend
+ * on T, the sizes, rank and n_adapters up to 64 (not on longer stacks), which
+ * choose the kernels.  T = 0 is a no-op.
  *
  * The status word (see MOE_EXL3_STATUS_OFFSET) reports BAD_INDEX for an id
  * outside [-1, n_adapters) (the token then has no adapter) and BAD_WIDTH for a

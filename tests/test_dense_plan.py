@@ -46,13 +46,14 @@ def plans(tmp_path_factory):
     return run
 
 
-def test_the_stacks_length_has_no_part(plans):
-    # adapters that no token names change neither tile nor split, hence no bits
+def test_a_long_stack_has_no_part(plans):
+    # from 64 adapters on, more of them that no token names change neither tile nor
+    # split, hence no bits
     for T in (1, 64, 65, 116, 198, 333, 1024, 2048, 3900, 7168, 16384):
         for K, N in ((2048, 4096), (840, 1984), (8200, 264)):
             for r in (8, 32, 256):
                 for w in (0, 1):
-                    calls = [f"lora {T} {K} {N} {n} {r} {w} 0" for n in (1, 2, 8, 64, 512, 4096, 65536)]
+                    calls = [f"lora {T} {K} {N} {n} {r} {w} 0" for n in (64, 65, 512, 4096, 65536)]
                     got = plans(calls)
                     assert got[0][0][0] != "error" and all(p == got[0] for p in got), calls
 
@@ -137,3 +138,12 @@ def test_plans_of_any_size(plans):
     assert len(refused) < len(calls) // 2   # beyond 2 GiB
     seen = {v for c, p in zip(calls, got) if c not in refused for v, _ in variants(c, p)}
     assert seen <= set(VARIANTS) and len(seen) >= len(VARIANTS) - 5, set(VARIANTS) - seen
+
+
+def test_an_ordinary_call_beside_a_long_stack(plans):
+    # a prompt of one request takes the large tiles, however many are loaded
+    for call, bm in (("7168 2048 4096", 256), ("1024 2048 4096", 128), ("1024 4096 4096", 128)):
+        T, K, N = call.split()
+        for n in (8, 64, 512, 3000, 65536):
+            (p,) = plans([f"lora {T} {K} {N} {n} 32 1 0"])
+            assert p[1][:3] == ["dense", str(LIN), str(bm)], (call, n, p)

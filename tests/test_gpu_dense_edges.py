@@ -95,10 +95,10 @@ def test_an_infinite_token_with_ranks_below_the_stacks(T, rank):
 
 @pytest.mark.parametrize("T", [1, 2, 40, 70, 116, 300, 1024, 4000])
 @pytest.mark.parametrize("K,N,r", [(840, 1984, 32), (264, 4096, 72)])
-def test_appended_adapters_change_no_bits(T, K, N, r):
+def test_adapters_appended_to_a_long_stack_change_no_bits(T, K, N, r):
     g = L._gen(T + N)
     dtype = torch.bfloat16
-    n, more = 3, 700
+    n, more = 64, 700   # a call is planned for 64 at most
     x, w = R.gauss(g, (T, K), 1.0, dtype), R.gauss(g, (N, K), K ** -0.5, dtype)
     a, b = R.gauss(g, (n, r, K), K ** -0.5, dtype), R.gauss(g, (n, N, r), 0.3, dtype)
     av, bv = (torch.full((more,) + t.shape[1:], float("nan"), dtype=dtype, device="cuda") for t in (a, b))

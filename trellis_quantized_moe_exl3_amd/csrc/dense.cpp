@@ -18,8 +18,8 @@ constexpr int64_t kSpanLimit = (int64_t)1 << 31;
 // for each this many stages (256 k; the last split takes what is left).
 constexpr int64_t kSplitBlocks = 256;
 constexpr int64_t kSplitStages = 4;
-// Adapters that a call is taken to name (plan_tiles).
-constexpr int64_t kNamedAdapters = 16;
+// Adapters that a call is taken to name at most (plan_tiles).
+constexpr int64_t kMostNamed = 64;
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -145,17 +145,17 @@ struct Tiles {
 // An adapter that a tile's tokens name costs 0.6 us for 64 ranks in a 128 x 128
 // tile, twice that in a 256 x 256 one; the wavefronts of a 64 x 64 tile share them,
 // and so do its splits (116 tokens, 62 adapters of 32, 1984 columns, 840 k: a call
-// of 53 us in 128 x 128, 17 in 64 x 64).  The host does not see the ids, and a
-// stack's length says nothing about them: a call is taken to name kNamedAdapters,
-// the tokens of a request standing together, so a tile of bm tokens kNamedAdapters
-// bm / T and one more.  (Priced by the stack's length, one request's 7168 tokens,
-// 2048 x 4096, rank 32, took 113 us with 8 adapters loaded and 199 with 3000.  Of
-// 36 calls whose tile differs, 1 to 59 adapters named, 16 takes 2% less time than
-// their number; 8 takes 3% more, with 133 tokens of 22 adapters 47.6 us for 24.4;
-// 32 and 64 take 2% and 3% less, but 359 tokens of 7 adapters 29.0 for 21.0.)
+// of 60 us in 128 x 128, 21 in 64 x 64).  Of n adapters a tile of bm tokens is taken
+// to name n bm / T and one more, the tokens of a request standing together.  The
+// host does not see the ids: n is the stack's length, but no more than kMostNamed,
+// as a longer stack says nothing about a call (one request's 7168 tokens, 2048 x
+// 4096, rank 32: 113 us with 8 adapters loaded, 199 with 3000 before this limit, 114
+// with it).  A fixed number for stacks of any length takes 1 to 2% less over 200
+// calls of 1 to 63 named adapters, but up to 1.8 times as long: 16, 219 tokens of
+// 51 adapters 31 -> 57 us; 64, 324 tokens of 5 adapters 16 -> 24.
 //
-// rank: of the adapters, 0 without any.
-Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K, int64_t rank = 0)
+// n, rank: of the adapters, 0 without any.
+Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K, int64_t n = 0, int64_t rank = 0)
 {
     const int64_t stages = stages_of(mode, K);
     const double s = (double)stages;
@@ -170,7 +170,7 @@ Tiles plan_tiles(int mode, int64_t M, int64_t N, int64_t K, int64_t rank = 0)
     };
     auto rounds = [&](int64_t tiles, int64_t at_once) { return (double)cdiv(tiles, at_once); };
     auto adapters = [&](int64_t b) {
-        return rank == 0 ? 0.0 : 0.6 * (double)(std::min(b, cdiv(kNamedAdapters * b, M) + 1) * cdiv(rank, 64));
+        return n == 0 ? 0.0 : 0.6 * (double)(std::min({n, b, cdiv(n * b, M) + 1}) * cdiv(rank, 64));
     };
     const double l64 = adapters(kDenseTile), l128 = adapters(kDenseSmall), l256 = 2 * adapters(kDenseLarge);
     const int64_t t64 = tiles_of(mode, M, N, kDenseTile), t128 = tiles_of(mode, M, N, kDenseSmall);
@@ -252,7 +252,7 @@ int launch_forward(int mode, int dtype, DenseArgs &a, float *part, void *stream)
     if (a.M <= kSkinnyTokens) {
         e = launch_dense_skinny(mode, bf16, a, (hipStream_t)stream);
     } else {
-        set_tiles(a, plan_tiles(mode, a.M, a.N, a.K, a.lora.rank), part);
+        set_tiles(a, plan_tiles(mode, a.M, a.N, a.K, std::min<int64_t>(a.lora.n, kMostNamed), a.lora.rank), part);
         e = launch_dense(mode, bf16, a, (hipStream_t)stream);
     }
     return e == hipSuccess ? MOE_EXL3_OK : MOE_EXL3_ERR_HIP;
