@@ -364,6 +364,8 @@ int moe_exl3_expand_block_scales(const uint16_t *block, int32_t n_trellis, int32
  * ld do not overlap), except where noted.  The workspace is as for
  * moe_exl3_layer: 256-byte aligned, ignored on entry, one per call in flight;
  * its need does not shrink with T, so the size for the largest T serves all.
+ * Calls of moe_exl3_lora_linear with tokens set its status word; those of the
+ * block leave it as it is.
  * The same inputs give the same bits on every call.
  */
 #define MOE_EXL3_ACT_SILU 0

@@ -129,18 +129,22 @@ struct Tiles {
 
 // The tile of a launch: the one whose rounds over the 256 CUs are estimated to
 // take the least time.  A round costs a fixed part (launch, first loads,
-// epilogue) and a part per 64 k, in us as measured on the block's forward pass,
-// 96 to 16384 tokens, hidden 512 to 8192, inter 256 to 8192 (calls one after the
-// other):
+// epilogue) and a part per 64 k, in us as fitted to the block's forward pass, 96
+// to 16384 tokens, hidden 512 to 8192, inter 256 to 8192 (calls one after the
+// other; the figures behind are the present kernels'):
 //   64 x 64     5 + 0.16 for 64 k up to 256 tiles, else 5.4 + 0.34 a round of 512
-//               (333 tokens, 1032 x 1384: 11.0; 128 x 128 takes 15.2)
-//   128 x 128   4 + 0.48 (1024 tokens, 4096 x 2048: 35.7; 64 x 64 takes 52,
-//               256 x 256 73)
-//   256 x 256   10 + 1.40 (4096 tokens, 4096 x 2048: 104; 128 x 128 takes 114)
+//               (333 tokens, 1032 x 1384: 10.9; 128 x 128 takes 14.8)
+//   128 x 128   4 + 0.48 (1024 tokens, 4096 x 2048: 38; 64 x 64 takes 52,
+//               256 x 256 79)
+//   256 x 256   10 + 1.40 (4096 tokens, 4096 x 2048: 104; 128 x 128 takes 116)
 // Few 64 x 64 tiles with a long k are cut along k, at the price of partial tiles
 // and a second launch: 11 + 0.16 for 64 k + 0.1 a split, into as many as make that
-// least (calls of 100 tokens, 8192 x 256: 12.4, uncut 22; 4096 x 512: 11.4, uncut
-// 14.1; but 200 tokens, 2048 x 1024: 10.1 uncut).
+// least (calls of 100 tokens, 8192 x 256: 12.5, uncut 24; 4096 x 512: 11.5, uncut
+// 14.9; but 200 tokens, 2048 x 1024: 10.3 uncut, 12.1 cut).
+// The estimates are there to order the tiles, which they did in each of 17 sizes
+// timed in all three; the times themselves can be half as long again, most where
+// rows do not begin on a 128-byte line, which has no term (198 tokens, 7528 x
+// 6144, 128 x 128: 61 estimated, 94 measured; 64 x 64 takes 103).
 //
 // An adapter that a tile's tokens name costs 0.6 us for 64 ranks in a 128 x 128
 // tile, twice that in a 256 x 256 one; the wavefronts of a 64 x 64 tile share them,
@@ -213,10 +217,10 @@ double merged_sum(const Tiles &a, const Tiles &b)
 // Whether both kinds of such blocks take less time in one launch, two blocks on
 // a CU: three quarters of the sum, at least the longest block, which its
 // neighbour slows down.  Whole steps, in one launch and in two, in us: 250 tokens,
-// 2048 x 2048: 33.9, 41.5; 1908, 1000 x 1376: 68.0, 76.3; 30, 8192 x 2048: 55, 67;
-// but with long blocks 128, 1536 x 4096: 45, 43; 60, 1664 x 5816: 65, 57.  Beyond
+// 2048 x 2048: 33.5, 41.5; 1908, 1000 x 1376: 67, 75; 30, 8192 x 2048: 54, 66;
+// but with long blocks 128, 1536 x 4096: 44, 40; 60, 1664 x 5816: 64, 51.  Beyond
 // a sum of 80 us each gradient fills the CUs by itself, in larger tiles: 3000
-// tokens, 2056 x 2056: 261, 236; 9000, 1024 x 1024: 200, 190.
+// tokens, 2056 x 2056: 256, 218 (9000, 1024 x 1024: 196 both ways).
 bool merge_pays(const Tiles &a, const Tiles &b, double apart)
 {
     const double sum = merged_sum(a, b);

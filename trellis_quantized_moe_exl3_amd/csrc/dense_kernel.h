@@ -686,12 +686,13 @@ MOE_DEV void dense_block(const DenseArgs &a, int block, LDS_AS uint16_t *const (
 // 32, 223; 4096 x 2048: 197, 194; with both in two of 64 they wait for the loads:
 // 304).  The gradients of the weights read both operands along their rows.
 //
-// The matrix cores are busy 62 to 71% of the CUs' time; the rest are waits at the
+// The matrix cores are busy 62 to 72% of the CUs' time; the rest are waits at the
 // stages' barriers, first loads and epilogues, which no other block covers, and
 // rounds that do not come out even (448 tiles on 256 CUs: 1.75 as 2).  4096 x 2048
-// bf16, forward 7168 tokens 194 us (1.24 PFLOP/s; 4104 x 2048: 223); 16384 tokens
-// with pre 460 us (1.20), dx 435 (1.26), dw 400 (1.37).  The library's bare products
-// of these sizes: 193, 367, 446 and 490 us, and 1.55 PFLOP/s for 8192^3.
+// bf16, forward 7168 tokens 190 to 200 us on different cards (1.20 to 1.27 PFLOP/s;
+// 4104 x 2048: 225); 16384 tokens with pre 452 to 463 us (1.19 to 1.22), dx 433 to
+// 455 (1.21 to 1.27), dw 405 to 426 (1.29 to 1.36).  The library's bare products of
+// these sizes: 193, 367, 446 and 490 us, and 1.55 PFLOP/s for 8192^3.
 template <int MODE, bool BF16, class S>
 __global__ __launch_bounds__(64 * S::NW, 2) void dense_kernel(DenseArgs a)
 {
