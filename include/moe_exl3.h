@@ -430,7 +430,8 @@ int moe_exl3_lora_workspace_size(const moe_exl3_lora_desc *desc, int64_t max_tok
 
 /*
  * y[t] = x[t] w^T + base[t] + scales[e] * b[e] (a[e] x[t]),  e = ids[t],
- * rounded once; a token with id -1 has no adapter.  x: device [T][K]; w:
+ * rounded once; a token with id -1 has no adapter (the stacks hold one at least:
+ * a plain projection takes ids of -1 beside them).  x: device [T][K]; w:
  * device [N][K], or NULL (no projection: the adapters alone, beside one that
  * is computed elsewhere); ids: device int32 [T], in any order (ids, scales and
  * ranks may be parts of longer arrays: 4-byte aligned); base: device
