@@ -452,6 +452,156 @@ int moe_exl3_lora_linear(const moe_exl3_lora_desc *desc, const void *x, int64_t 
                          const moe_exl3_lora_adapters *adapters, const int32_t *ids, const void *base, int64_t ldbase,
                          int64_t T, void *y, int64_t ldy, void *workspace, size_t ws_bytes, void *stream);
 
+/*
+ * Operators around the experts of a MoE layer whose experts are its user's own:
+ * tokens sorted by expert and back, dropout, and products with 4-bit weights.
+ * Together with a router (moe_exl3_route, or any other) they make a layer:
+ * sort, dispatch, the experts' products over the sorted rows (moe_exl3_w4_glu
+ * and moe_exl3_w4_linear for all experts in one call, or moe_exl3_glu and its
+ * backward pass for each), combine; and the same way back for the gradients.
+ *
+ * Types, row strides, overlaps and workspaces as for the dense operators; the
+ * 16-bit rows of tokens and the sorted ones may span any number of bytes.  The
+ * same inputs give the same bits on every call.
+ */
+typedef struct moe_exl3_tokens_desc {
+    int32_t hidden;      /* H, a multiple of 8, at most 65536 */
+    int32_t n_experts;   /* E, 1 .. 1024 */
+    int32_t top_k;       /* k, slots of a token, 1 .. 16 */
+    int32_t act_dtype;   /* MOE_EXL3_DT_F16 or MOE_EXL3_DT_BF16, of all rows */
+} moe_exl3_tokens_desc;
+
+/*
+ * Dropout from a counter-based generator: no mask is stored, a gradient's call
+ * draws the same numbers again.  rng: device uint64 [2], seed and offset, read
+ * when the call's work runs (a captured graph takes new ones from the same
+ * place) and never written.  Element (r, c) of a matrix with C columns owns 16
+ * bits: halfword c % 8 (low halves first) of Philox4x32-10 for the key `seed` and
+ * the counter offset + r ceil(C / 8) + c / 8, modulo 2^64, whose two low words come first; so a
+ * call on R rows takes R ceil(C / 8) counters, and the caller adds at least that
+ * to the offset before the next call that shall draw others.  An element is kept
+ * where its bits are >= n = round(65536 p), p rounded to the nearest multiple of
+ * 2^-16 (halves up), and then multiplied by 65536 / (65536 - n); a dropped one is a zero
+ * whatever it was (an infinity or a NaN too).  p = 0 keeps every element and p =
+ * 1 none.  rng is 8-byte aligned, and may be NULL where n is 0.
+ */
+typedef struct moe_exl3_drop {
+    double p;              /* 0 .. 1 */
+    const uint64_t *rng;
+} moe_exl3_drop;
+
+/* Workspace bytes of moe_exl3_sort for up to max_tokens. */
+int moe_exl3_sort_workspace_size(const moe_exl3_tokens_desc *desc, int64_t max_tokens, size_t *bytes);
+
+/*
+ * Tables of the slots a = t k + j sorted by expert, stably.  idx: device int32
+ * [T][k], a slot's expert or -1 (none); a token may name an expert twice.
+ * counts [E] and offsets [E + 1] (exclusive sums); sorted_ids [T k]: the slots
+ * in order, offsets[E] of them, what is behind stays as it was; pos [T k]: the
+ * inverse, -1 for a slot without expert.  counts and sorted_ids may be NULL.
+ * All 4-byte aligned.  T k < 2^31; T = 0 writes counts and offsets of zero.  The
+ * status word reports BAD_INDEX for an index outside [-1, E) (then as -1).
+ */
+int moe_exl3_sort(const moe_exl3_tokens_desc *desc, const int32_t *idx, int64_t T, int32_t *counts, int32_t *offsets,
+                  int32_t *sorted_ids, int32_t *pos, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Each token's row to its slots' sorted rows: out[pos[a]] = w[a] x[a / k], rounded
+ * once.  x: device [T][H]; out: device [rows][H]; pos: device int32 [T][k]; a slot
+ * whose pos is outside [0, rows) has no row (so -1, and rows past a capacity),
+ * the others' are distinct; rows that none names stay as they were.  w: device
+ * fp32 [T][k], weights on the experts' input, or NULL (1).  T < 2^31 and rows <
+ * 2^31, also below.
+ */
+int moe_exl3_dispatch(const moe_exl3_tokens_desc *desc, const void *x, int64_t ldx, const int32_t *pos, const float *w,
+                      int64_t T, int64_t rows, void *out, int64_t ldo, void *stream);
+
+/*
+ * Gradients of moe_exl3_dispatch: dx[t] = sum_j w[a] dout[pos[a]], in fp32 in
+ * order of j, rounded once (a token without rows: zeros), and dw[a] =
+ * <dout[pos[a]], x[t]> (device fp32 [T][k] or NULL; 0 for a slot without a row).
+ * dout: device [rows][H]; x is read for dw alone (NULL without it).
+ */
+int moe_exl3_dispatch_backward(const moe_exl3_tokens_desc *desc, const void *dout, int64_t lddo, const void *x,
+                               int64_t ldx, const int32_t *pos, const float *w, int64_t T, int64_t rows, void *dx,
+                               int64_t lddx, float *dw, void *stream);
+
+/*
+ * The sorted rows back at their tokens: y[t] = base[t] + D(sum_j w[a] z[pos[a]]),
+ * in fp32 in order of j, rounded once; D is the dropout `drop` of the [T][H] sums
+ * (NULL: none).  z: device [rows][H]; pos and w as for dispatch; base: device
+ * [T][H] (a shared expert, a residual) or NULL, may be y itself.
+ */
+int moe_exl3_combine(const moe_exl3_tokens_desc *desc, const void *z, int64_t ldz, const int32_t *pos, const float *w,
+                     const void *base, int64_t ldbase, const moe_exl3_drop *drop, int64_t T, int64_t rows, void *y,
+                     int64_t ldy, void *stream);
+
+/*
+ * Gradients of moe_exl3_combine from dy, with the same `drop` and numbers:
+ * dz[pos[a]] = w[a] D(dy[t]), rounded once (rows that no slot names stay as they
+ * were), and dw[a] = <D(dy[t]), z[pos[a]]> (device fp32 [T][k] or NULL; 0 for a
+ * slot without a row).  z is read for dw alone (NULL without it); dz may be z
+ * itself.  The gradient of base is dy.
+ */
+int moe_exl3_combine_backward(const moe_exl3_tokens_desc *desc, const void *dy, int64_t lddy, const void *z, int64_t ldz,
+                              const int32_t *pos, const float *w, const moe_exl3_drop *drop, int64_t T, int64_t rows,
+                              void *dz, int64_t lddz, float *dw, void *stream);
+
+/*
+ * y = residual + D(x), rounded once; with a gradient for x the same call gives
+ * D's gradient, D being its own.  x, y: device [rows][cols] of dtype F16, BF16 or F32, any
+ * row stride from cols up to 2^20; residual: the same or NULL.  y may be x or the
+ * residual itself (same address and stride).  `drop` is needed.
+ */
+int moe_exl3_dropout(int32_t dtype, const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                     const moe_exl3_drop *drop, int64_t rows, int64_t cols, void *y, int64_t ldy, void *stream);
+
+/*
+ * Products with 4-bit weights and group scales, W[n][k] = scale[n][k / group]
+ * (q[n][k] - zero[n][k / group]), dense or by expert.
+ */
+typedef struct moe_exl3_w4_desc {
+    int32_t n_in;        /* K, columns of x, a multiple of group */
+    int32_t n_out;       /* N, columns of the result, a multiple of 8 */
+    int32_t n_experts;   /* matrices in the stacks, 1 .. 1024 */
+    int32_t group;       /* k of one scale: 32, 64 or 128 */
+    int32_t act_dtype;   /* MOE_EXL3_DT_F16 or MOE_EXL3_DT_BF16, also of the scales */
+    int32_t act;         /* MOE_EXL3_ACT_*, of moe_exl3_w4_glu */
+} moe_exl3_w4_desc;
+
+/* A stack of matrices, device memory, contiguous. */
+typedef struct moe_exl3_w4 {
+    const void *codes;     /* uint8 [n_experts][N][K / 2]: q of k = 2 i in the low half of byte i,
+                              of 2 i + 1 in the high half */
+    const void *scales;    /* [n_experts][N][K / group] of act_dtype */
+    const uint8_t *zeros;  /* uint8 [n_experts][N][K / group], any value, or NULL: 8 */
+} moe_exl3_w4;
+
+/* Workspace bytes of moe_exl3_w4_linear and moe_exl3_w4_glu for up to max_rows. */
+int moe_exl3_w4_workspace_size(const moe_exl3_w4_desc *desc, int64_t max_rows, size_t *bytes);
+
+/*
+ * y[r] = x[r] W_e^T + base[r], rounded once, e the expert whose rows hold r:
+ * offsets[e] <= r < offsets[e + 1], as moe_exl3_sort and moe_exl3_route write them
+ * (device int32 [n_experts + 1], 4-byte aligned; with one expert NULL: every
+ * row).  Rows outside offsets[0] .. offsets[n_experts] stay as they were.  x:
+ * device [rows][K]; y: device [rows][N]; base: device [rows][N] or NULL, may be y
+ * itself.  Each matrix is below 2 GiB, the stacks may be larger.  The weights are not rounded: the
+ * products with q - zero are summed in fp32 for each group and its scale is applied
+ * there.  An element of x of magnitude 2^118 or more (an infinity among them) may make its row
+ * NaN; other rows do not see it.  Last bits may depend on the number of rows.
+ * The status word reports BAD_INDEX for offsets that descend or leave [0,
+ * rows]: they are clamped, and the rows concerned unspecified.
+ */
+int moe_exl3_w4_linear(const moe_exl3_w4_desc *desc, const void *x, int64_t ldx, const moe_exl3_w4 *w,
+                       const int32_t *offsets, const void *base, int64_t ldbase, int64_t rows, void *y, int64_t ldy,
+                       void *workspace, size_t ws_bytes, void *stream);
+
+/* h[r] = act(x[r] Wg_e^T) * (x[r] Wu_e^T), rounded once; otherwise as moe_exl3_w4_linear. */
+int moe_exl3_w4_glu(const moe_exl3_w4_desc *desc, const void *x, int64_t ldx, const moe_exl3_w4 *w_gate,
+                    const moe_exl3_w4 *w_up, const int32_t *offsets, int64_t rows, void *h, int64_t ldh,
+                    void *workspace, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,7 +30,10 @@ EXPORTS = ("moe_exl3_version", "moe_exl3_strerror", "moe_exl3_workspace_size",
            "moe_exl3_layer", "moe_exl3_layer_profiled", "moe_exl3_route", "moe_exl3_decode",
            "moe_exl3_repack", "moe_exl3_expand_block_scales", "moe_exl3_layer_noalloc",
            "moe_exl3_glu_workspace_size", "moe_exl3_glu_backward_workspace_size", "moe_exl3_glu",
-           "moe_exl3_glu_backward", "moe_exl3_lora_workspace_size", "moe_exl3_lora_linear")
+           "moe_exl3_glu_backward", "moe_exl3_lora_workspace_size", "moe_exl3_lora_linear",
+           "moe_exl3_sort_workspace_size", "moe_exl3_sort", "moe_exl3_dispatch", "moe_exl3_dispatch_backward",
+           "moe_exl3_combine", "moe_exl3_combine_backward", "moe_exl3_dropout", "moe_exl3_w4_workspace_size",
+           "moe_exl3_w4_linear", "moe_exl3_w4_glu")
 ACT_SILU, ACT_GELU_TANH = 0, 1
 SCRATCH_BYTES = 64 << 20
 ORDER_ROWMAJOR, ORDER_COLMAJOR, ORDER_COLGROUPS128 = 0, 1, 2
@@ -65,6 +68,23 @@ class LoraDesc(C.Structure):
 
 class LoraAdapters(C.Structure):
     _fields_ = [("a", C.c_void_p), ("b", C.c_void_p), ("scales", C.c_void_p), ("ranks", C.c_void_p)]
+
+
+class TokensDesc(C.Structure):
+    _fields_ = [("hidden", C.c_int32), ("n_experts", C.c_int32), ("top_k", C.c_int32), ("act_dtype", C.c_int32)]
+
+
+class Drop(C.Structure):
+    _fields_ = [("p", C.c_double), ("rng", C.c_void_p)]
+
+
+class W4Desc(C.Structure):
+    _fields_ = [("n_in", C.c_int32), ("n_out", C.c_int32), ("n_experts", C.c_int32), ("group", C.c_int32),
+                ("act_dtype", C.c_int32), ("act", C.c_int32)]
+
+
+class W4Weights(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("zeros", C.c_void_p)]
 
 
 class MoeError(RuntimeError):
@@ -115,8 +135,19 @@ def lib():
         l.moe_exl3_lora_linear.argtypes = [
             C.POINTER(LoraDesc), C.c_void_p, C.c_int64, C.c_void_p, C.POINTER(LoraAdapters), C.c_void_p, C.c_void_p,
             C.c_int64, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_size_t, C.c_void_p]
-        for f in ("moe_exl3_glu_workspace_size", "moe_exl3_glu_backward_workspace_size", "moe_exl3_glu",
-                  "moe_exl3_glu_backward", "moe_exl3_lora_workspace_size", "moe_exl3_lora_linear"):
+        p, i, z = C.c_void_p, C.c_int64, C.c_size_t
+        td, dr, wd, ww = C.POINTER(TokensDesc), C.POINTER(Drop), C.POINTER(W4Desc), C.POINTER(W4Weights)
+        l.moe_exl3_sort_workspace_size.argtypes = [td, i, C.POINTER(z)]
+        l.moe_exl3_sort.argtypes = [td, p, i, p, p, p, p, p, z, p]
+        l.moe_exl3_dispatch.argtypes = [td, p, i, p, p, i, i, p, i, p]
+        l.moe_exl3_dispatch_backward.argtypes = [td, p, i, p, i, p, p, i, i, p, i, p, p]
+        l.moe_exl3_combine.argtypes = [td, p, i, p, p, p, i, dr, i, i, p, i, p]
+        l.moe_exl3_combine_backward.argtypes = [td, p, i, p, i, p, p, dr, i, i, p, i, p, p]
+        l.moe_exl3_dropout.argtypes = [C.c_int32, p, i, p, i, dr, i, i, p, i, p]
+        l.moe_exl3_w4_workspace_size.argtypes = [wd, i, C.POINTER(z)]
+        l.moe_exl3_w4_linear.argtypes = [wd, p, i, ww, p, p, i, i, p, i, p, z, p]
+        l.moe_exl3_w4_glu.argtypes = [wd, p, i, ww, ww, p, i, p, i, p, z, p]
+        for f in EXPORTS[EXPORTS.index("moe_exl3_glu_workspace_size"):]:
             getattr(l, f).restype = C.c_int
         for f in ("moe_exl3_workspace_size", "moe_exl3_layer", "moe_exl3_layer_profiled",
                   "moe_exl3_route", "moe_exl3_decode", "moe_exl3_repack", "moe_exl3_expand_block_scales",
@@ -467,3 +498,229 @@ def lora_linear(desc: LoraDesc, x, w, lora_a, lora_b, ids, out, workspace, base=
     _check(lib().moe_exl3_lora_linear(C.byref(desc), x.data_ptr(), ldx, _ptr(w), C.byref(ad), ids.data_ptr(),
                                       _ptr(base), ldb, T, out.data_ptr(), ldy, workspace.data_ptr(),
                                       workspace.nbytes, _stream(stream, d)), "moe_exl3_lora_linear")
+
+
+# ---- operators around a MoE layer's own experts: sort, dispatch, combine,
+# dropout, products with 4-bit weights
+
+
+def make_tokens_desc(hidden: int, n_experts: int, top_k: int, act_dtype: int = DT_BF16) -> TokensDesc:
+    return TokensDesc(hidden, n_experts, top_k, act_dtype)
+
+
+def make_w4_desc(n_in: int, n_out: int, n_experts: int = 1, group: int = 128, act_dtype: int = DT_BF16,
+                 act: int = ACT_SILU) -> W4Desc:
+    return W4Desc(n_in, n_out, n_experts, group, act_dtype, act)
+
+
+def sort_workspace_size(desc: TokensDesc, max_tokens: int) -> int:
+    return _size("moe_exl3_sort_workspace_size", desc, max_tokens)
+
+
+def w4_workspace_size(desc: W4Desc, max_rows: int) -> int:
+    return _size("moe_exl3_w4_workspace_size", desc, max_rows)
+
+
+def _call_device(x, stream, what: str) -> int:
+    """The GPU of a call without a workspace: that of x, which must be the
+    current one, and of the stream."""
+    d = x.get_device()   # below 0: not on a GPU
+    if d < 0 or d != _torch().cuda.current_device():
+        raise ValueError(f"{what}: tensors must be on the current GPU, got {x.device}")
+    if stream is not None and stream.device != x.device:
+        raise ValueError(f"{what}: a stream of {stream.device}, tensors on {x.device}")
+    return d
+
+
+def _table(t, n: int, dtype, device: int, what: str) -> None:
+    """A contiguous table of n entries, of any shape."""
+    if t.numel() != n or t.dtype != dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous {dtype} on GPU {device}, got {tuple(t.shape)} {t.dtype} on "
+                         f"{t.device}")
+
+
+def _drop(p: float, rng, device: int, what: str):
+    """The dropout argument of a call (None: nothing is dropped)."""
+    if p == 0 and rng is None:
+        return None
+    if rng is None:
+        raise ValueError(f"{what}: dropout needs rng, two int64 on the GPU (seed and offset)")
+    torch = _torch()
+    if rng.numel() != 2 or rng.dtype not in (torch.int64, torch.uint64) or rng.get_device() != device \
+            or not rng.is_contiguous():
+        raise ValueError(f"{what}: rng must be two contiguous int64 (seed, offset) on GPU {device}")
+    return C.byref(Drop(p, rng.data_ptr()))
+
+
+def sort(desc: TokensDesc, idx, counts, offsets, sorted_ids, pos, workspace, stream=None) -> None:
+    """Tables of the slots sorted by expert (moe_exl3_sort).  idx int32 [T][k]
+    (-1: no expert); counts [E] or None, offsets [E + 1], sorted_ids [T k] or
+    None, pos [T k]: int32, written.  status(workspace) reports indexes out of
+    range."""
+    i32 = _torch().int32
+    d = _dense_device(idx, workspace, stream, "sort")
+    E, k = desc.n_experts, desc.top_k
+    T = idx.shape[0]
+    _whole(idx, (T, k), (i32,), d, "sort: idx")
+    _table(offsets, E + 1, i32, d, "sort: offsets")
+    _table(pos, T * k, i32, d, "sort: pos")
+    if counts is not None:
+        _table(counts, E, i32, d, "sort: counts")
+    if sorted_ids is not None:
+        _table(sorted_ids, T * k, i32, d, "sort: sorted_ids")
+    _check(lib().moe_exl3_sort(C.byref(desc), idx.data_ptr(), T, _ptr(counts), offsets.data_ptr(), _ptr(sorted_ids),
+                               pos.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream, d)),
+           "moe_exl3_sort")
+
+
+def _slots(desc: TokensDesc, T: int, pos, w, dw, device: int, what: str) -> None:
+    torch = _torch()
+    _table(pos, T * desc.top_k, torch.int32, device, what + ": pos")
+    if w is not None:
+        _table(w, T * desc.top_k, torch.float32, device, what + ": w")
+    if dw is not None:
+        _table(dw, T * desc.top_k, torch.float32, device, what + ": dw")
+
+
+def dispatch(desc: TokensDesc, x, pos, out, w=None, stream=None) -> None:
+    """out[pos[a]] = w[a] x[a // k] (moe_exl3_dispatch).  x [T][hidden], out
+    [rows][hidden]; pos int32 and w fp32 (or None) [T][k]."""
+    d = _call_device(x, stream, "dispatch")
+    types, T, H = _dense_dtypes(desc.act_dtype), x.shape[0], desc.hidden
+    ldx = _rows(x, T, H, types, d, "dispatch: x")
+    ldo = _rows(out, out.shape[0], H, types, d, "dispatch: out")
+    _slots(desc, T, pos, w, None, d, "dispatch")
+    _check(lib().moe_exl3_dispatch(C.byref(desc), x.data_ptr(), ldx, pos.data_ptr(), _ptr(w), T, out.shape[0],
+                                   out.data_ptr(), ldo, _stream(stream, d)), "moe_exl3_dispatch")
+
+
+def dispatch_backward(desc: TokensDesc, dout, x, pos, dx, w=None, dw=None, stream=None) -> None:
+    """Gradients of dispatch() from dout [rows][hidden]: dx [T][hidden], and dw
+    fp32 [T][k] where it is given (x is read for it alone, else maybe None)."""
+    d = _call_device(dx, stream, "dispatch_backward")
+    types, T, H = _dense_dtypes(desc.act_dtype), dx.shape[0], desc.hidden
+    lddx = _rows(dx, T, H, types, d, "dispatch_backward: dx")
+    lddo = _rows(dout, dout.shape[0], H, types, d, "dispatch_backward: dout")
+    ldx = H
+    if x is not None:
+        ldx = _rows(x, T, H, types, d, "dispatch_backward: x")
+    _slots(desc, T, pos, w, dw, d, "dispatch_backward")
+    _check(lib().moe_exl3_dispatch_backward(C.byref(desc), dout.data_ptr(), lddo, _ptr(x), ldx, pos.data_ptr(), _ptr(w),
+                                            T, dout.shape[0], dx.data_ptr(), lddx, _ptr(dw), _stream(stream, d)),
+           "moe_exl3_dispatch_backward")
+
+
+def combine(desc: TokensDesc, z, pos, y, w=None, base=None, p: float = 0.0, rng=None, stream=None) -> None:
+    """y[t] = base[t] + D(sum_j w[a] z[pos[a]]) (moe_exl3_combine), D dropout with
+    probability p from rng (int64 {seed, offset} on the GPU).  z [rows][hidden],
+    y and base [T][hidden]; pos int32 and w fp32 (or None) [T][k]."""
+    d = _call_device(y, stream, "combine")
+    types, T, H = _dense_dtypes(desc.act_dtype), y.shape[0], desc.hidden
+    ldy, ldz = _rows(y, T, H, types, d, "combine: y"), _rows(z, z.shape[0], H, types, d, "combine: z")
+    ldb = H
+    if base is not None:
+        ldb = _rows(base, T, H, types, d, "combine: base")
+    _slots(desc, T, pos, w, None, d, "combine")
+    _check(lib().moe_exl3_combine(C.byref(desc), z.data_ptr(), ldz, pos.data_ptr(), _ptr(w), _ptr(base), ldb,
+                                  _drop(p, rng, d, "combine"), T, z.shape[0], y.data_ptr(), ldy, _stream(stream, d)),
+           "moe_exl3_combine")
+
+
+def combine_backward(desc: TokensDesc, dy, z, pos, dz, w=None, dw=None, p: float = 0.0, rng=None, stream=None) -> None:
+    """Gradients of combine() from dy [T][hidden], with the p and rng of its call:
+    dz [rows][hidden] (may be z itself), and dw fp32 [T][k] where it is given (z
+    is read for it alone, else maybe None)."""
+    d = _call_device(dy, stream, "combine_backward")
+    types, T, H = _dense_dtypes(desc.act_dtype), dy.shape[0], desc.hidden
+    rows = dz.shape[0]
+    lddy, lddz = _rows(dy, T, H, types, d, "combine_backward: dy"), _rows(dz, rows, H, types, d, "combine_backward: dz")
+    ldz = H
+    if z is not None:
+        ldz = _rows(z, rows, H, types, d, "combine_backward: z")
+    _slots(desc, T, pos, w, dw, d, "combine_backward")
+    _check(lib().moe_exl3_combine_backward(C.byref(desc), dy.data_ptr(), lddy, _ptr(z), ldz, pos.data_ptr(), _ptr(w),
+                                           _drop(p, rng, d, "combine_backward"), T, rows, dz.data_ptr(), lddz, _ptr(dw),
+                                           _stream(stream, d)), "moe_exl3_combine_backward")
+
+
+def dropout(x, y, p: float, rng, residual=None, stream=None) -> None:
+    """y = residual + D(x) (moe_exl3_dropout), D dropout with probability p from
+    rng (int64 {seed, offset} on the GPU); with a gradient for x, D's gradient.  x,
+    y, residual: [rows][cols] bf16, fp16 or fp32."""
+    torch = _torch()
+    d = _call_device(x, stream, "dropout")
+    dt = {torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32}.get(x.dtype)
+    if dt is None or x.dim() != 2:
+        raise ValueError(f"dropout: x must be [rows][cols] bf16, fp16 or fp32, got {tuple(x.shape)} {x.dtype}")
+    rows, cols = x.shape
+    types = (x.dtype,)
+    ldx, ldy, ldr = _rows(x, rows, cols, types, d, "dropout: x"), _rows(y, rows, cols, types, d, "dropout: y"), cols
+    if residual is not None:
+        ldr = _rows(residual, rows, cols, types, d, "dropout: residual")
+    drop = _drop(p, rng, d, "dropout") or C.byref(Drop(0.0, None))
+    _check(lib().moe_exl3_dropout(dt, x.data_ptr(), ldx, _ptr(residual), ldr, drop, rows, cols, y.data_ptr(), ldy,
+                                  _stream(stream, d)), "moe_exl3_dropout")
+
+
+class W4:
+    """A stack of 4-bit matrices: codes uint8 [E][N][K / 2], scales [E][N][K /
+    group] of the activations' dtype, zeros uint8 [E][N][K / group] or None (8).
+    One matrix may leave out E.  Holds its tensors."""
+
+    def __init__(self, codes, scales, zeros=None):
+        self.codes, self.scales, self.zeros = (
+            t if t is None or t.dim() == 3 else t[None] for t in (codes, scales, zeros))
+        self.weights = W4Weights(self.codes.data_ptr(), self.scales.data_ptr(), _ptr(self.zeros))
+        self._checked = None
+
+    def check(self, desc: W4Desc, device: int, what: str):
+        key = (desc.n_in, desc.n_out, desc.n_experts, desc.group, desc.act_dtype, device)
+        if self._checked != key:
+            u8 = (_torch().uint8,)
+            E, N, K, G = desc.n_experts, desc.n_out, desc.n_in, max(1, desc.group)
+            _whole(self.codes, (E, N, K // 2), u8, device, what + ": codes")
+            _whole(self.scales, (E, N, K // G), _dense_dtypes(desc.act_dtype), device, what + ": scales")
+            if self.zeros is not None:
+                _whole(self.zeros, (E, N, K // G), u8, device, what + ": zeros")
+            self._checked = key
+        return C.byref(self.weights)
+
+
+def make_w4(codes, scales, zeros=None) -> W4:
+    return W4(codes, scales, zeros)
+
+
+def _w4_offsets(desc: W4Desc, offsets, device: int, what: str):
+    if offsets is not None:
+        _table(offsets, desc.n_experts + 1, _torch().int32, device, what + ": offsets")
+    elif desc.n_experts != 1:
+        raise ValueError(f"{what}: {desc.n_experts} experts need offsets")
+    return _ptr(offsets)
+
+
+def w4_linear(desc: W4Desc, x, w: W4, y, workspace, offsets=None, base=None, stream=None) -> None:
+    """y[r] = x[r] W_e^T + base[r] with 4-bit weights (moe_exl3_w4_linear), e the
+    expert of row r: offsets[e] <= r < offsets[e + 1] (int32 [E + 1]; None: one
+    expert).  x [rows][n_in], y and base [rows][n_out].  status(workspace)
+    reports offsets that descend or leave the rows."""
+    d = _dense_device(x, workspace, stream, "w4_linear")
+    types, R = _dense_dtypes(desc.act_dtype), x.shape[0]
+    ldx, ldy = _rows(x, R, desc.n_in, types, d, "w4_linear: x"), _rows(y, R, desc.n_out, types, d, "w4_linear: y")
+    ldb = desc.n_out
+    if base is not None:
+        ldb = _rows(base, R, desc.n_out, types, d, "w4_linear: base")
+    _check(lib().moe_exl3_w4_linear(C.byref(desc), x.data_ptr(), ldx, w.check(desc, d, "w4_linear"),
+                                    _w4_offsets(desc, offsets, d, "w4_linear"), _ptr(base), ldb, R, y.data_ptr(), ldy,
+                                    workspace.data_ptr(), workspace.nbytes, _stream(stream, d)), "moe_exl3_w4_linear")
+
+
+def w4_glu(desc: W4Desc, x, w_gate: W4, w_up: W4, h, workspace, offsets=None, stream=None) -> None:
+    """h[r] = act(x[r] Wg_e^T) * (x[r] Wu_e^T) with 4-bit weights
+    (moe_exl3_w4_glu); otherwise as w4_linear()."""
+    d = _dense_device(x, workspace, stream, "w4_glu")
+    types, R = _dense_dtypes(desc.act_dtype), x.shape[0]
+    ldx, ldh = _rows(x, R, desc.n_in, types, d, "w4_glu: x"), _rows(h, R, desc.n_out, types, d, "w4_glu: h")
+    _check(lib().moe_exl3_w4_glu(C.byref(desc), x.data_ptr(), ldx, w_gate.check(desc, d, "w4_glu: w_gate"),
+                                 w_up.check(desc, d, "w4_glu: w_up"), _w4_offsets(desc, offsets, d, "w4_glu"), R,
+                                 h.data_ptr(), ldh, workspace.data_ptr(), workspace.nbytes, _stream(stream, d)),
+           "moe_exl3_w4_glu")

@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmoe_exl3.so")
 SOURCES = ["route.hip", "decode.hip", "gemv.hip", "mfma.hip", "mfma8.hip", "combine.hip", "moe_exl3.cpp",
-           "glu.hip", "lora.hip", "dense.cpp"]
+           "glu.hip", "lora.hip", "dense.cpp", "tokens.hip", "tokens.cpp", "w4.hip", "w4.cpp"]
 # the benchmark's streaming-read probe (achievable HBM bandwidth), a library of its own
 BW_SOURCE = "bw_probe.hip"
 BW_LIB = os.path.join(HERE, "libmoe_exl3_bw.so")
@@ -47,7 +47,7 @@ def build(verbose: bool = False) -> str:
         procs = []
         objs = []
         for src in SOURCES:
-            obj = os.path.join(tmpdir, src.rsplit(".", 1)[0] + ".o")
+            obj = os.path.join(tmpdir, src + ".o")
             cmd = [cc, *flags(), "-c", os.path.join(CSRC, src), "-o", obj]
             if verbose:
                 print(" ".join(cmd), flush=True)

@@ -1,5 +1,6 @@
 // Host side of the dense operators: argument checks, workspace plans, launch
 // sequences.  Declarations and the full contract are in include/moe_exl3.h.
+#include "args.h"
 #include "dense.h"
 
 #include <algorithm>
@@ -9,80 +10,12 @@ using namespace moe;
 
 namespace {
 
-constexpr size_t kAlign = 256;
-constexpr int64_t kMaxSize = 65536;
-constexpr int64_t kMaxLd = 1 << 20;
-constexpr int64_t kSpanLimit = (int64_t)1 << 31;
-
 // k splits of 64 x 64 tiles: at most this many blocks (one a CU), and at most one
 // for each this many stages (256 k; the last split takes what is left).
 constexpr int64_t kSplitBlocks = 256;
 constexpr int64_t kSplitStages = 4;
 // Adapters that a call is taken to name at most (plan_tiles).
 constexpr int64_t kMostNamed = 64;
-
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-template <class T>
-T *at(void *ws, size_t off)
-{
-    return (T *)((char *)ws + off);
-}
-
-// A row-major 16-bit matrix argument.
-struct Mat {
-    const void *p;
-    int64_t rows, cols, ld;
-    int64_t span() const { return rows > 0 ? ((rows - 1) * ld + cols) * 2 : 0; }
-};
-
-// The rules of one matrix: address, row stride, extent.
-int check_mat(const Mat &m)
-{
-    if (m.rows == 0)
-        return MOE_EXL3_OK;
-    if (!m.p || m.ld < m.cols)
-        return MOE_EXL3_ERR_INVALID_ARG;
-    if (m.ld > kMaxLd)
-        return MOE_EXL3_ERR_UNSUPPORTED;
-    if (!aligned16(m.p) || m.ld % 8)
-        return MOE_EXL3_ERR_MISALIGNED;
-    if (m.rows > kSpanLimit || m.span() >= kSpanLimit)
-        return MOE_EXL3_ERR_UNSUPPORTED;
-    return MOE_EXL3_OK;
-}
-
-bool spans_meet(const void *a, int64_t an, const void *b, int64_t bn)
-{
-    return an > 0 && bn > 0 && (uintptr_t)a < (uintptr_t)b + (uint64_t)bn && (uintptr_t)b < (uintptr_t)a + (uint64_t)an;
-}
-
-// Whether two matrices share an element: their spans meet, unless they are
-// column ranges apart of one buffer (same ld).
-bool overlap(const Mat &a, const Mat &b)
-{
-    if (!a.p || !b.p || !spans_meet(a.p, a.span(), b.p, b.span()))
-        return false;
-    if (a.ld != b.ld)
-        return true;
-    const int64_t d = ((intptr_t)b.p - (intptr_t)a.p) / 2;
-    const int64_t r = ((d % a.ld) + a.ld) % a.ld;   // b's first column, from a's
-    return !(r >= a.cols && r + b.cols <= a.ld);
-}
-
-int check_dtype(int dt)
-{
-    return dt == MOE_EXL3_DT_F16 || dt == MOE_EXL3_DT_BF16 ? MOE_EXL3_OK : MOE_EXL3_ERR_UNSUPPORTED;
-}
-
-int check_size(int64_t v)
-{
-    if (v <= 0 || v % 8)
-        return MOE_EXL3_ERR_INVALID_ARG;
-    return v > kMaxSize ? MOE_EXL3_ERR_UNSUPPORTED : MOE_EXL3_OK;
-}
 
 int check_desc(const moe_exl3_glu_desc *d)
 {
@@ -306,15 +239,6 @@ LoraPlan plan_lora(const moe_exl3_lora_desc &d, int64_t T)
     o += T <= kSkinnyTokens ? 0 : align_up(part_bound(DENSE_LIN, T, d.n_out, d.n_in));
     p.total = o;
     return p;
-}
-
-int check_ws(const void *ws, size_t have, size_t need)
-{
-    if (!ws)
-        return MOE_EXL3_ERR_INVALID_ARG;
-    if ((uintptr_t)ws % kAlign)
-        return MOE_EXL3_ERR_MISALIGNED;
-    return have < need ? MOE_EXL3_ERR_WORKSPACE : MOE_EXL3_OK;
 }
 
 }  // namespace

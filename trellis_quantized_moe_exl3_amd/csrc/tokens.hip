@@ -1,0 +1,437 @@
+// Tokens sorted by expert and back, with weights and gradients, and dropout.
+#include "dense_gemm.h"
+#include "philox.h"
+#include "tokens.h"
+
+namespace moe {
+
+// ---------------------------------------------------------------- sort
+// Stable counting sort of the slots by expert.  A block holds kSortChunk slots,
+// a wavefront a run of them; slots of one expert in 64 consecutive ones are
+// ranked from ballots over the index bits, earlier ones from the wavefront's
+// counts, earlier wavefronts from theirs, and earlier blocks from the counts
+// that a first launch left.  No atomics: the tables are the same on each call.
+constexpr int kSortWaves = 16;
+constexpr int kSortIter = kSortChunk / kSortWaves / 64;
+
+MOE_DEV int scan64(int v, int l)   // inclusive, over a wavefront
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d, 64);
+        v += l >= d ? o : 0;
+    }
+    return v;
+}
+
+// counts[e] of the chunk and, at E, its slots with a bad index
+__global__ __launch_bounds__(1024) void sort_count_kernel(SortArgs a)
+{
+    extern __shared__ int32_t cnt[];
+    for (int e = threadIdx.x; e <= a.E; e += 1024)
+        cnt[e] = 0;
+    __syncthreads();
+    const int64_t a0 = (int64_t)blockIdx.x * kSortChunk;
+#pragma unroll
+    for (int i = 0; i < kSortChunk / 1024; ++i) {
+        const int64_t s = a0 + 1024 * i + threadIdx.x;
+        if (s < a.n) {
+            const int e = a.idx[s];
+            if (e != -1)
+                atomicAdd(&cnt[(unsigned)e < (unsigned)a.E ? e : a.E], 1);
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e <= a.E; e += 1024)
+        a.hist[(int64_t)blockIdx.x * (a.E + 1) + e] = cnt[e];
+}
+
+// counts of the blocks -> sums of the blocks before, the last row of all
+__global__ __launch_bounds__(64) void sort_scan_kernel(SortArgs a)
+{
+    const int e = blockIdx.x, l = threadIdx.x;
+    int run = 0;
+    for (int b0 = 0; b0 < a.nblk; b0 += 64) {
+        const int b = b0 + l;
+        int32_t *p = a.hist + (int64_t)b * (a.E + 1) + e;
+        const int v = b < a.nblk ? *p : 0;
+        const int s = scan64(v, l);
+        if (b < a.nblk)
+            *p = run + s - v;
+        run += __shfl(s, 63, 64);
+    }
+    if (l == 0)
+        a.hist[(int64_t)a.nblk * (a.E + 1) + e] = run;
+}
+
+__global__ __launch_bounds__(1024) void sort_kernel(SortArgs a)
+{
+    extern __shared__ int32_t first[];                          // [E]
+    uint16_t *cnt = (uint16_t *)(first + a.E);                  // [kSortWaves][E]
+    __shared__ int wsum[kSortWaves];
+    __shared__ int bad;
+    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63;
+    const int E = a.E, blk = blockIdx.x;
+    for (int i = tid; i < kSortWaves * E; i += 1024)
+        cnt[i] = 0;
+    if (tid == 0)
+        bad = 0;
+    int nbits = 0;
+    while ((1 << nbits) < E)
+        ++nbits;
+    const int64_t s0 = (int64_t)blk * kSortChunk + w * (64 * kSortIter) + l;
+    int ev[kSortIter], rank[kSortIter];
+#pragma unroll
+    for (int c = 0; c < kSortIter; ++c)
+        ev[c] = s0 + 64 * c < a.n ? a.idx[s0 + 64 * c] : -1;
+    __syncthreads();
+    uint16_t *mine = cnt + w * E;
+    bool wrong = false;
+#pragma unroll
+    for (int c = 0; c < kSortIter; ++c) {
+        const int e = ev[c];
+        const bool valid = (unsigned)e < (unsigned)E;
+        wrong |= !valid && e != -1;
+        uint64_t m = __ballot(valid);
+        for (int b = 0; b < nbits; ++b) {
+            const bool bit = (e >> b) & 1;
+            const uint64_t bb = __ballot(bit);
+            m &= bit ? bb : ~bb;
+        }
+        rank[c] = valid ? mine[e] + __popcll(m & ((1ull << l) - 1)) : 0;
+        wave_lds_fence();
+        if (valid && (m >> l) == 1ull)   // the last lane of its expert
+            mine[e] += (uint16_t)__popcll(m);
+        wave_lds_fence();
+    }
+    if (wrong)
+        bad = 1;
+    __syncthreads();
+    // per expert: the wavefronts' counts -> their sums before, the chunk's total
+    int own = 0, total = 0, before = 0;
+    if (tid < E)
+        for (int v = 0; v < kSortWaves; ++v) {
+            const int t = cnt[v * E + tid];
+            cnt[v * E + tid] = (uint16_t)own;
+            own += t;
+        }
+    const int64_t row = E + 1;
+    if (a.nblk == 1) {
+        total = own;
+    } else if (tid < E) {
+        if (a.nblk > kSortScan) {
+            before = a.hist[blk * row + tid];
+            total = a.hist[a.nblk * row + tid];
+        } else {
+            for (int b = 0; b < a.nblk; ++b) {
+                const int v = a.hist[b * row + tid];
+                total += v;
+                before += b < blk ? v : 0;
+            }
+        }
+    }
+    const int incl = scan64(total, l);
+    if (l == 63)
+        wsum[w] = incl;
+    __syncthreads();
+    int off = incl - total;
+    for (int v = 0; v < w; ++v)
+        off += wsum[v];
+    if (tid < E)
+        first[tid] = off + before;
+    if (blk == 0) {
+        if (tid < E) {
+            a.offsets[tid] = off;
+            if (tid == E - 1)
+                a.offsets[E] = off + total;
+            if (a.counts)
+                a.counts[tid] = total;
+        }
+        if (tid == 0) {
+            int faults = a.nblk == 1 ? bad : 0;
+            for (int b = a.nblk > kSortScan ? a.nblk : 0; a.nblk > 1 && b < (a.nblk > kSortScan ? a.nblk + 1 : a.nblk); ++b)
+                faults |= a.hist[b * row + E];
+            *a.status = faults ? MOE_EXL3_STATUS_BAD_INDEX : 0;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < kSortIter; ++c) {
+        const int64_t s = s0 + 64 * c;
+        if (s >= a.n)
+            break;
+        const int e = ev[c];
+        int p = -1;
+        if ((unsigned)e < (unsigned)E) {
+            p = first[e] + cnt[w * E + e] + rank[c];
+            if (a.sorted)
+                a.sorted[p] = (int32_t)s;
+        }
+        a.pos[s] = p;
+    }
+}
+
+hipError_t launch_sort(const SortArgs &a, hipStream_t s)
+{
+    if (a.nblk > 1) {
+        sort_count_kernel<<<(unsigned)a.nblk, 1024, (a.E + 1) * sizeof(int32_t), s>>>(a);
+        if (a.nblk > kSortScan)
+            sort_scan_kernel<<<(unsigned)(a.E + 1), 64, 0, s>>>(a);
+    }
+    sort_kernel<<<(unsigned)a.nblk, 1024, a.E * sizeof(int32_t) + kSortWaves * a.E * sizeof(uint16_t), s>>>(a);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- rows
+template <bool BF16>
+MOE_DEV void unpack8(u32x4 r, float (&v)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = act_to_f32<BF16>((uint16_t)r[j]);
+        v[2 * j + 1] = act_to_f32<BF16>((uint16_t)(r[j] >> 16));
+    }
+}
+
+template <bool BF16>
+MOE_DEV u32x4 round8(const float (&v)[8])
+{
+    return (u32x4){pack16<BF16>(v[0], v[1]), pack16<BF16>(v[2], v[3]), pack16<BF16>(v[4], v[5]),
+                   pack16<BF16>(v[6], v[7])};
+}
+
+// The products' sums of a block's lanes -> dw, in a fixed order.
+template <int KB>
+MOE_DEV void store_dots(const TokenArgs &a, int64_t t, const float (&dot)[KB])
+{
+    __shared__ float part[4][KB];
+    const int w = threadIdx.x >> 6, l = threadIdx.x & 63, nw = blockDim.x >> 6;
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+        float v = dot[j];
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1)
+            v += __shfl_xor(v, d, 64);
+        if (l == 0)
+            part[w][j] = v;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < a.k) {
+        float v = part[0][threadIdx.x];
+        for (int i = 1; i < nw; ++i)
+            v += part[i][threadIdx.x];
+        a.dw[t * a.k + threadIdx.x] = v;
+    }
+}
+
+// One block per token.
+template <bool BF16, int KB, bool DOT>
+__global__ __launch_bounds__(256) void spread_kernel(TokenArgs a)
+{
+    const int64_t t = blockIdx.x;
+    int pos[KB];
+    float w[KB], dot[KB];
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+        pos[j] = j < a.k ? a.pos[t * a.k + j] : -1;
+        if ((uint32_t)pos[j] >= (uint64_t)a.rows)
+            pos[j] = -1;
+        w[j] = j < a.k && a.w ? a.w[t * a.k + j] : 1.0f;
+        dot[j] = 0.0f;
+    }
+    const uint64_t groups = (uint64_t)(a.H / 8);
+    uint64_t seed = 0, offset = 0;
+    if (a.drop.rng) {
+        seed = a.drop.rng[0];
+        offset = a.drop.rng[1] + t * groups;
+    }
+    for (int c = threadIdx.x; c < a.H / 8; c += blockDim.x) {
+        float x[8];
+        unpack8<BF16>(*(const u32x4 *)(a.x + t * a.ldx + 8 * c), x);
+        u32x4 z[KB];
+        if constexpr (DOT)
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+                if (pos[j] >= 0)
+                    z[j] = *(const u32x4 *)(a.z + pos[j] * a.ldz + 8 * c);
+        if (a.drop.rng)
+            drop8(a.drop, seed, offset + c, x);
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            if (pos[j] < 0)
+                continue;
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = w[j] * x[i];
+            *(u32x4 *)(a.out + pos[j] * a.ldo + 8 * c) = round8<BF16>(v);
+            if constexpr (DOT) {
+                unpack8<BF16>(z[j], v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    dot[j] = fmaf(x[i], v[i], dot[j]);
+            }
+        }
+    }
+    if constexpr (DOT)
+        store_dots<KB>(a, t, dot);
+}
+
+template <bool BF16, int KB, bool DOT>
+__global__ __launch_bounds__(256) void gather_kernel(TokenArgs a)
+{
+    const int64_t t = blockIdx.x;
+    int pos[KB];
+    float w[KB], dot[KB];
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+        pos[j] = j < a.k ? a.pos[t * a.k + j] : -1;
+        if ((uint32_t)pos[j] >= (uint64_t)a.rows)
+            pos[j] = -1;
+        w[j] = j < a.k && a.w ? a.w[t * a.k + j] : 1.0f;
+        dot[j] = 0.0f;
+    }
+    const uint64_t groups = (uint64_t)(a.H / 8);
+    uint64_t seed = 0, offset = 0;
+    if (a.drop.rng) {
+        seed = a.drop.rng[0];
+        offset = a.drop.rng[1] + t * groups;
+    }
+    for (int c = threadIdx.x; c < a.H / 8; c += blockDim.x) {
+        u32x4 z[KB];
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+            if (pos[j] >= 0)
+                z[j] = *(const u32x4 *)(a.z + pos[j] * a.ldz + 8 * c);
+        float x[8], y[8];
+        if constexpr (DOT)
+            unpack8<BF16>(*(const u32x4 *)(a.x + t * a.ldx + 8 * c), x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            y[i] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            if (pos[j] < 0)
+                continue;
+            float v[8];
+            unpack8<BF16>(z[j], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                y[i] = fmaf(w[j], v[i], y[i]);
+                if constexpr (DOT)
+                    dot[j] = fmaf(x[i], v[i], dot[j]);
+            }
+        }
+        if (a.drop.rng)
+            drop8(a.drop, seed, offset + c, y);
+        if (a.base) {
+            float b[8];
+            unpack8<BF16>(*(const u32x4 *)(a.base + t * a.ldbase + 8 * c), b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                y[i] += b[i];
+        }
+        *(u32x4 *)(a.out + t * a.ldo + 8 * c) = round8<BF16>(y);
+    }
+    if constexpr (DOT)
+        store_dots<KB>(a, t, dot);
+}
+
+template <bool BF16, bool SPREAD, int KB>
+void launch_rows(const TokenArgs &a, hipStream_t s)
+{
+    const unsigned threads = (unsigned)min(256, (a.H / 8 + 63) / 64 * 64);
+    if constexpr (SPREAD) {
+        if (a.dw)
+            spread_kernel<BF16, KB, true><<<(unsigned)a.T, threads, 0, s>>>(a);
+        else
+            spread_kernel<BF16, KB, false><<<(unsigned)a.T, threads, 0, s>>>(a);
+    } else {
+        if (a.dw)
+            gather_kernel<BF16, KB, true><<<(unsigned)a.T, threads, 0, s>>>(a);
+        else
+            gather_kernel<BF16, KB, false><<<(unsigned)a.T, threads, 0, s>>>(a);
+    }
+}
+
+template <bool BF16, bool SPREAD>
+hipError_t launch_rows_k(const TokenArgs &a, hipStream_t s)
+{
+    if (a.k <= 2)
+        launch_rows<BF16, SPREAD, 2>(a, s);
+    else if (a.k <= 4)
+        launch_rows<BF16, SPREAD, 4>(a, s);
+    else if (a.k <= 8)
+        launch_rows<BF16, SPREAD, 8>(a, s);
+    else
+        launch_rows<BF16, SPREAD, 16>(a, s);
+    return hipGetLastError();
+}
+
+hipError_t launch_spread(bool bf16, const TokenArgs &a, hipStream_t s)
+{
+    return bf16 ? launch_rows_k<true, true>(a, s) : launch_rows_k<false, true>(a, s);
+}
+
+hipError_t launch_gather(bool bf16, const TokenArgs &a, hipStream_t s)
+{
+    return bf16 ? launch_rows_k<true, false>(a, s) : launch_rows_k<false, false>(a, s);
+}
+
+// ---------------------------------------------------------------- dropout
+template <int DT>
+MOE_DEV float load1(const void *p, int64_t i)
+{
+    if constexpr (DT == MOE_EXL3_DT_F32)
+        return ((const float *)p)[i];
+    else
+        return act_to_f32<DT == MOE_EXL3_DT_BF16>(((const uint16_t *)p)[i]);
+}
+
+template <int DT>
+MOE_DEV void store1(void *p, int64_t i, float v)
+{
+    if constexpr (DT == MOE_EXL3_DT_F32)
+        ((float *)p)[i] = v;
+    else
+        ((uint16_t *)p)[i] = DT == MOE_EXL3_DT_BF16 ? f32_to_bf16_bits(v) : f32_to_f16_bits(v);
+}
+
+// One thread for eight columns of a row.
+template <int DT>
+__global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a)
+{
+    const int64_t groups = (a.cols + 7) / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= a.rows * groups)
+        return;
+    const int64_t r = i / groups;
+    const int c = 8 * (int)(i - r * groups), n = min(8, a.cols - c);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = j < n ? load1<DT>(a.x, r * a.ldx + c + j) : 0.0f;
+    if (a.drop.rng)
+        drop8(a.drop, a.drop.rng[0], a.drop.rng[1] + i, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < n) {
+            if (a.residual)
+                v[j] += load1<DT>(a.residual, r * a.ldr + c + j);
+            store1<DT>(a.y, r * a.ldy + c + j, v[j]);
+        }
+}
+
+hipError_t launch_dropout(int dtype, const DropoutArgs &a, hipStream_t s)
+{
+    const unsigned grid = (unsigned)((a.rows * ((a.cols + 7) / 8) + 255) / 256);
+    if (dtype == MOE_EXL3_DT_BF16)
+        dropout_kernel<MOE_EXL3_DT_BF16><<<grid, 256, 0, s>>>(a);
+    else if (dtype == MOE_EXL3_DT_F16)
+        dropout_kernel<MOE_EXL3_DT_F16><<<grid, 256, 0, s>>>(a);
+    else
+        dropout_kernel<MOE_EXL3_DT_F32><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace moe
