@@ -16,19 +16,27 @@
 
 namespace moe {
 
-// Rows a block's tile holds.
-constexpr int kW4Rows = 16;
-
 // Eight codes -> eight 16-bit numbers 16 + q, in the order of permute8().
+// sixteen: sixteen<BF16>(), in a register.
 template <bool BF16>
-MOE_DEV u32x4 expand8(uint32_t c)
+MOE_DEV u32x4 expand8(uint32_t c, uint32_t sixteen)
 {
-    if constexpr (BF16)   // 16 = 0x4180, steps of 1 at bit 3
-        return (u32x4){((c << 3) & 0x00780078u) | 0x41804180u, ((c >> 1) & 0x00780078u) | 0x41804180u,
-                       ((c >> 5) & 0x00780078u) | 0x41804180u, ((c >> 9) & 0x00780078u) | 0x41804180u};
-    else                  // 16 = 0x4C00, steps of 1 at bit 6
-        return (u32x4){((c << 6) & 0x03C003C0u) | 0x4C004C00u, ((c << 2) & 0x03C003C0u) | 0x4C004C00u,
-                       ((c >> 2) & 0x03C003C0u) | 0x4C004C00u, ((c >> 6) & 0x03C003C0u) | 0x4C004C00u};
+    if constexpr (BF16)   // steps of 1 at bit 3
+        return (u32x4){((c << 3) & 0x00780078u) | sixteen, ((c >> 1) & 0x00780078u) | sixteen,
+                       ((c >> 5) & 0x00780078u) | sixteen, ((c >> 9) & 0x00780078u) | sixteen};
+    else                  // at bit 6
+        return (u32x4){((c << 6) & 0x03C003C0u) | sixteen, ((c << 2) & 0x03C003C0u) | sixteen,
+                       ((c >> 2) & 0x03C003C0u) | sixteen, ((c >> 6) & 0x03C003C0u) | sixteen};
+}
+
+// 16 twice.  Hidden from the compiler in a vector register: with both constants
+// known it takes an instruction each for and and or, as one may hold one of them.
+template <bool BF16>
+MOE_DEV uint32_t sixteen()
+{
+    uint32_t v = BF16 ? 0x41804180u : 0x4C004C00u;
+    asm("" : "+v"(v));
+    return v;
 }
 
 // k 0..7 -> 0 4 1 5 2 6 3 7: what the two halves of a code dword give in turn.
@@ -44,18 +52,19 @@ struct W4Tile {
     int e, row, n;
 };
 
+template <int NW>
 MOE_DEV W4Tile w4_tile(const W4Args &a, int c, int tile_rows)
 {
     if (!a.offsets) {
         const int row = c * tile_rows;
         return {0, row, row < a.R ? min(tile_rows, a.R - row) : 0};
     }
-    __shared__ int found[3], wsum[4];
+    __shared__ int found[3], wsum[NW];
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63;
     if (tid == 0)
         found[2] = 0;
     int before = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 256) {
+    for (int e0 = 0; e0 < a.E; e0 += 64 * NW) {
         __syncthreads();
         const int e = e0 + tid;
         int lo = 0, hi = 0;
@@ -74,7 +83,7 @@ MOE_DEV W4Tile w4_tile(const W4Args &a, int c, int tile_rows)
             wsum[w] = v;
         __syncthreads();
         int first = before + v - tiles;
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < NW; ++i) {
             first += i < w ? wsum[i] : 0;
             before += wsum[i];
         }
@@ -107,82 +116,344 @@ MOE_DEV void w4_status(const W4Args &a)
         *a.status = bad ? MOE_EXL3_STATUS_BAD_INDEX : 0;
 }
 
-template <bool BF16, bool GLU>
-__global__ __launch_bounds__(256) void w4_kernel(W4Args a)
-{
-    constexpr int NW = GLU ? 2 : 1;
-    __shared__ float red[4][NW][16][17];
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63;
-    if (blockIdx.x == 0)
-        w4_status(a);
-    const int nt = (a.N + 15) / 16, n0 = (int)(blockIdx.x % nt) * 16;
-    const W4Tile t = w4_tile(a, blockIdx.x / nt, kW4Rows);
-    if (t.n == 0)
-        return;
-    const int n = n0 + (l & 15), q = l >> 4;
-    const bool in = n < a.N;
-    const int G = a.K >> a.group_log2;
-    const int64_t col = (int64_t)t.e * a.N + (in ? n : 0);
-    const uint32_t one = BF16 ? 0x3F803F80u : 0x3C003C00u;
-    const u32x4 ones = {one, one, one, one};
-    const uint16_t *xr = a.x + (int64_t)(t.row + min(l & 15, t.n - 1)) * a.ldx;
-    f32x4 acc[NW] = {}, tmp[NW] = {}, sum = {};
-    const int steps = 1 << (a.group_log2 - 5);   // of 32 k, a group
-    for (int g = w; g < G; g += 4) {
+// ---- tiles of few rows, k cut over the wavefronts of a block
+//
+// A wavefront takes the k in shares of 256 (a 128-byte line of each code row) in
+// turn and streams its own codes and rows of x through its own slots in LDS, with
+// no barrier until the block's sums meet.  16-byte loads straight to LDS, eight lanes
+// a line: in registers, with a row for every lane, each lane would be a
+// memory transaction.
+//   codes  NJ x 16 rows (columns n) of 128 bytes, two slots.  Piece p of 16 bytes
+//          (32 k) of row r lies in place p ^ (r / 2 % 8): the 64 lanes that read a
+//          dword each (16 rows, one piece) hit 64 banks
+//   x      ROWS rows of XK = 256 / XS k, two slots.  Piece p (8 k) of row r lies in
+//          place p ^ swizzle(r)
+//   scales, zeros   one element a lane in registers, a share ahead; a lane takes
+//          its column's from the lane that has it
+template <bool BF16, int GLOG, int ROWS, int NJ, bool GLU>
+struct W4Stream {
+    static constexpr int MR = (ROWS + 15) / 16;                  // blocks of 16 rows
+    static constexpr int XS = ROWS <= 4 ? 1 : ROWS <= 16 ? 2 : 4; // x slots of a share
+    static constexpr int XK = 256 / XS;
+    static constexpr int kPieces = XK / 8;                       // of a row of x
+    static constexpr int kXLoads = ROWS * XK / 512, kCLoads = 2 * NJ;
+    static constexpr int kXHalves = ROWS * XK, kCHalves = NJ * 1024;   // of a slot
+    static constexpr int kSteps = 8 / XS;                        // of 32 k, a slot of x
+    static constexpr int GS = 256 >> GLOG;                       // groups of a share
+    static constexpr int kGroupSteps = 8 / GS;
+    static constexpr int kScales = GS == 2 ? (NJ + 1) / 2 : NJ * GS / 4;
+    static_assert(kXLoads * 512 == kXHalves, "whole loads");
+
+    __amdgpu_buffer_rsrc_t x, c[2];
+    uint32_t xoff[kXLoads], coff[kCLoads];
+    const uint16_t *sp[kScales];
+    const uint8_t *zp[kScales];
+    int l, K, G;
+    uint32_t base16;
+    uint16_t snext[kScales];
+    uint8_t znext[kScales];
+    uint32_t now[kScales], zmask[kScales];   // scale | zero << 16
+    f32x4 acc[MR][NJ], tmp[MR][NJ], sum[MR];
+
+    MOE_DEV static int swizzle(int r) { return XS == 1 ? (r & 3) << 2 : XS == 2 ? r & 15 : (r >> 1) & 7; }
+
+    MOE_DEV void init(const W4Args &a, const W4Tile &t, int n0, int lane)
+    {
+        l = lane;
+        K = a.K;
+        G = K >> GLOG;
+        const int64_t matrix = (int64_t)t.e * a.N;
+        x = buf_rsrc(a.x + (int64_t)t.row * a.ldx, (uint32_t)(((t.n - 1) * a.ldx + K) * 2));
 #pragma unroll
-        for (int i = 0; i < NW; ++i)
-            tmp[i] = (f32x4){};
-        sum = (f32x4){};
-        for (int s = 0; s < steps; ++s) {
-            const int k = (g << a.group_log2) + 32 * s + 8 * q;
-            const u32x4 xf = permute8(*(const u32x4 *)(xr + k));
-            sum = dense_mfma<BF16>(xf, ones, sum);
+        for (int i = 0; i < (GLU ? 2 : 1); ++i)
+            c[i] = buf_rsrc(a.codes[i] + matrix * (K / 2), (uint32_t)a.N * (uint32_t)(K / 2));
 #pragma unroll
-            for (int i = 0; i < NW; ++i) {
-                const uint32_t c = *(const uint32_t *)(a.codes[i] + col * (a.K / 2) + k / 2);
-                tmp[i] = dense_mfma<BF16>(xf, expand8<BF16>(c), tmp[i]);
-            }
+        for (int i = 0; i < kXLoads; ++i) {
+            const int s = 64 * i + l, r = s / kPieces, k = 8 * ((s % kPieces) ^ swizzle(r));
+            xoff[i] = r < t.n ? (uint32_t)((r * a.ldx + k) * 2) : kOutOfRange;
         }
 #pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            const float sc = act_to_f32<BF16>(a.scales[i][col * G + g]);
-            const float z = 16.0f + (a.zeros[i] ? (float)a.zeros[i][col * G + g] : 8.0f);
+        for (int i = 0; i < kCLoads; ++i) {
+            const int r = 8 * i + (l >> 3), p = (l & 7) ^ ((r >> 1) & 7);
+            coff[i] = (uint32_t)column(n0, r) * (uint32_t)(K / 2) + 16 * p;
+        }
+        base16 = sixteen<BF16>();
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                acc[i][r] = fmaf(sc, fmaf(-z, sum[r], tmp[i][r]), acc[i][r]);
+        for (int i = 0; i < kScales; ++i) {
+            const int r = min(GS == 2 ? 32 * i + (l >> 1) : 16 * (i / (GS / 4)) + (l >> 2), 16 * NJ - 1);
+            const int m = GLU && r >= 8 * NJ;
+            const int64_t row = (matrix + min(column(n0, r), a.N - 1)) * G;
+            sp[i] = (m ? a.scales[1] : a.scales[0]) + row;
+            const uint8_t *z = m ? a.zeros[1] : a.zeros[0];
+            zmask[i] = z ? 0xFF0000u : 0u;
+            // (without zeros some bytes of the scales are read and masked off)
+            zp[i] = (z ? z : (const uint8_t *)(m ? a.scales[1] : a.scales[0])) + row;
         }
     }
+    // Column of the matrix that row r of the codes' tile is.
+    MOE_DEV static int column(int n0, int r) { return n0 + (GLU ? r % (8 * NJ) : r); }
+
+    MOE_DEV void load_x(int k0, LDS_AS uint16_t *lds)
+    {
 #pragma unroll
-    for (int i = 0; i < NW; ++i)
+        for (int i = 0; i < kXLoads; ++i) {
+            const int s = 64 * i + l, k = k0 + 8 * ((s % kPieces) ^ swizzle(s / kPieces));
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(x, (LDS_AS void *)(lds + 512 * i), 16,
+                                                     k < K ? xoff[i] + 2 * (uint32_t)k0 : kOutOfRange, 0, 0, 0);
+        }
+    }
+    MOE_DEV void load_codes(int k0, LDS_AS uint16_t *lds)
+    {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            red[w][i][4 * q + r][l & 15] = acc[i][r];
-    __syncthreads();
-    const int m = tid >> 4, c = tid & 15, nn = n0 + c;
-    if (m >= t.n || nn >= a.N)
-        return;
-    float v[NW];
+        for (int i = 0; i < kCLoads; ++i) {
+            const int r = 8 * i + (l >> 3), k = k0 + 32 * ((l & 7) ^ ((r >> 1) & 7));
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(c[GLU && i >= NJ], (LDS_AS void *)(lds + 512 * i), 16,
+                                                     k < K ? coff[i] + (uint32_t)(k0 / 2) : kOutOfRange, 0, 0, 0);
+        }
+    }
+    // (Groups past the last one read it again: their x and codes are zeros.)
+    MOE_DEV void load_scales(int k0)
+    {
 #pragma unroll
-    for (int i = 0; i < NW; ++i)
-        v[i] = (red[0][i][m][c] + red[1][i][m][c]) + (red[2][i][m][c] + red[3][i][m][c]);
-    float y = v[0];
+        for (int i = 0; i < kScales; ++i) {
+            const int g = min((k0 >> GLOG) + (GS == 2 ? l & 1 : (l & 3) + 4 * (i % (GS / 4))), G - 1);
+            snext[i] = sp[i][g];
+            znext[i] = zp[i][g];
+        }
+    }
+    // The k of a slot of x, number j of its share.
+    MOE_DEV void slot(int j, const u32x4 (&xf)[kSteps][MR], const uint32_t (&cf)[kSteps][NJ])
+    {
+        const uint32_t one = BF16 ? 0x3F803F80u : 0x3C003C00u;
+        const u32x4 ones = {one, one, one, one};
+#pragma unroll
+        for (int h = 0; h < kSteps; ++h) {
+            const int step = kSteps * j + h;
+            const bool first = step % kGroupSteps == 0;
+            u32x4 xp[MR];
+#pragma unroll
+            for (int i = 0; i < MR; ++i) {
+                xp[i] = permute8(xf[h][i]);
+                sum[i] = dense_mfma<BF16>(xp[i], ones, first ? (f32x4){} : sum[i]);
+            }
+#pragma unroll
+            for (int q = 0; q < NJ; ++q) {
+                const u32x4 w = expand8<BF16>(cf[h][q], base16);
+#pragma unroll
+                for (int i = 0; i < MR; ++i)
+                    tmp[i][q] = dense_mfma<BF16>(xp[i], w, first ? (f32x4){} : tmp[i][q]);
+            }
+            if (step % kGroupSteps != kGroupSteps - 1)
+                continue;
+            const int g = step / kGroupSteps;
+#pragma unroll
+            for (int q = 0; q < NJ; ++q) {
+                const int from = GS == 2 ? (16 * (q & 1) + (l & 15)) * 2 + g : (l & 15) * 4 + (g & 3);
+                const uint32_t v = __builtin_amdgcn_ds_bpermute(4 * from, now[GS == 2 ? q >> 1 : q * (GS / 4) + (g >> 2)]);
+                const float s = act_to_f32<BF16>((uint16_t)v), z = 16.0f + (float)(v >> 16);
+#pragma unroll
+                for (int i = 0; i < MR; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[i][q][r] = fmaf(s, fmaf(-z, sum[i][r], tmp[i][q][r]), acc[i][q][r]);
+            }
+            // here, not after the share: the compiler would hold every group's sums
+            // until then
+#pragma unroll
+            for (int q = 0; q < NJ; ++q)
+#pragma unroll
+                for (int i = 0; i < MR; ++i)
+                    asm volatile("" : "+v"(acc[i][q]));
+        }
+    }
+    // Slot j of share `s`; what is loaded next: slot j of x two on, after the
+    // last one the codes of share + 2 steps, after the first the scales of the
+    // next.  (Counts: the loads that may stay in flight are the slot and the
+    // codes issued after the ones needed here.)
+    template <int J>
+    MOE_DEV void run_slot(int s, int stride, LDS_AS uint16_t *xs, LDS_AS uint16_t *cs)
+    {
+        __builtin_amdgcn_sched_barrier(0);
+        wait_vmcnt<kXLoads + (J == 0 ? kCLoads : 0)>();
+        u32x4 xf[kSteps][MR];
+        uint32_t cf[kSteps][NJ];
+#pragma unroll
+        for (int h = 0; h < kSteps; ++h) {
+#pragma unroll
+            for (int i = 0; i < MR; ++i) {
+                const int r = 16 * i + (ROWS < 16 ? l & (ROWS - 1) : l & 15), p = 4 * h + (l >> 4);
+                xf[h][i] = *(const LDS_AS u32x4 *)(xs + r * XK + 8 * (p ^ swizzle(r)));
+            }
+#pragma unroll
+            for (int q = 0; q < NJ; ++q) {
+                const int r = 16 * q + (l & 15), p = kSteps * J + h;
+                cf[h][q] = *(const LDS_AS uint32_t *)(cs + r * 64 + 8 * (p ^ ((r >> 1) & 7)) + 2 * (l >> 4));
+            }
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the slots are free
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (J == 0) {
+#pragma unroll
+            for (int i = 0; i < kScales; ++i)
+                now[i] = snext[i] | (((uint32_t)znext[i] << 16) & zmask[i]) | (zmask[i] ? 0u : 8u << 16);
+            load_scales(256 * (s + stride));
+        }
+        if constexpr (J == XS - 1)
+            load_codes(256 * (s + 2 * stride), cs);
+        constexpr int next = J + 2;
+        load_x(256 * (s + next / XS * stride) + XK * (next % XS), xs);
+        __builtin_amdgcn_sched_barrier(0);
+        slot(J, xf, cf);
+    }
+    MOE_DEV void share(int s, int stride, LDS_AS uint16_t *x0, LDS_AS uint16_t *x1, LDS_AS uint16_t *cs)
+    {
+        run_slot<0>(s, stride, x0, cs);
+        if constexpr (XS >= 2)
+            run_slot<1>(s, stride, x1, cs);
+        if constexpr (XS == 4) {
+            run_slot<2>(s, stride, x0, cs);
+            run_slot<3>(s, stride, x1, cs);
+        }
+    }
+    // Shares first, first + stride, ..
+    MOE_DEV void run(int first, int stride, LDS_AS uint16_t *x0, LDS_AS uint16_t *x1, LDS_AS uint16_t *c0,
+                     LDS_AS uint16_t *c1)
+    {
+#pragma unroll
+        for (int i = 0; i < MR; ++i)
+#pragma unroll
+            for (int q = 0; q < NJ; ++q)
+                acc[i][q] = (f32x4){};
+        const int end = (K + 255) / 256;
+        if (first >= end)
+            return;
+        load_scales(256 * first);
+        load_codes(256 * first, c0);
+        load_x(256 * first, x0);
+        load_codes(256 * (first + stride), c1);
+        load_x(XS == 1 ? 256 * (first + stride) : 256 * first + XK, x1);
+        for (int s = first; s < end; s += 2 * stride) {
+            share(s, stride, x0, x1, c0);
+            // (past the end: zeros; one share's second slot of x is its own)
+            if constexpr (XS == 1)
+                share(s + stride, stride, x1, x0, c1);
+            else
+                share(s + stride, stride, x0, x1, c1);
+        }
+        wait_vmcnt<0>();   // the loads past the end still write LDS
+    }
+};
+
+// Columns of a tile.
+constexpr int w4_cols(bool glu, int nj) { return 16 * (glu ? nj / 2 : nj); }
+
+template <bool BF16, bool GLU>
+MOE_DEV void w4_store(const W4Args &a, int64_t row, int n, float g, float u)
+{
+    float y = g;
     if constexpr (GLU)
-        y = (a.act == MOE_EXL3_ACT_SILU ? act_value<MOE_EXL3_ACT_SILU>(v[0]) : act_value<MOE_EXL3_ACT_GELU_TANH>(v[0])) *
-            v[1];
-    const int64_t row = t.row + m;
+        y = (a.act == MOE_EXL3_ACT_SILU ? act_value<MOE_EXL3_ACT_SILU>(g) : act_value<MOE_EXL3_ACT_GELU_TANH>(g)) * u;
     if (a.base)
-        y += act_to_f32<BF16>(a.base[row * a.ldbase + nn]);
-    a.y[row * a.ldy + nn] = BF16 ? f32_to_bf16_bits(y) : f32_to_f16_bits(y);
+        y += act_to_f32<BF16>(a.base[row * a.ldbase + n]);
+    a.y[row * a.ldy + n] = BF16 ? f32_to_bf16_bits(y) : f32_to_f16_bits(y);
+}
+
+template <bool BF16, bool GLU, int GLOG, int ROWS, int NJ, int NW>
+__global__ __launch_bounds__(64 * NW, ROWS == 4 && NW == 4 ? 3 : 1) void w4_split_kernel(W4Args a)
+{
+    using S = W4Stream<BF16, GLOG, ROWS, NJ, GLU>;
+    __shared__ __align__(1024) uint16_t x0[NW * S::kXHalves], x1[NW * S::kXHalves], c0[NW * S::kCHalves],
+        c1[NW * S::kCHalves];
+    static_assert(S::MR * NJ * 1024 <= S::kXHalves * 2, "sums fit a slot of x");
+    const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if (blockIdx.x == 0)
+        w4_status(a);
+    constexpr int kCols = w4_cols(GLU, NJ);
+    const int nt = (a.N + kCols - 1) / kCols, n0 = (int)(blockIdx.x % nt) * kCols;
+    const W4Tile t = w4_tile<NW>(a, blockIdx.x / nt, ROWS);
+    if (t.n == 0)
+        return;
+    S st;
+    st.init(a, t, n0, l);
+    LDS_AS uint16_t *mine = (LDS_AS uint16_t *)x0 + w * S::kXHalves;
+    st.run(w, NW, mine, (LDS_AS uint16_t *)x1 + w * S::kXHalves, (LDS_AS uint16_t *)c0 + w * S::kCHalves,
+           (LDS_AS uint16_t *)c1 + w * S::kCHalves);
+    // each wavefront's sums in its own first slot of x
+#pragma unroll
+    for (int i = 0; i < S::MR; ++i)
+#pragma unroll
+        for (int q = 0; q < NJ; ++q)
+            ((LDS_AS f32x4 *)mine)[64 * (i * NJ + q) + l] = st.acc[i][q];
+    __syncthreads();
+    constexpr int kUnits = S::MR * (GLU ? NJ / 2 : NJ);   // of 64 x 4 results
+    const LDS_AS f32x4 *red = (const LDS_AS f32x4 *)((LDS_AS uint16_t *)x0);
+    for (int u = w; u < kUnits; u += NW) {
+        const int i = u / (kUnits / S::MR), q = u % (kUnits / S::MR);
+        auto total = [&](int q) {
+            f32x4 v = red[64 * (i * NJ + q) + l];
+#pragma unroll
+            for (int s = 1; s < NW; ++s)
+                v += red[s * (S::kXHalves / 8) + 64 * (i * NJ + q) + l];
+            return v;
+        };
+        const f32x4 g = total(q), up = GLU ? total(q + NJ / 2) : g;
+        const int n = n0 + 16 * q + (l & 15);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int m = 16 * i + 4 * (l >> 4) + r;
+            if (m < t.n && n < a.N)
+                w4_store<BF16, GLU>(a, t.row + m, n, g[r], up[r]);
+        }
+    }
+}
+
+// Tiles of at most `rows` rows that a call can have.
+unsigned w4_tiles(const W4Args &a, int rows)
+{
+    return (unsigned)(a.offsets ? a.R / rows + min(a.E, a.R) : (a.R + rows - 1) / rows);
+}
+
+template <bool BF16, bool GLU, int GLOG, int ROWS, int NJ, int NW>
+void launch_split(const W4Args &a, hipStream_t s)
+{
+    const unsigned grid = w4_tiles(a, ROWS) * (unsigned)((a.N + w4_cols(GLU, NJ) - 1) / w4_cols(GLU, NJ));
+    w4_split_kernel<BF16, GLU, GLOG, ROWS, NJ, NW><<<grid, 64 * NW, 0, s>>>(a);
+}
+
+template <bool BF16, bool GLU, int GLOG>
+void launch_group(const W4Args &a, hipStream_t s)
+{
+    constexpr int NJ = GLU ? 2 : 1;
+    const int rows = a.offsets ? a.R / a.E : a.R;   // of an expert, on average
+    if (rows <= 4) {
+        if (w4_tiles(a, 4) * (unsigned)((a.N + 15) / 16) < 512)
+            launch_split<BF16, GLU, GLOG, 4, NJ, 8>(a, s);
+        else
+            launch_split<BF16, GLU, GLOG, 4, NJ, 4>(a, s);
+    } else if (rows <= 16) {
+        launch_split<BF16, GLU, GLOG, 16, NJ, 8>(a, s);
+    } else {
+        launch_split<BF16, GLU, GLOG, 64, 2, 4>(a, s);
+    }
+}
+
+template <bool BF16, bool GLU>
+void launch_type(const W4Args &a, hipStream_t s)
+{
+    if (a.group_log2 == 5)
+        launch_group<BF16, GLU, 5>(a, s);
+    else if (a.group_log2 == 6)
+        launch_group<BF16, GLU, 6>(a, s);
+    else
+        launch_group<BF16, GLU, 7>(a, s);
 }
 
 hipError_t launch_w4(bool bf16, bool glu, const W4Args &a, hipStream_t s)
 {
-    const unsigned grid = (unsigned)((a.N + 15) / 16) *
-                          (unsigned)(a.offsets ? a.R / kW4Rows + min(a.E, a.R) : (a.R + kW4Rows - 1) / kW4Rows);
     if (bf16)
-        glu ? w4_kernel<true, true><<<grid, 256, 0, s>>>(a) : w4_kernel<true, false><<<grid, 256, 0, s>>>(a);
+        glu ? launch_type<true, true>(a, s) : launch_type<true, false>(a, s);
     else
-        glu ? w4_kernel<false, true><<<grid, 256, 0, s>>>(a) : w4_kernel<false, false><<<grid, 256, 0, s>>>(a);
+        glu ? launch_type<false, true>(a, s) : launch_type<false, false>(a, s);
     return hipGetLastError();
 }
 
