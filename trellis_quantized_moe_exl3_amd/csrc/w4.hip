@@ -153,6 +153,7 @@ struct W4Stream {
     uint16_t snext[kScales];
     uint8_t znext[kScales];
     uint32_t now[kScales], zmask[kScales];   // scale | zero << 16
+    uint32_t xat, cat;   // byte addresses in the slots of the lane's fragments of step 0
     f32x4 acc[MR][NJ], tmp[MR][NJ], sum[MR];
 
     MOE_DEV static int swizzle(int r) { return XS == 1 ? (r & 3) << 2 : XS == 2 ? r & 15 : (r >> 1) & 7; }
@@ -162,6 +163,9 @@ struct W4Stream {
         l = lane;
         K = a.K;
         G = K >> GLOG;
+        const int r = ROWS < 16 ? l & (ROWS - 1) : l & 15;
+        xat = (uint32_t)(r * 2 * XK + 16 * ((l >> 4) ^ swizzle(r)));
+        cat = (uint32_t)((l & 15) * 128 + 16 * ((l & 15) >> 1) + 4 * (l >> 4));
         const int64_t matrix = (int64_t)t.e * a.N;
         x = buf_rsrc(a.x + (int64_t)t.row * a.ldx, (uint32_t)(((t.n - 1) * a.ldx + K) * 2));
 #pragma unroll
@@ -280,15 +284,11 @@ struct W4Stream {
 #pragma unroll
         for (int h = 0; h < kSteps; ++h) {
 #pragma unroll
-            for (int i = 0; i < MR; ++i) {
-                const int r = 16 * i + (ROWS < 16 ? l & (ROWS - 1) : l & 15), p = 4 * h + (l >> 4);
-                xf[h][i] = *(const LDS_AS u32x4 *)(xs + r * XK + 8 * (p ^ swizzle(r)));
-            }
+            for (int i = 0; i < MR; ++i)
+                xf[h][i] = *(const LDS_AS u32x4 *)((const LDS_AS char *)xs + (xat ^ (64u * h)) + 32 * XK * i);
 #pragma unroll
-            for (int q = 0; q < NJ; ++q) {
-                const int r = 16 * q + (l & 15), p = kSteps * J + h;
-                cf[h][q] = *(const LDS_AS uint32_t *)(cs + r * 64 + 8 * (p ^ ((r >> 1) & 7)) + 2 * (l >> 4));
-            }
+            for (int q = 0; q < NJ; ++q)
+                cf[h][q] = *(const LDS_AS uint32_t *)((const LDS_AS char *)cs + (cat ^ (16u * (kSteps * J + h))) + 2048 * q);
         }
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the slots are free
         __builtin_amdgcn_sched_barrier(0);
@@ -407,6 +407,270 @@ __global__ __launch_bounds__(64 * NW, ROWS == 4 && NW == 4 ? 3 : 1) void w4_spli
     }
 }
 
+// ---- tiles of many rows, columns over the wavefronts of a block
+//
+// 128 rows and 256 columns (a gated pair: 128 of each) by 2 x 4 wavefronts of 64 x
+// 64.  x and the codes pass through LDS in stages of 128 k, which all
+// wavefronts load and share; a ring of three, one barrier a stage.
+//   x      128 rows of 256 bytes, piece p (8 k) of row r in place p ^ (r % 16)
+//   codes  256 rows of 64 bytes, piece p (32 k) of row r in place p ^ (r / 4 % 4)
+template <bool BF16, int GLOG, bool GLU>
+struct W4Wide {
+    static constexpr int kRows = 128, kCols = 256, kStage = 128, NW = 8, MR = 4, NJ = 4;
+    static constexpr int kXLoads = kRows * kStage * 2 / 1024 / NW, kCLoads = kCols * kStage / 2 / 1024 / NW;
+    static constexpr int kXHalves = kRows * kStage, kCHalves = kCols * kStage / 4;   // of a stage
+    static constexpr int GS = kStage >> GLOG, kGroupSteps = 4 / GS;
+
+    __amdgpu_buffer_rsrc_t x, c[2];
+    uint32_t xoff[kXLoads], coff[kCLoads];
+    const uint16_t *sp[GS];
+    const uint8_t *zp[GS];
+    uint32_t zmask;
+    int l, w, K, G;
+    uint32_t base16;
+    uint16_t snext[GS];
+    uint8_t znext[GS];
+    uint32_t now[GS];
+    uint32_t xat, cat;   // byte addresses in a stage's slots of the lane's fragments of step 0
+    f32x4 acc[MR][NJ], tmp[MR][NJ], sum[MR];
+
+    // Column of the matrix that row r of the codes' tile is: a wavefront's 64
+    // hold (GLU) 32 of the gate and the same 32 of the other.
+    MOE_DEV static int column(int n0, int r) { return n0 + (GLU ? r / 64 * 32 + r % 32 : r); }
+    MOE_DEV static bool second(int r) { return GLU && r % 64 >= 32; }
+
+    MOE_DEV void init(const W4Args &a, const W4Tile &t, int n0, int lane, int wave)
+    {
+        l = lane;
+        w = wave;
+        K = a.K;
+        G = K >> GLOG;
+        base16 = sixteen<BF16>();
+        xat = (uint32_t)((64 * (w >> 2) + (l & 15)) * 256 + 16 * ((l >> 4) ^ (l & 15)));
+        cat = (uint32_t)((64 * (w & 3) + (l & 15)) * 64 + 16 * ((l >> 2) & 3) + 4 * (l >> 4));
+        const int64_t matrix = (int64_t)t.e * a.N;
+        x = buf_rsrc(a.x + (int64_t)t.row * a.ldx, (uint32_t)(((t.n - 1) * a.ldx + K) * 2));
+#pragma unroll
+        for (int i = 0; i < (GLU ? 2 : 1); ++i)
+            c[i] = buf_rsrc(a.codes[i] + matrix * (K / 2), (uint32_t)a.N * (uint32_t)(K / 2));
+#pragma unroll
+        for (int i = 0; i < kXLoads; ++i) {
+            const int r = xrow(i);
+            xoff[i] = r < t.n ? (uint32_t)((r * a.ldx + xk(i)) * 2) : kOutOfRange;
+        }
+#pragma unroll
+        for (int i = 0; i < kCLoads; ++i)
+            coff[i] = (uint32_t)column(n0, crow(i)) * (uint32_t)(K / 2) + (uint32_t)ck(i) / 2;
+        zmask = 0;
+#pragma unroll
+        for (int i = 0; i < GS; ++i) {
+            const int r = 64 * (w & 3) + 64 / GS * i + l / GS;
+            const bool up = second(r);
+            const int64_t row = (matrix + min(column(n0, r), a.N - 1)) * G;
+            sp[i] = (up ? a.scales[1] : a.scales[0]) + row;
+            const uint8_t *z = up ? a.zeros[1] : a.zeros[0];
+            zp[i] = (z ? z : (const uint8_t *)(up ? a.scales[1] : a.scales[0])) + row;
+            zmask |= z ? 1u << i : 0u;
+        }
+    }
+    // Row and first k of the 16 bytes of x, of codes, that lane l's load i holds.
+    MOE_DEV int xrow(int i) const { return 4 * (w * kXLoads + i) + (l >> 4); }
+    MOE_DEV int xk(int i) const { return 8 * ((l & 15) ^ (xrow(i) & 15)); }
+    MOE_DEV int crow(int i) const { return 16 * (w * kCLoads + i) + (l >> 2); }
+    MOE_DEV int ck(int i) const { return 32 * ((l & 3) ^ ((crow(i) >> 2) & 3)); }
+
+    MOE_DEV void load(int k0, LDS_AS uint16_t *xs, LDS_AS uint16_t *cs)
+    {
+#pragma unroll
+        for (int i = 0; i < kXLoads; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(x, (LDS_AS void *)(xs + 512 * (w * kXLoads + i)), 16,
+                                                     k0 + xk(i) < K ? xoff[i] + 2 * (uint32_t)k0 : kOutOfRange, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kCLoads; ++i) {
+            // (32 rows a load of a pair's: the same matrix for all lanes)
+            const bool up = second(16 * (w * kCLoads + i));
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(up ? c[1] : c[0], (LDS_AS void *)(cs + 512 * (w * kCLoads + i)), 16,
+                                                     k0 + ck(i) < K ? coff[i] + (uint32_t)(k0 / 2) : kOutOfRange, 0, 0,
+                                                     0);
+        }
+    }
+    MOE_DEV void load_scales(int k0)
+    {
+#pragma unroll
+        for (int i = 0; i < GS; ++i) {
+            const int g = min((k0 >> GLOG) + l % GS, G - 1);
+            snext[i] = sp[i][g];
+            znext[i] = zp[i][g];
+        }
+    }
+    // Stage at k0, from its slots; the stage two on goes to the slots read last.
+    MOE_DEV void stage(int k0, const LDS_AS uint16_t *xs, const LDS_AS uint16_t *cs, LDS_AS uint16_t *xnext,
+                       LDS_AS uint16_t *cnext)
+    {
+        __builtin_amdgcn_sched_barrier(0);
+        wait_vmcnt<kXLoads + kCLoads>();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < GS; ++i)
+            now[i] = snext[i] | ((zmask >> i) & 1u ? (uint32_t)znext[i] << 16 : 8u << 16);
+        load_scales(k0 + kStage);
+        load(k0 + 2 * kStage, xnext, cnext);
+        __builtin_amdgcn_sched_barrier(0);
+        const uint32_t one = BF16 ? 0x3F803F80u : 0x3C003C00u;
+        const u32x4 ones = {one, one, one, one};
+        // a step's fragments are read while the one before is multiplied (the
+        // fences keep the compiler from reading all of a stage's at its start, for
+        // which there are no registers)
+        u32x4 xn[MR];
+        uint32_t cn[NJ];
+        auto read = [&](int h) {
+#pragma unroll
+            for (int i = 0; i < MR; ++i)
+                xn[i] = *(const LDS_AS u32x4 *)((const LDS_AS char *)xs + (xat ^ (64u * h)) + 4096 * i);
+#pragma unroll
+            for (int q = 0; q < NJ; ++q)
+                cn[q] = *(const LDS_AS uint32_t *)((const LDS_AS char *)cs + (cat ^ (16u * h)) + 1024 * q);
+        };
+        read(0);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const bool first = h % kGroupSteps == 0;
+            u32x4 xp[MR];
+            uint32_t cf[NJ];
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < MR; ++i)
+                xp[i] = permute8(xn[i]);
+#pragma unroll
+            for (int q = 0; q < NJ; ++q)
+                cf[q] = cn[q];
+            if (h < 3)
+                read(h + 1);
+#pragma unroll
+            for (int i = 0; i < MR; ++i)
+                sum[i] = dense_mfma<BF16>(xp[i], ones, first ? (f32x4){} : sum[i]);
+#pragma unroll
+            for (int q = 0; q < NJ; ++q) {
+                const u32x4 v = expand8<BF16>(cf[q], base16);
+#pragma unroll
+                for (int i = 0; i < MR; ++i)
+                    tmp[i][q] = dense_mfma<BF16>(xp[i], v, first ? (f32x4){} : tmp[i][q]);
+            }
+            if (h % kGroupSteps != kGroupSteps - 1)
+                continue;
+            const int g = h / kGroupSteps;
+#pragma unroll
+            for (int q = 0; q < NJ; ++q) {
+                const int e = (16 * q % (64 / GS) + (l & 15)) * GS + g;
+                const uint32_t v = __builtin_amdgcn_ds_bpermute(4 * e, now[16 * q * GS / 64]);
+                const float s = act_to_f32<BF16>((uint16_t)v), z = 16.0f + (float)(v >> 16);
+#pragma unroll
+                for (int i = 0; i < MR; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[i][q][r] = fmaf(s, fmaf(-z, sum[i][r], tmp[i][q][r]), acc[i][q][r]);
+            }
+#pragma unroll
+            for (int q = 0; q < NJ; ++q)
+#pragma unroll
+                for (int i = 0; i < MR; ++i)
+                    asm volatile("" : "+v"(acc[i][q]));
+        }
+    }
+    MOE_DEV void run(LDS_AS uint16_t *const (&xs)[3], LDS_AS uint16_t *const (&cs)[3])
+    {
+#pragma unroll
+        for (int i = 0; i < MR; ++i)
+#pragma unroll
+            for (int q = 0; q < NJ; ++q)
+                acc[i][q] = (f32x4){};
+        load_scales(0);
+        load(0, xs[0], cs[0]);
+        load(kStage, xs[1], cs[1]);
+        int k = 0;
+        for (; k + 2 * kStage < K; k += 3 * kStage) {
+            stage(k, xs[0], cs[0], xs[2], cs[2]);
+            stage(k + kStage, xs[1], cs[1], xs[0], cs[0]);
+            stage(k + 2 * kStage, xs[2], cs[2], xs[1], cs[1]);
+        }
+        if (k < K) {
+            stage(k, xs[0], cs[0], xs[2], cs[2]);
+            if (k + kStage < K)
+                stage(k + kStage, xs[1], cs[1], xs[0], cs[0]);
+        }
+        wait_vmcnt<0>();   // the loads past the end still write LDS
+    }
+};
+
+template <bool BF16, bool GLU, int GLOG>
+__global__ __launch_bounds__(512) void w4_wide_kernel(W4Args a)
+{
+    using S = W4Wide<BF16, GLOG, GLU>;
+    // (slots apart for the compiler, which waits for loads into an array it reads)
+    __shared__ __align__(1024) uint16_t x0[S::kXHalves], x1[S::kXHalves], x2[S::kXHalves], c0[S::kCHalves],
+        c1[S::kCHalves], c2[S::kCHalves];
+    const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if (blockIdx.x == 0)
+        w4_status(a);
+    constexpr int kCols = GLU ? S::kCols / 2 : S::kCols;
+    const int nt = (a.N + kCols - 1) / kCols, mt = gridDim.x / nt;
+    int c = blockIdx.x / nt, n = blockIdx.x % nt;
+    if (mt % 8 == 0)
+        xcd_map(blockIdx.x, nt, c, n);
+    const W4Tile t = w4_tile<S::NW>(a, c, S::kRows);
+    if (t.n == 0)
+        return;
+    const int n0 = n * kCols;
+    S st;
+    st.init(a, t, n0, l, w);
+    LDS_AS uint16_t *const xs[3] = {(LDS_AS uint16_t *)x0, (LDS_AS uint16_t *)x1, (LDS_AS uint16_t *)x2};
+    LDS_AS uint16_t *const cs[3] = {(LDS_AS uint16_t *)c0, (LDS_AS uint16_t *)c1, (LDS_AS uint16_t *)c2};
+    st.run(xs, cs);
+    __syncthreads();
+    // results through LDS, for stores of 16 bytes: a wavefront turns 16 rows at
+    // a time, the 16-column block q of row r in place q ^ (r / 4 % 4)
+    constexpr int kOut = GLU ? 32 : 64;   // columns of a wavefront
+    LDS_AS float *mine = (LDS_AS float *)(w < 4 ? xs[0] : xs[1]) + (w & 3) * 16 * 64;
+    const int row0 = 64 * (w >> 2), col0 = n0 + kOut * (w & 3);
+#pragma unroll
+    for (int i = 0; i < S::MR; ++i) {
+        wave_lds_fence();
+#pragma unroll
+        for (int q = 0; q < kOut / 16; ++q)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float v = st.acc[i][q][r];
+                if constexpr (GLU)
+                    v = (a.act == MOE_EXL3_ACT_SILU ? act_value<MOE_EXL3_ACT_SILU>(v)
+                                                    : act_value<MOE_EXL3_ACT_GELU_TANH>(v)) *
+                        st.acc[i][q + 2][r];
+                const int m = 4 * (l >> 4) + r;
+                mine[m * kOut + 16 * (q ^ ((l >> 4) & (kOut / 16 - 1))) + (l & 15)] = v;
+            }
+        wave_lds_fence();
+        constexpr int kLanes = kOut / 8;   // of a row
+#pragma unroll
+        for (int p = 0; p < 16 * kLanes / 64; ++p) {
+            const int m = (64 / kLanes) * p + l / kLanes, col = 8 * (l % kLanes);
+            const LDS_AS float *at = mine + m * kOut + 16 * ((col >> 4) ^ ((m >> 2) & (kOut / 16 - 1))) + (col & 15);
+            f32x4 v[2] = {*(const LDS_AS f32x4 *)at, *(const LDS_AS f32x4 *)(at + 4)};
+            const int row = row0 + 16 * i + m;
+            if (row >= t.n || col0 + col >= a.N)
+                continue;
+            if (a.base) {
+                const u32x4 b = *(const u32x4 *)(a.base + (int64_t)(t.row + row) * a.ldbase + col0 + col);
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    v[d >> 1][2 * (d & 1)] += act_to_f32<BF16>((uint16_t)b[d]);
+                    v[d >> 1][2 * (d & 1) + 1] += act_to_f32<BF16>((uint16_t)(b[d] >> 16));
+                }
+            }
+            *(u32x4 *)(a.y + (int64_t)(t.row + row) * a.ldy + col0 + col) = pack8<BF16>(v[0], v[1]);
+        }
+    }
+}
+
 // Tiles of at most `rows` rows that a call can have.
 unsigned w4_tiles(const W4Args &a, int rows)
 {
@@ -432,8 +696,14 @@ void launch_group(const W4Args &a, hipStream_t s)
             launch_split<BF16, GLU, GLOG, 4, NJ, 4>(a, s);
     } else if (rows <= 16) {
         launch_split<BF16, GLU, GLOG, 16, NJ, 8>(a, s);
-    } else {
+    } else if (rows <= 96) {
         launch_split<BF16, GLU, GLOG, 64, 2, 4>(a, s);
+    } else {
+        constexpr int kCols = GLU ? 128 : 256;
+        unsigned mt = w4_tiles(a, 128);
+        if (mt >= 16)
+            mt = (mt + 7) / 8 * 8;
+        w4_wide_kernel<BF16, GLU, GLOG><<<mt * (unsigned)((a.N + kCols - 1) / kCols), 512, 0, s>>>(a);
     }
 }
 
