@@ -13,6 +13,7 @@
 // of the sums' 24 bits.
 #include "dense_kernel.h"
 #include "w4.h"
+#include <stdlib.h>
 
 namespace moe {
 
@@ -410,34 +411,43 @@ __global__ __launch_bounds__(64 * NW, ROWS == 4 && NW == 4 ? 3 : 1) void w4_spli
 // ---- tiles of many rows, columns over the wavefronts of a block
 //
 // 128 rows and 256 columns (a gated pair: 128 of each) by 2 x 4 wavefronts of 64 x
-// 64.  x and the codes pass through LDS in stages of 128 k, which all
+// 64, or 64 rows and 128 columns by 1 x 4 of 64 x 32.  x and the codes pass through LDS in stages of 128 k, which all
 // wavefronts load and share; a ring of three, one barrier a stage.
-//   x      128 rows of 256 bytes, piece p (8 k) of row r in place p ^ (r % 16)
-//   codes  256 rows of 64 bytes, piece p (32 k) of row r in place p ^ (r / 4 % 4)
-template <bool BF16, int GLOG, bool GLU>
+//   x      rows of 256 bytes, piece p (8 k) of row r in place p ^ (r % 16)
+//   codes  rows of 64 bytes, piece p (32 k) of row r in place p ^ (r / 4 % 4)
+// While a stage is multiplied each wavefront prepares the 16 rows of x of the next
+// that it has loaded itself: it writes them back in the order of expand8() and
+// leaves their groups' sums beside them, once instead of once for each
+// wavefront that reads them.  Without zeros all columns subtract the same (16 +
+// 8) sum x, which then is what a group's products start from.
+template <bool BF16, int GLOG, bool GLU, bool ZEROS, int NW, int NJ>
 struct W4Wide {
-    static constexpr int kRows = 128, kCols = 256, kStage = 128, NW = 8, MR = 4, NJ = 4;
+    static constexpr int kRows = 16 * NW, kCols = 64 * NJ, kStage = 128, MR = 4;
+    static constexpr int kOwn = 16 * NJ;   // code rows of a wavefront
     static constexpr int kXLoads = kRows * kStage * 2 / 1024 / NW, kCLoads = kCols * kStage / 2 / 1024 / NW;
     static constexpr int kXHalves = kRows * kStage, kCHalves = kCols * kStage / 4;   // of a stage
     static constexpr int GS = kStage >> GLOG, kGroupSteps = 4 / GS;
+    static constexpr int kSums = GS * kRows;   // of a stage
+    static constexpr int kScales = (kOwn * GS + 63) / 64;
+    static_assert(kXLoads * 4 * NW == kRows, "a wavefront prepares the rows it loads");
+    static_assert(kCLoads * 16 * NW == kCols, "whole loads");
 
     __amdgpu_buffer_rsrc_t x, c[2];
     uint32_t xoff[kXLoads], coff[kCLoads];
-    const uint16_t *sp[GS];
-    const uint8_t *zp[GS];
+    const uint16_t *sp[kScales];
+    const uint8_t *zp[kScales];
     uint32_t zmask;
     int l, w, K, G;
     uint32_t base16;
-    uint16_t snext[GS];
-    uint8_t znext[GS];
-    uint32_t now[GS];
-    uint32_t xat, cat;   // byte addresses in a stage's slots of the lane's fragments of step 0
-    f32x4 acc[MR][NJ], tmp[MR][NJ], sum[MR];
+    uint16_t snext[kScales];
+    uint8_t znext[kScales];
+    uint32_t now[kScales];   // scale | zero << 16
+    f32x4 acc[MR][NJ], tmp[MR][NJ];
 
-    // Column of the matrix that row r of the codes' tile is: a wavefront's 64
-    // hold (GLU) 32 of the gate and the same 32 of the other.
-    MOE_DEV static int column(int n0, int r) { return n0 + (GLU ? r / 64 * 32 + r % 32 : r); }
-    MOE_DEV static bool second(int r) { return GLU && r % 64 >= 32; }
+    // Column of the matrix that row r of the codes' tile is: of a wavefront's, half
+    // are (GLU) the gate's and half the same columns of the other.
+    MOE_DEV static int column(int n0, int r) { return n0 + (GLU ? r / kOwn * (kOwn / 2) + r % (kOwn / 2) : r); }
+    MOE_DEV static bool second(int r) { return GLU && r % kOwn >= kOwn / 2; }
 
     MOE_DEV void init(const W4Args &a, const W4Tile &t, int n0, int lane, int wave)
     {
@@ -446,8 +456,9 @@ struct W4Wide {
         K = a.K;
         G = K >> GLOG;
         base16 = sixteen<BF16>();
-        xat = (uint32_t)((64 * (w >> 2) + (l & 15)) * 256 + 16 * ((l >> 4) ^ (l & 15)));
-        cat = (uint32_t)((64 * (w & 3) + (l & 15)) * 64 + 16 * ((l >> 2) & 3) + 4 * (l >> 4));
+        xat = xaddr(16 * MR * (w >> 2));
+        pat = xaddr(16 * w);
+        cat = (uint32_t)((kOwn * (w & 3) + (l & 15)) * 64 + 16 * ((l >> 2) & 3) + 4 * (l >> 4));
         const int64_t matrix = (int64_t)t.e * a.N;
         x = buf_rsrc(a.x + (int64_t)t.row * a.ldx, (uint32_t)(((t.n - 1) * a.ldx + K) * 2));
 #pragma unroll
@@ -463,12 +474,13 @@ struct W4Wide {
             coff[i] = (uint32_t)column(n0, crow(i)) * (uint32_t)(K / 2) + (uint32_t)ck(i) / 2;
         zmask = 0;
 #pragma unroll
-        for (int i = 0; i < GS; ++i) {
-            const int r = 64 * (w & 3) + 64 / GS * i + l / GS;
+        for (int i = 0; i < kScales; ++i) {
+            const int r = kOwn * (w & 3) + min((64 * i + l) / GS, kOwn - 1);
             const bool up = second(r);
             const int64_t row = (matrix + min(column(n0, r), a.N - 1)) * G;
             sp[i] = (up ? a.scales[1] : a.scales[0]) + row;
             const uint8_t *z = up ? a.zeros[1] : a.zeros[0];
+            // (one of a pair may have none: some bytes of the scales are read and masked off)
             zp[i] = (z ? z : (const uint8_t *)(up ? a.scales[1] : a.scales[0])) + row;
             zmask |= z ? 1u << i : 0u;
         }
@@ -479,97 +491,169 @@ struct W4Wide {
     MOE_DEV int crow(int i) const { return 16 * (w * kCLoads + i) + (l >> 2); }
     MOE_DEV int ck(int i) const { return 32 * ((l & 3) ^ ((crow(i) >> 2) & 3)); }
 
+    // (Past K lies the next row, or nothing, which reads as zeros: no step takes it.)
     MOE_DEV void load(int k0, LDS_AS uint16_t *xs, LDS_AS uint16_t *cs)
     {
 #pragma unroll
         for (int i = 0; i < kXLoads; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(x, (LDS_AS void *)(xs + 512 * (w * kXLoads + i)), 16,
-                                                     k0 + xk(i) < K ? xoff[i] + 2 * (uint32_t)k0 : kOutOfRange, 0, 0, 0);
+                                                     xoff[i] + 2 * (uint32_t)k0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < kCLoads; ++i) {
-            // (32 rows a load of a pair's: the same matrix for all lanes)
+            // (16 rows a load: of one matrix)
             const bool up = second(16 * (w * kCLoads + i));
             __builtin_amdgcn_raw_ptr_buffer_load_lds(up ? c[1] : c[0], (LDS_AS void *)(cs + 512 * (w * kCLoads + i)), 16,
-                                                     k0 + ck(i) < K ? coff[i] + (uint32_t)(k0 / 2) : kOutOfRange, 0, 0,
-                                                     0);
+                                                     coff[i] + (uint32_t)(k0 / 2), 0, 0, 0);
         }
     }
+    // (Groups past the last one read it again.)
     MOE_DEV void load_scales(int k0)
     {
 #pragma unroll
-        for (int i = 0; i < GS; ++i) {
+        for (int i = 0; i < kScales; ++i) {
             const int g = min((k0 >> GLOG) + l % GS, G - 1);
             snext[i] = sp[i][g];
-            znext[i] = zp[i][g];
+            if constexpr (ZEROS)
+                znext[i] = zp[i][g];
         }
     }
-    // Stage at k0, from its slots; the stage two on goes to the slots read last.
-    MOE_DEV void stage(int k0, const LDS_AS uint16_t *xs, const LDS_AS uint16_t *cs, LDS_AS uint16_t *xnext,
-                       LDS_AS uint16_t *cnext)
+    // Byte addresses in a stage's slots of the lane's fragments of step 0: of the
+    // rows this wavefront multiplies, of those it prepares, of its codes.
+    uint32_t xat, pat, cat;
+    MOE_DEV uint32_t xaddr(int r0) const { return (uint32_t)((r0 + (l & 15)) * 256 + 16 * ((l >> 4) ^ (l & 15))); }
+
+    // The preparation of this wavefront's rows of x, in three parts.
+    u32x4 raw[4];
+    MOE_DEV void prepare_read(const LDS_AS uint16_t *xs)
     {
-        __builtin_amdgcn_sched_barrier(0);
-        wait_vmcnt<kXLoads + kCLoads>();
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < GS; ++i)
-            now[i] = snext[i] | ((zmask >> i) & 1u ? (uint32_t)znext[i] << 16 : 8u << 16);
-        load_scales(k0 + kStage);
-        load(k0 + 2 * kStage, xnext, cnext);
-        __builtin_amdgcn_sched_barrier(0);
-        const uint32_t one = BF16 ? 0x3F803F80u : 0x3C003C00u;
+        for (int h = 0; h < 4; ++h)
+            raw[h] = *(const LDS_AS u32x4 *)((const LDS_AS char *)xs + (pat ^ (64u * h)));
+    }
+    MOE_DEV void prepare_write(LDS_AS uint16_t *xs)
+    {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            raw[h] = permute8(raw[h]);
+            *(LDS_AS u32x4 *)((LDS_AS char *)xs + (pat ^ (64u * h))) = raw[h];
+        }
+    }
+    MOE_DEV void prepare_sums(LDS_AS float *sums)
+    {
+        // 1, or -24 twice
+        const uint32_t one = ZEROS ? (BF16 ? 0x3F803F80u : 0x3C003C00u) : (BF16 ? 0xC1C0C1C0u : 0xCE00CE00u);
         const u32x4 ones = {one, one, one, one};
-        // a step's fragments are read while the one before is multiplied (the
-        // fences keep the compiler from reading all of a stage's at its start, for
-        // which there are no registers)
-        u32x4 xn[MR];
-        uint32_t cn[NJ];
-        auto read = [&](int h) {
+        f32x4 sum[GS];
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            sum[h / kGroupSteps] =
+                dense_mfma<BF16>(raw[h], ones, h % kGroupSteps == 0 ? (f32x4){} : sum[h / kGroupSteps]);
+        if ((l & 15) == 0)   // (all 16 columns of the product are the same)
+#pragma unroll
+            for (int g = 0; g < GS; ++g)
+                *(LDS_AS f32x4 *)(sums + kRows * g + 16 * w + 4 * (l >> 4)) = sum[g];
+    }
+    // Fragments of step h of a stage, read while the step before is multiplied.
+    u32x4 xn[MR];
+    uint32_t cn[NJ];
+    f32x4 sn[MR];
+    MOE_DEV void read(int h, const LDS_AS uint16_t *xs, const LDS_AS uint16_t *cs, const LDS_AS float *sums)
+    {
+        if (!ZEROS && h % kGroupSteps == 0)   // (with zeros: where they are needed)
 #pragma unroll
             for (int i = 0; i < MR; ++i)
-                xn[i] = *(const LDS_AS u32x4 *)((const LDS_AS char *)xs + (xat ^ (64u * h)) + 4096 * i);
+                sn[i] = *(const LDS_AS f32x4 *)(sums + kRows * (h / kGroupSteps) + 64 * (w >> 2) + 16 * i + 4 * (l >> 4));
 #pragma unroll
-            for (int q = 0; q < NJ; ++q)
-                cn[q] = *(const LDS_AS uint32_t *)((const LDS_AS char *)cs + (cat ^ (16u * h)) + 1024 * q);
-        };
-        read(0);
+        for (int i = 0; i < MR; ++i)
+            xn[i] = *(const LDS_AS u32x4 *)((const LDS_AS char *)xs + (xat ^ (64u * h)) + 4096 * i);
+#pragma unroll
+        for (int q = 0; q < NJ; ++q)
+            cn[q] = *(const LDS_AS uint32_t *)((const LDS_AS char *)cs + (cat ^ (16u * h)) + 1024 * q);
+    }
+    // Every wavefront has read the stage and prepared its part of the next one.
+    MOE_DEV void meet()
+    {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    // The stage at k0, from its slots, and meanwhile the preparation of the next;
+    // before its last step all its fragments are in registers, and the stage
+    // three on is loaded in its place.
+    // TAIL: it may have fewer than four steps.
+    template <bool TAIL>
+    MOE_DEV void stage(int k0, LDS_AS uint16_t *xs, LDS_AS uint16_t *cs, const LDS_AS float *sums,
+                       LDS_AS uint16_t *xnext, LDS_AS uint16_t *cnext, LDS_AS float *snext_)
+    {
+        f32x4 sum[MR];
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             const bool first = h % kGroupSteps == 0;
+            const int g = h / kGroupSteps;
+            if (TAIL && k0 + 32 * h >= K)
+                break;
+            // (the addresses of a step are computed for it: kept, all of them cost
+            // registers that there are not, and a spill waits for all loads in
+            // flight)
+            asm volatile("" : "+v"(xat), "+v"(pat), "+v"(cat));
             u32x4 xp[MR];
             uint32_t cf[NJ];
+            if (h == 3)
+                meet();
             __builtin_amdgcn_sched_barrier(0);
+            if (!ZEROS && first)
+#pragma unroll
+                for (int i = 0; i < MR; ++i)
+                    sum[i] = sn[i];
 #pragma unroll
             for (int i = 0; i < MR; ++i)
-                xp[i] = permute8(xn[i]);
+                xp[i] = xn[i];
 #pragma unroll
             for (int q = 0; q < NJ; ++q)
                 cf[q] = cn[q];
-            if (h < 3)
-                read(h + 1);
+            if (h == 0) {
+                wait_vmcnt<kXLoads + kCLoads>();   // the next stage is here, but for its preparation
 #pragma unroll
-            for (int i = 0; i < MR; ++i)
-                sum[i] = dense_mfma<BF16>(xp[i], ones, first ? (f32x4){} : sum[i]);
+                for (int i = 0; i < kScales; ++i)
+                    now[i] = ZEROS ? snext[i] | ((zmask >> i) & 1u ? (uint32_t)znext[i] << 16 : 8u << 16) : snext[i];
+                load_scales(k0 + kStage);
+            }
+            if (h == 1)
+                prepare_read(xnext);
+            if (h == 2)
+                prepare_write(xnext);
+            if (h < 3) {
+                read(h + 1, xs, cs, sums);
+            } else {
+                load(k0 + 3 * kStage, xs, cs);
+                read(0, xnext, cnext, snext_);
+            }
 #pragma unroll
             for (int q = 0; q < NJ; ++q) {
                 const u32x4 v = expand8<BF16>(cf[q], base16);
 #pragma unroll
                 for (int i = 0; i < MR; ++i)
-                    tmp[i][q] = dense_mfma<BF16>(xp[i], v, first ? (f32x4){} : tmp[i][q]);
+                    tmp[i][q] = dense_mfma<BF16>(xp[i], v, !first ? tmp[i][q] : ZEROS ? (f32x4){} : sum[i]);
             }
+            if (h == 2)
+                prepare_sums(snext_);
             if (h % kGroupSteps != kGroupSteps - 1)
                 continue;
-            const int g = h / kGroupSteps;
+            if constexpr (ZEROS)
+#pragma unroll
+                for (int i = 0; i < MR; ++i)
+                    sum[i] = *(const LDS_AS f32x4 *)(sums + kRows * g + 64 * (w >> 2) + 16 * i + 4 * (l >> 4));
 #pragma unroll
             for (int q = 0; q < NJ; ++q) {
-                const int e = (16 * q % (64 / GS) + (l & 15)) * GS + g;
-                const uint32_t v = __builtin_amdgcn_ds_bpermute(4 * e, now[16 * q * GS / 64]);
+                const int e = (16 * q + (l & 15)) * GS + g;   // (its register does not depend on the lane)
+                const uint32_t v = __builtin_amdgcn_ds_bpermute(4 * (e & 63), now[16 * q * GS / 64]);
                 const float s = act_to_f32<BF16>((uint16_t)v), z = 16.0f + (float)(v >> 16);
 #pragma unroll
                 for (int i = 0; i < MR; ++i)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        acc[i][q][r] = fmaf(s, fmaf(-z, sum[i][r], tmp[i][q][r]), acc[i][q][r]);
+                        acc[i][q][r] = fmaf(s, ZEROS ? fmaf(-z, sum[i][r], tmp[i][q][r]) : tmp[i][q][r], acc[i][q][r]);
             }
 #pragma unroll
             for (int q = 0; q < NJ; ++q)
@@ -578,7 +662,7 @@ struct W4Wide {
                     asm volatile("" : "+v"(acc[i][q]));
         }
     }
-    MOE_DEV void run(LDS_AS uint16_t *const (&xs)[3], LDS_AS uint16_t *const (&cs)[3])
+    MOE_DEV void run(LDS_AS uint16_t *const (&xs)[3], LDS_AS uint16_t *const (&cs)[3], LDS_AS float *const (&sums)[3])
     {
 #pragma unroll
         for (int i = 0; i < MR; ++i)
@@ -586,30 +670,41 @@ struct W4Wide {
             for (int q = 0; q < NJ; ++q)
                 acc[i][q] = (f32x4){};
         load_scales(0);
+        __builtin_amdgcn_sched_barrier(0);
         load(0, xs[0], cs[0]);
         load(kStage, xs[1], cs[1]);
+        load(2 * kStage, xs[2], cs[2]);
+        __builtin_amdgcn_sched_barrier(0);
+        wait_vmcnt<2 * (kXLoads + kCLoads)>();
+        prepare_read(xs[0]);
+        prepare_write(xs[0]);
+        prepare_sums(sums[0]);
+        meet();
+        read(0, xs[0], cs[0], sums[0]);
         int k = 0;
-        for (; k + 2 * kStage < K; k += 3 * kStage) {
-            stage(k, xs[0], cs[0], xs[2], cs[2]);
-            stage(k + kStage, xs[1], cs[1], xs[0], cs[0]);
-            stage(k + 2 * kStage, xs[2], cs[2], xs[1], cs[1]);
+        for (; k + 3 * kStage <= K; k += 3 * kStage) {
+            stage<false>(k, xs[0], cs[0], sums[0], xs[1], cs[1], sums[1]);
+            stage<false>(k + kStage, xs[1], cs[1], sums[1], xs[2], cs[2], sums[2]);
+            stage<false>(k + 2 * kStage, xs[2], cs[2], sums[2], xs[0], cs[0], sums[0]);
         }
-        if (k < K) {
-            stage(k, xs[0], cs[0], xs[2], cs[2]);
-            if (k + kStage < K)
-                stage(k + kStage, xs[1], cs[1], xs[0], cs[0]);
-        }
+        if (k < K)
+            stage<true>(k, xs[0], cs[0], sums[0], xs[1], cs[1], sums[1]);
+        if (k + kStage < K)
+            stage<true>(k + kStage, xs[1], cs[1], sums[1], xs[2], cs[2], sums[2]);
+        if (k + 2 * kStage < K)
+            stage<true>(k + 2 * kStage, xs[2], cs[2], sums[2], xs[0], cs[0], sums[0]);
         wait_vmcnt<0>();   // the loads past the end still write LDS
     }
 };
 
-template <bool BF16, bool GLU, int GLOG>
-__global__ __launch_bounds__(512) void w4_wide_kernel(W4Args a)
+template <bool BF16, bool GLU, int GLOG, bool ZEROS, int NW, int NJ>
+__global__ __launch_bounds__(64 * NW) void w4_wide_kernel(W4Args a)
 {
-    using S = W4Wide<BF16, GLOG, GLU>;
+    using S = W4Wide<BF16, GLOG, GLU, ZEROS, NW, NJ>;
     // (slots apart for the compiler, which waits for loads into an array it reads)
     __shared__ __align__(1024) uint16_t x0[S::kXHalves], x1[S::kXHalves], x2[S::kXHalves], c0[S::kCHalves],
         c1[S::kCHalves], c2[S::kCHalves];
+    __shared__ __align__(16) float s0[S::kSums], s1[S::kSums], s2[S::kSums];
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     if (blockIdx.x == 0)
         w4_status(a);
@@ -618,7 +713,7 @@ __global__ __launch_bounds__(512) void w4_wide_kernel(W4Args a)
     int c = blockIdx.x / nt, n = blockIdx.x % nt;
     if (mt % 8 == 0)
         xcd_map(blockIdx.x, nt, c, n);
-    const W4Tile t = w4_tile<S::NW>(a, c, S::kRows);
+    const W4Tile t = w4_tile<NW>(a, c, S::kRows);
     if (t.n == 0)
         return;
     const int n0 = n * kCols;
@@ -626,13 +721,14 @@ __global__ __launch_bounds__(512) void w4_wide_kernel(W4Args a)
     st.init(a, t, n0, l, w);
     LDS_AS uint16_t *const xs[3] = {(LDS_AS uint16_t *)x0, (LDS_AS uint16_t *)x1, (LDS_AS uint16_t *)x2};
     LDS_AS uint16_t *const cs[3] = {(LDS_AS uint16_t *)c0, (LDS_AS uint16_t *)c1, (LDS_AS uint16_t *)c2};
-    st.run(xs, cs);
+    LDS_AS float *const sums[3] = {(LDS_AS float *)s0, (LDS_AS float *)s1, (LDS_AS float *)s2};
+    st.run(xs, cs, sums);
     __syncthreads();
     // results through LDS, for stores of 16 bytes: a wavefront turns 16 rows at
     // a time, the 16-column block q of row r in place q ^ (r / 4 % 4)
-    constexpr int kOut = GLU ? 32 : 64;   // columns of a wavefront
+    constexpr int kOut = GLU ? S::kOwn / 2 : S::kOwn;   // columns of a wavefront
     LDS_AS float *mine = (LDS_AS float *)(w < 4 ? xs[0] : xs[1]) + (w & 3) * 16 * 64;
-    const int row0 = 64 * (w >> 2), col0 = n0 + kOut * (w & 3);
+    const int row0 = 16 * S::MR * (w >> 2), col0 = n0 + kOut * (w & 3);
 #pragma unroll
     for (int i = 0; i < S::MR; ++i) {
         wave_lds_fence();
@@ -644,19 +740,19 @@ __global__ __launch_bounds__(512) void w4_wide_kernel(W4Args a)
                 if constexpr (GLU)
                     v = (a.act == MOE_EXL3_ACT_SILU ? act_value<MOE_EXL3_ACT_SILU>(v)
                                                     : act_value<MOE_EXL3_ACT_GELU_TANH>(v)) *
-                        st.acc[i][q + 2][r];
+                        st.acc[i][q + NJ / 2][r];
                 const int m = 4 * (l >> 4) + r;
                 mine[m * kOut + 16 * (q ^ ((l >> 4) & (kOut / 16 - 1))) + (l & 15)] = v;
             }
         wave_lds_fence();
         constexpr int kLanes = kOut / 8;   // of a row
 #pragma unroll
-        for (int p = 0; p < 16 * kLanes / 64; ++p) {
+        for (int p = 0; p < (16 * kLanes + 63) / 64; ++p) {
             const int m = (64 / kLanes) * p + l / kLanes, col = 8 * (l % kLanes);
-            const LDS_AS float *at = mine + m * kOut + 16 * ((col >> 4) ^ ((m >> 2) & (kOut / 16 - 1))) + (col & 15);
+            const LDS_AS float *at = mine + (m & 15) * kOut + 16 * ((col >> 4) ^ ((m >> 2) & (kOut / 16 - 1))) + (col & 15);
             f32x4 v[2] = {*(const LDS_AS f32x4 *)at, *(const LDS_AS f32x4 *)(at + 4)};
             const int row = row0 + 16 * i + m;
-            if (row >= t.n || col0 + col >= a.N)
+            if (m >= 16 || row >= t.n || col0 + col >= a.N)
                 continue;
             if (a.base) {
                 const u32x4 b = *(const u32x4 *)(a.base + (int64_t)(t.row + row) * a.ldbase + col0 + col);
@@ -684,11 +780,36 @@ void launch_split(const W4Args &a, hipStream_t s)
     w4_split_kernel<BF16, GLU, GLOG, ROWS, NJ, NW><<<grid, 64 * NW, 0, s>>>(a);
 }
 
+template <bool BF16, bool GLU, int GLOG, int NW, int NJ>
+void launch_wide(const W4Args &a, hipStream_t s)
+{
+    constexpr int kCols = 64 * NJ / (GLU ? 2 : 1);
+    unsigned mt = w4_tiles(a, 16 * NW);
+    if (mt >= 16)
+        mt = (mt + 7) / 8 * 8;
+    const unsigned grid = mt * (unsigned)((a.N + kCols - 1) / kCols);
+    if (a.zeros[0] || a.zeros[1])
+        w4_wide_kernel<BF16, GLU, GLOG, true, NW, NJ><<<grid, 64 * NW, 0, s>>>(a);
+    else
+        w4_wide_kernel<BF16, GLU, GLOG, false, NW, NJ><<<grid, 64 * NW, 0, s>>>(a);
+}
+
 template <bool BF16, bool GLU, int GLOG>
 void launch_group(const W4Args &a, hipStream_t s)
 {
     constexpr int NJ = GLU ? 2 : 1;
     const int rows = a.offsets ? a.R / a.E : a.R;   // of an expert, on average
+    static const char *force = getenv("W4");
+    if (force) {
+        if (*force == '4') launch_split<BF16, GLU, GLOG, 4, NJ, 8>(a, s);
+        else if (*force == 'q') launch_split<BF16, GLU, GLOG, 4, NJ, 4>(a, s);
+        else if (*force == '1') launch_split<BF16, GLU, GLOG, 16, NJ, 8>(a, s);
+        else if (*force == '3') launch_split<BF16, GLU, GLOG, 32, 2, 8>(a, s);
+        else if (*force == '6') launch_split<BF16, GLU, GLOG, 64, 2, 4>(a, s);
+        else if (*force == 's') launch_wide<BF16, GLU, GLOG, 4, 2>(a, s);
+        else launch_wide<BF16, GLU, GLOG, 8, 4>(a, s);
+        return;
+    }
     if (rows <= 4) {
         if (w4_tiles(a, 4) * (unsigned)((a.N + 15) / 16) < 512)
             launch_split<BF16, GLU, GLOG, 4, NJ, 8>(a, s);
@@ -697,13 +818,9 @@ void launch_group(const W4Args &a, hipStream_t s)
     } else if (rows <= 16) {
         launch_split<BF16, GLU, GLOG, 16, NJ, 8>(a, s);
     } else if (rows <= 96) {
-        launch_split<BF16, GLU, GLOG, 64, 2, 4>(a, s);
+        launch_split<BF16, GLU, GLOG, 32, 2, 8>(a, s);
     } else {
-        constexpr int kCols = GLU ? 128 : 256;
-        unsigned mt = w4_tiles(a, 128);
-        if (mt >= 16)
-            mt = (mt + 7) / 8 * 8;
-        w4_wide_kernel<BF16, GLU, GLOG><<<mt * (unsigned)((a.N + kCols - 1) / kCols), 512, 0, s>>>(a);
+        launch_wide<BF16, GLU, GLOG, 8, 4>(a, s);
     }
 }
 
