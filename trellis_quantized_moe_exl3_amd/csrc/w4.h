@@ -26,6 +26,7 @@ struct W4Args {
     int R, K, N, E;
     int group_log2;            // 5, 6 or 7
     int act;                   // of a gated pair
+    int tiles;                 // tiles of columns that a block takes in turn
 };
 
 hipError_t launch_w4(bool bf16, bool glu, const W4Args &a, hipStream_t s);

@@ -13,7 +13,9 @@
 // of the sums' 24 bits.
 #include "dense_kernel.h"
 #include "w4.h"
-#include <stdlib.h>
+
+#include <algorithm>
+#include <cmath>
 
 namespace moe {
 
@@ -139,6 +141,7 @@ struct W4Stream {
     static constexpr int kPieces = XK / 8;                       // of a row of x
     static constexpr int kXLoads = ROWS * XK / 512, kCLoads = 2 * NJ;
     static constexpr int kXHalves = ROWS * XK, kCHalves = NJ * 1024;   // of a slot
+    static constexpr int kCols = 16 * (GLU ? NJ / 2 : NJ);      // columns of a tile
     static constexpr int kSteps = 8 / XS;                        // of 32 k, a slot of x
     static constexpr int GS = 256 >> GLOG;                       // groups of a share
     static constexpr int kGroupSteps = 8 / GS;
@@ -149,7 +152,8 @@ struct W4Stream {
     uint32_t xoff[kXLoads], coff[kCLoads];
     const uint16_t *sp[kScales];
     const uint8_t *zp[kScales];
-    int l, K, G;
+    int scol[kScales];
+    int l, K, G, N;
     uint32_t base16;
     uint16_t snext[kScales];
     uint8_t znext[kScales];
@@ -164,6 +168,7 @@ struct W4Stream {
         l = lane;
         K = a.K;
         G = K >> GLOG;
+        N = a.N;
         const int r = ROWS < 16 ? l & (ROWS - 1) : l & 15;
         xat = (uint32_t)(r * 2 * XK + 16 * ((l >> 4) ^ swizzle(r)));
         cat = (uint32_t)((l & 15) * 128 + 16 * ((l & 15) >> 1) + 4 * (l >> 4));
@@ -187,7 +192,8 @@ struct W4Stream {
         for (int i = 0; i < kScales; ++i) {
             const int r = min(GS == 2 ? 32 * i + (l >> 1) : 16 * (i / (GS / 4)) + (l >> 2), 16 * NJ - 1);
             const int m = GLU && r >= 8 * NJ;
-            const int64_t row = (matrix + min(column(n0, r), a.N - 1)) * G;
+            const int64_t row = matrix * G;
+            scol[i] = column(n0, r);
             sp[i] = (m ? a.scales[1] : a.scales[0]) + row;
             const uint8_t *z = m ? a.zeros[1] : a.zeros[0];
             zmask[i] = z ? 0xFF0000u : 0u;
@@ -198,6 +204,11 @@ struct W4Stream {
     // Column of the matrix that row r of the codes' tile is.
     MOE_DEV static int column(int n0, int r) { return n0 + (GLU ? r % (8 * NJ) : r); }
 
+    // What a wavefront's share is: its first k (K: none) and its tile of columns.
+    struct Pos {
+        int k, tile;
+    };
+
     MOE_DEV void load_x(int k0, LDS_AS uint16_t *lds)
     {
 #pragma unroll
@@ -207,23 +218,25 @@ struct W4Stream {
                                                      k < K ? xoff[i] + 2 * (uint32_t)k0 : kOutOfRange, 0, 0, 0);
         }
     }
-    MOE_DEV void load_codes(int k0, LDS_AS uint16_t *lds)
+    MOE_DEV void load_codes(const Pos &at, LDS_AS uint16_t *lds)
     {
+        const uint32_t o = (uint32_t)(at.tile * kCols) * (uint32_t)(K / 2) + (uint32_t)(at.k / 2);
 #pragma unroll
         for (int i = 0; i < kCLoads; ++i) {
-            const int r = 8 * i + (l >> 3), k = k0 + 32 * ((l & 7) ^ ((r >> 1) & 7));
+            const int r = 8 * i + (l >> 3), k = at.k + 32 * ((l & 7) ^ ((r >> 1) & 7));
             __builtin_amdgcn_raw_ptr_buffer_load_lds(c[GLU && i >= NJ], (LDS_AS void *)(lds + 512 * i), 16,
-                                                     k < K ? coff[i] + (uint32_t)(k0 / 2) : kOutOfRange, 0, 0, 0);
+                                                     k < K ? coff[i] + o : kOutOfRange, 0, 0, 0);
         }
     }
     // (Groups past the last one read it again: their x and codes are zeros.)
-    MOE_DEV void load_scales(int k0)
+    MOE_DEV void load_scales(const Pos &at)
     {
 #pragma unroll
         for (int i = 0; i < kScales; ++i) {
-            const int g = min((k0 >> GLOG) + (GS == 2 ? l & 1 : (l & 3) + 4 * (i % (GS / 4))), G - 1);
-            snext[i] = sp[i][g];
-            znext[i] = zp[i][g];
+            const int g = min((at.k >> GLOG) + (GS == 2 ? l & 1 : (l & 3) + 4 * (i % (GS / 4))), G - 1);
+            const uint32_t o = (uint32_t)min(scol[i] + at.tile * kCols, N - 1) * (uint32_t)G + (uint32_t)g;
+            snext[i] = sp[i][o];
+            znext[i] = zp[i][o];
         }
     }
     // The k of a slot of x, number j of its share.
@@ -271,12 +284,12 @@ struct W4Stream {
                     asm volatile("" : "+v"(acc[i][q]));
         }
     }
-    // Slot j of share `s`; what is loaded next: slot j of x two on, after the
-    // last one the codes of share + 2 steps, after the first the scales of the
-    // next.  (Counts: the loads that may stay in flight are the slot and the
-    // codes issued after the ones needed here.)
+    // Slot J of the share at[0]; what is loaded next: the slot of x two on, after the
+    // last one the codes of the share two on, before the first the scales of the
+    // next.  (The loads that may stay in flight are the slot and the codes issued
+    // after the ones needed here.)
     template <int J>
-    MOE_DEV void run_slot(int s, int stride, LDS_AS uint16_t *xs, LDS_AS uint16_t *cs)
+    MOE_DEV void run_slot(const Pos (&at)[3], LDS_AS uint16_t *xs, LDS_AS uint16_t *cs)
     {
         __builtin_amdgcn_sched_barrier(0);
         wait_vmcnt<kXLoads + (J == 0 ? kCLoads : 0)>();
@@ -297,56 +310,85 @@ struct W4Stream {
 #pragma unroll
             for (int i = 0; i < kScales; ++i)
                 now[i] = snext[i] | (((uint32_t)znext[i] << 16) & zmask[i]) | (zmask[i] ? 0u : 8u << 16);
-            load_scales(256 * (s + stride));
+            load_scales(at[1]);
         }
         if constexpr (J == XS - 1)
-            load_codes(256 * (s + 2 * stride), cs);
-        constexpr int next = J + 2;
-        load_x(256 * (s + next / XS * stride) + XK * (next % XS), xs);
+            load_codes(at[2], cs);
+        load_x(at[(J + 2) / XS].k + XK * ((J + 2) % XS), xs);
         __builtin_amdgcn_sched_barrier(0);
         slot(J, xf, cf);
     }
-    MOE_DEV void share(int s, int stride, LDS_AS uint16_t *x0, LDS_AS uint16_t *x1, LDS_AS uint16_t *cs)
+    MOE_DEV void share(const Pos (&at)[3], LDS_AS uint16_t *x0, LDS_AS uint16_t *x1, LDS_AS uint16_t *cs)
     {
-        run_slot<0>(s, stride, x0, cs);
+        run_slot<0>(at, x0, cs);
         if constexpr (XS >= 2)
-            run_slot<1>(s, stride, x1, cs);
+            run_slot<1>(at, x1, cs);
         if constexpr (XS == 4) {
-            run_slot<2>(s, stride, x0, cs);
-            run_slot<3>(s, stride, x1, cs);
+            run_slot<2>(at, x0, cs);
+            run_slot<3>(at, x1, cs);
         }
     }
-    // Shares first, first + stride, ..
-    MOE_DEV void run(int first, int stride, LDS_AS uint16_t *x0, LDS_AS uint16_t *x1, LDS_AS uint16_t *c0,
-                     LDS_AS uint16_t *c1)
+    MOE_DEV void clear()
     {
 #pragma unroll
         for (int i = 0; i < MR; ++i)
 #pragma unroll
             for (int q = 0; q < NJ; ++q)
                 acc[i][q] = (f32x4){};
-        const int end = (K + 255) / 256;
-        if (first >= end)
-            return;
-        load_scales(256 * first);
-        load_codes(256 * first, c0);
-        load_x(256 * first, x0);
-        load_codes(256 * (first + stride), c1);
-        load_x(XS == 1 ? 256 * (first + stride) : 256 * first + XK, x1);
-        for (int s = first; s < end; s += 2 * stride) {
-            share(s, stride, x0, x1, c0);
-            // (past the end: zeros; one share's second slot of x is its own)
+    }
+    // Of each of the block's tiles of columns the shares first, first + stride, ..;
+    // the same number for every wavefront, some past the end (zeros).  `flush` takes
+    // the sums of a tile while the next one's shares are on their way.
+    template <class F>
+    MOE_DEV void run(int first, int stride, int tiles, LDS_AS uint16_t *x0, LDS_AS uint16_t *x1, LDS_AS uint16_t *c0,
+                     LDS_AS uint16_t *c1, F flush)
+    {
+        const int per = (K + 256 * stride - 1) / (256 * stride);
+        auto after = [&](const Pos &p) {
+            Pos n = {p.k + 256 * stride, p.tile};
+            if (n.k >= 256 * stride * per)
+                n = {256 * first, p.tile + 1};
+            if (n.tile >= tiles)
+                n.k = K;   // (and no further: its columns may not exist)
+            return n;
+        };
+        Pos at[3] = {{256 * first, 0}, {}, {}};
+        at[1] = after(at[0]);
+        at[2] = after(at[1]);
+        load_scales(at[0]);
+        load_codes(at[0], c0);
+        load_x(at[0].k, x0);
+        load_codes(at[1], c1);
+        load_x(XS == 1 ? at[1].k : at[0].k + XK, x1);
+        clear();
+        int left = per;
+        auto done = [&] {   // of a share: the next one, and whether there is one
+            if (--left == 0) {
+                flush(at[0].tile);
+                left = per;
+                clear();
+                if (at[0].tile + 1 >= tiles)
+                    return true;
+            }
+            at[0] = at[1];
+            at[1] = at[2];
+            at[2] = after(at[2]);
+            return false;
+        };
+        for (;;) {
+            share(at, x0, x1, c0);
+            if (done())
+                break;
             if constexpr (XS == 1)
-                share(s + stride, stride, x1, x0, c1);
+                share(at, x1, x0, c1);
             else
-                share(s + stride, stride, x0, x1, c1);
+                share(at, x0, x1, c1);
+            if (done())
+                break;
         }
         wait_vmcnt<0>();   // the loads past the end still write LDS
     }
 };
-
-// Columns of a tile.
-constexpr int w4_cols(bool glu, int nj) { return 16 * (glu ? nj / 2 : nj); }
 
 template <bool BF16, bool GLU>
 MOE_DEV void w4_store(const W4Args &a, int64_t row, int n, float g, float u)
@@ -359,53 +401,70 @@ MOE_DEV void w4_store(const W4Args &a, int64_t row, int n, float g, float u)
     a.y[row * a.ldy + n] = BF16 ? f32_to_bf16_bits(y) : f32_to_f16_bits(y);
 }
 
+// A block takes `a.tiles` tiles of columns in turn, so that its start (the
+// offsets, the first loads) is paid once for them.
 template <bool BF16, bool GLU, int GLOG, int ROWS, int NJ, int NW>
-__global__ __launch_bounds__(64 * NW, ROWS == 4 && NW == 4 ? 3 : 1) void w4_split_kernel(W4Args a)
+__global__ __launch_bounds__(64 * NW, ROWS <= 4 ? 3 : 2) void w4_split_kernel(W4Args a)
 {
     using S = W4Stream<BF16, GLOG, ROWS, NJ, GLU>;
+    constexpr bool kApart = ROWS <= 16;          // the sums have LDS of their own
+    constexpr int kLanes = ROWS <= 4 ? 16 : 64;  // that hold rows of the tile
+    constexpr int kBlocks = S::MR * NJ;
     __shared__ __align__(1024) uint16_t x0[NW * S::kXHalves], x1[NW * S::kXHalves], c0[NW * S::kCHalves],
         c1[NW * S::kCHalves];
-    static_assert(S::MR * NJ * 1024 <= S::kXHalves * 2, "sums fit a slot of x");
+    __shared__ f32x4 own[kApart ? NW * kBlocks * kLanes : 1];
+    static_assert(kApart || kBlocks * 1024 <= S::kXHalves * 2, "sums fit a slot of x");
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     if (blockIdx.x == 0)
         w4_status(a);
-    constexpr int kCols = w4_cols(GLU, NJ);
-    const int nt = (a.N + kCols - 1) / kCols, n0 = (int)(blockIdx.x % nt) * kCols;
+    const int nt = (a.N + S::kCols * a.tiles - 1) / (S::kCols * a.tiles);
+    const int n0 = (int)(blockIdx.x % nt) * S::kCols * a.tiles;
     const W4Tile t = w4_tile<NW>(a, blockIdx.x / nt, ROWS);
     if (t.n == 0)
         return;
     S st;
     st.init(a, t, n0, l);
     LDS_AS uint16_t *mine = (LDS_AS uint16_t *)x0 + w * S::kXHalves;
-    st.run(w, NW, mine, (LDS_AS uint16_t *)x1 + w * S::kXHalves, (LDS_AS uint16_t *)c0 + w * S::kCHalves,
-           (LDS_AS uint16_t *)c1 + w * S::kCHalves);
-    // each wavefront's sums in its own first slot of x
+    constexpr int kStep = kApart ? kBlocks * kLanes : S::kXHalves / 8;   // between the wavefronts' sums
+    LDS_AS f32x4 *red = kApart ? (LDS_AS f32x4 *)own : (LDS_AS f32x4 *)((LDS_AS uint16_t *)x0);
+    auto meet = [] {
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto flush = [&](int tile) {
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!kApart)
+            wait_vmcnt<0>();   // (one tile only: the loads past the end)
+        else if (tile > 0)
+            meet();   // the last tile's sums are read
+        if (l < kLanes)
 #pragma unroll
-    for (int i = 0; i < S::MR; ++i)
+            for (int i = 0; i < kBlocks; ++i)
+                red[w * kStep + kLanes * i + l] = st.acc[i / NJ][i % NJ];
+        meet();
+        constexpr int kAcross = GLU ? NJ / 2 : NJ, kUnits = S::MR * kAcross;   // of 64 x 4 results
+        for (int u = w; u < kUnits; u += NW) {
+            const int i = u / kAcross, q = u % kAcross;
+            auto total = [&](int q) {
+                f32x4 v = red[kLanes * (i * NJ + q) + (l & (kLanes - 1))];
 #pragma unroll
-        for (int q = 0; q < NJ; ++q)
-            ((LDS_AS f32x4 *)mine)[64 * (i * NJ + q) + l] = st.acc[i][q];
-    __syncthreads();
-    constexpr int kUnits = S::MR * (GLU ? NJ / 2 : NJ);   // of 64 x 4 results
-    const LDS_AS f32x4 *red = (const LDS_AS f32x4 *)((LDS_AS uint16_t *)x0);
-    for (int u = w; u < kUnits; u += NW) {
-        const int i = u / (kUnits / S::MR), q = u % (kUnits / S::MR);
-        auto total = [&](int q) {
-            f32x4 v = red[64 * (i * NJ + q) + l];
+                for (int s = 1; s < NW; ++s)
+                    v += red[s * kStep + kLanes * (i * NJ + q) + (l & (kLanes - 1))];
+                return v;
+            };
+            const f32x4 g = total(q), up = GLU ? total(q + NJ / 2) : g;
+            const int n = n0 + S::kCols * tile + 16 * q + (l & 15);
 #pragma unroll
-            for (int s = 1; s < NW; ++s)
-                v += red[s * (S::kXHalves / 8) + 64 * (i * NJ + q) + l];
-            return v;
-        };
-        const f32x4 g = total(q), up = GLU ? total(q + NJ / 2) : g;
-        const int n = n0 + 16 * q + (l & 15);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int m = 16 * i + 4 * (l >> 4) + r;
-            if (m < t.n && n < a.N)
-                w4_store<BF16, GLU>(a, t.row + m, n, g[r], up[r]);
+            for (int r = 0; r < 4; ++r) {
+                const int m = 16 * i + 4 * (l >> 4) + r;
+                if (m < t.n && n < a.N)
+                    w4_store<BF16, GLU>(a, t.row + m, n, g[r], up[r]);
+            }
         }
-    }
+    };
+    st.run(w, NW, a.tiles, mine, (LDS_AS uint16_t *)x1 + w * S::kXHalves, (LDS_AS uint16_t *)c0 + w * S::kCHalves,
+           (LDS_AS uint16_t *)c1 + w * S::kCHalves, flush);
 }
 
 // ---- tiles of many rows, columns over the wavefronts of a block
@@ -773,11 +832,20 @@ unsigned w4_tiles(const W4Args &a, int rows)
     return (unsigned)(a.offsets ? a.R / rows + min(a.E, a.R) : (a.R + rows - 1) / rows);
 }
 
-template <bool BF16, bool GLU, int GLOG, int ROWS, int NJ, int NW>
+// Tiles of columns are dealt so that about as many blocks are left as the CUs
+// hold at once, but at most four to a block (64 rows of 40 experts, 2048 x 4096:
+// 55 us with one each, 43 with two, 39 with four, 42 with eight; 64 at 58 experts'
+// pairs of 4096 x 2048: 124, 106, 106, 109; one row, 4096 x 4096, whose 256
+// blocks leave room on each CU: 6.2, 9.1, 14.9, 26.3).
+template <bool BF16, bool GLU, int GLOG, int ROWS, int NJ>
 void launch_split(const W4Args &a, hipStream_t s)
 {
-    const unsigned grid = w4_tiles(a, ROWS) * (unsigned)((a.N + w4_cols(GLU, NJ) - 1) / w4_cols(GLU, NJ));
-    w4_split_kernel<BF16, GLU, GLOG, ROWS, NJ, NW><<<grid, 64 * NW, 0, s>>>(a);
+    constexpr int kCols = 16 * (GLU ? NJ / 2 : NJ);
+    constexpr unsigned kAtOnce = NJ == 1 ? 1536 : 800;
+    const unsigned mt = w4_tiles(a, ROWS), nt = (unsigned)((a.N + kCols - 1) / kCols);
+    W4Args b = a;
+    b.tiles = ROWS <= 16 ? (int)min(max((mt * nt + kAtOnce / 2) / kAtOnce, 1u), min(4u, nt)) : 1;
+    w4_split_kernel<BF16, GLU, GLOG, ROWS, NJ, 4><<<mt * ((nt + b.tiles - 1) / b.tiles), 256, 0, s>>>(b);
 }
 
 template <bool BF16, bool GLU, int GLOG, int NW, int NJ>
@@ -794,33 +862,79 @@ void launch_wide(const W4Args &a, hipStream_t s)
         w4_wide_kernel<BF16, GLU, GLOG, false, NW, NJ><<<grid, 64 * NW, 0, s>>>(a);
 }
 
+// The variants: rows and columns of a tile (of a gated pair half as many columns
+// from 32 on).
+enum W4Variant { W4_4x16, W4_4x32, W4_16x16, W4_16x32, W4_32x32, W4_64x128, W4_128x256 };
+
+// The variant of a call, by estimates of its time in us: a part that a block
+// takes alone on a CU, and one that 256 blocks (one a CU, others beside them) add, each
+// with a part per 128 k.  Fitted to 1 to 4096 rows of 4096 x 4096, 2048 x 4096
+// (pairs) and 512 x 8192, and there to order the variants, which they do but for
+// near ties (4096 x 4096, us measured for the seven in this order, - not run:
+//   1 row      6.3   7.4   6.9   8.2   10.0  35   65
+//   16        11.2  10.0   7.2   8.4   10.1  35   66
+//   64        34    27    15.6  11.9   10.7  36   67
+//   256        -     -    45    38     27    37   68
+//   1024       -     -     -     -     95    54   68
+//   4096       -     -     -     -    351   209  156
+// and 64 experts of 2048 x 4096 with 256 rows in all: 88, 75, 87, 76, 122, 103, 146;
+// with 4096: -, -, 340, 268, 300, 170, 187).  Of experts the host knows the number
+// alone: as many as there are rows are taken to have some, half a tile is lost
+// to each one's last rows, and one with many rows beside empty ones costs more
+// than it would alone (16384 rows at 4 of 64 experts take the variant for all 64).
+template <bool GLU>
+W4Variant choose(const W4Args &a)
+{
+    struct Cost {
+        W4Variant v;
+        double rows, cols, alone, alone_k, more, more_k;
+        int at_once;   // blocks that start together, where a last few cost a round
+    };
+    // (of a pair the first two kinds have the columns of the narrow and the work of the wide)
+    static const Cost kCosts[] = {
+        {W4_4x16, 4, 16, 4.2, 0.065, 0.3, GLU ? 0.085 : 0.05, 1},
+        {W4_4x32, 4, 32, 4.1, 0.105, 0.57, 0.07, 1},
+        {W4_16x16, 16, 16, 4.8, 0.07, 0.3, GLU ? 0.095 : 0.06, 1},
+        {W4_16x32, 16, 32, 4.3, 0.127, 0.7, 0.105, 1},
+        {W4_32x32, 32, GLU ? 16 : 32, 4.7, 0.17, 1.7, 0.11, 1},
+        {W4_64x128, 64, GLU ? 64 : 128, 4.5, 0.95, 2.0, 0.70, 512},
+        {W4_128x256, 128, GLU ? 128 : 256, 6.8, 1.85, 5.7, 2.29, 256},
+    };
+    const double k = a.K / 128.0;
+    // finer groups, and zeros, cost the wide tiles' products more
+    const double fine = (a.group_log2 == 5 ? 1.5 : a.group_log2 == 6 ? 1.2 : 1.0) * (a.zeros[0] || a.zeros[1] ? 1.1 : 1.0);
+    const double n = a.offsets ? min(a.E, a.R) : 1, rows = a.R / n;
+    W4Variant best = W4_4x16;
+    double least = 0;
+    for (const Cost &c : kCosts) {
+        if (GLU && (c.v == W4_4x32 || c.v == W4_16x32))
+            continue;
+        const double f = c.rows >= 64 ? fine : 1.0;
+        const double tiles = a.offsets ? n * max(1.0, rows / c.rows + 0.5) : ceil(rows / c.rows);
+        double blocks = tiles * ceil(a.N / c.cols);
+        if (c.at_once > 1 && blocks > 256)
+            blocks = ceil(blocks / c.at_once) * c.at_once;
+        const double us = max(c.alone + c.alone_k * f * k, 3 + blocks / 256 * (c.more + c.more_k * f * k));
+        if (least == 0 || us < least) {
+            least = us;
+            best = c.v;
+        }
+    }
+    return best;
+}
+
 template <bool BF16, bool GLU, int GLOG>
 void launch_group(const W4Args &a, hipStream_t s)
 {
-    constexpr int NJ = GLU ? 2 : 1;
-    const int rows = a.offsets ? a.R / a.E : a.R;   // of an expert, on average
-    static const char *force = getenv("W4");
-    if (force) {
-        if (*force == '4') launch_split<BF16, GLU, GLOG, 4, NJ, 8>(a, s);
-        else if (*force == 'q') launch_split<BF16, GLU, GLOG, 4, NJ, 4>(a, s);
-        else if (*force == '1') launch_split<BF16, GLU, GLOG, 16, NJ, 8>(a, s);
-        else if (*force == '3') launch_split<BF16, GLU, GLOG, 32, 2, 8>(a, s);
-        else if (*force == '6') launch_split<BF16, GLU, GLOG, 64, 2, 4>(a, s);
-        else if (*force == 's') launch_wide<BF16, GLU, GLOG, 4, 2>(a, s);
-        else launch_wide<BF16, GLU, GLOG, 8, 4>(a, s);
-        return;
-    }
-    if (rows <= 4) {
-        if (w4_tiles(a, 4) * (unsigned)((a.N + 15) / 16) < 512)
-            launch_split<BF16, GLU, GLOG, 4, NJ, 8>(a, s);
-        else
-            launch_split<BF16, GLU, GLOG, 4, NJ, 4>(a, s);
-    } else if (rows <= 16) {
-        launch_split<BF16, GLU, GLOG, 16, NJ, 8>(a, s);
-    } else if (rows <= 96) {
-        launch_split<BF16, GLU, GLOG, 32, 2, 8>(a, s);
-    } else {
-        launch_wide<BF16, GLU, GLOG, 8, 4>(a, s);
+    constexpr int kOne = GLU ? 2 : 1;   // 16-column blocks of the narrow tiles
+    switch (choose<GLU>(a)) {
+    case W4_4x16: return launch_split<BF16, GLU, GLOG, 4, kOne>(a, s);
+    case W4_4x32: return launch_split<BF16, GLU, GLOG, 4, 2>(a, s);
+    case W4_16x16: return launch_split<BF16, GLU, GLOG, 16, kOne>(a, s);
+    case W4_16x32: return launch_split<BF16, GLU, GLOG, 16, 2>(a, s);
+    case W4_32x32: return launch_split<BF16, GLU, GLOG, 32, 2>(a, s);
+    case W4_64x128: return launch_wide<BF16, GLU, GLOG, 4, 2>(a, s);
+    case W4_128x256: return launch_wide<BF16, GLU, GLOG, 8, 4>(a, s);
     }
 }
 
