@@ -33,7 +33,7 @@ int check_desc(const moe_exl3_tokens_desc *d)
 
 bool slots_fit(const moe_exl3_tokens_desc &d, int64_t T) { return T <= kMaxRows / d.top_k; }
 
-int64_t sort_blocks(int64_t n) { return cdiv(n, kSortChunk); }
+int64_t sort_blocks(int64_t n) { return n <= kSortAlone ? 1 : cdiv(n, kSortChunk); }
 
 size_t sort_bytes(const moe_exl3_tokens_desc &d, int64_t T)
 {
@@ -145,7 +145,7 @@ int moe_exl3_sort(const moe_exl3_tokens_desc *desc, const int32_t *idx, int64_t 
     a.idx = idx;
     a.n = n;
     a.E = (int)E;
-    a.nblk = (int)std::max<int64_t>(1, sort_blocks(n));   // no slots: the tables of none
+    a.nblk = (int)sort_blocks(n);   // (no slots: one block writes the tables of none)
     a.hist = at<int32_t>(workspace, kAlign);
     a.counts = counts;
     a.offsets = offsets;

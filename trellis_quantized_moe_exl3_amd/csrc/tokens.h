@@ -12,8 +12,9 @@ namespace moe {
 
 constexpr int kMaxTopK = 16;
 constexpr int kMaxExperts = 1024;
-// Slots of one block of the sort; calls of at most that many take one launch.
-constexpr int kSortChunk = 4096;
+// Slots of one block of the sort, and up to how many one block does it all.
+constexpr int kSortChunk = 2048;
+constexpr int kSortAlone = 4096;
 // Blocks up to which each block of the sort adds up the others' counts itself.
 constexpr int kSortScan = 64;
 
@@ -59,6 +60,7 @@ struct DropoutArgs {
     void *y;
     int64_t ldx, ldr, ldy, rows;
     int cols;
+    uint64_t counter;   // of the first row, beside the generator's offset
     Drop drop;
 };
 

@@ -3,16 +3,18 @@
 #include "philox.h"
 #include "tokens.h"
 
+#include <algorithm>
+
 namespace moe {
 
 // ---------------------------------------------------------------- sort
-// Stable counting sort of the slots by expert.  A block holds kSortChunk slots,
-// a wavefront a run of them; slots of one expert in 64 consecutive ones are
+// Stable counting sort of the slots by expert.  A block holds a chunk of slots (4096
+// where it is the only one, else 2048: the ballots of 16 wavefronts take 3 us for
+// 4096), a wavefront a run of them; slots of one expert in 64 consecutive ones are
 // ranked from ballots over the index bits, earlier ones from the wavefront's
 // counts, earlier wavefronts from theirs, and earlier blocks from the counts
 // that a first launch left.  No atomics: the tables are the same on each call.
 constexpr int kSortWaves = 16;
-constexpr int kSortIter = kSortChunk / kSortWaves / 64;
 
 MOE_DEV int scan64(int v, int l)   // inclusive, over a wavefront
 {
@@ -33,7 +35,7 @@ __global__ __launch_bounds__(1024) void sort_count_kernel(SortArgs a)
     __syncthreads();
     const int64_t a0 = (int64_t)blockIdx.x * kSortChunk;
 #pragma unroll
-    for (int i = 0; i < kSortChunk / 1024; ++i) {
+    for (int i = 0; i < kSortChunk / 1024; ++i) {   // (blocks of several only)
         const int64_t s = a0 + 1024 * i + threadIdx.x;
         if (s < a.n) {
             const int e = a.idx[s];
@@ -64,8 +66,10 @@ __global__ __launch_bounds__(64) void sort_scan_kernel(SortArgs a)
         a.hist[(int64_t)a.nblk * (a.E + 1) + e] = run;
 }
 
+template <int ITER>
 __global__ __launch_bounds__(1024) void sort_kernel(SortArgs a)
 {
+    constexpr int kSortIter = ITER;
     extern __shared__ int32_t first[];                          // [E]
     uint16_t *cnt = (uint16_t *)(first + a.E);                  // [kSortWaves][E]
     __shared__ int wsum[kSortWaves];
@@ -79,16 +83,39 @@ __global__ __launch_bounds__(1024) void sort_kernel(SortArgs a)
     int nbits = 0;
     while ((1 << nbits) < E)
         ++nbits;
-    const int64_t s0 = (int64_t)blk * kSortChunk + w * (64 * kSortIter) + l;
+    const int64_t s0 = ((int64_t)blk * kSortWaves + w) * (64 * kSortIter) + l;
     int ev[kSortIter], rank[kSortIter];
 #pragma unroll
     for (int c = 0; c < kSortIter; ++c)
         ev[c] = s0 + 64 * c < a.n ? a.idx[s0 + 64 * c] : -1;
+    // the blocks' counts, all of them in flight at once (the others wrote them on
+    // other XCDs: 2 us a round trip)
+    const int64_t row = E + 1;
+    int total = 0, before = 0;
+    if (a.nblk > kSortScan) {
+        if (tid < E) {
+            before = a.hist[blk * row + tid];
+            total = a.hist[a.nblk * row + tid];
+        }
+    } else if (a.nblk > 1 && tid < E) {
+        int v[kSortScan];
+#pragma unroll
+        for (int b = 0; b < kSortScan; ++b)
+            v[b] = b < a.nblk ? a.hist[b * row + tid] : 0;
+#pragma unroll
+        for (int b = 0; b < kSortScan; ++b) {
+            total += v[b];
+            before += b < blk ? v[b] : 0;
+        }
+    }
     __syncthreads();
     uint16_t *mine = cnt + w * E;
     bool wrong = false;
 #pragma unroll
     for (int c = 0; c < kSortIter; ++c) {
+        rank[c] = 0;
+        if (s0 - l + 64 * c >= a.n)   // (the whole wavefront)
+            break;
         const int e = ev[c];
         const bool valid = (unsigned)e < (unsigned)E;
         wrong |= !valid && e != -1;
@@ -108,35 +135,32 @@ __global__ __launch_bounds__(1024) void sort_kernel(SortArgs a)
         bad = 1;
     __syncthreads();
     // per expert: the wavefronts' counts -> their sums before, the chunk's total
-    int own = 0, total = 0, before = 0;
-    if (tid < E)
+    // (of the wavefronts that have slots)
+    const int waves =
+        (int)min<int64_t>(kSortWaves, (a.n - (s0 - l) + 64 * kSortIter - 1) / (64 * kSortIter) + w);
+    int own = 0;
+    if (tid < E) {
+        int t[kSortWaves];
+#pragma unroll
+        for (int v = 0; v < kSortWaves; ++v)
+            t[v] = v < waves ? cnt[v * E + tid] : 0;
+#pragma unroll
         for (int v = 0; v < kSortWaves; ++v) {
-            const int t = cnt[v * E + tid];
-            cnt[v * E + tid] = (uint16_t)own;
-            own += t;
-        }
-    const int64_t row = E + 1;
-    if (a.nblk == 1) {
-        total = own;
-    } else if (tid < E) {
-        if (a.nblk > kSortScan) {
-            before = a.hist[blk * row + tid];
-            total = a.hist[a.nblk * row + tid];
-        } else {
-            for (int b = 0; b < a.nblk; ++b) {
-                const int v = a.hist[b * row + tid];
-                total += v;
-                before += b < blk ? v : 0;
-            }
+            if (v < waves)
+                cnt[v * E + tid] = (uint16_t)own;
+            own += t[v];
         }
     }
+    if (a.nblk == 1)
+        total = own;
     const int incl = scan64(total, l);
     if (l == 63)
         wsum[w] = incl;
     __syncthreads();
     int off = incl - total;
-    for (int v = 0; v < w; ++v)
-        off += wsum[v];
+#pragma unroll
+    for (int v = 0; v < kSortWaves; ++v)
+        off += v < w ? wsum[v] : 0;
     if (tid < E)
         first[tid] = off + before;
     if (blk == 0) {
@@ -178,7 +202,12 @@ hipError_t launch_sort(const SortArgs &a, hipStream_t s)
         if (a.nblk > kSortScan)
             sort_scan_kernel<<<(unsigned)(a.E + 1), 64, 0, s>>>(a);
     }
-    sort_kernel<<<(unsigned)a.nblk, 1024, a.E * sizeof(int32_t) + kSortWaves * a.E * sizeof(uint16_t), s>>>(a);
+    const size_t lds = a.E * sizeof(int32_t) + kSortWaves * a.E * sizeof(uint16_t);
+    static_assert(kSortChunk == 2 * 64 * kSortWaves && kSortAlone == 4 * 64 * kSortWaves, "slots of a block");
+    if (a.nblk == 1)
+        sort_kernel<4><<<1, 1024, lds, s>>>(a);
+    else
+        sort_kernel<2><<<(unsigned)a.nblk, 1024, lds, s>>>(a);
     return hipGetLastError();
 }
 
@@ -253,7 +282,7 @@ __global__ __launch_bounds__(256) void spread_kernel(TokenArgs a)
 #pragma unroll
             for (int j = 0; j < KB; ++j)
                 if (pos[j] >= 0)
-                    z[j] = *(const u32x4 *)(a.z + pos[j] * a.ldz + 8 * c);
+                    z[j] = __builtin_nontemporal_load((const u32x4 *)(a.z + pos[j] * a.ldz + 8 * c));
         if (a.drop.rng)
             drop8(a.drop, seed, offset + c, x);
 #pragma unroll
@@ -264,7 +293,7 @@ __global__ __launch_bounds__(256) void spread_kernel(TokenArgs a)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] = w[j] * x[i];
-            *(u32x4 *)(a.out + pos[j] * a.ldo + 8 * c) = round8<BF16>(v);
+            __builtin_nontemporal_store(round8<BF16>(v), (u32x4 *)(a.out + pos[j] * a.ldo + 8 * c));
             if constexpr (DOT) {
                 unpack8<BF16>(z[j], v);
 #pragma unroll
@@ -302,7 +331,7 @@ __global__ __launch_bounds__(256) void gather_kernel(TokenArgs a)
 #pragma unroll
         for (int j = 0; j < KB; ++j)
             if (pos[j] >= 0)
-                z[j] = *(const u32x4 *)(a.z + pos[j] * a.ldz + 8 * c);
+                z[j] = __builtin_nontemporal_load((const u32x4 *)(a.z + pos[j] * a.ldz + 8 * c));
         float x[8], y[8];
         if constexpr (DOT)
             unpack8<BF16>(*(const u32x4 *)(a.x + t * a.ldx + 8 * c), x);
@@ -331,7 +360,7 @@ __global__ __launch_bounds__(256) void gather_kernel(TokenArgs a)
             for (int i = 0; i < 8; ++i)
                 y[i] += b[i];
         }
-        *(u32x4 *)(a.out + t * a.ldo + 8 * c) = round8<BF16>(y);
+        __builtin_nontemporal_store(round8<BF16>(y), (u32x4 *)(a.out + t * a.ldo + 8 * c));
     }
     if constexpr (DOT)
         store_dots<KB>(a, t, dot);
@@ -397,41 +426,149 @@ MOE_DEV void store1(void *p, int64_t i, float v)
         ((uint16_t *)p)[i] = DT == MOE_EXL3_DT_BF16 ? f32_to_bf16_bits(v) : f32_to_f16_bits(v);
 }
 
-// One thread for eight columns of a row.
+// Eight consecutive elements at any address of theirs (rows of an odd length
+// begin anywhere; 16-byte accesses need no alignment here).
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
 template <int DT>
-__global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a)
-{
-    const int64_t groups = (a.cols + 7) / 8;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= a.rows * groups)
-        return;
-    const int64_t r = i / groups;
-    const int c = 8 * (int)(i - r * groups), n = min(8, a.cols - c);
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        v[j] = j < n ? load1<DT>(a.x, r * a.ldx + c + j) : 0.0f;
-    if (a.drop.rng)
-        drop8(a.drop, a.drop.rng[0], a.drop.rng[1] + i, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j < n) {
-            if (a.residual)
-                v[j] += load1<DT>(a.residual, r * a.ldr + c + j);
-            store1<DT>(a.y, r * a.ldy + c + j, v[j]);
+struct Eight {
+    u32x4 v[DT == MOE_EXL3_DT_F32 ? 2 : 1];
+    MOE_DEV void load(const void *p, int64_t i)
+    {
+        if constexpr (DT == MOE_EXL3_DT_F32) {
+            v[0] = __builtin_nontemporal_load((const u32x4_any *)((const float *)p + i));
+            v[1] = __builtin_nontemporal_load((const u32x4_any *)((const float *)p + i + 4));
+        } else {
+            v[0] = __builtin_nontemporal_load((const u32x4_any *)((const uint16_t *)p + i));
         }
+    }
+    MOE_DEV void get(float (&f)[8]) const
+    {
+        if constexpr (DT == MOE_EXL3_DT_F32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                f[j] = __uint_as_float(v[j / 4][j % 4]);
+        } else {
+            unpack8<DT == MOE_EXL3_DT_BF16>(v[0], f);
+        }
+    }
+    MOE_DEV void set(const float (&f)[8])
+    {
+        if constexpr (DT == MOE_EXL3_DT_F32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j / 4][j % 4] = __float_as_uint(f[j]);
+        } else {
+            v[0] = round8<DT == MOE_EXL3_DT_BF16>(f);
+        }
+    }
+    MOE_DEV void store(void *p, int64_t i) const
+    {
+        if constexpr (DT == MOE_EXL3_DT_F32) {
+            __builtin_nontemporal_store(v[0], (u32x4_any *)((float *)p + i));
+            __builtin_nontemporal_store(v[1], (u32x4_any *)((float *)p + i + 4));
+        } else {
+            __builtin_nontemporal_store(v[0], (u32x4_any *)((uint16_t *)p + i));
+        }
+    }
+};
+
+// A thread takes eight columns of a row (one counter), kDropGroups times.
+constexpr int kDropGroups = 2;
+
+template <int DT, bool RES>
+__global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, uint32_t groups, uint32_t total)
+{
+    const uint32_t i0 = blockIdx.x * (256 * kDropGroups) + threadIdx.x;
+    Eight<DT> x[kDropGroups], res[kDropGroups];
+    uint32_t row[kDropGroups], col[kDropGroups];
+    bool whole[kDropGroups];
+#pragma unroll
+    for (int u = 0; u < kDropGroups; ++u) {
+        const uint32_t i = i0 + 256 * u;
+        row[u] = i / groups;
+        col[u] = 8 * (i - row[u] * groups);
+        whole[u] = i < total && col[u] + 8 <= (uint32_t)a.cols;
+        if (whole[u]) {
+            x[u].load(a.x, row[u] * a.ldx + col[u]);
+            if (RES)
+                res[u].load(a.residual, row[u] * a.ldr + col[u]);
+        }
+    }
+    uint64_t seed = 0, offset = 0;
+    if (a.drop.rng) {
+        seed = a.drop.rng[0];
+        offset = a.drop.rng[1] + a.counter;
+    }
+#pragma unroll
+    for (int u = 0; u < kDropGroups; ++u) {
+        const uint32_t i = i0 + 256 * u;
+        if (i >= total)
+            return;
+        float v[8], b[8];
+        if (whole[u]) {
+            x[u].get(v);
+            if (a.drop.rng)
+                drop8(a.drop, seed, offset + i, v);
+            if (RES) {
+                res[u].get(b);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] += b[j];
+            }
+            x[u].set(v);
+            x[u].store(a.y, row[u] * a.ldy + col[u]);
+            continue;
+        }
+        // the last columns of a row that is no multiple of eight
+        const int n = a.cols - (int)col[u];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = j < n ? load1<DT>(a.x, row[u] * a.ldx + col[u] + j) : 0.0f;
+            b[j] = RES && j < n ? load1<DT>(a.residual, row[u] * a.ldr + col[u] + j) : 0.0f;
+        }
+        if (a.drop.rng)
+            drop8(a.drop, seed, offset + i, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n)
+                store1<DT>(a.y, row[u] * a.ldy + col[u] + j, RES ? v[j] + b[j] : v[j]);
+    }
 }
 
-hipError_t launch_dropout(int dtype, const DropoutArgs &a, hipStream_t s)
+template <int DT>
+void launch_dropout_type(const DropoutArgs &a, uint32_t groups, uint32_t total, hipStream_t s)
 {
-    const unsigned grid = (unsigned)((a.rows * ((a.cols + 7) / 8) + 255) / 256);
-    if (dtype == MOE_EXL3_DT_BF16)
-        dropout_kernel<MOE_EXL3_DT_BF16><<<grid, 256, 0, s>>>(a);
-    else if (dtype == MOE_EXL3_DT_F16)
-        dropout_kernel<MOE_EXL3_DT_F16><<<grid, 256, 0, s>>>(a);
+    const unsigned grid = (total + 256 * kDropGroups - 1) / (256 * kDropGroups);
+    if (a.residual)
+        dropout_kernel<DT, true><<<grid, 256, 0, s>>>(a, groups, total);
     else
-        dropout_kernel<MOE_EXL3_DT_F32><<<grid, 256, 0, s>>>(a);
-    return hipGetLastError();
+        dropout_kernel<DT, false><<<grid, 256, 0, s>>>(a, groups, total);
+}
+
+hipError_t launch_dropout(int dtype, const DropoutArgs &args, hipStream_t s)
+{
+    const int64_t groups = (args.cols + 7) / 8;
+    const int64_t step = std::max<int64_t>(1, ((int64_t)1 << 30) / groups);   // rows whose groups 32 bits number
+    const int64_t size = dtype == MOE_EXL3_DT_F32 ? 4 : 2;
+    DropoutArgs a = args;
+    for (int64_t r = 0; r < args.rows; r += step) {
+        a.rows = std::min(step, args.rows - r);
+        a.x = (const char *)args.x + r * args.ldx * size;
+        a.residual = args.residual ? (const char *)args.residual + r * args.ldr * size : nullptr;
+        a.y = (char *)args.y + r * args.ldy * size;
+        a.counter = (uint64_t)(r * groups);
+        const uint32_t total = (uint32_t)(a.rows * groups);
+        if (dtype == MOE_EXL3_DT_BF16)
+            launch_dropout_type<MOE_EXL3_DT_BF16>(a, (uint32_t)groups, total, s);
+        else if (dtype == MOE_EXL3_DT_F16)
+            launch_dropout_type<MOE_EXL3_DT_F16>(a, (uint32_t)groups, total, s);
+        else
+            launch_dropout_type<MOE_EXL3_DT_F32>(a, (uint32_t)groups, total, s);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace moe
