@@ -73,7 +73,7 @@ def test_linear(T, K, N, E, group, dtype):
         D.assert_close(y, ref, bound, f"zeros {zeros}", 2 * R.half_step(dtype))
         if b is not None:   # in place
             z, _ = D.inside(base)
-            M.w4_linear(d, x, M.make_w4(*s), z, D.poisoned(256), offsets=_offsets(bounds), base=z)
+            M.w4_linear(d, x, M.make_w4(*s), z, D.poisoned(M.w4_workspace_size(d, T)), offsets=_offsets(bounds), base=z)
             assert torch.equal(z, y)
 
 

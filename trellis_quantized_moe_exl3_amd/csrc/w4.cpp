@@ -75,7 +75,7 @@ int run(const moe_exl3_w4_desc *desc, const void *x, int64_t ldx, const moe_exl3
     for (int i = 0; i < n; ++i)
         if (meets_weights(my, *desc, *w[i]))
             return MOE_EXL3_ERR_INVALID_ARG;
-    if ((rc = check_ws(workspace, ws_bytes, kAlign)))
+    if ((rc = check_ws(workspace, ws_bytes, kAlign + align_up(w4_scratch(rows, desc->n_experts)))))
         return rc;
     W4Args a{};
     a.x = (const uint16_t *)x;
@@ -92,6 +92,7 @@ int run(const moe_exl3_w4_desc *desc, const void *x, int64_t ldx, const moe_exl3
     a.y = (uint16_t *)y;
     a.ldy = ldy;
     a.status = at<int32_t>(workspace, MOE_EXL3_STATUS_OFFSET);
+    a.scratch = at<int32_t>(workspace, kAlign);
     a.R = (int)rows;
     a.K = (int)K;
     a.N = (int)N;
@@ -115,7 +116,7 @@ int moe_exl3_w4_workspace_size(const moe_exl3_w4_desc *desc, int64_t max_rows, s
         return MOE_EXL3_ERR_INVALID_ARG;
     if (!rows_fit(max_rows, desc->n_in) || !rows_fit(max_rows, desc->n_out))
         return MOE_EXL3_ERR_UNSUPPORTED;
-    *bytes = kAlign;
+    *bytes = kAlign + align_up(w4_scratch(max_rows, desc->n_experts));
     return MOE_EXL3_OK;
 }
 

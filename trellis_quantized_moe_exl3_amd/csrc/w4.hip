@@ -49,15 +49,32 @@ MOE_DEV u32x4 permute8(u32x4 x)
                    __builtin_amdgcn_perm(x[3], x[1], 0x05040100u), __builtin_amdgcn_perm(x[3], x[1], 0x07060302u)};
 }
 
-// The tile number `c` of a call: its expert and rows (n = 0: past the last one).
+// The tile number `c` of a launch: its expert and rows (n = 0: past the last one).
 // Every thread of the block calls it.
 struct W4Tile {
     int e, row, n;
 };
 
+// Rows of expert e, clamped into the call's.
+MOE_DEV void w4_rows(const W4Args &a, int e, int &lo, int &hi)
+{
+    lo = hi = 0;
+    if (e < a.E) {
+        lo = min(max(a.offsets[e], 0), a.R);
+        hi = min(max(a.offsets[e + 1], lo), a.R);
+    }
+}
+
 template <int NW>
 MOE_DEV W4Tile w4_tile(const W4Args &a, int c, int tile_rows)
 {
+    if (a.list) {
+        // (the entry behind the last one may be read; the list has room for it)
+        const int4 t = a.list[c];
+        const int n = __builtin_amdgcn_readfirstlane(*a.count);
+        return {__builtin_amdgcn_readfirstlane(t.x), __builtin_amdgcn_readfirstlane(t.y),
+                c < n ? __builtin_amdgcn_readfirstlane(t.z) : 0};
+    }
     if (!a.offsets) {
         const int row = c * tile_rows;
         return {0, row, row < a.R ? min(tile_rows, a.R - row) : 0};
@@ -70,11 +87,8 @@ MOE_DEV W4Tile w4_tile(const W4Args &a, int c, int tile_rows)
     for (int e0 = 0; e0 < a.E; e0 += 64 * NW) {
         __syncthreads();
         const int e = e0 + tid;
-        int lo = 0, hi = 0;
-        if (e < a.E) {
-            lo = min(max(a.offsets[e], 0), a.R);
-            hi = min(max(a.offsets[e + 1], lo), a.R);
-        }
+        int lo, hi;
+        w4_rows(a, e, lo, hi);
         const int tiles = (hi - lo + tile_rows - 1) / tile_rows;
         int v = tiles;
 #pragma unroll
@@ -103,7 +117,7 @@ MOE_DEV W4Tile w4_tile(const W4Args &a, int c, int tile_rows)
 
 // Offsets that are not ascending within the rows.
 MOE_DEV void w4_status(const W4Args &a)
-{
+{   // (every thread of a block)
     __shared__ int bad;
     if (threadIdx.x == 0)
         bad = 0;
@@ -117,6 +131,82 @@ MOE_DEV void w4_status(const W4Args &a)
     __syncthreads();
     if (threadIdx.x == 0)
         *a.status = bad ? MOE_EXL3_STATUS_BAD_INDEX : 0;
+}
+
+// The tiles of a call's two launches, each an expert, its first row and their
+// number, from the offsets, in one block.  Experts of more than `limit` rows make up the second list
+// if their tiles take the first variant longer than the second.
+__global__ __launch_bounds__(1024) void w4_list_kernel(W4Args a, W4Lists lists)
+{
+    __shared__ int first[2][1024], last[1024];   // of an expert's tiles in either list; its last row
+    __shared__ int wsum[2][16], crowd[2][16];
+    const int e = threadIdx.x, w = e >> 6, l = e & 63;
+    w4_status(a);
+    int lo, hi;
+    w4_rows(a, e, lo, hi);
+    const int rows = hi - lo;
+    const bool many = rows > lists.limit;
+    int t[2], v[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        t[i] = (rows + lists.rows[i] - 1) / lists.rows[i];
+        v[i] = many ? t[i] : 0;
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1)
+            v[i] += __shfl_xor(v[i], d, 64);
+        if (l == 0)
+            crowd[i][w] = v[i];
+    }
+    __syncthreads();
+    v[0] = v[1] = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        v[0] += crowd[0][i];
+        v[1] += crowd[1][i];
+    }
+    const bool two = (float)v[0] * lists.us[0] > 1.5f * fmaxf((float)v[1] * lists.us[1], lists.least_us);
+    t[0] = two && many ? 0 : t[0];
+    t[1] = two && many ? t[1] : 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        v[i] = t[i];
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(v[i], d, 64);
+            v[i] += l >= d ? o : 0;
+        }
+        if (l == 63)
+            wsum[i][w] = v[i];
+    }
+    __syncthreads();
+    int total[2] = {};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int before = v[i] - t[i];
+#pragma unroll
+        for (int s = 0; s < 16; ++s) {
+            before += s < w ? wsum[i][s] : 0;
+            total[i] += wsum[i][s];
+        }
+        first[i][e] = before;
+        if (e == 0)
+            *lists.count[i] = total[i];
+    }
+    last[e] = hi;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        for (int c = e; c < total[i]; c += 1024) {
+            // the last expert whose tiles begin at c or before (those without tiles
+            // begin where the next one's do)
+            int at = 0;
+#pragma unroll
+            for (int step = 512; step > 0; step >>= 1)
+                if (first[i][at + step] <= c)
+                    at += step;
+            const int row = min(max(a.offsets[at], 0), a.R) + (c - first[i][at]) * lists.rows[i];
+            lists.list[i][c] = make_int4(at, row, min(lists.rows[i], last[at] - row), 0);
+        }
 }
 
 // ---- tiles of few rows, k cut over the wavefronts of a block
@@ -415,7 +505,7 @@ __global__ __launch_bounds__(64 * NW, ROWS <= 4 ? 3 : 2) void w4_split_kernel(W4
     __shared__ f32x4 own[kApart ? NW * kBlocks * kLanes : 1];
     static_assert(kApart || kBlocks * 1024 <= S::kXHalves * 2, "sums fit a slot of x");
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0 && !a.list)
         w4_status(a);
     const int nt = (a.N + S::kCols * a.tiles - 1) / (S::kCols * a.tiles);
     const int n0 = (int)(blockIdx.x % nt) * S::kCols * a.tiles;
@@ -765,7 +855,7 @@ __global__ __launch_bounds__(64 * NW) void w4_wide_kernel(W4Args a)
         c1[S::kCHalves], c2[S::kCHalves];
     __shared__ __align__(16) float s0[S::kSums], s1[S::kSums], s2[S::kSums];
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0 && !a.list)
         w4_status(a);
     constexpr int kCols = GLU ? S::kCols / 2 : S::kCols;
     const int nt = (a.N + kCols - 1) / kCols, mt = gridDim.x / nt;
@@ -826,10 +916,11 @@ __global__ __launch_bounds__(64 * NW) void w4_wide_kernel(W4Args a)
     }
 }
 
-// Tiles of at most `rows` rows that a call can have.
-unsigned w4_tiles(const W4Args &a, int rows)
+// Tiles of at most `rows` rows that a launch can have, of experts with more than
+// `over` rows.
+unsigned w4_tiles(const W4Args &a, int rows, int over = 0)
 {
-    return (unsigned)(a.offsets ? a.R / rows + min(a.E, a.R) : (a.R + rows - 1) / rows);
+    return (unsigned)(a.offsets ? a.R / rows + min(a.E, a.R / (over + 1)) : (a.R + rows - 1) / rows);
 }
 
 // Tiles of columns are dealt so that about as many blocks are left as the CUs
@@ -842,17 +933,19 @@ void launch_split(const W4Args &a, hipStream_t s)
 {
     constexpr int kCols = 16 * (GLU ? NJ / 2 : NJ);
     constexpr unsigned kAtOnce = NJ == 1 ? 1536 : 800;
-    const unsigned mt = w4_tiles(a, ROWS), nt = (unsigned)((a.N + kCols - 1) / kCols);
+    const unsigned mt = w4_tiles(a, ROWS, a.over);
+    unsigned nt = (unsigned)((a.N + kCols - 1) / kCols);
     W4Args b = a;
     b.tiles = ROWS <= 16 ? (int)min(max((mt * nt + kAtOnce / 2) / kAtOnce, 1u), min(4u, nt)) : 1;
-    w4_split_kernel<BF16, GLU, GLOG, ROWS, NJ, 4><<<mt * ((nt + b.tiles - 1) / b.tiles), 256, 0, s>>>(b);
+    nt = (nt + b.tiles - 1) / b.tiles;
+    w4_split_kernel<BF16, GLU, GLOG, ROWS, NJ, 4><<<mt * nt, 256, 0, s>>>(b);
 }
 
 template <bool BF16, bool GLU, int GLOG, int NW, int NJ>
 void launch_wide(const W4Args &a, hipStream_t s)
 {
     constexpr int kCols = 64 * NJ / (GLU ? 2 : 1);
-    unsigned mt = w4_tiles(a, 16 * NW);
+    unsigned mt = w4_tiles(a, 16 * NW, a.over);
     if (mt >= 16)
         mt = (mt + 7) / 8 * 8;
     const unsigned grid = mt * (unsigned)((a.N + kCols - 1) / kCols);
@@ -866,7 +959,7 @@ void launch_wide(const W4Args &a, hipStream_t s)
 // from 32 on).
 enum W4Variant { W4_4x16, W4_4x32, W4_16x16, W4_16x32, W4_32x32, W4_64x128, W4_128x256 };
 
-// The variant of a call, by estimates of its time in us: a part that a block
+// The variants of a call, by estimates of their time in us: a part that a block
 // takes alone on a CU, and one that 256 blocks (one a CU, others beside them) add, each
 // with a part per 128 k.  Fitted to 1 to 4096 rows of 4096 x 4096, 2048 x 4096
 // (pairs) and 512 x 8192, and there to order the variants, which they do but for
@@ -878,20 +971,17 @@ enum W4Variant { W4_4x16, W4_4x32, W4_16x16, W4_16x32, W4_32x32, W4_64x128, W4_1
 //   1024       -     -     -     -     95    54   68
 //   4096       -     -     -     -    351   209  156
 // and 64 experts of 2048 x 4096 with 256 rows in all: 88, 75, 87, 76, 122, 103, 146;
-// with 4096: -, -, 340, 268, 300, 170, 187).  Of experts the host knows the number
-// alone: as many as there are rows are taken to have some, half a tile is lost
-// to each one's last rows, and one with many rows beside empty ones costs more
-// than it would alone (16384 rows at 4 of 64 experts take the variant for all 64).
+// with 4096: -, -, 340, 268, 300, 170, 187).
+struct W4Cost {
+    W4Variant v;
+    double rows, cols, alone, alone_k, more, more_k;
+    int at_once;   // blocks that start together, where a last few cost a round
+};
+
 template <bool GLU>
-W4Variant choose(const W4Args &a)
-{
-    struct Cost {
-        W4Variant v;
-        double rows, cols, alone, alone_k, more, more_k;
-        int at_once;   // blocks that start together, where a last few cost a round
-    };
-    // (of a pair the first two kinds have the columns of the narrow and the work of the wide)
-    static const Cost kCosts[] = {
+struct W4Estimate {
+    // (a pair's narrow tiles have the work of 32 columns)
+    static constexpr W4Cost kCosts[] = {
         {W4_4x16, 4, 16, 4.2, 0.065, 0.3, GLU ? 0.085 : 0.05, 1},
         {W4_4x32, 4, 32, 4.1, 0.105, 0.57, 0.07, 1},
         {W4_16x16, 16, 16, 4.8, 0.07, 0.3, GLU ? 0.095 : 0.06, 1},
@@ -900,34 +990,58 @@ W4Variant choose(const W4Args &a)
         {W4_64x128, 64, GLU ? 64 : 128, 4.5, 0.95, 2.0, 0.70, 512},
         {W4_128x256, 128, GLU ? 128 : 256, 6.8, 1.85, 5.7, 2.29, 256},
     };
-    const double k = a.K / 128.0;
-    // finer groups, and zeros, cost the wide tiles' products more
-    const double fine = (a.group_log2 == 5 ? 1.5 : a.group_log2 == 6 ? 1.2 : 1.0) * (a.zeros[0] || a.zeros[1] ? 1.1 : 1.0);
-    const double n = a.offsets ? min(a.E, a.R) : 1, rows = a.R / n;
-    W4Variant best = W4_4x16;
-    double least = 0;
-    for (const Cost &c : kCosts) {
-        if (GLU && (c.v == W4_4x32 || c.v == W4_16x32))
-            continue;
-        const double f = c.rows >= 64 ? fine : 1.0;
-        const double tiles = a.offsets ? n * max(1.0, rows / c.rows + 0.5) : ceil(rows / c.rows);
-        double blocks = tiles * ceil(a.N / c.cols);
+    double k, N, fine;
+
+    explicit W4Estimate(const W4Args &a) : k(a.K / 128.0), N(a.N)
+    {
+        // finer groups, and zeros, cost the wide tiles' products more
+        fine = (a.group_log2 == 5 ? 1.5 : a.group_log2 == 6 ? 1.2 : 1.0) * (a.zeros[0] || a.zeros[1] ? 1.1 : 1.0);
+    }
+    double steps(const W4Cost &c) const { return (c.rows >= 64 ? fine : 1.0) * k; }
+    // 256 blocks' part of what this many tiles of rows cost.
+    double more(const W4Cost &c, double tiles) const
+    {
+        double blocks = tiles * ceil(N / c.cols);
         if (c.at_once > 1 && blocks > 256)
             blocks = ceil(blocks / c.at_once) * c.at_once;
-        const double us = max(c.alone + c.alone_k * f * k, 3 + blocks / 256 * (c.more + c.more_k * f * k));
-        if (least == 0 || us < least) {
-            least = us;
-            best = c.v;
-        }
+        return blocks / 256 * (c.more + c.more_k * steps(c));
     }
-    return best;
-}
+    // The variant for `rows` rows at each of n experts (half a tile is lost to
+    // each one's last rows).
+    const W4Cost &best(double n, double rows) const
+    {
+        const W4Cost *found = nullptr;
+        double least = 0;
+        for (const W4Cost &c : kCosts) {
+            if (GLU && (c.v == W4_4x32 || c.v == W4_16x32))
+                continue;
+            const double tiles = n > 1 ? n * std::max(1.0, rows / c.rows + 0.5) : ceil(rows / c.rows);
+            const double us = std::max(c.alone + c.alone_k * steps(c), 3 + more(c, tiles));
+            if (!found || us < least) {
+                least = us;
+                found = &c;
+            }
+        }
+        return *found;
+    }
+    // The rows of an expert up to which variant a costs less than b.
+    int limit(const W4Cost &a, const W4Cost &b) const
+    {
+        auto cost = [&](const W4Cost &c, int rows) {
+            return ceil(rows / c.rows) * ceil(N / c.cols) * (c.more + c.more_k * steps(c));
+        };
+        for (const int rows : {16, 32, 48, 64, 96, 128, 192, 256, 384, 512})
+            if (cost(b, rows + 1) < cost(a, rows + 1))
+                return rows;
+        return INT32_MAX;
+    }
+};
 
 template <bool BF16, bool GLU, int GLOG>
-void launch_group(const W4Args &a, hipStream_t s)
+void launch_variant(W4Variant v, const W4Args &a, hipStream_t s)
 {
     constexpr int kOne = GLU ? 2 : 1;   // 16-column blocks of the narrow tiles
-    switch (choose<GLU>(a)) {
+    switch (v) {
     case W4_4x16: return launch_split<BF16, GLU, GLOG, 4, kOne>(a, s);
     case W4_4x32: return launch_split<BF16, GLU, GLOG, 4, 2>(a, s);
     case W4_16x16: return launch_split<BF16, GLU, GLOG, 16, kOne>(a, s);
@@ -936,6 +1050,50 @@ void launch_group(const W4Args &a, hipStream_t s)
     case W4_64x128: return launch_wide<BF16, GLU, GLOG, 4, 2>(a, s);
     case W4_128x256: return launch_wide<BF16, GLU, GLOG, 8, 4>(a, s);
     }
+}
+
+// Of experts the host knows the number alone.  The first variant is the one for
+// rows spread over all of them.  From kW4Listed rows on, where another one is better
+// for all rows at one expert, a launch in that variant takes the crowded ones if
+// there are enough of them (us without and with it: 8071 rows at 3 of 261
+// experts, pairs of 1472 x 2000: 678, 184; 348 at 8 of 67, 928 x 6792: 87, 38; 4096 at
+// 2 of 256, 2048 x 4096: 252, 128; but 256 rows spread over 64 experts, with a list
+// and a launch for nothing: 73, 83).
+template <bool BF16, bool GLU, int GLOG>
+void launch_group(const W4Args &args, hipStream_t s)
+{
+    const W4Estimate<GLU> est(args);
+    W4Args a = args;
+    a.over = 0;
+    a.list = nullptr;
+    const W4Cost &all = est.best(1, a.R);
+    if (!a.offsets || a.E == 1)
+        return launch_variant<BF16, GLU, GLOG>(all.v, a, s);
+    const double n = std::min(a.E, a.R);
+    const W4Cost &spread = est.best(n, a.R / n);
+    const int limit = est.limit(spread, all);
+    if (a.R < kW4Listed || all.rows <= spread.rows || limit >= a.R)
+        return launch_variant<BF16, GLU, GLOG>(spread.v, a, s);
+    W4Lists lists{};
+    lists.limit = limit;
+    lists.least_us = (float)(all.alone + all.alone_k * est.steps(all));
+    const W4Cost *both[] = {&spread, &all};
+    for (int i = 0; i < 2; ++i) {
+        lists.rows[i] = (int)both[i]->rows;
+        lists.us[i] = (float)(ceil(est.N / both[i]->cols) / 256 * (both[i]->more + both[i]->more_k * est.steps(*both[i])));
+        lists.count[i] = a.scratch + i;
+    }
+    lists.list[0] = (int4 *)(a.scratch + 4);
+    lists.list[1] = lists.list[0] + w4_tiles(a, lists.rows[0]) + 1;
+    w4_list_kernel<<<1, 1024, 0, s>>>(a, lists);
+    a.list = lists.list[1];
+    a.count = lists.count[1];
+    a.over = limit;
+    launch_variant<BF16, GLU, GLOG>(all.v, a, s);
+    a.over = 0;
+    a.list = lists.list[0];
+    a.count = lists.count[0];
+    launch_variant<BF16, GLU, GLOG>(spread.v, a, s);
 }
 
 template <bool BF16, bool GLU>
