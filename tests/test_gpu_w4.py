@@ -108,6 +108,59 @@ def test_integers_are_exact(T, K, N, E, group, dtype):
     assert torch.equal(y, ref.to(dtype))
 
 
+# Sizes that between them take every tile, several tiles of columns a block, and
+# two launches over lists of tiles (a second one for crowded experts)
+VARIANTS = [(64, 288, 1032, 6, 32), (24, 2048, 12296, 6, 64), (24, 288, 12296, 6, 32), (24, 896, 12296, 1, 128),
+            (40, 288, 1032, 50, 32), (150, 800, 4104, 50, 32), (150, 896, 12296, 50, 128), (300, 2016, 4104, 50, 32),
+            (300, 288, 20008, 50, 32), (800, 832, 1032, 50, 64), (150, 288, 4104, 1, 32), (300, 288, 20008, 1, 32),
+            (150, 2048, 20008, 6, 128), (2000, 288, 1032, 50, 32), (800, 2048, 264, 50, 64), (1300, 416, 776, 7, 32)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("T,K,N,E,group", VARIANTS)
+def test_every_tile(T, K, N, E, group, glu, dtype):
+    g = _gen(T + K + E)
+    d = M.make_w4_desc(K, N, E, group, D.DT[dtype])
+    x, _ = D.inside(D.gauss(g, (T, K), 1.0, dtype))
+    base = None if glu else D.inside(D.gauss(g, (T, N), 1.0, dtype))[0]
+    # rows spread, rows crowded at the last expert or at two in between (some
+    # empty, some with a row or two), and all of them at one
+    few = min(E - 1, T // 8)
+    spreads = {"spread": _split(g, T, E, 1, 2), "last": list(range(E)) + [T] if E <= T else None,
+               "two": [0] * (E // 3 + 1) + [T // 2] * (E - E // 3 - 1) + [T], "one": [0] * (E // 2 + 1) + [T] * (E - E // 2),
+               "first": [0] + [T - few + i for i in range(few)] + [T] * (E - few)}
+    for i, (what, bounds) in enumerate(spreads.items()):
+        if bounds is None:
+            continue
+        assert len(bounds) == E + 1 and all(a <= b for a, b in zip(bounds, bounds[1:]))
+        stacks = [_stack(g, E, N, K, group, dtype, (i + j) % 2 == 0) for j in range(2 if glu else 1)]
+        y = _run(d, x, stacks, _offsets(bounds), base, dtype)
+        ref, bound = R.w4(x, stacks, bounds, base, M.ACT_SILU, dtype)
+        rows = slice(bounds[0], bounds[-1])
+        D.assert_close(y[rows], ref[rows], bound[rows], what)
+        assert (y[:bounds[0]] == 77.0).all() and (y[bounds[-1]:] == 77.0).all(), what
+        if E == 1:
+            break
+
+
+@pytest.mark.parametrize("T,E", [(100, 1024), (128, 1024), (3000, 1024), (200, 1), (5000, 2)])
+def test_lists_of_many_and_few_experts(T, E):
+    # one row here and there, the last expert crowded
+    g = _gen(E)
+    dtype = torch.bfloat16
+    K, N = 256, 264
+    d = M.make_w4_desc(K, N, E, 128, M.DT_BF16)
+    x = D.gauss(g, (T, K), 1.0, dtype)
+    s = _stack(g, E, N, K, 128, dtype)
+    for crowd in (0, T // 2, T - 1):
+        cuts = torch.sort(torch.randint(0, T - crowd + 1, (E - 1,), generator=g, device="cuda")).values.tolist()
+        bounds = [0] + cuts + [T]
+        y = _run(d, x, [s], _offsets(bounds), None, dtype)
+        ref, bound = R.w4(x, [s], bounds, None, None, dtype)
+        D.assert_close(y, ref, bound, f"crowd {crowd}")
+
+
 @pytest.mark.parametrize("glu", [False, True])
 @pytest.mark.parametrize("T,E", [(9, 3), (64, 5), (200, 4), (700, 9), (3000, 2)])
 def test_rows_outside_the_offsets_stay(T, E, glu):
@@ -185,6 +238,30 @@ def test_bad_offsets_are_reported(bad):
         stacks = [_stack(g, E, N, K, group, dtype) for _ in range(n)]
         _run(d, x, stacks, _offsets(bad), None, dtype, M.STATUS_BAD_INDEX)
         _run(d, x, stacks, _offsets([0, 3, 9, 40]), None, dtype)
+
+
+@pytest.mark.parametrize("case", ["descend", "below", "beyond", "swapped", "extremes"])
+def test_bad_offsets_of_listed_tiles_are_reported(case):
+    # (overlapping experts have more tiles than the rows have: the lists and the
+    # launches end where the call's size says)
+    g = _gen(4)
+    dtype = torch.bfloat16
+    T, K, N, E = 700, 256, 136, 40
+    d = M.make_w4_desc(K, N, E, 64, M.DT_BF16)
+    x, s = D.gauss(g, (T, K), 1.0, dtype), _stack(g, E, N, K, 64, dtype)
+    bounds = _split(g, T, E)
+    if case == "descend":
+        bounds[5:] = [T if i % 2 else 0 for i in range(E + 1 - 5)]
+    elif case == "below":
+        bounds[0] = -7
+    elif case == "beyond":
+        bounds[-1] = T + 1
+    elif case == "swapped":
+        bounds = bounds[::-1]
+    else:
+        bounds = [2 ** 31 - 1 if i % 2 else -2 ** 31 for i in range(E + 1)]
+    _run(d, x, [s], _offsets(bounds), None, dtype, M.STATUS_BAD_INDEX)
+    _run(d, x, [s, s], _offsets(bounds), None, dtype, M.STATUS_BAD_INDEX)
 
 
 @pytest.mark.parametrize("T", [6, 600])

@@ -27,10 +27,11 @@ struct W4Args {
     int group_log2;            // 5, 6 or 7
     int act;                   // of a gated pair
     int32_t *scratch;          // from kW4Listed rows on: w4_scratch() bytes
-    // a launch over a list of tiles (else NULL), of experts with more than `over` rows
+    // a launch over a list of at most `most` tiles (else NULL), of experts with more
+    // than `over` rows
     const int4 *list;
     const int32_t *count;
-    int over;
+    int most, over;
     int tiles;                 // tiles of columns that a block takes in turn
 };
 
@@ -42,6 +43,7 @@ constexpr int kW4Listed = 128;
 struct W4Lists {
     int4 *list[2];
     int32_t *count[2];
+    int most[2];            // tiles that they have room for, and one more
     int rows[2];            // of a tile
     float us[2], least_us;  // estimates: a tile of rows in either, the second launch at least
     int limit;              // experts of more rows may go to the second

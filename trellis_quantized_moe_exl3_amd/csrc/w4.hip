@@ -69,8 +69,8 @@ template <int NW>
 MOE_DEV W4Tile w4_tile(const W4Args &a, int c, int tile_rows)
 {
     if (a.list) {
-        // (the entry behind the last one may be read; the list has room for it)
-        const int4 t = a.list[c];
+        // (an entry past the last one may be read: the list has room for one)
+        const int4 t = a.list[min(c, a.most)];
         const int n = __builtin_amdgcn_readfirstlane(*a.count);
         return {__builtin_amdgcn_readfirstlane(t.x), __builtin_amdgcn_readfirstlane(t.y),
                 c < n ? __builtin_amdgcn_readfirstlane(t.z) : 0};
@@ -188,6 +188,8 @@ __global__ __launch_bounds__(1024) void w4_list_kernel(W4Args a, W4Lists lists)
             before += s < w ? wsum[i][s] : 0;
             total[i] += wsum[i][s];
         }
+        // (offsets that descend may make more tiles than the rows have)
+        total[i] = min(total[i], lists.most[i]);
         first[i][e] = before;
         if (e == 0)
             *lists.count[i] = total[i];
@@ -1082,17 +1084,20 @@ void launch_group(const W4Args &args, hipStream_t s)
         lists.rows[i] = (int)both[i]->rows;
         lists.us[i] = (float)(ceil(est.N / both[i]->cols) / 256 * (both[i]->more + both[i]->more_k * est.steps(*both[i])));
         lists.count[i] = a.scratch + i;
+        lists.most[i] = (int)w4_tiles(a, lists.rows[i]);
     }
     lists.list[0] = (int4 *)(a.scratch + 4);
-    lists.list[1] = lists.list[0] + w4_tiles(a, lists.rows[0]) + 1;
+    lists.list[1] = lists.list[0] + lists.most[0] + 1;
     w4_list_kernel<<<1, 1024, 0, s>>>(a, lists);
     a.list = lists.list[1];
     a.count = lists.count[1];
+    a.most = lists.most[1];
     a.over = limit;
     launch_variant<BF16, GLU, GLOG>(all.v, a, s);
     a.over = 0;
     a.list = lists.list[0];
     a.count = lists.count[0];
+    a.most = lists.most[0];
     launch_variant<BF16, GLU, GLOG>(spread.v, a, s);
 }
 
