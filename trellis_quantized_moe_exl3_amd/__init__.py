@@ -238,15 +238,16 @@ def status(workspace) -> int:
     return int(workspace.view(torch.uint8)[STATUS_OFFSET:STATUS_OFFSET + 4].cpu().view(torch.int32).item())
 
 
-_torch_mod = _raw_stream = None
+_torch_mod = _raw_stream = _current_device = None
 
 
 def _torch():
     """torch, and its lookup of the current stream's handle (building a Stream
     object costs as much as a launch; used where torch has no such lookup)."""
-    global _torch_mod, _raw_stream
+    global _torch_mod, _raw_stream, _current_device
     if _torch_mod is None:
         import torch
+        _current_device = torch.cuda.current_device
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda device: torch.cuda.current_stream(device).cuda_stream)
         _torch_mod = torch
@@ -525,18 +526,21 @@ def _call_device(x, stream, what: str) -> int:
     """The GPU of a call without a workspace: that of x, which must be the
     current one, and of the stream."""
     d = x.get_device()   # below 0: not on a GPU
-    if d < 0 or d != _torch().cuda.current_device():
+    if _torch_mod is None:
+        _torch()
+    if d < 0 or d != _current_device():
         raise ValueError(f"{what}: tensors must be on the current GPU, got {x.device}")
     if stream is not None and stream.device != x.device:
         raise ValueError(f"{what}: a stream of {stream.device}, tensors on {x.device}")
     return d
 
 
-def _table(t, n: int, dtype, device: int, what: str) -> None:
-    """A contiguous table of n entries, of any shape."""
-    if t.numel() != n or t.dtype != dtype or t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"{what}: expected {n} contiguous {dtype} on GPU {device}, got {tuple(t.shape)} {t.dtype} on "
-                         f"{t.device}")
+def _table(t, n: int, dtype, device: int, what: str, name: str) -> int:
+    """Address of a contiguous table of n entries, of any shape."""
+    if t.numel() != n or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what}: {name}: expected {n} contiguous {dtype} on GPU {device}, got {tuple(t.shape)} "
+                         f"{t.dtype} on {t.device}")
+    return t.data_ptr()
 
 
 def _drop(p: float, rng, device: int, what: str):
@@ -559,27 +563,24 @@ def sort(desc: TokensDesc, idx, counts, offsets, sorted_ids, pos, workspace, str
     range."""
     i32 = _torch().int32
     d = _dense_device(idx, workspace, stream, "sort")
-    E, k = desc.n_experts, desc.top_k
-    T = idx.shape[0]
+    E, k, T = desc.n_experts, desc.top_k, idx.shape[0]
     _whole(idx, (T, k), (i32,), d, "sort: idx")
-    _table(offsets, E + 1, i32, d, "sort: offsets")
-    _table(pos, T * k, i32, d, "sort: pos")
+    offsets, pos = _table(offsets, E + 1, i32, d, "sort", "offsets"), _table(pos, T * k, i32, d, "sort", "pos")
     if counts is not None:
-        _table(counts, E, i32, d, "sort: counts")
+        counts = _table(counts, E, i32, d, "sort", "counts")
     if sorted_ids is not None:
-        _table(sorted_ids, T * k, i32, d, "sort: sorted_ids")
-    _check(lib().moe_exl3_sort(C.byref(desc), idx.data_ptr(), T, _ptr(counts), offsets.data_ptr(), _ptr(sorted_ids),
-                               pos.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream, d)),
-           "moe_exl3_sort")
+        sorted_ids = _table(sorted_ids, T * k, i32, d, "sort", "sorted_ids")
+    _check(lib().moe_exl3_sort(C.byref(desc), idx.data_ptr(), T, counts, offsets, sorted_ids, pos, workspace.data_ptr(),
+                               workspace.nbytes, _stream(stream, d)), "moe_exl3_sort")
 
 
-def _slots(desc: TokensDesc, T: int, pos, w, dw, device: int, what: str) -> None:
-    torch = _torch()
-    _table(pos, T * desc.top_k, torch.int32, device, what + ": pos")
-    if w is not None:
-        _table(w, T * desc.top_k, torch.float32, device, what + ": w")
-    if dw is not None:
-        _table(dw, T * desc.top_k, torch.float32, device, what + ": dw")
+def _slots(desc: TokensDesc, T: int, pos, w, dw, device: int, what: str):
+    """Addresses of the slots' tables (None: none)."""
+    n = T * desc.top_k
+    torch = _torch_mod
+    return (_table(pos, n, torch.int32, device, what, "pos"),
+            None if w is None else _table(w, n, torch.float32, device, what, "w"),
+            None if dw is None else _table(dw, n, torch.float32, device, what, "dw"))
 
 
 def dispatch(desc: TokensDesc, x, pos, out, w=None, stream=None) -> None:
@@ -589,8 +590,8 @@ def dispatch(desc: TokensDesc, x, pos, out, w=None, stream=None) -> None:
     types, T, H = _dense_dtypes(desc.act_dtype), x.shape[0], desc.hidden
     ldx = _rows(x, T, H, types, d, "dispatch: x")
     ldo = _rows(out, out.shape[0], H, types, d, "dispatch: out")
-    _slots(desc, T, pos, w, None, d, "dispatch")
-    _check(lib().moe_exl3_dispatch(C.byref(desc), x.data_ptr(), ldx, pos.data_ptr(), _ptr(w), T, out.shape[0],
+    pos, w, _ = _slots(desc, T, pos, w, None, d, "dispatch")
+    _check(lib().moe_exl3_dispatch(C.byref(desc), x.data_ptr(), ldx, pos, w, T, out.shape[0],
                                    out.data_ptr(), ldo, _stream(stream, d)), "moe_exl3_dispatch")
 
 
@@ -604,9 +605,9 @@ def dispatch_backward(desc: TokensDesc, dout, x, pos, dx, w=None, dw=None, strea
     ldx = H
     if x is not None:
         ldx = _rows(x, T, H, types, d, "dispatch_backward: x")
-    _slots(desc, T, pos, w, dw, d, "dispatch_backward")
-    _check(lib().moe_exl3_dispatch_backward(C.byref(desc), dout.data_ptr(), lddo, _ptr(x), ldx, pos.data_ptr(), _ptr(w),
-                                            T, dout.shape[0], dx.data_ptr(), lddx, _ptr(dw), _stream(stream, d)),
+    pos, w, dw = _slots(desc, T, pos, w, dw, d, "dispatch_backward")
+    _check(lib().moe_exl3_dispatch_backward(C.byref(desc), dout.data_ptr(), lddo, _ptr(x), ldx, pos, w, T, dout.shape[0],
+                                            dx.data_ptr(), lddx, dw, _stream(stream, d)),
            "moe_exl3_dispatch_backward")
 
 
@@ -620,8 +621,8 @@ def combine(desc: TokensDesc, z, pos, y, w=None, base=None, p: float = 0.0, rng=
     ldb = H
     if base is not None:
         ldb = _rows(base, T, H, types, d, "combine: base")
-    _slots(desc, T, pos, w, None, d, "combine")
-    _check(lib().moe_exl3_combine(C.byref(desc), z.data_ptr(), ldz, pos.data_ptr(), _ptr(w), _ptr(base), ldb,
+    pos, w, _ = _slots(desc, T, pos, w, None, d, "combine")
+    _check(lib().moe_exl3_combine(C.byref(desc), z.data_ptr(), ldz, pos, w, _ptr(base), ldb,
                                   _drop(p, rng, d, "combine"), T, z.shape[0], y.data_ptr(), ldy, _stream(stream, d)),
            "moe_exl3_combine")
 
@@ -637,9 +638,9 @@ def combine_backward(desc: TokensDesc, dy, z, pos, dz, w=None, dw=None, p: float
     ldz = H
     if z is not None:
         ldz = _rows(z, rows, H, types, d, "combine_backward: z")
-    _slots(desc, T, pos, w, dw, d, "combine_backward")
-    _check(lib().moe_exl3_combine_backward(C.byref(desc), dy.data_ptr(), lddy, _ptr(z), ldz, pos.data_ptr(), _ptr(w),
-                                           _drop(p, rng, d, "combine_backward"), T, rows, dz.data_ptr(), lddz, _ptr(dw),
+    pos, w, dw = _slots(desc, T, pos, w, dw, d, "combine_backward")
+    _check(lib().moe_exl3_combine_backward(C.byref(desc), dy.data_ptr(), lddy, _ptr(z), ldz, pos, w,
+                                           _drop(p, rng, d, "combine_backward"), T, rows, dz.data_ptr(), lddz, dw,
                                            _stream(stream, d)), "moe_exl3_combine_backward")
 
 
@@ -692,10 +693,10 @@ def make_w4(codes, scales, zeros=None) -> W4:
 
 def _w4_offsets(desc: W4Desc, offsets, device: int, what: str):
     if offsets is not None:
-        _table(offsets, desc.n_experts + 1, _torch().int32, device, what + ": offsets")
-    elif desc.n_experts != 1:
+        return _table(offsets, desc.n_experts + 1, _torch().int32, device, what, "offsets")
+    if desc.n_experts != 1:
         raise ValueError(f"{what}: {desc.n_experts} experts need offsets")
-    return _ptr(offsets)
+    return None
 
 
 def w4_linear(desc: W4Desc, x, w: W4, y, workspace, offsets=None, base=None, stream=None) -> None:
