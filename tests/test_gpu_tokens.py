@@ -284,6 +284,27 @@ def test_rows_past_four_gib():
     assert not out.any()
 
 
+def test_more_tokens_than_one_grid_holds():
+    # 2^26 tokens and some at 64 threads each are past 2^32 threads
+    T, H = 2 ** 26 + 5, 8
+    d = M.make_tokens_desc(H, 2, 1, M.DT_BF16)
+    x = (torch.arange(T, dtype=torch.int32, device="cuda") % 251).to(torch.bfloat16)[:, None].expand(T, H).contiguous()
+    pos = torch.arange(T - 1, -1, -1, dtype=torch.int32, device="cuda")[:, None]
+    out, y, dw = torch.zeros_like(x), torch.zeros_like(x), torch.full((T, 1), 7.0, device="cuda")
+    M.dispatch(d, x, pos, out)
+    assert torch.equal(out, x.flip(0))
+    M.combine(d, out, pos, y)
+    assert torch.equal(y, x)
+    y.zero_()
+    M.dispatch_backward(d, out, x, pos, y, dw=dw)
+    assert torch.equal(y, x) and torch.equal(dw[:, 0], 8 * x[:, 0].float().square())
+    rng = torch.tensor([3, 5], device="cuda")
+    M.combine(d, out, pos, y, p=0.5, rng=rng)   # the last rows' counters
+    tail = torch.empty_like(x[-9:])
+    M.dropout(x[-9:].contiguous(), tail, 0.5, torch.tensor([3, 5 + T - 9], device="cuda"))
+    assert torch.equal(y[-9:], tail)
+
+
 @pytest.mark.parametrize("T", [0, 4])
 def test_no_tokens_or_no_rows(T):
     d = M.make_tokens_desc(16, 4, 2)

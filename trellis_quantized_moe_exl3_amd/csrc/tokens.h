@@ -51,6 +51,7 @@ struct TokenArgs {
     const float *w;        // [T][k] or NULL: 1
     float *dw;             // [T][k] or NULL: <x or its dropped form, z>
     int64_t T, rows;       // tokens, sorted rows
+    int64_t first;         // token of a launch
     int H, k;
     Drop drop;
 };

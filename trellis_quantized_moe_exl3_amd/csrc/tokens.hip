@@ -275,7 +275,7 @@ MOE_DEV void store_dots(const TokenArgs &a, int64_t t, const float (&dot)[KB])
 template <bool BF16, int KB, bool DOT>
 __global__ __launch_bounds__(256) void spread_kernel(TokenArgs a)
 {
-    const int64_t t = blockIdx.x;
+    const int64_t t = a.first + blockIdx.x;
     int pos[KB];
     float w[KB], dot[KB];
 #pragma unroll
@@ -327,7 +327,7 @@ __global__ __launch_bounds__(256) void spread_kernel(TokenArgs a)
 template <bool BF16, int KB, bool DOT>
 __global__ __launch_bounds__(256) void gather_kernel(TokenArgs a)
 {
-    const int64_t t = blockIdx.x;
+    const int64_t t = a.first + blockIdx.x;
     int pos[KB];
     float w[KB], dot[KB];
 #pragma unroll
@@ -385,34 +385,44 @@ __global__ __launch_bounds__(256) void gather_kernel(TokenArgs a)
 }
 
 template <bool BF16, bool SPREAD, int KB>
-void launch_rows(const TokenArgs &a, hipStream_t s)
+void launch_rows(const TokenArgs &a, unsigned tokens, hipStream_t s)
 {
     const unsigned threads = (unsigned)min(256, (a.H / 8 + 63) / 64 * 64);
     if constexpr (SPREAD) {
         if (a.dw)
-            spread_kernel<BF16, KB, true><<<(unsigned)a.T, threads, 0, s>>>(a);
+            spread_kernel<BF16, KB, true><<<tokens, threads, 0, s>>>(a);
         else
-            spread_kernel<BF16, KB, false><<<(unsigned)a.T, threads, 0, s>>>(a);
+            spread_kernel<BF16, KB, false><<<tokens, threads, 0, s>>>(a);
     } else {
         if (a.dw)
-            gather_kernel<BF16, KB, true><<<(unsigned)a.T, threads, 0, s>>>(a);
+            gather_kernel<BF16, KB, true><<<tokens, threads, 0, s>>>(a);
         else
-            gather_kernel<BF16, KB, false><<<(unsigned)a.T, threads, 0, s>>>(a);
+            gather_kernel<BF16, KB, false><<<tokens, threads, 0, s>>>(a);
     }
 }
 
+// A launch takes 2^23 tokens at most: with 256 threads each, half of the 2^32 threads
+// that a grid may have.
 template <bool BF16, bool SPREAD>
-hipError_t launch_rows_k(const TokenArgs &a, hipStream_t s)
+hipError_t launch_rows_k(const TokenArgs &args, hipStream_t s)
 {
-    if (a.k <= 2)
-        launch_rows<BF16, SPREAD, 2>(a, s);
-    else if (a.k <= 4)
-        launch_rows<BF16, SPREAD, 4>(a, s);
-    else if (a.k <= 8)
-        launch_rows<BF16, SPREAD, 8>(a, s);
-    else
-        launch_rows<BF16, SPREAD, 16>(a, s);
-    return hipGetLastError();
+    constexpr int64_t kTokens = 1 << 23;
+    TokenArgs a = args;
+    for (a.first = 0; a.first < a.T; a.first += kTokens) {
+        const unsigned n = (unsigned)std::min(kTokens, a.T - a.first);
+        if (a.k <= 2)
+            launch_rows<BF16, SPREAD, 2>(a, n, s);
+        else if (a.k <= 4)
+            launch_rows<BF16, SPREAD, 4>(a, n, s);
+        else if (a.k <= 8)
+            launch_rows<BF16, SPREAD, 8>(a, n, s);
+        else
+            launch_rows<BF16, SPREAD, 16>(a, n, s);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_spread(bool bf16, const TokenArgs &a, hipStream_t s)
