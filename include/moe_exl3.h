@@ -510,8 +510,8 @@ int moe_exl3_sort(const moe_exl3_tokens_desc *desc, const int32_t *idx, int64_t 
  * once.  x: device [T][H]; out: device [rows][H]; pos: device int32 [T][k]; a slot
  * whose pos is outside [0, rows) has no row (so -1, and rows past a capacity),
  * the others' are distinct; rows that none names stay as they were.  w: device
- * fp32 [T][k], weights on the experts' input, or NULL (1).  T < 2^31 and rows <
- * 2^31, also below.
+ * fp32 [T][k], weights on the experts' input, or NULL (1).  T k < 2^31 and rows <
+ * 2^31, also below, where T = 0 is a no-op as it is here.
  */
 int moe_exl3_dispatch(const moe_exl3_tokens_desc *desc, const void *x, int64_t ldx, const int32_t *pos, const float *w,
                       int64_t T, int64_t rows, void *out, int64_t ldo, void *stream);
@@ -588,10 +588,11 @@ int moe_exl3_w4_workspace_size(const moe_exl3_w4_desc *desc, int64_t max_rows, s
  * device [rows][K]; y: device [rows][N]; base: device [rows][N] or NULL, may be y
  * itself.  Each matrix is below 2 GiB, the stacks may be larger.  The weights are not rounded: the
  * products with q - zero are summed in fp32 for each group and its scale is applied
- * there.  An element of x of magnitude 2^118 or more (an infinity among them) may make its row
- * NaN; other rows do not see it.  Last bits may depend on the number of rows.
- * The status word reports BAD_INDEX for offsets that descend or leave [0,
- * rows]: they are clamped, and the rows concerned unspecified.
+ * there.  Elements of x of magnitude 2^110 or more (an infinity among them) may make their row
+ * NaN, and an infinite scale its column; other rows and columns do not see them.  Last bits
+ * may depend on the number of rows.  The status word reports BAD_INDEX for
+ * offsets that descend or leave [0, rows]: they are clamped, and the rows concerned
+ * unspecified.  rows = 0 is a no-op.
  */
 int moe_exl3_w4_linear(const moe_exl3_w4_desc *desc, const void *x, int64_t ldx, const moe_exl3_w4 *w,
                        const int32_t *offsets, const void *base, int64_t ldbase, int64_t rows, void *y, int64_t ldy,

@@ -245,6 +245,18 @@ def test_binding_refuses_what_the_kernels_could_not_read():
             call()
 
 
+def test_weights_hold_the_memory_they_were_made_with():
+    codes, scales = torch.zeros(2, 8, 16, dtype=torch.uint8), torch.ones(2, 8, 1, dtype=torch.bfloat16)
+    w = M.make_w4(codes, scales)
+    at = codes.data_ptr()
+    codes.data = torch.ones(2, 8, 64, dtype=torch.uint8)   # other memory for the caller's tensor
+    assert w.weights.codes == w.codes.data_ptr() == at and w.codes.shape == (2, 8, 16) and w.zeros is None
+    with pytest.raises(AttributeError):
+        w.codes = codes
+    one = M.make_w4(codes[0], scales[0], torch.zeros(8, 1, dtype=torch.uint8))
+    assert one.codes.shape == (1, 8, 64) and one.zeros.shape == (1, 8, 1)
+
+
 def test_keep_matches_a_plain_loop():
     # the vectorised mask against single counters
     kept, f = R.keep(3, 11, 0.25, 9, 2 ** 64 - 2)

@@ -666,13 +666,18 @@ def dropout(x, y, p: float, rng, residual=None, stream=None) -> None:
 class W4:
     """A stack of 4-bit matrices: codes uint8 [E][N][K / 2], scales [E][N][K /
     group] of the activations' dtype, zeros uint8 [E][N][K / group] or None (8).
-    One matrix may leave out E.  Holds its tensors."""
+    One matrix may leave out E.  It holds the memory that the tensors have here:
+    values written there later count, other memory given to the tensors does not."""
 
     def __init__(self, codes, scales, zeros=None):
-        self.codes, self.scales, self.zeros = (
-            t if t is None or t.dim() == 3 else t[None] for t in (codes, scales, zeros))
-        self.weights = W4Weights(self.codes.data_ptr(), self.scales.data_ptr(), _ptr(self.zeros))
+        self._held = tuple(t if t is None else t.detach() if t.dim() == 3 else t.detach()[None]
+                           for t in (codes, scales, zeros))
+        self.weights = W4Weights(*(_ptr(t) for t in self._held))
         self._checked = None
+
+    codes = property(lambda self: self._held[0])
+    scales = property(lambda self: self._held[1])
+    zeros = property(lambda self: self._held[2])
 
     def check(self, desc: W4Desc, device: int, what: str):
         key = (desc.n_in, desc.n_out, desc.n_experts, desc.group, desc.act_dtype, device)

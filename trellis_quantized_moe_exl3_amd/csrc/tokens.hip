@@ -13,7 +13,10 @@ namespace moe {
 // 4096), a wavefront a run of them; slots of one expert in 64 consecutive ones are
 // ranked from ballots over the index bits, earlier ones from the wavefront's
 // counts, earlier wavefronts from theirs, and earlier blocks from the counts
-// that a first launch left.  No atomics: the tables are the same on each call.
+// that a first launch left.  A slot's place never comes from an atomic (only the
+// first launch's totals do): the tables are the same on each call.  Bound by latency: 3.8 us for 64
+// slots, of which 2.2 are an empty launch's; 12.6 for 57344 in two launches, the
+// second with its scattered writes 8.8; 18.2 for 131072.
 constexpr int kSortWaves = 16;
 
 MOE_DEV int scan64(int v, int l)   // inclusive, over a wavefront
@@ -500,7 +503,11 @@ struct Eight {
     }
 };
 
-// A thread takes eight columns of a row (one counter), kDropGroups times.
+// A thread takes eight columns of a row (one counter), kDropGroups times, all their
+// loads in flight before the first is used.  Bound by memory: 16384 x 4096 in bf16 with a
+// residual 60.6 us, its gradient 44.4 (6.6 and 6.0 TB/s, a 64 MiB copy 6.9); with a
+// 64-bit division for the row, element-wise tails and ordinary accesses both
+// took 323 us instead of 113.
 constexpr int kDropGroups = 2;
 
 template <int DT, bool RES>

@@ -80,7 +80,6 @@ int run(const moe_exl3_w4_desc *desc, const void *x, int64_t ldx, const moe_exl3
     W4Args a{};
     a.x = (const uint16_t *)x;
     a.ldx = ldx;
-    a.xbytes = (uint32_t)mx.span();
     for (int i = 0; i < n; ++i) {
         a.codes[i] = (const uint8_t *)w[i]->codes;
         a.scales[i] = (const uint16_t *)w[i]->scales;

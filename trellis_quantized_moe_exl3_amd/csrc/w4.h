@@ -13,7 +13,6 @@ namespace moe {
 struct W4Args {
     const uint16_t *x;
     int64_t ldx;
-    uint32_t xbytes;           // from the first to the last element
     const uint8_t *codes[2];   // [E][N][K/2]; two: a gated pair
     const uint16_t *scales[2]; // [E][N][K/group]
     const uint8_t *zeros[2];   // [E][N][K/group] or NULL: 8

@@ -134,8 +134,9 @@ MOE_DEV void w4_status(const W4Args &a)
 }
 
 // The tiles of a call's two launches, each an expert, its first row and their
-// number, from the offsets, in one block.  Experts of more than `limit` rows make up the second list
-// if their tiles take the first variant longer than the second.
+// number, from the offsets, in one block.  Experts of more than `limit` rows make up
+// the second list if their tiles take the first variant half as long again as the
+// second at least.  Bound by latency (two reads of the offsets, four barriers).
 __global__ __launch_bounds__(1024) void w4_list_kernel(W4Args a, W4Lists lists)
 {
     __shared__ int first[2][1024], last[1024];   // of an expert's tiles in either list; its last row
@@ -225,6 +226,11 @@ __global__ __launch_bounds__(1024) void w4_list_kernel(W4Args a, W4Lists lists)
 //          place p ^ swizzle(r)
 //   scales, zeros   one element a lane in registers, a share ahead; a lane takes
 //          its column's from the lane that has it
+// Where the rows are few the codes bound it: 64 rows at 58 experts' pairs of 4096 x
+// 2048 take 103 us, 502 MB at 4.9 TB/s (a 1 GiB copy reaches 5.1).  A small matrix
+// ends before its stream is at full rate (1 row, 2048 x 4096: 4.2 us, of which 2.2 are
+// those of an empty launch), and 32 rows a tile are bound by what a tile costs
+// alone: its start, its share of k, the meeting (64 rows, 4096 x 4096: 11 us).
 template <bool BF16, int GLOG, int ROWS, int NJ, bool GLU>
 struct W4Stream {
     static constexpr int MR = (ROWS + 15) / 16;                  // blocks of 16 rows
@@ -494,7 +500,8 @@ MOE_DEV void w4_store(const W4Args &a, int64_t row, int n, float g, float u)
 }
 
 // A block takes `a.tiles` tiles of columns in turn, so that its start (the
-// offsets, the first loads) is paid once for them.
+// offsets, the first loads) is paid once for them.  Its wavefronts' sums meet in LDS
+// in their order, so that the same rows give the same bits.
 template <bool BF16, bool GLU, int GLOG, int ROWS, int NJ, int NW>
 __global__ __launch_bounds__(64 * NW, ROWS <= 4 ? 3 : 2) void w4_split_kernel(W4Args a)
 {
@@ -512,7 +519,7 @@ __global__ __launch_bounds__(64 * NW, ROWS <= 4 ? 3 : 2) void w4_split_kernel(W4
     const int nt = (a.N + S::kCols * a.tiles - 1) / (S::kCols * a.tiles);
     const int n0 = (int)(blockIdx.x % nt) * S::kCols * a.tiles;
     const W4Tile t = w4_tile<NW>(a, blockIdx.x / nt, ROWS);
-    if (t.n == 0)
+    if (t.n <= 0)
         return;
     S st;
     st.init(a, t, n0, l);
@@ -571,6 +578,11 @@ __global__ __launch_bounds__(64 * NW, ROWS <= 4 ? 3 : 2) void w4_split_kernel(W4
 // leaves their groups' sums beside them, once instead of once for each
 // wavefront that reads them.  Without zeros all columns subtract the same (16 +
 // 8) sum x, which then is what a group's products start from.
+// Bound by what a SIMD issues: of its two wavefronts' instructions a product takes 8
+// clocks and each of the four vector instructions beside it (two that make it the
+// code's 16-bit numbers, one of the group's scale) 4, so that the matrix cores are
+// busy 41% (16384 rows at 32 experts of 2048 x 4096: 355 us, 775 TFLOP/s; one
+// matrix 4096 x 4096, 4096 rows: 151 us, 910).  A tile's start and end are 5.7 us of its 42 there.
 template <bool BF16, int GLOG, bool GLU, bool ZEROS, int NW, int NJ>
 struct W4Wide {
     static constexpr int kRows = 16 * NW, kCols = 64 * NJ, kStage = 128, MR = 4;
@@ -865,7 +877,7 @@ __global__ __launch_bounds__(64 * NW) void w4_wide_kernel(W4Args a)
     if (mt % 8 == 0)
         xcd_map(blockIdx.x, nt, c, n);
     const W4Tile t = w4_tile<NW>(a, c, S::kRows);
-    if (t.n == 0)
+    if (t.n <= 0)
         return;
     const int n0 = n * kCols;
     S st;
