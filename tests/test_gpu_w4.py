@@ -144,6 +144,30 @@ def test_every_tile(T, K, N, E, group, glu, dtype):
             break
 
 
+# Narrow tiles whose k eight wavefronts share: each of them, k that does not come
+# out even, wavefronts without any
+EIGHTS = [(1, 1024, 8, 1, 128), (3, 1056, 1000, 1, 32), (2, 1024, 8184, 1, 128), (4, 1088, 6000, 1, 64), (9, 1376, 520, 1, 32),
+          (16, 2112, 4096, 1, 64), (15, 1056, 8184, 1, 32), (12, 4096, 8000, 1, 128), (17, 4160, 4088, 1, 64),
+          (100, 4128, 2040, 1, 32), (9, 1152, 264, 4, 64), (40, 1440, 136, 6, 32), (3, 65536, 8, 1, 128)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("T,K,N,E,group", EIGHTS)
+def test_tiles_of_eight_wavefronts(T, K, N, E, group, glu, dtype):
+    g = _gen(T + K + E)
+    d = M.make_w4_desc(K, N, E, group, D.DT[dtype])
+    x, _ = D.inside(D.gauss(g, (T, K), 1.0, dtype))
+    base = None if glu else D.inside(D.gauss(g, (T, N), 1.0, dtype))[0]
+    bounds = _split(g, T, E)
+    for zeros in (False, True):
+        stacks = [_stack(g, E, N, K, group, dtype, zeros) for j in range(2 if glu else 1)]
+        y = _run(d, x, stacks, _offsets(bounds), base, dtype)
+        ref, bound = R.w4(x, stacks, bounds, base, M.ACT_SILU, dtype)
+        D.assert_close(y, ref, bound, f"zeros {zeros}")
+        assert torch.equal(y, _run(d, x, stacks, _offsets(bounds), base, dtype))
+
+
 @pytest.mark.parametrize("T,E", [(100, 1024), (128, 1024), (3000, 1024), (200, 1), (5000, 2)])
 def test_lists_of_many_and_few_experts(T, E):
     # one row here and there, the last expert crowded

@@ -228,9 +228,9 @@ __global__ __launch_bounds__(1024) void w4_list_kernel(W4Args a, W4Lists lists)
 //          its column's from the lane that has it
 // Where the rows are few the codes bound it: 64 rows at 58 experts' pairs of 4096 x
 // 2048 take 103 us, 502 MB at 4.9 TB/s (a 1 GiB copy reaches 5.1).  A small matrix
-// ends before its stream is at full rate (1 row, 2048 x 4096: 4.2 us, of which 2.2 are
+// ends before its stream is at full rate (1 row, 2048 x 4096: 4.0 us, of which 2.2 are
 // those of an empty launch), and 32 rows a tile are bound by what a tile costs
-// alone: its start, its share of k, the meeting (64 rows, 4096 x 4096: 11 us).
+// alone: its start, its share of k, the meeting (64 rows, 4096 x 4096: 9.8 us).
 template <bool BF16, int GLOG, int ROWS, int NJ, bool GLU>
 struct W4Stream {
     static constexpr int MR = (ROWS + 15) / 16;                  // blocks of 16 rows
@@ -503,7 +503,7 @@ MOE_DEV void w4_store(const W4Args &a, int64_t row, int n, float g, float u)
 // offsets, the first loads) is paid once for them.  Its wavefronts' sums meet in LDS
 // in their order, so that the same rows give the same bits.
 template <bool BF16, bool GLU, int GLOG, int ROWS, int NJ, int NW>
-__global__ __launch_bounds__(64 * NW, ROWS <= 4 ? 3 : 2) void w4_split_kernel(W4Args a)
+__global__ __launch_bounds__(64 * NW, ROWS <= 4 && NW == 4 ? 3 : 2) void w4_split_kernel(W4Args a)
 {
     using S = W4Stream<BF16, GLOG, ROWS, NJ, GLU>;
     constexpr bool kApart = ROWS <= 16;          // the sums have LDS of their own
@@ -934,8 +934,13 @@ __global__ __launch_bounds__(64 * NW) void w4_wide_kernel(W4Args a)
 // `over` rows.
 unsigned w4_tiles(const W4Args &a, int rows, int over = 0)
 {
-    return (unsigned)(a.offsets ? a.R / rows + min(a.E, a.R / (over + 1)) : (a.R + rows - 1) / rows);
+    return (unsigned)(a.offsets && a.E > 1 ? a.R / rows + min(a.E, a.R / (over + 1)) : (a.R + rows - 1) / rows);
 }
+
+// A narrow tile that has its CU to itself gets eight wavefronts for its k and not
+// four, if each has 128 k at least (4096 x 4096: 1 row 5.85 us with four, 5.4 with eight,
+// 16 rows 6.75, 6.3, 64 rows of group 64 11.0, 9.9; 2048 x 1024: 4.6, 4.2).
+bool w4_eight(double blocks, int K) { return blocks <= 256 && K >= 1024; }
 
 // Tiles of columns are dealt so that about as many blocks are left as the CUs
 // hold at once, but at most four to a block (64 rows of 40 experts, 2048 x 4096:
@@ -952,7 +957,10 @@ void launch_split(const W4Args &a, hipStream_t s)
     W4Args b = a;
     b.tiles = ROWS <= 16 ? (int)min(max((mt * nt + kAtOnce / 2) / kAtOnce, 1u), min(4u, nt)) : 1;
     nt = (nt + b.tiles - 1) / b.tiles;
-    w4_split_kernel<BF16, GLU, GLOG, ROWS, NJ, 4><<<mt * nt, 256, 0, s>>>(b);
+    if (w4_eight(mt * nt, a.K))
+        w4_split_kernel<BF16, GLU, GLOG, ROWS, NJ, 8><<<mt * nt, 512, 0, s>>>(b);
+    else
+        w4_split_kernel<BF16, GLU, GLOG, ROWS, NJ, 4><<<mt * nt, 256, 0, s>>>(b);
 }
 
 template <bool BF16, bool GLU, int GLOG, int NW, int NJ>
@@ -977,7 +985,8 @@ enum W4Variant { W4_4x16, W4_4x32, W4_16x16, W4_16x32, W4_32x32, W4_64x128, W4_1
 // takes alone on a CU, and one that 256 blocks (one a CU, others beside them) add, each
 // with a part per 128 k.  Fitted to 1 to 4096 rows of 4096 x 4096, 2048 x 4096
 // (pairs) and 512 x 8192, and there to order the variants, which they do but for
-// near ties (4096 x 4096, us measured for the seven in this order, - not run:
+// near ties (4096 x 4096, us measured for the seven in this order, the narrow ones
+// with four wavefronts, - not run:
 //   1 row      6.3   7.4   6.9   8.2   10.0  35   65
 //   16        11.2  10.0   7.2   8.4   10.1  35   66
 //   64        34    27    15.6  11.9   10.7  36   67
@@ -1004,9 +1013,10 @@ struct W4Estimate {
         {W4_64x128, 64, GLU ? 64 : 128, 4.5, 0.95, 2.0, 0.70, 512},
         {W4_128x256, 128, GLU ? 128 : 256, 6.8, 1.85, 5.7, 2.29, 256},
     };
+    int K;
     double k, N, fine;
 
-    explicit W4Estimate(const W4Args &a) : k(a.K / 128.0), N(a.N)
+    explicit W4Estimate(const W4Args &a) : K(a.K), k(a.K / 128.0), N(a.N)
     {
         // finer groups, and zeros, cost the wide tiles' products more
         fine = (a.group_log2 == 5 ? 1.5 : a.group_log2 == 6 ? 1.2 : 1.0) * (a.zeros[0] || a.zeros[1] ? 1.1 : 1.0);
@@ -1030,7 +1040,8 @@ struct W4Estimate {
             if (GLU && (c.v == W4_4x32 || c.v == W4_16x32))
                 continue;
             const double tiles = n > 1 ? n * std::max(1.0, rows / c.rows + 0.5) : ceil(rows / c.rows);
-            const double us = std::max(c.alone + c.alone_k * steps(c), 3 + more(c, tiles));
+            const double part = c.rows < 64 && w4_eight(tiles * ceil(N / c.cols), K) ? 0.7 : 1.0;
+            const double us = std::max(c.alone + part * c.alone_k * steps(c), 3 + more(c, tiles));
             if (!found || us < least) {
                 least = us;
                 found = &c;
