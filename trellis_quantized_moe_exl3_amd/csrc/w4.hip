@@ -744,8 +744,9 @@ struct W4Wide {
     // The stage at k0, from its slots, and meanwhile the preparation of the next;
     // before its last step all its fragments are in registers, and the stage
     // three on is loaded in its place.
-    // TAIL: it may have fewer than four steps.
-    template <bool TAIL>
+    // TAIL: one of the last three, number TAIL of them, which load nothing (the
+    // loads past the end would be waited for); it may have fewer than four steps.
+    template <int TAIL>
     MOE_DEV void stage(int k0, LDS_AS uint16_t *xs, LDS_AS uint16_t *cs, const LDS_AS float *sums,
                        LDS_AS uint16_t *xnext, LDS_AS uint16_t *cnext, LDS_AS float *snext_)
     {
@@ -776,7 +777,7 @@ struct W4Wide {
             for (int q = 0; q < NJ; ++q)
                 cf[q] = cn[q];
             if (h == 0) {
-                wait_vmcnt<kXLoads + kCLoads>();   // the next stage is here, but for its preparation
+                wait_vmcnt<TAIL <= 1 ? kXLoads + kCLoads : 0>();   // the next stage is here, but for its preparation
 #pragma unroll
                 for (int i = 0; i < kScales; ++i)
                     now[i] = ZEROS ? snext[i] | ((zmask >> i) & 1u ? (uint32_t)znext[i] << 16 : 8u << 16) : snext[i];
@@ -789,7 +790,8 @@ struct W4Wide {
             if (h < 3) {
                 read(h + 1, xs, cs, sums);
             } else {
-                load(k0 + 3 * kStage, xs, cs);
+                if constexpr (!TAIL)
+                    load(k0 + 3 * kStage, xs, cs);
                 read(0, xnext, cnext, snext_);
             }
 #pragma unroll
@@ -845,18 +847,17 @@ struct W4Wide {
         meet();
         read(0, xs[0], cs[0], sums[0]);
         int k = 0;
-        for (; k + 3 * kStage <= K; k += 3 * kStage) {
-            stage<false>(k, xs[0], cs[0], sums[0], xs[1], cs[1], sums[1]);
-            stage<false>(k + kStage, xs[1], cs[1], sums[1], xs[2], cs[2], sums[2]);
-            stage<false>(k + 2 * kStage, xs[2], cs[2], sums[2], xs[0], cs[0], sums[0]);
+        for (; k + 3 * kStage < K; k += 3 * kStage) {
+            stage<0>(k, xs[0], cs[0], sums[0], xs[1], cs[1], sums[1]);
+            stage<0>(k + kStage, xs[1], cs[1], sums[1], xs[2], cs[2], sums[2]);
+            stage<0>(k + 2 * kStage, xs[2], cs[2], sums[2], xs[0], cs[0], sums[0]);
         }
-        if (k < K)
-            stage<true>(k, xs[0], cs[0], sums[0], xs[1], cs[1], sums[1]);
+        stage<1>(k, xs[0], cs[0], sums[0], xs[1], cs[1], sums[1]);
         if (k + kStage < K)
-            stage<true>(k + kStage, xs[1], cs[1], sums[1], xs[2], cs[2], sums[2]);
+            stage<2>(k + kStage, xs[1], cs[1], sums[1], xs[2], cs[2], sums[2]);
         if (k + 2 * kStage < K)
-            stage<true>(k + 2 * kStage, xs[2], cs[2], sums[2], xs[0], cs[0], sums[0]);
-        wait_vmcnt<0>();   // the loads past the end still write LDS
+            stage<3>(k + 2 * kStage, xs[2], cs[2], sums[2], xs[0], cs[0], sums[0]);
+        wait_vmcnt<0>();   // loads past the end still write LDS
     }
 };
 
