@@ -581,8 +581,8 @@ __global__ __launch_bounds__(64 * NW, ROWS <= 4 && NW == 4 ? 3 : 2) void w4_spli
 // Bound by what a SIMD issues: of its two wavefronts' instructions a product takes 8
 // clocks and each of the four vector instructions beside it (two that make it the
 // code's 16-bit numbers, one of the group's scale) 4, so that the matrix cores are
-// busy 41% (16384 rows at 32 experts of 2048 x 4096: 355 us, 775 TFLOP/s; one
-// matrix 4096 x 4096, 4096 rows: 151 us, 910).  A tile's start and end are 5.7 us of its 42 there.
+// busy 41% (16384 rows at 32 experts of 2048 x 4096: 354 us, 777 TFLOP/s, where
+// tiles that are not full add 12%; one matrix 4096 x 4096, 4096 rows: 148 us, 929).
 template <bool BF16, int GLOG, bool GLU, bool ZEROS, int NW, int NJ>
 struct W4Wide {
     static constexpr int kRows = 16 * NW, kCols = 64 * NJ, kStage = 128, MR = 4;
@@ -746,7 +746,8 @@ struct W4Wide {
     // three on is loaded in its place.
     // TAIL: one of the last three, number TAIL of them, which load nothing (the
     // loads past the end would be waited for); it may have fewer than four steps.
-    template <int TAIL>
+    // IDLE: of a wavefront without rows, which loads and prepares its part alone.
+    template <int TAIL, bool IDLE>
     MOE_DEV void stage(int k0, LDS_AS uint16_t *xs, LDS_AS uint16_t *cs, const LDS_AS float *sums,
                        LDS_AS uint16_t *xnext, LDS_AS uint16_t *cnext, LDS_AS float *snext_)
     {
@@ -766,34 +767,42 @@ struct W4Wide {
             if (h == 3)
                 meet();
             __builtin_amdgcn_sched_barrier(0);
-            if (!ZEROS && first)
+            if (!IDLE && !ZEROS && first)
 #pragma unroll
                 for (int i = 0; i < MR; ++i)
                     sum[i] = sn[i];
+            if constexpr (!IDLE) {
 #pragma unroll
-            for (int i = 0; i < MR; ++i)
-                xp[i] = xn[i];
+                for (int i = 0; i < MR; ++i)
+                    xp[i] = xn[i];
 #pragma unroll
-            for (int q = 0; q < NJ; ++q)
-                cf[q] = cn[q];
+                for (int q = 0; q < NJ; ++q)
+                    cf[q] = cn[q];
+            }
             if (h == 0) {
                 wait_vmcnt<TAIL <= 1 ? kXLoads + kCLoads : 0>();   // the next stage is here, but for its preparation
+                if constexpr (!IDLE) {
 #pragma unroll
-                for (int i = 0; i < kScales; ++i)
-                    now[i] = ZEROS ? snext[i] | ((zmask >> i) & 1u ? (uint32_t)znext[i] << 16 : 8u << 16) : snext[i];
-                load_scales(k0 + kStage);
+                    for (int i = 0; i < kScales; ++i)
+                        now[i] = ZEROS ? snext[i] | ((zmask >> i) & 1u ? (uint32_t)znext[i] << 16 : 8u << 16) : snext[i];
+                    load_scales(k0 + kStage);
+                }
             }
             if (h == 1)
                 prepare_read(xnext);
             if (h == 2)
                 prepare_write(xnext);
-            if (h < 3) {
-                read(h + 1, xs, cs, sums);
-            } else {
-                if constexpr (!TAIL)
-                    load(k0 + 3 * kStage, xs, cs);
-                read(0, xnext, cnext, snext_);
+            if (h == 3 && !TAIL)
+                load(k0 + 3 * kStage, xs, cs);
+            if constexpr (IDLE) {
+                if (h == 2)
+                    prepare_sums(snext_);
+                continue;
             }
+            if (h < 3)
+                read(h + 1, xs, cs, sums);
+            else
+                read(0, xnext, cnext, snext_);
 #pragma unroll
             for (int q = 0; q < NJ; ++q) {
                 const u32x4 v = expand8<BF16>(cf[q], base16);
@@ -827,7 +836,8 @@ struct W4Wide {
                     asm volatile("" : "+v"(acc[i][q]));
         }
     }
-    MOE_DEV void run(LDS_AS uint16_t *const (&xs)[3], LDS_AS uint16_t *const (&cs)[3], LDS_AS float *const (&sums)[3])
+    MOE_DEV void run(bool idle, LDS_AS uint16_t *const (&xs)[3], LDS_AS uint16_t *const (&cs)[3],
+                     LDS_AS float *const (&sums)[3])
     {
 #pragma unroll
         for (int i = 0; i < MR; ++i)
@@ -845,19 +855,28 @@ struct W4Wide {
         prepare_write(xs[0]);
         prepare_sums(sums[0]);
         meet();
-        read(0, xs[0], cs[0], sums[0]);
+        if (idle) {
+            stages<true>(xs, cs, sums);
+        } else {
+            read(0, xs[0], cs[0], sums[0]);
+            stages<false>(xs, cs, sums);
+        }
+        wait_vmcnt<0>();   // loads past the end still write LDS
+    }
+    template <bool IDLE>
+    MOE_DEV void stages(LDS_AS uint16_t *const (&xs)[3], LDS_AS uint16_t *const (&cs)[3], LDS_AS float *const (&sums)[3])
+    {
         int k = 0;
         for (; k + 3 * kStage < K; k += 3 * kStage) {
-            stage<0>(k, xs[0], cs[0], sums[0], xs[1], cs[1], sums[1]);
-            stage<0>(k + kStage, xs[1], cs[1], sums[1], xs[2], cs[2], sums[2]);
-            stage<0>(k + 2 * kStage, xs[2], cs[2], sums[2], xs[0], cs[0], sums[0]);
+            stage<0, IDLE>(k, xs[0], cs[0], sums[0], xs[1], cs[1], sums[1]);
+            stage<0, IDLE>(k + kStage, xs[1], cs[1], sums[1], xs[2], cs[2], sums[2]);
+            stage<0, IDLE>(k + 2 * kStage, xs[2], cs[2], sums[2], xs[0], cs[0], sums[0]);
         }
-        stage<1>(k, xs[0], cs[0], sums[0], xs[1], cs[1], sums[1]);
+        stage<1, IDLE>(k, xs[0], cs[0], sums[0], xs[1], cs[1], sums[1]);
         if (k + kStage < K)
-            stage<2>(k + kStage, xs[1], cs[1], sums[1], xs[2], cs[2], sums[2]);
+            stage<2, IDLE>(k + kStage, xs[1], cs[1], sums[1], xs[2], cs[2], sums[2]);
         if (k + 2 * kStage < K)
-            stage<3>(k + 2 * kStage, xs[2], cs[2], sums[2], xs[0], cs[0], sums[0]);
-        wait_vmcnt<0>();   // loads past the end still write LDS
+            stage<3, IDLE>(k + 2 * kStage, xs[2], cs[2], sums[2], xs[0], cs[0], sums[0]);
     }
 };
 
@@ -886,7 +905,10 @@ __global__ __launch_bounds__(64 * NW) void w4_wide_kernel(W4Args a)
     LDS_AS uint16_t *const xs[3] = {(LDS_AS uint16_t *)x0, (LDS_AS uint16_t *)x1, (LDS_AS uint16_t *)x2};
     LDS_AS uint16_t *const cs[3] = {(LDS_AS uint16_t *)c0, (LDS_AS uint16_t *)c1, (LDS_AS uint16_t *)c2};
     LDS_AS float *const sums[3] = {(LDS_AS float *)s0, (LDS_AS float *)s1, (LDS_AS float *)s2};
-    st.run(xs, cs, sums);
+    // an expert's last tile may have no rows for the upper wavefronts: the lower
+    // ones then have the SIMDs to themselves (16384 rows at 64 experts, 2048 x 4096:
+    // 400 us with all of them multiplying, 388)
+    st.run(NW == 8 && t.n <= 16 * S::MR * (w >> 2), xs, cs, sums);
     __syncthreads();
     // results through LDS, for stores of 16 bytes: a wavefront turns 16 rows at
     // a time, the 16-column block q of row r in place q ^ (r / 4 % 4)
