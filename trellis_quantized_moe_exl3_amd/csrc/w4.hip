@@ -581,7 +581,7 @@ __global__ __launch_bounds__(64 * NW, ROWS <= 4 && NW == 4 ? 3 : 2) void w4_spli
 // Bound by what a SIMD issues: of its two wavefronts' instructions a product takes 8
 // clocks and each of the four vector instructions beside it (two that make it the
 // code's 16-bit numbers, one of the group's scale) 4, so that the matrix cores are
-// busy 41% (16384 rows at 32 experts of 2048 x 4096: 354 us, 777 TFLOP/s, where
+// busy 40% (16384 rows at 32 experts of 2048 x 4096: 354 us, 777 TFLOP/s, where
 // tiles that are not full add 12%; one matrix 4096 x 4096, 4096 rows: 148 us, 929).
 template <bool BF16, int GLOG, bool GLU, bool ZEROS, int NW, int NJ>
 struct W4Wide {
