@@ -569,7 +569,10 @@ typedef struct moe_exl3_w4_desc {
     int32_t act;         /* MOE_EXL3_ACT_*, of moe_exl3_w4_glu */
 } moe_exl3_w4_desc;
 
-/* A stack of matrices, device memory, contiguous. */
+/*
+ * A stack of matrices, device memory, contiguous; one of a longer stack's as well
+ * (n_experts 1).  codes and scales are 16-byte aligned, zeros 8-byte.
+ */
 typedef struct moe_exl3_w4 {
     const void *codes;     /* uint8 [n_experts][N][K / 2]: q of k = 2 i in the low half of byte i,
                               of 2 i + 1 in the high half */

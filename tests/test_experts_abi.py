@@ -219,6 +219,16 @@ def test_w4_glu_refused(kw, code):
     assert _w4(_w4d(), glu=True, **kw) == code
 
 
+@pytest.mark.parametrize("glu", [False, True])
+def test_w4_takes_the_zeros_of_one_expert(glu):
+    # N K / group is a multiple of 8, of 16 not always (1032 x 1376 in groups of
+    # 32): where the next expert's zeros begin.  (128 bytes are too few: the
+    # workspace is what is refused last)
+    assert _w4(_w4d(), zeros=A[3] + 8, n=128, glu=glu) == WSP
+    for off in (1, 2, 4, 12):
+        assert _w4(_w4d(), zeros=A[3] + off, n=128, glu=glu) == MIS
+
+
 def test_calls_without_work_return_before_any_launch():
     d = _tokens()
     assert _dispatch(d, T=0, x=None, pos=None, out=None) == M.OK

@@ -288,6 +288,24 @@ def test_bad_offsets_of_listed_tiles_are_reported(case):
     _run(d, x, [s, s], _offsets(bounds), None, dtype, M.STATUS_BAD_INDEX)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T", [1, 40, 700])
+def test_one_expert_out_of_a_stack(T, dtype):
+    # its zeros begin at an odd multiple of 8 bytes
+    g = _gen(T)
+    K, N, E, group = 1376, 1032, 4, 32
+    d = M.make_w4_desc(K, N, 1, group, D.DT[dtype])
+    x = D.gauss(g, (T, K), 1.0, dtype)
+    stacks = [_stack(g, E, N, K, group, dtype) for _ in range(2)]
+    for e in (1, 3):
+        one = [tuple(t[e] for t in s) for s in stacks]
+        assert one[0][2].data_ptr() % 16 == 8
+        for n in (1, 2):
+            y = _run(d, x, one[:n], None, None, dtype)
+            ref, bound = R.w4(x, [tuple(t[e:e + 1] for t in s) for s in stacks[:n]], [0, T], None, M.ACT_SILU, dtype)
+            D.assert_close(y, ref, bound, f"expert {e}, {n}")
+
+
 @pytest.mark.parametrize("T", [6, 600])
 def test_stacks_past_four_gib(T):
     g = _gen(T)

@@ -28,11 +28,14 @@ int check_desc(const moe_exl3_w4_desc *d)
 // Rows of this length must be addressable.
 bool rows_fit(int64_t R, int64_t cols) { return R < kSpanLimit && R * cols * 2 < kSpanLimit; }
 
+// (One expert's zeros in a stack begin at a multiple of 8, N being one; its codes
+// and scales at one of 16.)
 int check_weights(const moe_exl3_w4 *w)
 {
     if (!w || !w->codes || !w->scales)
         return MOE_EXL3_ERR_INVALID_ARG;
-    return aligned16(w->codes) && aligned16(w->scales) && aligned16(w->zeros) ? MOE_EXL3_OK : MOE_EXL3_ERR_MISALIGNED;
+    return aligned16(w->codes) && aligned16(w->scales) && (uintptr_t)w->zeros % 8 == 0 ? MOE_EXL3_OK
+                                                                                       : MOE_EXL3_ERR_MISALIGNED;
 }
 
 bool meets_weights(const Mat &out, const moe_exl3_w4_desc &d, const moe_exl3_w4 &w)
