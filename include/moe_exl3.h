@@ -550,8 +550,11 @@ int moe_exl3_combine_backward(const moe_exl3_tokens_desc *desc, const void *dy, 
 /*
  * y = residual + D(x), rounded once; with a gradient for x the same call gives
  * D's gradient, D being its own.  x, y: device [rows][cols] of dtype F16, BF16 or F32, any
- * row stride from cols up to 2^20; residual: the same or NULL.  y may be x or the
- * residual itself (same address and stride).  `drop` is needed.
+ * row stride from cols up to 2^20; residual: the same or NULL.  The first row of each
+ * is at a 16-byte aligned address, wherever the stride puts the others: a part of
+ * a matrix with rows of an odd length begins at every eighth row (F32: fourth), and at
+ * another one it is refused (MISALIGNED).  y may be x or the residual itself (same
+ * address and stride).  `drop` is needed.
  */
 int moe_exl3_dropout(int32_t dtype, const void *x, int64_t ldx, const void *residual, int64_t ldr,
                      const moe_exl3_drop *drop, int64_t rows, int64_t cols, void *y, int64_t ldy, void *stream);

@@ -196,6 +196,17 @@ def test_dropout_refused(kw, code):
     assert _dropout(**kw) == code
 
 
+@pytest.mark.parametrize("dt,size", [(M.DT_BF16, 2), (M.DT_F16, 2), (M.DT_F32, 4)])
+def test_dropout_of_a_part_begins_at_16_bytes(dt, size):
+    # rows of 1381: from row 16 / size on each 16th byte, not from those between.
+    # (What passes the checks of addresses is refused for the generator inside y.)
+    for row in range(1, 16 // size + 1):
+        for name, base in (("x", A[0]), ("res", A[1]), ("y", A[3])):
+            at = base + row * 1381 * size
+            kw = {"rng": (at if name == "y" else A[3]) // 8 * 8 + 64, name: at}
+            assert _dropout(dt=dt, ldx=1381, ldr=1381, ldy=1381, cols=1381, **kw) == (INV if row == 16 // size else MIS)
+
+
 W4S = [
     (dict(x=None), INV), (dict(codes=None), INV), (dict(scales=None), INV), (dict(null=True), INV), (dict(y=None), INV),
     (dict(ws=None), INV), (dict(offsets=None), INV), (dict(rows=-1), INV), (dict(ldx=504), INV), (dict(ldy=0), INV),

@@ -353,6 +353,28 @@ def test_dropout(rows, cols, dtype):
                         assert torch.equal(mine, keep)
 
 
+@pytest.mark.parametrize("dtype", TYPES + [torch.float32])
+@pytest.mark.parametrize("cols", [1, 1381])
+def test_dropout_of_the_last_rows(cols, dtype):
+    # a part of each matrix, from a row that is at 16 bytes although those beside
+    # it are not: the same numbers as in a call on all rows, from the counters of
+    # the row it begins with; rows before and behind it stay
+    first, rows = 16 // dtype.itemsize, 41
+    g = _gen(cols)
+    x, r = D.gauss(g, (rows, cols), 1.0, dtype), D.gauss(g, (rows, cols), 1.0, dtype)
+    rng = _rng(g)
+    whole = torch.empty_like(x)
+    M.dropout(x, whole, 0.4, rng, residual=r)
+    y = torch.full_like(x, 77.0)
+    later = rng + torch.tensor([0, first * -(-cols // 8)], device="cuda")
+    M.dropout(x[first:-3], y[first:-3], 0.4, later, residual=r[first:-3])
+    assert torch.equal(y[first:-3], whole[first:-3])
+    assert (y[:first] == 77.0).all() and (y[-3:] == 77.0).all()
+    with pytest.raises(M.MoeError) as e:
+        M.dropout(x[1:], y[1:], 0.4, rng)
+    assert e.value.code == M.ERR_MISALIGNED
+
+
 @pytest.mark.parametrize("seed,offset", [(0, 0), (-1, -1), (-1, -3), (1 << 40, (1 << 32) - 2), (7, -(1 << 63))])
 def test_dropout_counters_wrap(seed, offset):
     rng = torch.tensor([seed, offset], dtype=torch.int64, device="cuda")

@@ -647,7 +647,8 @@ def combine_backward(desc: TokensDesc, dy, z, pos, dz, w=None, dw=None, p: float
 def dropout(x, y, p: float, rng, residual=None, stream=None) -> None:
     """y = residual + D(x) (moe_exl3_dropout), D dropout with probability p from
     rng (int64 {seed, offset} on the GPU); with a gradient for x, D's gradient.  x,
-    y, residual: [rows][cols] bf16, fp16 or fp32."""
+    y, residual: [rows][cols] bf16, fp16 or fp32, rows apart by any stride, the
+    first at a 16-byte aligned address."""
     torch = _torch()
     d = _call_device(x, stream, "dropout")
     dt = {torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32}.get(x.dtype)
