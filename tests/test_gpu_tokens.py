@@ -47,8 +47,8 @@ def _check_sort(idx, E):
         assert (w[:3] == -77).all() and (w[3 + m:] == -77).all()
 
 
-# T, k, E: one slot, one expert, the most of them, chunks of 4096 slots and one
-# more or less, calls of more than 64 chunks
+# T, k, E: one slot, one expert, the most of them, 4096 slots (what one block
+# sorts alone) and one more or less, calls of up to 64 chunks of 2048 slots and of more
 SORTS = [(1, 1, 1), (1, 16, 1024), (3, 2, 5), (8, 8, 288), (64, 8, 288), (512, 8, 288), (513, 8, 64), (4095, 1, 7),
          (4096, 1, 1023), (4097, 1, 1024), (1000, 13, 100), (7168, 8, 288), (16384, 8, 1), (16385, 16, 40),
          (32768, 8, 1024), (40000, 15, 1000)]
@@ -62,6 +62,27 @@ def test_sort(T, k, E):
     # crowded experts, and slots without one
     skew = (torch.rand(T, k, generator=g, device="cuda") ** 4 * E).to(torch.int32)
     _check_sort(torch.where(torch.rand(T, k, generator=g, device="cuda") < 0.2, -1, skew), E)
+
+
+# Whole chunks and one slot more; 64 chunks (each block adds up the counts of all
+# others) and the first slot of a 65th (a launch of its own does)
+@pytest.mark.parametrize("T,k,E", [(768, 8, 288), (1229, 5, 288), (1229, 5, 1024), (16384, 8, 288), (16384, 8, 1024),
+                                   (43691, 3, 288), (43691, 3, 1024)])
+def test_sort_at_the_ends_of_chunks(T, k, E):
+    assert T * k % 2048 in (0, 1)
+    g = _gen(T + E)
+    idx = torch.randint(0, E, (T, k), generator=g, device="cuda").to(torch.int32)
+    _check_sort(idx, E)
+    skew = (torch.rand(T, k, generator=g, device="cuda") ** 4 * E).to(torch.int32)
+    skew = torch.where(torch.rand(T, k, generator=g, device="cuda") < 0.2, -1, skew)
+    skew[-1, -1] = E - 1   # the last slot has an expert
+    _check_sort(skew, E)
+    # an index out of range in the first chunk and in the last
+    for t in (0, T - 1):
+        wrong = skew.clone()
+        wrong[t, k - 1] = E
+        assert _sort(wrong, E)[-1] == M.STATUS_BAD_INDEX
+        _check_sort(wrong, E)
 
 
 @pytest.mark.parametrize("value", ["none", "first", "last"])
