@@ -108,8 +108,9 @@ def test_integers_are_exact(T, K, N, E, group, dtype):
     assert torch.equal(y, ref.to(dtype))
 
 
-# Sizes that between them take every tile, several tiles of columns a block, and
-# two launches over lists of tiles (a second one for crowded experts)
+# Sizes that between them take tiles of every shape, several tiles of columns a
+# block, and two launches over lists of tiles (a second one for crowded experts);
+# the kernels that they leave out are test_gpu_w4_tiles.py's
 VARIANTS = [(64, 288, 1032, 6, 32), (24, 2048, 12296, 6, 64), (24, 288, 12296, 6, 32), (24, 896, 12296, 1, 128),
             (40, 288, 1032, 50, 32), (150, 800, 4104, 50, 32), (150, 896, 12296, 50, 128), (300, 2016, 4104, 50, 32),
             (300, 288, 20008, 50, 32), (800, 832, 1032, 50, 64), (150, 288, 4104, 1, 32), (300, 288, 20008, 1, 32),

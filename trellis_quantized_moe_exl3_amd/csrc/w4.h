@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "moe_exl3.h"
+#include "w4_plan.h"
 
 namespace moe {
 
@@ -26,19 +27,14 @@ struct W4Args {
     int group_log2;            // 5, 6 or 7
     int act;                   // of a gated pair
     int32_t *scratch;          // from kW4Listed rows on: w4_scratch() bytes
-    // a launch over a list of at most `most` tiles (else NULL), of experts with more
-    // than `over` rows
+    // a launch over a list of at most `most` tiles (else NULL)
     const int4 *list;
     const int32_t *count;
-    int most, over;
+    int most;
     int tiles;                 // tiles of columns that a block takes in turn
 };
 
-// Rows from which a call may take two launches over lists of its experts' tiles
-// (in one launch each block finds its own tile).
-constexpr int kW4Listed = 128;
-
-// The two lists of a call.
+// The two lists of a call (W4Plan), and where they and their lengths go.
 struct W4Lists {
     int4 *list[2];
     int32_t *count[2];
@@ -47,14 +43,6 @@ struct W4Lists {
     float us[2], least_us;  // estimates: a tile of rows in either, the second launch at least
     int limit;              // experts of more rows may go to the second
 };
-
-// Bytes of the lists and their lengths: tiles of 4 rows and of 16 at least, one
-// for each expert's last rows, one entry to read past the end.
-inline size_t w4_scratch(int64_t R, int64_t E)
-{
-    const int64_t n = E < R ? E : R;
-    return R < kW4Listed || E == 1 ? 0 : (size_t)(16 + 16 * (R / 4 + n + 1 + R / 16 + n + 1));
-}
 
 hipError_t launch_w4(bool bf16, bool glu, const W4Args &a, hipStream_t s);
 

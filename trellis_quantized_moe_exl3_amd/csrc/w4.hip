@@ -14,9 +14,6 @@
 #include "dense_kernel.h"
 #include "w4.h"
 
-#include <algorithm>
-#include <cmath>
-
 namespace moe {
 
 // Eight codes -> eight 16-bit numbers 16 + q, in the order of permute8().
@@ -953,198 +950,66 @@ __global__ __launch_bounds__(64 * NW) void w4_wide_kernel(W4Args a)
     }
 }
 
-// Tiles of at most `rows` rows that a launch can have, of experts with more than
-// `over` rows.
-unsigned w4_tiles(const W4Args &a, int rows, int over = 0)
-{
-    return (unsigned)(a.offsets && a.E > 1 ? a.R / rows + min(a.E, a.R / (over + 1)) : (a.R + rows - 1) / rows);
-}
-
-// A narrow tile that has its CU to itself gets eight wavefronts for its k and not
-// four, if each has 128 k at least (4096 x 4096: 1 row 5.85 us with four, 5.4 with eight,
-// 16 rows 6.75, 6.3, 64 rows of group 64 11.0, 9.9; 2048 x 1024: 4.6, 4.2).
-bool w4_eight(double blocks, int K) { return blocks <= 256 && K >= 1024; }
-
-// Tiles of columns are dealt so that about as many blocks are left as the CUs
-// hold at once, but at most four to a block (64 rows of 40 experts, 2048 x 4096:
-// 55 us with one each, 43 with two, 39 with four, 42 with eight; 64 at 58 experts'
-// pairs of 4096 x 2048: 124, 106, 106, 109; one row, 4096 x 4096, whose 256
-// blocks leave room on each CU: 6.2, 9.1, 14.9, 26.3).
 template <bool BF16, bool GLU, int GLOG, int ROWS, int NJ>
-void launch_split(const W4Args &a, hipStream_t s)
+void launch_split(const W4Launch &p, W4Args a, hipStream_t s)
 {
-    constexpr int kCols = 16 * (GLU ? NJ / 2 : NJ);
-    constexpr unsigned kAtOnce = NJ == 1 ? 1536 : 800;
-    const unsigned mt = w4_tiles(a, ROWS, a.over);
-    unsigned nt = (unsigned)((a.N + kCols - 1) / kCols);
-    W4Args b = a;
-    b.tiles = ROWS <= 16 ? (int)min(max((mt * nt + kAtOnce / 2) / kAtOnce, 1u), min(4u, nt)) : 1;
-    nt = (nt + b.tiles - 1) / b.tiles;
-    if (w4_eight(mt * nt, a.K))
-        w4_split_kernel<BF16, GLU, GLOG, ROWS, NJ, 8><<<mt * nt, 512, 0, s>>>(b);
+    a.tiles = p.tiles;
+    if (p.waves == 8)
+        w4_split_kernel<BF16, GLU, GLOG, ROWS, NJ, 8><<<p.grid, 512, 0, s>>>(a);
     else
-        w4_split_kernel<BF16, GLU, GLOG, ROWS, NJ, 4><<<mt * nt, 256, 0, s>>>(b);
+        w4_split_kernel<BF16, GLU, GLOG, ROWS, NJ, 4><<<p.grid, 256, 0, s>>>(a);
 }
 
 template <bool BF16, bool GLU, int GLOG, int NW, int NJ>
-void launch_wide(const W4Args &a, hipStream_t s)
+void launch_wide(const W4Launch &p, const W4Args &a, hipStream_t s)
 {
-    constexpr int kCols = 64 * NJ / (GLU ? 2 : 1);
-    unsigned mt = w4_tiles(a, 16 * NW, a.over);
-    if (mt >= 16)
-        mt = (mt + 7) / 8 * 8;
-    const unsigned grid = mt * (unsigned)((a.N + kCols - 1) / kCols);
     if (a.zeros[0] || a.zeros[1])
-        w4_wide_kernel<BF16, GLU, GLOG, true, NW, NJ><<<grid, 64 * NW, 0, s>>>(a);
+        w4_wide_kernel<BF16, GLU, GLOG, true, NW, NJ><<<p.grid, 64 * NW, 0, s>>>(a);
     else
-        w4_wide_kernel<BF16, GLU, GLOG, false, NW, NJ><<<grid, 64 * NW, 0, s>>>(a);
+        w4_wide_kernel<BF16, GLU, GLOG, false, NW, NJ><<<p.grid, 64 * NW, 0, s>>>(a);
 }
-
-// The variants: rows and columns of a tile (of a gated pair half as many columns
-// from 32 on).
-enum W4Variant { W4_4x16, W4_4x32, W4_16x16, W4_16x32, W4_32x32, W4_64x128, W4_128x256 };
-
-// The variants of a call, by estimates of their time in us: a part that a block
-// takes alone on a CU, and one that 256 blocks (one a CU, others beside them) add, each
-// with a part per 128 k.  Fitted to 1 to 4096 rows of 4096 x 4096, 2048 x 4096
-// (pairs) and 512 x 8192, and there to order the variants, which they do but for
-// near ties (4096 x 4096, us measured for the seven in this order, the narrow ones
-// with four wavefronts, - not run:
-//   1 row      6.3   7.4   6.9   8.2   10.0  35   65
-//   16        11.2  10.0   7.2   8.4   10.1  35   66
-//   64        34    27    15.6  11.9   10.7  36   67
-//   256        -     -    45    38     27    37   68
-//   1024       -     -     -     -     95    54   68
-//   4096       -     -     -     -    351   209  156
-// and 64 experts of 2048 x 4096 with 256 rows in all: 88, 75, 87, 76, 122, 103, 146;
-// with 4096: -, -, 340, 268, 300, 170, 187).
-struct W4Cost {
-    W4Variant v;
-    double rows, cols, alone, alone_k, more, more_k;
-    int at_once;   // blocks that start together, where a last few cost a round
-};
-
-template <bool GLU>
-struct W4Estimate {
-    // (a pair's narrow tiles have the work of 32 columns)
-    static constexpr W4Cost kCosts[] = {
-        {W4_4x16, 4, 16, 4.2, 0.065, 0.3, GLU ? 0.085 : 0.05, 1},
-        {W4_4x32, 4, 32, 4.1, 0.105, 0.57, 0.07, 1},
-        {W4_16x16, 16, 16, 4.8, 0.07, 0.3, GLU ? 0.095 : 0.06, 1},
-        {W4_16x32, 16, 32, 4.3, 0.127, 0.7, 0.105, 1},
-        {W4_32x32, 32, GLU ? 16 : 32, 4.7, 0.17, 1.7, 0.11, 1},
-        {W4_64x128, 64, GLU ? 64 : 128, 4.5, 0.95, 2.0, 0.70, 512},
-        {W4_128x256, 128, GLU ? 128 : 256, 6.8, 1.85, 5.7, 2.29, 256},
-    };
-    int K;
-    double k, N, fine;
-
-    explicit W4Estimate(const W4Args &a) : K(a.K), k(a.K / 128.0), N(a.N)
-    {
-        // finer groups, and zeros, cost the wide tiles' products more
-        fine = (a.group_log2 == 5 ? 1.5 : a.group_log2 == 6 ? 1.2 : 1.0) * (a.zeros[0] || a.zeros[1] ? 1.1 : 1.0);
-    }
-    double steps(const W4Cost &c) const { return (c.rows >= 64 ? fine : 1.0) * k; }
-    // 256 blocks' part of what this many tiles of rows cost.
-    double more(const W4Cost &c, double tiles) const
-    {
-        double blocks = tiles * ceil(N / c.cols);
-        if (c.at_once > 1 && blocks > 256)
-            blocks = ceil(blocks / c.at_once) * c.at_once;
-        return blocks / 256 * (c.more + c.more_k * steps(c));
-    }
-    // The variant for `rows` rows at each of n experts (half a tile is lost to
-    // each one's last rows).
-    const W4Cost &best(double n, double rows) const
-    {
-        const W4Cost *found = nullptr;
-        double least = 0;
-        for (const W4Cost &c : kCosts) {
-            if (GLU && (c.v == W4_4x32 || c.v == W4_16x32))
-                continue;
-            const double tiles = n > 1 ? n * std::max(1.0, rows / c.rows + 0.5) : ceil(rows / c.rows);
-            const double part = c.rows < 64 && w4_eight(tiles * ceil(N / c.cols), K) ? 0.7 : 1.0;
-            const double us = std::max(c.alone + part * c.alone_k * steps(c), 3 + more(c, tiles));
-            if (!found || us < least) {
-                least = us;
-                found = &c;
-            }
-        }
-        return *found;
-    }
-    // The rows of an expert up to which variant a costs less than b.
-    int limit(const W4Cost &a, const W4Cost &b) const
-    {
-        auto cost = [&](const W4Cost &c, int rows) {
-            return ceil(rows / c.rows) * ceil(N / c.cols) * (c.more + c.more_k * steps(c));
-        };
-        for (const int rows : {16, 32, 48, 64, 96, 128, 192, 256, 384, 512})
-            if (cost(b, rows + 1) < cost(a, rows + 1))
-                return rows;
-        return INT32_MAX;
-    }
-};
 
 template <bool BF16, bool GLU, int GLOG>
-void launch_variant(W4Variant v, const W4Args &a, hipStream_t s)
+void launch_variant(const W4Launch &p, const W4Args &a, hipStream_t s)
 {
     constexpr int kOne = GLU ? 2 : 1;   // 16-column blocks of the narrow tiles
-    switch (v) {
-    case W4_4x16: return launch_split<BF16, GLU, GLOG, 4, kOne>(a, s);
-    case W4_4x32: return launch_split<BF16, GLU, GLOG, 4, 2>(a, s);
-    case W4_16x16: return launch_split<BF16, GLU, GLOG, 16, kOne>(a, s);
-    case W4_16x32: return launch_split<BF16, GLU, GLOG, 16, 2>(a, s);
-    case W4_32x32: return launch_split<BF16, GLU, GLOG, 32, 2>(a, s);
-    case W4_64x128: return launch_wide<BF16, GLU, GLOG, 4, 2>(a, s);
-    case W4_128x256: return launch_wide<BF16, GLU, GLOG, 8, 4>(a, s);
+    switch (p.v) {
+    case W4_4x16: return launch_split<BF16, GLU, GLOG, 4, kOne>(p, a, s);
+    case W4_4x32: return launch_split<BF16, GLU, GLOG, 4, 2>(p, a, s);
+    case W4_16x16: return launch_split<BF16, GLU, GLOG, 16, kOne>(p, a, s);
+    case W4_16x32: return launch_split<BF16, GLU, GLOG, 16, 2>(p, a, s);
+    case W4_32x32: return launch_split<BF16, GLU, GLOG, 32, 2>(p, a, s);
+    case W4_64x128: return launch_wide<BF16, GLU, GLOG, 4, 2>(p, a, s);
+    case W4_128x256: return launch_wide<BF16, GLU, GLOG, 8, 4>(p, a, s);
     }
 }
 
-// Of experts the host knows the number alone.  The first variant is the one for
-// rows spread over all of them.  From kW4Listed rows on, where another one is better
-// for all rows at one expert, a launch in that variant takes the crowded ones if
-// there are enough of them (us without and with it: 8071 rows at 3 of 261
-// experts, pairs of 1472 x 2000: 678, 184; 348 at 8 of 67, 928 x 6792: 87, 38; 4096 at
-// 2 of 256, 2048 x 4096: 252, 128; but 256 rows spread over 64 experts, with a list
-// and a launch for nothing: 73, 83).
 template <bool BF16, bool GLU, int GLOG>
 void launch_group(const W4Args &args, hipStream_t s)
 {
-    const W4Estimate<GLU> est(args);
+    const W4Plan p = w4_plan({args.R, args.K, args.N, args.E, GLOG, args.zeros[0] || args.zeros[1], GLU});
     W4Args a = args;
-    a.over = 0;
     a.list = nullptr;
-    const W4Cost &all = est.best(1, a.R);
-    if (!a.offsets || a.E == 1)
-        return launch_variant<BF16, GLU, GLOG>(all.v, a, s);
-    const double n = std::min(a.E, a.R);
-    const W4Cost &spread = est.best(n, a.R / n);
-    const int limit = est.limit(spread, all);
-    if (a.R < kW4Listed || all.rows <= spread.rows || limit >= a.R)
-        return launch_variant<BF16, GLU, GLOG>(spread.v, a, s);
+    if (!p.listed)
+        return launch_variant<BF16, GLU, GLOG>(p.launch[0], a, s);
     W4Lists lists{};
-    lists.limit = limit;
-    lists.least_us = (float)(all.alone + all.alone_k * est.steps(all));
-    const W4Cost *both[] = {&spread, &all};
     for (int i = 0; i < 2; ++i) {
-        lists.rows[i] = (int)both[i]->rows;
-        lists.us[i] = (float)(ceil(est.N / both[i]->cols) / 256 * (both[i]->more + both[i]->more_k * est.steps(*both[i])));
         lists.count[i] = a.scratch + i;
-        lists.most[i] = (int)w4_tiles(a, lists.rows[i]);
+        lists.most[i] = p.most[i];
+        lists.rows[i] = p.rows[i];
+        lists.us[i] = p.us[i];
     }
+    lists.least_us = p.least_us;
+    lists.limit = p.limit;
     lists.list[0] = (int4 *)(a.scratch + 4);
     lists.list[1] = lists.list[0] + lists.most[0] + 1;
     w4_list_kernel<<<1, 1024, 0, s>>>(a, lists);
-    a.list = lists.list[1];
-    a.count = lists.count[1];
-    a.most = lists.most[1];
-    a.over = limit;
-    launch_variant<BF16, GLU, GLOG>(all.v, a, s);
-    a.over = 0;
-    a.list = lists.list[0];
-    a.count = lists.count[0];
-    a.most = lists.most[0];
-    launch_variant<BF16, GLU, GLOG>(spread.v, a, s);
+    for (int i = 1; i >= 0; --i) {
+        a.list = lists.list[i];
+        a.count = lists.count[i];
+        a.most = lists.most[i];
+        launch_variant<BF16, GLU, GLOG>(p.launch[i], a, s);
+    }
 }
 
 template <bool BF16, bool GLU>
