@@ -227,7 +227,9 @@ __global__ __launch_bounds__(1024) void w4_list_kernel(W4Args a, W4Lists lists)
 // 2048 take 103 us, 502 MB at 4.9 TB/s (a 1 GiB copy reaches 5.1).  A small matrix
 // ends before its stream is at full rate (1 row, 2048 x 4096: 4.0 us, of which 2.2 are
 // those of an empty launch), and 32 rows a tile are bound by what a tile costs
-// alone: its start, its share of k, the meeting (64 rows, 4096 x 4096: 9.8 us).
+// alone: its start, the loads of its share of k in turn (of 32 rows a slot of x holds
+// 64 k, so the 512 k of a wavefront are eight of them, two in flight), the meeting
+// (64 rows, 4096 x 4096: 9.3 us).
 template <bool BF16, int GLOG, int ROWS, int NJ, bool GLU>
 struct W4Stream {
     static constexpr int MR = (ROWS + 15) / 16;                  // blocks of 16 rows
@@ -575,11 +577,14 @@ __global__ __launch_bounds__(64 * NW, ROWS <= 4 && NW == 4 ? 3 : 2) void w4_spli
 // leaves their groups' sums beside them, once instead of once for each
 // wavefront that reads them.  Without zeros all columns subtract the same (16 +
 // 8) sum x, which then is what a group's products start from.
-// Bound by what a SIMD issues: of its two wavefronts' instructions a product takes 8
-// clocks and each of the four vector instructions beside it (two that make it the
-// code's 16-bit numbers, one of the group's scale) 4, so that the matrix cores are
-// busy 40% (16384 rows at 32 experts of 2048 x 4096: 354 us, 777 TFLOP/s, where
-// tiles that are not full add 12%; one matrix 4096 x 4096, 4096 rows: 148 us, 929).
+// A SIMD issues a product in 8 clocks and another vector instruction in 4.  Four go
+// with a product: two make the codes 16-bit numbers, one applies the group's scale,
+// and about one is for addresses, the scales and the preparation.  So 24 clocks of
+// issue stand against 16 of the matrix unit: 220 us of 16384 rows at 32 experts of 2048 x
+// 4096, which take 354 (777 TFLOP/s; tiles that are not full add 12%) with the matrix
+// cores busy 40%.  The rest are waits: eight wavefronts in step, one block a CU, at
+// a barrier a stage, and a tile's start and end.  One matrix 4096 x 4096, 4096 rows:
+// 144 to 148 us (929 to 954 TFLOP/s).
 template <bool BF16, int GLOG, bool GLU, bool ZEROS, int NW, int NJ>
 struct W4Wide {
     static constexpr int kRows = 16 * NW, kCols = 64 * NJ, kStage = 128, MR = 4;

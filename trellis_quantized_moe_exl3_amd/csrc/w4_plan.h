@@ -66,20 +66,20 @@ inline unsigned w4_tiles(const W4Size &s, int rows, int over = 0)
 // 16 rows 6.75, 6.3, 64 rows of group 64 11.0, 9.9; 2048 x 1024: 4.6, 4.2).
 inline bool w4_eight(double blocks, int K) { return blocks <= 256 && K >= 1024; }
 
-// Estimates of the variants' time in us: a part that a block
-// takes alone on a CU, and one that 256 blocks (one a CU, others beside them) add, each
-// with a part per 128 k.  Fitted to 1 to 4096 rows of 4096 x 4096, 2048 x 4096
-// (pairs) and 512 x 8192, and there to order the variants, which they do but for
-// near ties (4096 x 4096, us measured for the seven in this order, the narrow ones
-// with four wavefronts, - not run:
-//   1 row      6.3   7.4   6.9   8.2   10.0  35   65
-//   16        11.2  10.0   7.2   8.4   10.1  35   66
-//   64        34    27    15.6  11.9   10.7  36   67
-//   256        -     -    45    38     27    37   68
-//   1024       -     -     -     -     95    54   68
-//   4096       -     -     -     -    351   209  156
-// and 64 experts of 2048 x 4096 with 256 rows in all: 88, 75, 87, 76, 122, 103, 146;
-// with 4096: -, -, 340, 268, 300, 170, 187).
+// Estimates of the variants' time in us: a part that a block takes alone on a CU, and
+// one that 256 blocks (one a CU, others beside them) add, each with a part per 128
+// k.  Fitted to 1 to 4096 rows of 4096 x 4096, 2048 x 4096 (pairs) and 512 x 8192,
+// with four wavefronts to every narrow tile and wide tiles a twentieth slower than now;
+// they are there to order the variants, which they do but for near ties.  Measured
+// (4096 x 4096, us of the seven in this order, each as it is launched):
+//   1 row      5.8   6.8   6.5   7.6   8.8   35   50
+//   16        11.5  10.1   6.9   7.8   9.0   35   50
+//   64        36    31    15.8  11.6   9.4   35   50
+//   256      110    88    46    40    26     36   66
+//   1024     402   305   140   112    90     53   66
+//   4096    1425  1135   544   425   350    194  147
+// and 64 experts of 2048 x 4096 with 256 rows in all: 95, 78, 90, 77, 122, 101, 110;
+// with 4096: 866, 693, 352, 287, 300, 168, 167.
 struct W4Cost {
     W4Variant v;
     double rows, cols, alone, alone_k, more, more_k;
@@ -174,8 +174,10 @@ inline W4Launch w4_launch(const W4Size &s, const W4Cost &c, int over)
 // for all rows at one expert, a launch in that variant takes the crowded ones if
 // there are enough of them (us without and with it: 8071 rows at 3 of 261
 // experts, pairs of 1472 x 2000: 678, 184; 348 at 8 of 67, 928 x 6792: 87, 38; 4096 at
-// 2 of 256, 2048 x 4096: 252, 128; but 256 rows spread over 64 experts, with a list
-// and a launch for nothing: 73, 83).
+// 2 of 256, 2048 x 4096: 252, 128; but with a list and a launch for nothing 256 rows
+// spread over 64 experts: 77, 85, 1000: 115, 115).  Fewer rows are always taken as
+// spread (100 rows, 4096 x 4096, tiles of 4 rows and of 16: at 100 of 288 experts 173
+// us and 253, but at one of them 47 and 30).
 template <bool GLU>
 W4Plan w4_plan(const W4Size &s)
 {
