@@ -266,6 +266,21 @@ def test_binding_refuses_what_the_kernels_could_not_read():
             call()
 
 
+def test_a_single_column_has_no_stride():
+    # a row transposed is contiguous rows of one element, whatever the stride that
+    # a tensor names for its columns
+    f32 = (torch.float32,)
+    row = torch.zeros(1, 5)
+    assert row.t().stride() == (1, 5) and row.t().is_contiguous()
+    assert M._rows(row.t(), 5, 1, f32, -1, "x") == 1
+    assert M._rows(torch.zeros(5, 7)[:, 3:4], 5, 1, f32, -1, "x") == 7
+    for t in (torch.zeros(2, 5).t(), torch.zeros(5, 4)[:, ::2]):
+        with pytest.raises(ValueError):
+            M._rows(t, 5, 2, f32, -1, "x")
+    with pytest.raises(ValueError):
+        M._rows(torch.zeros(1, 1).expand(5, 1), 5, 1, f32, -1, "x")
+
+
 def test_weights_hold_the_memory_they_were_made_with():
     codes, scales = torch.zeros(2, 8, 16, dtype=torch.uint8), torch.ones(2, 8, 1, dtype=torch.bfloat16)
     w = M.make_w4(codes, scales)

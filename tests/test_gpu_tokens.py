@@ -396,6 +396,13 @@ def test_dropout_of_the_last_rows(cols, dtype):
     assert e.value.code == M.ERR_MISALIGNED
 
 
+def test_dropout_of_a_transposed_row():
+    row, rng = D.gauss(_gen(5), (1, 300), 1.0, torch.float32), torch.tensor([8, 9], device="cuda")
+    y = torch.zeros(300, 1, device="cuda")
+    M.dropout(row.t(), y, 0.5, rng)
+    assert torch.equal(y.double(), R.drop(row.t().double(), 0.5, rng))
+
+
 @pytest.mark.parametrize("seed,offset", [(0, 0), (-1, -1), (-1, -3), (1 << 40, (1 << 32) - 2), (7, -(1 << 63))])
 def test_dropout_counters_wrap(seed, offset):
     rng = torch.tensor([seed, offset], dtype=torch.int64, device="cuda")

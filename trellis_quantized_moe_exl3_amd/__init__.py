@@ -402,14 +402,14 @@ def _dense_dtypes(act_dtype: int):
 
 def _rows(t, rows: int, cols: int, types, device: int, what: str) -> int:
     """Row stride of a [rows][cols] activation on a GPU (unit column stride,
-    rows apart by any stride; a single row has none)."""
+    rows apart by any stride; a single row or column has none)."""
     if t.shape != (rows, cols) or t.dtype not in types or t.get_device() != device:
         raise ValueError(f"{what}: expected [{rows}][{cols}] {types[0]} on GPU {device}, got {tuple(t.shape)} "
                          f"{t.dtype} on {t.device}")
     ld, step = t.stride()
     if rows <= 1:
         ld = cols
-    if step != 1 or ld < cols:
+    if (step != 1 and cols != 1) or ld < cols:
         raise ValueError(f"{what}: rows must be contiguous and apart, got strides {t.stride()}")
     return ld
 
